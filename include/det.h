@@ -41,7 +41,17 @@ extern "C" {
 /* DET_I32 is accepted by det_scan only (Warp "Deterministic Execution", section "Pattern 2:
  * Slot Allocation": the count-scan-write workflow's prefix scan over int32 slot counts); its
  * sums wrap modulo 2^32 as two's complement, which no association order can change. */
-typedef enum { DET_F32 = 0, DET_F64 = 1, DET_I32 = 2 } det_dtype;
+/* DET_F16, DET_BF16: storage types of the language-model operators only (they compute in f32).
+ * DET_E4M3 (8-bit floats: 4 exponent and 3 mantissa bits, largest 448, no infinity): the output
+ * type of det_rms_norm only. */
+typedef enum {
+    DET_F32 = 0,
+    DET_F64 = 1,
+    DET_I32 = 2,
+    DET_F16 = 3,
+    DET_BF16 = 4,
+    DET_E4M3 = 5
+} det_dtype;
 
 typedef enum {
     DET_SUCCESS = 0,
@@ -212,6 +222,147 @@ det_status det_scatter_add_running(const void* values, const int32_t* index, int
                                    int64_t row_len, det_dtype dtype, void* out, int64_t num_out,
                                    void* prev, int64_t* n_skipped, void* ws, size_t ws_bytes,
                                    void* stream);
+
+/* ------------------------------------------------------------------ language-model operators
+ *
+ * Norm, relative position bias and token log probabilities, forward and backward.  dtype is
+ * DET_F32, DET_F16 or DET_BF16 (else DET_ERROR_UNSUPPORTED): the type of every tensor not
+ * declared float, int32 or int64 below.  Everything between loading and the one rounding on
+ * storing is f32 (the bias table's last sums f64).  Every sum's order is fixed by the sizes
+ * that its comment names, never by the launch, so the bits depend on the arguments alone; the
+ * results of a row depend on that row alone, not on the rows beside it or their number.
+ * Strides count elements; the innermost dimension is contiguous.  No wait inside any kernel
+ * depends on another workgroup. */
+
+/* Root-mean-square norm of rows, with the residual's addition before and 8-bit codes behind:
+ *   h = x + residual (x where residual is NULL; used unrounded)
+ *   rstd = 1 / sqrt(sum(h^2) / d + eps);  y = (h * rstd) * weight
+ *   y_dtype DET_E4M3: for every group of neighbouring elements of a row, m = max(|y|, 2^-100),
+ *   code = round(y * (448 / m)), scale = m / 448.
+ * Order of the row's sum: fixed by d.
+ * x, residual:  [rows] rows of d elements, x_stride and residual_stride apart (>= d when
+ *               rows > 1).  residual may be NULL.
+ * weight:       [d].
+ * h:            [rows * d], x + residual rounded to dtype; NULL if and only if residual is.
+ *               h may be x or residual itself where that is contiguous (written in place).
+ * y:            [rows * d] of y_dtype, which is dtype or DET_E4M3.
+ * group:        for codes 32, 64 or 128 elements (a row's last group may be shorter), or 0 for
+ *               one scale a row; 0 otherwise.
+ * scales:       float [rows * ceil(d / group)] (group 0: [rows]) for codes, else NULL.
+ * rstd:         NULL, or float [rows] for the backward pass.
+ * d >= 1 when rows > 0; eps >= 0 and finite.  rows * d up to 2^62. */
+det_status det_rms_norm(const void* x, int64_t x_stride, const void* residual,
+                        int64_t residual_stride, const void* weight, int64_t rows, int64_t d,
+                        det_dtype dtype, double eps, void* h, void* y, det_dtype y_dtype,
+                        int64_t group, float* scales, float* rstd, void* stream);
+
+/* Bytes of workspace det_rms_norm_backward needs (0 when the arguments are invalid). */
+size_t det_rms_norm_backward_workspace_size(int64_t rows, int64_t d, det_dtype dtype);
+
+/* Gradients of det_rms_norm's y in dtype: with xhat = h * rstd,
+ *   dx = rstd * (dy weight - xhat * sum(dy weight xhat) / d) (+ dh)
+ *   dweight = sum over the rows of dy * xhat
+ * dx is also the gradient of the residual.
+ * dy, h:    [rows] rows of d elements, dy_stride and h_stride apart; h as det_rms_norm wrote it
+ *           (x itself where there was no residual).
+ * rstd:     float [rows], as det_rms_norm wrote it.
+ * dh:       NULL, or the gradient that reaches h from elsewhere, dh_stride apart.
+ * dx:       [rows * d]; may be dy, h or dh itself where that is contiguous and d <= 16384.
+ * dweight:  [d], written (zero for no rows).
+ * Order: a row's sum fixed by d; dweight's fixed by (rows, d): strips of rows in ascending
+ * order, then the strips. */
+det_status det_rms_norm_backward(const void* dy, int64_t dy_stride, const void* h,
+                                 int64_t h_stride, const void* weight, const float* rstd,
+                                 const void* dh, int64_t dh_stride, int64_t rows, int64_t d,
+                                 det_dtype dtype, void* dx, void* dweight, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* det_relative_bias flags */
+#define DET_BIAS_BIDIRECTIONAL 1u /* own buckets for keys after the query */
+#define DET_BIAS_CAUSAL 2u        /* keys after the query are masked */
+#define DET_BIAS_MAX_BUCKETS 256
+
+/* A learned relative position bias by buckets, alone or added to attention scores:
+ *   out[b, h, i, j] = (scores[b, h, i, j] +) table[bucket(j - i - offset_b), h], and -inf
+ * where the masks leave nothing: j > i + offset_b when DET_BIAS_CAUSAL, and j or i + offset_b at
+ * or past lengths[b].  A masked place is -inf whatever its score holds.
+ * bucket(r): a side has n = num_buckets buckets (half of them, rounded down, when
+ * DET_BIAS_BIDIRECTIONAL; r > 0 then takes the second half, else r > 0 counts as distance 0).
+ * Distances a below n/2 (rounded down) have a bucket each; beyond, bucket n/2 + floor((n - n/2)
+ * log(a / (n/2)) / log(max_distance / (n/2))), at most n - 1.  The borders are computed in whole
+ * numbers: a distance on a border lies above it.
+ * table:     [num_buckets * heads], a row for each bucket.
+ * q_offset:  position of query 0 among the keys; q_offsets: NULL, or int32 [batch], one for each
+ *            sequence in its place.
+ * lengths:   NULL, or int32 [batch]; values above q or k mean no padding, below 1 that every
+ *            place is masked.
+ * scores:    NULL, or [batch, heads, q, k] with strides (stride_b, stride_h, stride_q, 1); a
+ *            stride may be 0.
+ * out:       [batch * heads * q * k].  May be scores itself where that is contiguous.
+ * 2 <= n per side, num_buckets <= DET_BIAS_MAX_BUCKETS, n/2 < max_distance < 2^31, 1 <= heads < 65536,
+ * |q_offset| < 2^40.  Nothing is summed but the score and its bias. */
+det_status det_relative_bias(const void* table, int64_t num_buckets, int64_t heads,
+                             int64_t max_distance, unsigned flags, int64_t batch, int64_t q,
+                             int64_t k, int64_t q_offset, const int32_t* q_offsets,
+                             const int32_t* lengths, const void* scores, int64_t stride_b,
+                             int64_t stride_h, int64_t stride_q, det_dtype dtype, void* out,
+                             void* stream);
+
+/* Bytes of workspace det_relative_bias_backward needs (0 when the arguments are invalid). */
+size_t det_relative_bias_backward_workspace_size(int64_t batch, int64_t heads, int64_t q,
+                                                 int64_t k, int64_t num_buckets, det_dtype dtype);
+
+/* The table's gradient: dtable[c, h] = sum of dout[b, h, i, j] over the unmasked places with
+ * bucket c.  dout at masked places is not used, whatever it holds.
+ * dout:     [batch, heads, q, k] with strides (stride_b, stride_h, stride_q, 1).
+ * dtable:   [num_buckets * heads], written.
+ * dscores:  NULL, or [batch * heads * q * k]: dout with zeros at the masked places (the gradient
+ *           of the scores).  May be dout itself where that is contiguous.
+ * The other arguments as for det_relative_bias.
+ * Order, fixed by (batch, q, k): every diagonal of a strip of query rows in row order, the
+ * diagonals of a bucket, then the strips in f64. */
+det_status det_relative_bias_backward(const void* dout, int64_t stride_b, int64_t stride_h,
+                                      int64_t stride_q, int64_t num_buckets, int64_t heads,
+                                      int64_t max_distance, unsigned flags, int64_t batch,
+                                      int64_t q, int64_t k, int64_t q_offset,
+                                      const int32_t* q_offsets, const int32_t* lengths,
+                                      det_dtype dtype, void* dtable, void* dscores, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+#define DET_LOGPROB_MAX_TOP 64
+#define DET_LOGPROB_MAX_TOP_VOCAB 1048576
+
+/* Log probabilities of given tokens: with z = scale * logits, per row
+ *   lse = log(sum exp z);  logp = z[target] - lse;  entropy = -sum p log p, p = exp(z - lse)
+ *   top_logp, top_ids: the `top` largest logits, descending, ties to the lower index (both zeros
+ *   alike, a NaN like -inf).
+ * logits:    [rows] rows of vocab elements, row_stride apart (>= vocab when rows > 1).
+ * targets:   int64 [rows]; one outside [0, vocab) is not scored: its logp is 0.
+ * logp, entropy, lse:  float [rows].
+ * top:       0 .. min(vocab, DET_LOGPROB_MAX_TOP); above 0, vocab is at most
+ *            DET_LOGPROB_MAX_TOP_VOCAB (DET_ERROR_TOO_LARGE).
+ * top_logp, top_ids:  float and int64 [rows * top], NULL when top is 0.
+ * A row of -inf alone has lse -inf, entropy 0, logp -inf.  vocab >= 1 when rows > 0; scale > 0
+ * and finite.  Order of a row's sums: fixed by vocab. */
+det_status det_token_logprobs(const void* logits, int64_t row_stride, const int64_t* targets,
+                              int64_t rows, int64_t vocab, det_dtype dtype, double scale,
+                              float* logp, float* entropy, float* lse, int64_t top,
+                              float* top_logp, int64_t* top_ids, void* stream);
+
+/* Gradient of det_token_logprobs for the logits:
+ *   dlogits = scale * (dlogp * (hit - p) - dentropy * p * (log p + entropy))
+ * where hit is 1 at the target; a target outside [0, vocab) takes no dlogp.
+ * lse, entropy:  float [rows], as det_token_logprobs wrote them for these logits and scale.
+ * dlogp:         float [rows].
+ * dentropy:      NULL (then entropy may be NULL too), or float [rows].
+ * dlogits:       [rows] rows of vocab elements, dlogits_stride apart; may be logits itself (with
+ *                its stride).  A row of -inf alone has gradient 0. */
+det_status det_token_logprobs_backward(const void* logits, int64_t row_stride,
+                                       const int64_t* targets, const float* lse,
+                                       const float* dlogp, const float* entropy,
+                                       const float* dentropy, int64_t rows, int64_t vocab,
+                                       det_dtype dtype, double scale, void* dlogits,
+                                       int64_t dlogits_stride, void* stream);
 
 /* ------------------------------------------------------------------ introspection */
 

@@ -74,6 +74,72 @@ det_status scatter_running_launch(const void* values, const int32_t* index, int6
                                   int64_t row_len, det_dtype dt, void* out, int64_t num_out,
                                   void* prev, int64_t* n_skipped, void* ws, hipStream_t s);
 
+// ---- language-model operators (arguments checked by the caller)
+inline size_t lm_size(det_dtype d) { return d == DET_F32 ? 4 : d == DET_E4M3 ? 1 : 2; }
+
+struct NormCall {
+    const void *x, *residual, *weight;
+    void *h, *y;
+    float *scales, *rstd;
+    int64_t x_stride, residual_stride, rows, d, group;
+    float eps;
+    det_dtype dtype;
+    bool codes;        // y holds e4m3 codes
+};
+det_status norm_launch(const NormCall& c, hipStream_t s);
+
+struct NormBackCall {
+    const void *dy, *h, *weight, *dh;
+    const float* rstd;
+    void *dx, *dweight;
+    int64_t dy_stride, h_stride, dh_stride, rows, d;
+    det_dtype dtype;
+};
+size_t norm_backward_workspace(int64_t rows, int64_t d);
+det_status norm_backward_launch(const NormBackCall& c, void* ws, hipStream_t s);
+
+constexpr int kBiasMaxSide = 128;      // buckets of one side of the relative position bias
+struct BiasCall {
+    const void *table, *scores;        // table NULL: the scores alone, masked
+    void* out;
+    int64_t sb, sh, sq;                // strides of scores (backward: of dout)
+    int64_t batch, heads, q, k, q_offset, max_distance;
+    const int32_t *q_offsets, *lengths;
+    int buckets;
+    bool bidirectional, causal;
+    float fill;                        // what a masked place of out gets
+    det_dtype dtype;
+};
+// first distance of each of a side's n buckets
+void relbias_starts(int n, int64_t distance, int* starts);
+det_status bias_launch(const BiasCall& c, hipStream_t s);
+size_t bias_backward_workspace(int64_t batch, int64_t heads, int64_t q, int64_t k, int buckets);
+det_status bias_backward_launch(const BiasCall& c, const void* dout, void* dtable, void* ws,
+                                hipStream_t s);
+
+struct LogpCall {
+    const void* logits;
+    const int64_t* targets;
+    float *logp, *entropy, *lse, *top_logp;
+    int64_t* top_ids;
+    int64_t stride, rows, vocab;
+    int top;
+    float scale;
+    det_dtype dtype;
+};
+det_status logprob_launch(const LogpCall& c, hipStream_t s);
+
+struct LogpBackCall {
+    const void* logits;
+    const int64_t* targets;
+    const float *lse, *dlogp, *entropy, *dentropy;
+    void* dlogits;
+    int64_t stride, dstride, rows, vocab;
+    float scale;
+    det_dtype dtype;
+};
+det_status logprob_backward_launch(const LogpBackCall& c, hipStream_t s);
+
 // Workgroups of `block` threads of kernel `fn` with `dyn_lds` bytes of dynamic LDS that are
 // resident on the current device at once (occupancy x compute units), cached per device,
 // kernel and LDS size; 0 if the runtime cannot tell.  *per_cu (optional) receives the

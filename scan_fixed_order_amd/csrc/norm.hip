@@ -1,0 +1,576 @@
+// norm.hip -- root-mean-square norm of rows, with the residual's addition before it, 8-bit
+// output with scales behind it, and its backward pass.
+//
+// Mathematics, per row of d elements, everything between the load and the last rounding in f32:
+//   h = x + residual;  rstd = 1 / sqrt(sum(h^2) / d + eps);  y = h * rstd * weight
+//   8 bits: m = max |y| of a group (at least 2^-100); code = e4m3(y * (448 / m)); scale = m / 448
+//   dx = rstd * (dy w - xhat * sum(dy w xhat) / d) + dh,  xhat = h * rstd;  dweight = sum of
+//   dy * xhat over the rows.
+//
+// Order: lane t of the row's team holds elements 8 (t + j * team) .. + 8 for j = 0, 1, ...; it
+// adds its own in that order, the wave adds its lanes by the adjacent-lanes tree, and the wave
+// sums are added in wave order.  The team's size depends on d alone, so a row's bits depend
+// neither on the other rows nor on their number.  dweight: strips of rows in ascending order,
+// then the strips (k_col_sums); the strip length depends on (rows, d) alone.
+#include "det_internal.h"
+#include "lm_device.h"
+
+namespace det {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kTinyMax = 0x1p-100f;
+
+// Lanes per row: one wave up to 512 elements, else enough for two vectors a lane where that
+// fits (the row stays in registers between the sum and the output).
+template <int TEAM>
+struct Team {
+    static constexpr int kBlock = TEAM < 256 ? 256 : TEAM;
+    static constexpr int kRows = kBlock / TEAM;      // rows a workgroup holds at a time
+    static constexpr int kWaves = TEAM / 64;
+};
+
+// Sum over the team in the fixed order above; uniform over the team.  `slots`: kWaves floats of
+// LDS.  Every thread of the workgroup calls it.
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float v, float* slots) {
+    v = wave_pw(v);
+    if constexpr (TEAM > 64) {
+        if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = slots[0];
+#pragma unroll
+        for (int w = 1; w < TEAM / 64; ++w) v = v + slots[w];
+    }
+    return v;
+}
+
+template <int TEAM>
+__device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t* slots) {
+    v = wave_max(v);
+    if constexpr (TEAM > 64) {
+        if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = slots[0];
+#pragma unroll
+        for (int w = 1; w < TEAM / 64; ++w) v = umax(v, slots[w]);
+    }
+    return v;
+}
+
+// Largest |y| of 8 elements as its bits: they order like the magnitudes, and a NaN's lie above
+// infinity's, so a NaN reaches its group's scale.
+__device__ __forceinline__ uint32_t max_bits(const float (&y)[kVec]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) m = umax(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+    return m;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t n, const float (&y)[kVec], float f) {
+    uint32_t lo = 0, hi = 0;
+    lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0] * f, y[1] * f, (int)lo, false);
+    lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2] * f, y[3] * f, (int)lo, true);
+    hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4] * f, y[5] * f, (int)hi, false);
+    hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[6] * f, y[7] * f, (int)hi, true);
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
+    if (n >= kVec) {
+        *reinterpret_cast<u32x2_a1*>(p) = u32x2{lo, hi};
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (i < n) p[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+    }
+}
+
+struct NormArgs {
+    const void* x;
+    const void* res;      // NULL: none
+    const void* w;
+    void* h;              // written when res is given
+    void* y;              // of the input's type, or codes
+    float* scales;
+    float* rstd;          // NULL: not written
+    int64_t x_stride, res_stride, rows, d;
+    int group;            // 8 bits: 32, 64, 128, or 0 for the row
+    float eps;
+};
+
+// y or codes of one vector; m: the row's largest |y| bits where the group is the row
+template <typename T, bool Q8>
+__device__ __forceinline__ void put(const NormArgs& a, int64_t row, int64_t c, int64_t n,
+                                    const float (&y)[kVec], uint32_t m) {
+    if constexpr (!Q8) {
+        if (n > 0) write8(static_cast<T*>(a.y) + row * a.d + c, n, y);
+    } else {
+        if (a.group) {
+            m = max_bits(y);      // every lane of the wave takes part; lanes past the row hold 0
+            m = umax(m, xor_partner<1>(m));
+            m = umax(m, xor_partner<2>(m));
+            if (a.group >= 64) m = umax(m, xor_partner<4>(m));
+            if (a.group >= 128) m = umax(m, xor_partner<8>(m));
+        }
+        const float top = __uint_as_float(umax(m, __float_as_uint(kTinyMax)));
+        if (n > 0) {
+            store_codes(static_cast<uint8_t*>(a.y) + row * a.d + c, n, y, kE4m3Max / top);
+            if (a.group) {
+                if (c % a.group == 0)
+                    a.scales[row * ((a.d + a.group - 1) / a.group) + c / a.group] = top / kE4m3Max;
+            } else if (c == 0) {
+                a.scales[row] = top / kE4m3Max;
+            }
+        }
+    }
+}
+
+// One row per team, the row in registers: NV vectors a lane.  Bound by HBM: every element is
+// read once and written once.
+template <typename T, int TEAM, int NV, bool RES, bool Q8>
+__global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
+    constexpr int kRows = Team<TEAM>::kRows, kWaves = Team<TEAM>::kWaves;
+    __shared__ float s_sum[kRows][kWaves];
+    __shared__ uint32_t s_max[kRows][kWaves];
+    const int team = threadIdx.x / TEAM, t = threadIdx.x % TEAM;
+    for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows;
+         first += (int64_t)gridDim.x * kRows) {
+    const bool live = first + team < a.rows;
+    const int64_t row = live ? first + team : a.rows - 1;   // a spare team repeats the last row, unwritten
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    const T* res = static_cast<const T*>(a.res) + (RES ? row * a.res_stride : 0);
+    const T* w = static_cast<const T*>(a.w);
+
+    float h[NV][kVec];
+    float r[NV][kVec];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = (int64_t)kVec * (t + j * TEAM);
+        read8(x + c, a.d - c, 0.0f, h[j]);
+        if constexpr (RES) read8(res + c, a.d - c, 0.0f, r[j]);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if constexpr (RES) {
+            const int64_t c = (int64_t)kVec * (t + j * TEAM);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) h[j][i] += r[j][i];
+            if (live && a.d > c) write8(static_cast<T*>(a.h) + row * a.d + c, a.d - c, h[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sum = fmaf(h[j][i], h[j][i], sum);
+    }
+    sum = team_sum<TEAM>(sum, s_sum[team % kRows]);
+    const float rstd = 1.0f / sqrtf(sum / (float)a.d + a.eps);
+    if (a.rstd && live && t == 0) a.rstd[row] = rstd;
+
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = (int64_t)kVec * (t + j * TEAM);
+        float g[kVec];
+        read8(w + c, a.d - c, 0.0f, g);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) h[j][i] = (h[j][i] * rstd) * g[i];
+        if constexpr (Q8) m = umax(m, max_bits(h[j]));
+    }
+    if constexpr (Q8) {
+        if (!a.group) m = team_max<TEAM>(m, s_max[team % kRows]);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = (int64_t)kVec * (t + j * TEAM);
+        put<T, Q8>(a, row, c, live ? a.d - c : 0, h[j], m);
+    }
+    if constexpr (TEAM > 64) __syncthreads();      // the LDS slots are written again
+    }
+}
+
+// Rows longer than the registers hold: the same order in a loop, the row read again for the
+// output (and for a whole row's scale).
+template <typename T, bool RES, bool Q8>
+__global__ __launch_bounds__(1024) void k_rms_norm_long(NormArgs a) {
+    constexpr int TEAM = 1024;
+    __shared__ float s_sum[16];
+    __shared__ uint32_t s_max[16];
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    const T* res = static_cast<const T*>(a.res) + (RES ? row * a.res_stride : 0);
+    const T* w = static_cast<const T*>(a.w);
+    const int64_t steps = (a.d + TEAM * kVec - 1) / (TEAM * kVec);
+    const auto sums = [&](int64_t c, float (&h)[kVec]) {
+        read8(x + c, a.d - c, 0.0f, h);
+        if constexpr (RES) {
+            float r[kVec];
+            read8(res + c, a.d - c, 0.0f, r);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) h[i] += r[i];
+        }
+    };
+    float sum = 0.0f;
+    for (int64_t j = 0; j < steps; ++j) {
+        const int64_t c = kVec * (threadIdx.x + j * TEAM);
+        float h[kVec];
+        sums(c, h);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sum = fmaf(h[i], h[i], sum);
+    }
+    sum = team_sum<TEAM>(sum, s_sum);
+    const float rstd = 1.0f / sqrtf(sum / (float)a.d + a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+    const auto outputs = [&](int64_t c, float (&h)[kVec], bool last) {
+        sums(c, h);
+        float g[kVec];
+        read8(w + c, a.d - c, 0.0f, g);
+        if constexpr (RES) {
+            // only now: h may be x itself
+            if (last && a.d > c) write8(static_cast<T*>(a.h) + row * a.d + c, a.d - c, h);
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) h[i] = (h[i] * rstd) * g[i];
+    };
+    uint32_t m = 0;
+    if constexpr (Q8) {
+        if (!a.group) {
+            for (int64_t j = 0; j < steps; ++j) {
+                float h[kVec];
+                outputs(kVec * (threadIdx.x + j * TEAM), h, false);
+                m = umax(m, max_bits(h));
+            }
+            m = team_max<TEAM>(m, s_max);
+        }
+    }
+    for (int64_t j = 0; j < steps; ++j) {
+        const int64_t c = kVec * (threadIdx.x + j * TEAM);
+        float h[kVec];
+        outputs(c, h, true);
+        put<T, Q8>(a, row, c, a.d - c, h, m);
+    }
+    __syncthreads();      // the LDS slots are written again
+    }
+}
+
+// ---------------------------------------------------------------- backward
+
+struct NormBackArgs {
+    const void* dy;
+    const void* h;
+    const void* w;
+    const void* dh;       // NULL: none
+    const float* rstd;
+    void* dx;
+    float* part;          // [strips][d], the strips' sums of dy * xhat
+    int64_t dy_stride, h_stride, dh_stride, rows, d, strip;
+};
+
+// A team walks its strip of rows and keeps the strip's column sums in registers.  Bound by HBM.
+template <typename T, int TEAM, int NV, bool DH>
+__global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBackArgs a) {
+    constexpr int kRows = Team<TEAM>::kRows, kWaves = Team<TEAM>::kWaves;
+    __shared__ float s_sum[2][kRows][kWaves];
+    const int team = threadIdx.x / TEAM, t = threadIdx.x % TEAM;
+    const int64_t strip = (int64_t)blockIdx.x * kRows + team;
+    const int64_t begin = strip * a.strip;
+    const T* w = static_cast<const T*>(a.w);
+    float g[NV][kVec], acc[NV][kVec];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = (int64_t)kVec * (t + j * TEAM);
+        read8(w + c, a.d - c, 0.0f, g[j]);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) acc[j][i] = 0.0f;
+    }
+    // every team of the workgroup takes the same number of steps (barriers)
+    for (int64_t k = 0; k < a.strip; ++k) {
+        const int64_t row = begin + k < a.rows ? begin + k : a.rows - 1;
+        const bool live = begin + k < a.rows;
+        const T* hp = static_cast<const T*>(a.h) + row * a.h_stride;
+        const T* dyp = static_cast<const T*>(a.dy) + row * a.dy_stride;
+        const T* dhp = static_cast<const T*>(a.dh) + (DH ? row * a.dh_stride : 0);
+        const float rstd = a.rstd[row];
+        float h[NV][kVec], dy[NV][kVec], e[NV][kVec];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = (int64_t)kVec * (t + j * TEAM);
+            read8(hp + c, a.d - c, 0.0f, h[j]);
+            read8(dyp + c, a.d - c, 0.0f, dy[j]);
+            if constexpr (DH) read8(dhp + c, a.d - c, 0.0f, e[j]);
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                h[j][i] *= rstd;
+                const float p = dy[j][i] * h[j][i];
+                if (live) acc[j][i] += p;
+                dy[j][i] *= g[j][i];
+                sum = fmaf(dy[j][i], h[j][i], sum);
+            }
+        }
+        const float mean = team_sum<TEAM>(sum, s_sum[k & 1][team % kRows]) / (float)a.d;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = (int64_t)kVec * (t + j * TEAM);
+            float o[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                o[i] = rstd * fmaf(-h[j][i], mean, dy[j][i]);
+                if constexpr (DH) o[i] += e[j][i];
+            }
+            if (live && a.d > c) write8(static_cast<T*>(a.dx) + row * a.d + c, a.d - c, o);
+        }
+    }
+    if (begin < a.rows) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = (int64_t)kVec * (t + j * TEAM);
+            if (a.d > c) write8(a.part + strip * a.d + c, a.d - c, acc[j]);
+        }
+    }
+}
+
+// The dx of rows longer than the registers hold (the row read twice); the strips' sums are
+// k_rms_norm_strips's.
+template <typename T, bool DH>
+__global__ __launch_bounds__(1024) void k_rms_norm_backward_long(NormBackArgs a) {
+    constexpr int TEAM = 1024;
+    __shared__ float s_sum[16];
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* w = static_cast<const T*>(a.w);
+    const T* hp = static_cast<const T*>(a.h) + row * a.h_stride;
+    const T* dyp = static_cast<const T*>(a.dy) + row * a.dy_stride;
+    const T* dhp = static_cast<const T*>(a.dh) + (DH ? row * a.dh_stride : 0);
+    const float rstd = a.rstd[row];
+    const int64_t steps = (a.d + TEAM * kVec - 1) / (TEAM * kVec);
+    const auto both = [&](int64_t c, float (&h)[kVec], float (&dy)[kVec]) {
+        float g[kVec];
+        read8(hp + c, a.d - c, 0.0f, h);
+        read8(dyp + c, a.d - c, 0.0f, dy);
+        read8(w + c, a.d - c, 0.0f, g);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            h[i] *= rstd;
+            dy[i] *= g[i];
+        }
+    };
+    float sum = 0.0f;
+    for (int64_t j = 0; j < steps; ++j) {
+        float h[kVec], dy[kVec];
+        both(kVec * (threadIdx.x + j * TEAM), h, dy);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sum = fmaf(dy[i], h[i], sum);
+    }
+    const float mean = team_sum<TEAM>(sum, s_sum) / (float)a.d;
+    for (int64_t j = 0; j < steps; ++j) {
+        const int64_t c = kVec * (threadIdx.x + j * TEAM);
+        float h[kVec], dy[kVec], e[kVec];
+        both(c, h, dy);
+        if constexpr (DH) read8(dhp + c, a.d - c, 0.0f, e);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            dy[i] = rstd * fmaf(-h[i], mean, dy[i]);
+            if constexpr (DH) dy[i] += e[i];
+        }
+        if (a.d > c) write8(static_cast<T*>(a.dx) + row * a.d + c, a.d - c, dy);
+    }
+    __syncthreads();      // the LDS slots are written again
+    }
+}
+
+// The strips' sums of dy * xhat for long rows: a lane owns 8 columns of one strip.
+template <typename T>
+__global__ __launch_bounds__(256) void k_rms_norm_strips(NormBackArgs a) {
+    const int64_t c = kVec * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    const int64_t strip = blockIdx.y, begin = strip * a.strip;
+    if (c >= a.d) return;
+    const int64_t end = begin + a.strip < a.rows ? begin + a.strip : a.rows;
+    float acc[kVec] = {};
+    for (int64_t row = begin; row < end; ++row) {
+        float h[kVec], dy[kVec];
+        read8(static_cast<const T*>(a.h) + row * a.h_stride + c, a.d - c, 0.0f, h);
+        read8(static_cast<const T*>(a.dy) + row * a.dy_stride + c, a.d - c, 0.0f, dy);
+        const float rstd = a.rstd[row];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const float p = dy[i] * (h[i] * rstd);
+            acc[i] += p;
+        }
+    }
+    write8(a.part + strip * a.d + c, a.d - c, acc);
+}
+
+// dweight[c] = the strips' sums added: lane group k of 64 adds strips k, k + 64, ... in that
+// order, then the 64 groups join by a halving tree.  16 lanes x 4 columns a workgroup.
+template <typename T>
+__global__ __launch_bounds__(1024) void k_col_sums(const float* part, int64_t strips, int64_t d,
+                                                   T* out) {
+    __shared__ float s[64][64];
+    const int quad = threadIdx.x & 15, grp = threadIdx.x >> 4;
+    const int64_t c = (int64_t)blockIdx.x * 64 + 4 * quad;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c + 4 <= d) {
+#pragma unroll 4
+        for (int64_t k = grp; k < strips; k += 64) {
+            const f32x4 q = *reinterpret_cast<const f32x4_a4*>(part + k * d + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += q[i];
+        }
+    } else {
+        for (int64_t k = grp; k < strips; k += 64)
+            for (int i = 0; i < 4; ++i)
+                if (c + i < d) v[i] += part[k * d + c + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[grp][4 * quad + i] = v[i];
+    __syncthreads();
+    for (int n = 32; n > 0; n >>= 1) {
+        for (int i = threadIdx.x; i < n * 64; i += 1024) s[i >> 6][i & 63] += s[(i >> 6) + n][i & 63];
+        __syncthreads();
+    }
+    const int64_t o = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && o < d) out[o] = (T)s[0][threadIdx.x];
+}
+
+// ---------------------------------------------------------------- launches
+
+// Rows a strip: enough strips to fill the GPU (512 teams of 256 lanes at the widest), at least
+// 4 rows each so that the strips' sums stay small beside the rows.
+int64_t strip_rows(int64_t rows, int64_t d) {
+    const int64_t teams = d <= 512 ? 2048 : 512;
+    const int64_t r = (rows + teams - 1) / teams;
+    return r < 4 ? 4 : r;
+}
+
+// workgroups a launch starts at most (a grid holds fewer than 2^32 threads); each walks the rows
+unsigned grid_of(int64_t wgs) { return (unsigned)(wgs < (1 << 21) ? wgs : (1 << 21)); }
+
+constexpr int64_t kRowInRegs = 16384;        // forward: up to 2 vectors a lane of 1024
+
+template <typename T, int TEAM, int NV>
+void norm_in_regs(const NormArgs& a, bool q8, hipStream_t s) {
+    const dim3 grid(grid_of((a.rows + Team<TEAM>::kRows - 1) / Team<TEAM>::kRows));
+    const dim3 block(Team<TEAM>::kBlock);
+    KernelTimer kt("k_rms_norm", s);
+    if (a.res) {
+        if (q8)
+            k_rms_norm<T, TEAM, NV, true, true><<<grid, block, 0, s>>>(a);
+        else
+            k_rms_norm<T, TEAM, NV, true, false><<<grid, block, 0, s>>>(a);
+    } else {
+        if (q8)
+            k_rms_norm<T, TEAM, NV, false, true><<<grid, block, 0, s>>>(a);
+        else
+            k_rms_norm<T, TEAM, NV, false, false><<<grid, block, 0, s>>>(a);
+    }
+}
+
+template <typename T>
+void norm_typed(const NormArgs& a, bool q8, hipStream_t s) {
+    if (a.d <= 512) {
+        norm_in_regs<T, 64, 1>(a, q8, s);
+    } else if (a.d <= 1024) {
+        norm_in_regs<T, 64, 2>(a, q8, s);
+    } else if (a.d <= 2048) {
+        norm_in_regs<T, 256, 1>(a, q8, s);
+    } else if (a.d <= 4096) {
+        norm_in_regs<T, 256, 2>(a, q8, s);
+    } else if (a.d <= 6144) {
+        norm_in_regs<T, 256, 3>(a, q8, s);
+    } else if (a.d <= 8192) {
+        norm_in_regs<T, 512, 2>(a, q8, s);
+    } else if (a.d <= kRowInRegs) {
+        norm_in_regs<T, 1024, 2>(a, q8, s);
+    } else {
+        const dim3 grid(grid_of(a.rows)), block(1024);
+        KernelTimer kt("k_rms_norm_long", s);
+        if (a.res) {
+            if (q8)
+                k_rms_norm_long<T, true, true><<<grid, block, 0, s>>>(a);
+            else
+                k_rms_norm_long<T, true, false><<<grid, block, 0, s>>>(a);
+        } else {
+            if (q8)
+                k_rms_norm_long<T, false, true><<<grid, block, 0, s>>>(a);
+            else
+                k_rms_norm_long<T, false, false><<<grid, block, 0, s>>>(a);
+        }
+    }
+}
+
+template <typename T, int TEAM, int NV>
+void back_in_regs(const NormBackArgs& a, int64_t strips, hipStream_t s) {
+    const dim3 grid((unsigned)((strips + Team<TEAM>::kRows - 1) / Team<TEAM>::kRows));
+    const dim3 block(Team<TEAM>::kBlock);
+    KernelTimer kt("k_rms_norm_backward", s);
+    if (a.dh)
+        k_rms_norm_backward<T, TEAM, NV, true><<<grid, block, 0, s>>>(a);
+    else
+        k_rms_norm_backward<T, TEAM, NV, false><<<grid, block, 0, s>>>(a);
+}
+
+template <typename T>
+det_status back_typed(const NormBackArgs& a, void* dw, hipStream_t s) {
+    const int64_t strips = (a.rows + a.strip - 1) / a.strip;
+    if (a.rows > 0) {
+        if (a.d <= 512) {
+            back_in_regs<T, 64, 1>(a, strips, s);
+        } else if (a.d <= 2048) {
+            back_in_regs<T, 256, 1>(a, strips, s);
+        } else if (a.d <= 4096) {
+            back_in_regs<T, 512, 1>(a, strips, s);
+        } else if (a.d <= 8192) {
+            back_in_regs<T, 1024, 1>(a, strips, s);
+        } else if (a.d <= kRowInRegs) {
+            back_in_regs<T, 1024, 2>(a, strips, s);
+        } else {
+            {
+                KernelTimer kt("k_rms_norm_backward_long", s);
+                if (a.dh)
+                    k_rms_norm_backward_long<T, true><<<dim3(grid_of(a.rows)), dim3(1024), 0, s>>>(a);
+                else
+                    k_rms_norm_backward_long<T, false><<<dim3(grid_of(a.rows)), dim3(1024), 0, s>>>(a);
+            }
+            KernelTimer kt("k_rms_norm_strips", s);
+            const dim3 grid((unsigned)((a.d + 256 * kVec - 1) / (256 * kVec)), (unsigned)strips);
+            k_rms_norm_strips<T><<<grid, dim3(256), 0, s>>>(a);
+        }
+        const det_status st = launch_status();
+        if (st != DET_SUCCESS) return st;
+    }
+    KernelTimer kt("k_col_sums", s);
+    k_col_sums<T><<<dim3((unsigned)((a.d + 63) / 64)), dim3(1024), 0, s>>>(
+        a.part, strips, a.d, static_cast<T*>(dw));
+    return launch_status();
+}
+
+}  // namespace
+
+size_t norm_backward_workspace(int64_t rows, int64_t d) {
+    const int64_t r = strip_rows(rows, d), strips = (rows + r - 1) / r;
+    return round_up((size_t)strips * (size_t)d * sizeof(float), 256) + 256;
+}
+
+det_status norm_launch(const NormCall& c, hipStream_t s) {
+    const NormArgs a{c.x, c.residual, c.weight, c.h, c.y, c.scales, c.rstd, c.x_stride,
+                     c.residual_stride, c.rows, c.d, (int)c.group, c.eps};
+    switch (c.dtype) {
+        case DET_F32: norm_typed<float>(a, c.codes, s); break;
+        case DET_F16: norm_typed<_Float16>(a, c.codes, s); break;
+        default: norm_typed<__bf16>(a, c.codes, s); break;
+    }
+    return launch_status();
+}
+
+det_status norm_backward_launch(const NormBackCall& c, void* ws, hipStream_t s) {
+    const NormBackArgs a{c.dy, c.h, c.weight, c.dh, c.rstd, c.dx, static_cast<float*>(ws),
+                         c.dy_stride, c.h_stride, c.dh_stride, c.rows, c.d,
+                         strip_rows(c.rows, c.d)};
+    switch (c.dtype) {
+        case DET_F32: return back_typed<float>(a, c.dweight, s);
+        case DET_F16: return back_typed<_Float16>(a, c.dweight, s);
+        default: return back_typed<__bf16>(a, c.dweight, s);
+    }
+}
+
+}  // namespace det

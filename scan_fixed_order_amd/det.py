@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
-from typing import Optional
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
@@ -20,8 +20,13 @@ LIB_PATH = os.path.join(_HERE, "libdet.so")
 DET_F32 = 0
 DET_F64 = 1
 DET_I32 = 2      # det_scan only
+DET_F16 = 3      # the language-model operators only, like DET_BF16
+DET_BF16 = 4
+DET_E4M3 = 5     # det_rms_norm's 8-bit output only
 DET_SCAN_EXCLUSIVE = 1
 DET_SCAN_REVERSE = 2
+DET_BIAS_BIDIRECTIONAL = 1
+DET_BIAS_CAUSAL = 2
 
 _STATUS = {
     0: "DET_SUCCESS",
@@ -71,6 +76,25 @@ def lib() -> ctypes.CDLL:
     L.det_scatter_add_running_workspace_size.restype = sz
     L.det_scatter_add_running.argtypes = [p, p, i64, i64, i, p, i64, p, p, p, sz, p]
     L.det_scatter_add_running.restype = i
+    d = ctypes.c_double
+    L.det_rms_norm.argtypes = [p, i64, p, i64, p, i64, i64, i, d, p, p, i, i64, p, p, p]
+    L.det_rms_norm.restype = i
+    L.det_rms_norm_backward_workspace_size.argtypes = [i64, i64, i]
+    L.det_rms_norm_backward_workspace_size.restype = sz
+    L.det_rms_norm_backward.argtypes = [p, i64, p, i64, p, p, p, i64, i64, i64, i, p, p, p, sz, p]
+    L.det_rms_norm_backward.restype = i
+    L.det_relative_bias.argtypes = [p, i64, i64, i64, u, i64, i64, i64, i64, p, p, p, i64, i64,
+                                    i64, i, p, p]
+    L.det_relative_bias.restype = i
+    L.det_relative_bias_backward_workspace_size.argtypes = [i64, i64, i64, i64, i64, i]
+    L.det_relative_bias_backward_workspace_size.restype = sz
+    L.det_relative_bias_backward.argtypes = [p, i64, i64, i64, i64, i64, i64, u, i64, i64, i64,
+                                             i64, p, p, i, p, p, p, sz, p]
+    L.det_relative_bias_backward.restype = i
+    L.det_token_logprobs.argtypes = [p, i64, p, i64, i64, i, d, p, p, p, i64, p, p, p]
+    L.det_token_logprobs.restype = i
+    L.det_token_logprobs_backward.argtypes = [p, i64, p, p, p, p, p, i64, i64, i, d, p, i64, p]
+    L.det_token_logprobs_backward.restype = i
     L.det_spec_version.argtypes, L.det_spec_version.restype = [], i
     L.det_spec_constants.argtypes = [ctypes.POINTER(i64)] * 4
     L.det_spec_constants.restype = None
@@ -335,6 +359,409 @@ def gather(values: torch.Tensor, index: torch.Tensor) -> torch.Tensor:
     if index.numel() and (int(index.min()) < 0 or int(index.max()) >= values.shape[0]):
         raise IndexError("gather index out of range")
     return _Gather.apply(values, index)
+
+
+# ------------------------------------------------------------------ language-model operators
+
+_LM_TYPES = {torch.float32: DET_F32, torch.float16: DET_F16, torch.bfloat16: DET_BF16}
+
+
+def _lm_code(t: torch.Tensor) -> int:
+    code = _LM_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"the language-model operators take float32, float16 and bfloat16, "
+                        f"got {t.dtype}")
+    return code
+
+
+def _same(t: torch.Tensor, like: torch.Tensor, what: str) -> torch.Tensor:
+    if t.dtype != like.dtype:
+        raise TypeError(f"{what} must be {like.dtype}, got {t.dtype}")
+    return t
+
+
+def _of(t: torch.Tensor, dtype: torch.dtype, shape, what: str) -> torch.Tensor:
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _flat(t)
+
+
+def _row_stride(t: torch.Tensor, what: str) -> int:
+    """Elements between neighbouring rows of ``t`` (its last dimension is a row)."""
+    n = t.shape[-1]
+    if t.is_contiguous():
+        return n
+    if t.stride(-1) == 1 or n == 1:
+        stride = None          # of the innermost leading dimension longer than 1, then of all
+        for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+            if size == 1:
+                continue
+            if stride is None:
+                stride, span = st, st * size
+            elif st == span:
+                span = st * size
+            else:
+                break
+        else:
+            if stride is None:
+                return n
+            if stride >= n:
+                return stride
+    raise ValueError(f"det needs the rows of {what} contiguous and evenly spaced")
+
+
+class RmsNorm(NamedTuple):
+    """y; h = x + residual as stored (x itself without a residual) and rstd, which the backward
+    pass takes; scales of an 8-bit y, else None."""
+    y: torch.Tensor
+    h: torch.Tensor
+    rstd: torch.Tensor
+    scales: Optional[torch.Tensor]
+
+
+def det_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                 residual: Optional[torch.Tensor] = None, quant: Optional[torch.dtype] = None,
+                 group: int = 0) -> RmsNorm:
+    """Root-mean-square norm of the rows (last dimension) of ``x + residual``, times ``weight``.
+
+    x, residual: [..., d] of one type (float32, float16, bfloat16), rows contiguous and evenly
+    spaced; weight: [d].  Computed in f32; a row's bits depend on that row alone.
+    ``quant=torch.float8_e4m3fn``: y holds 8-bit codes and scales [..., ceil(d / group)] their
+    scales, one for every ``group`` (32, 64, 128) neighbouring channels, or with ``group=0``
+    one a row; y * scale stands for the normed value."""
+    code = _lm_code(x)
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    shape, d = x.shape, x.shape[-1]
+    _of(weight, x.dtype, (d,), "weight")
+    stride = _row_stride(x, "x")
+    h, res_stride = None, 0
+    if residual is not None:
+        if _same(residual, x, "residual").shape != shape:
+            raise ValueError("residual must have the shape of x")
+        res_stride = _row_stride(residual, "residual")
+        h = torch.empty(shape, dtype=x.dtype, device=x.device)
+    rows = x.numel() // d if d else 0
+    y_code, scales, y_type = code, None, x.dtype
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+    if quant is not None:
+        if quant != torch.float8_e4m3fn:
+            raise TypeError(f"quant must be torch.float8_e4m3fn, got {quant}")
+        if group not in (0, 32, 64, 128):
+            raise ValueError("group must be 0, 32, 64 or 128")
+        y_code, y_type = DET_E4M3, quant
+        scales = torch.empty((*shape[:-1], -(-d // group) if group else 1), dtype=torch.float32,
+                             device=x.device)
+    elif group:
+        raise ValueError("group is for an 8-bit output")
+    y = torch.empty(shape, dtype=y_type, device=x.device)
+    _check(lib().det_rms_norm(_dev_ptr(x), stride, _dev_ptr(residual), res_stride,
+                              _dev_ptr(weight), rows, d, code, eps, _dev_ptr(h), _dev_ptr(y),
+                              y_code, group, _dev_ptr(scales), _dev_ptr(rstd),
+                              _stream(x.device)), "det_rms_norm")
+    return RmsNorm(y, x if h is None else h, rstd, scales)
+
+
+@functools.lru_cache(maxsize=256)
+def det_rms_norm_backward_workspace_size(rows: int, d: int, dtype_code: int) -> int:
+    return lib().det_rms_norm_backward_workspace_size(rows, d, dtype_code)
+
+
+def det_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                          rstd: torch.Tensor, dh: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None
+                          ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dx, dweight) of det_rms_norm's ``y``; ``h`` and ``rstd`` as det_rms_norm returned them.
+    ``dh``: the gradient that reaches h from elsewhere (the residual stream), added to dx.  dx is
+    also the residual's gradient.  dweight's sum over the rows has an order fixed by their
+    number."""
+    code = _lm_code(h)
+    if h.dim() < 1:
+        raise ValueError("h must have at least one dimension")
+    d = h.shape[-1]
+    _of(weight, h.dtype, (d,), "weight")
+    _of(rstd, torch.float32, h.shape[:-1], "rstd")
+    if _same(dy, h, "dy").shape != h.shape:
+        raise ValueError("dy must have the shape of h")
+    dh_stride = 0
+    if dh is not None:
+        if _same(dh, h, "dh").shape != h.shape:
+            raise ValueError("dh must have the shape of h")
+        dh_stride = _row_stride(dh, "dh")
+    rows = h.numel() // d if d else 0
+    dev = h.device
+    dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
+    dweight = torch.empty(d, dtype=h.dtype, device=dev)
+    w = _workspace(det_rms_norm_backward_workspace_size(rows, d, code), dev, ws)
+    _check(lib().det_rms_norm_backward(_dev_ptr(dy), _row_stride(dy, "dy"), _dev_ptr(h),
+                                       _row_stride(h, "h"), _dev_ptr(weight), _dev_ptr(rstd),
+                                       _dev_ptr(dh), dh_stride, rows, d, code, _dev_ptr(dx),
+                                       _dev_ptr(dweight), _dev_ptr(w),
+                                       w.numel() * w.element_size(), _stream(dev)),
+           "det_rms_norm_backward")
+    return dx, dweight
+
+
+def _bias_masks(q_offset, lengths: Optional[torch.Tensor], batch: Optional[int]):
+    """(batch, whole-number offset, its tensor or None); the tensors' own checks."""
+    offsets = q_offset if torch.is_tensor(q_offset) else None
+    for t, what in ((offsets, "q_offset"), (lengths, "lengths")):
+        if t is None:
+            continue
+        if t.dim() != 1:
+            raise ValueError(f"{what} must be one-dimensional")
+        if batch is None:
+            batch = t.shape[0]
+        _of(t, torch.int32, (batch,), what)
+    return 1 if batch is None else batch, 0 if offsets is not None else int(q_offset), offsets
+
+
+def _bias_strides(t: torch.Tensor, what: str):
+    if t.dim() != 4:
+        raise ValueError(f"{what} must be [batch, heads, q, k]")
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise ValueError(f"det needs the rows of {what} contiguous")
+    return t.stride()[:3]
+
+
+def _bias_flags(bidirectional: bool, causal: bool) -> int:
+    return (DET_BIAS_BIDIRECTIONAL if bidirectional else 0) | (DET_BIAS_CAUSAL if causal else 0)
+
+
+def det_relative_bias(table: torch.Tensor, q: int, k: int, scores: Optional[torch.Tensor] = None,
+                      max_distance: int = 128, bidirectional: bool = True, causal: bool = False,
+                      q_offset: Union[int, torch.Tensor] = 0,
+                      lengths: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A learned relative position bias [batch, heads, q, k], added to ``scores`` where given.
+
+    table: [buckets, heads]; the bias of query i and key j is the row of the bucket that
+    j - (i + q_offset) falls into: near distances have a bucket each, farther ones share them by
+    the logarithm up to ``max_distance``; ``bidirectional`` gives keys after the query the
+    second half of the buckets.  Masked places are -inf: keys after the query when ``causal``,
+    and keys and queries at or past ``lengths`` (int32 [batch]).  ``q_offset``: query 0's
+    position among the keys, a whole number or int32 [batch].  Without scores, lengths or a
+    tensor of offsets batch is 1: one bias serves every sequence.  ``scores``: [batch, heads,
+    q, k] of the table's type, rows contiguous, other strides free; ``out`` may be scores."""
+    code = _lm_code(table)
+    if table.dim() != 2:
+        raise ValueError("table must be [buckets, heads]")
+    buckets, heads = _flat(table).shape
+    sb = sh = sq = 0
+    batch = None
+    if scores is not None:
+        sb, sh, sq = _bias_strides(_same(scores, table, "scores"), "scores")
+        batch = scores.shape[0]
+        if scores.shape[1:] != (heads, q, k):
+            raise ValueError(f"scores must be [batch, {heads}, {q}, {k}]")
+    batch, offset, offsets = _bias_masks(q_offset, lengths, batch)
+    if out is None:
+        out = torch.empty((batch, heads, q, k), dtype=table.dtype, device=table.device)
+    else:
+        _of(out, table.dtype, (batch, heads, q, k), "out")
+    _check(lib().det_relative_bias(_dev_ptr(table), buckets, heads, max_distance,
+                                   _bias_flags(bidirectional, causal), batch, q, k, offset,
+                                   _dev_ptr(offsets), _dev_ptr(lengths), _dev_ptr(scores), sb, sh,
+                                   sq, code, _dev_ptr(out), _stream(table.device)),
+           "det_relative_bias")
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def det_relative_bias_backward_workspace_size(batch: int, heads: int, q: int, k: int,
+                                              num_buckets: int, dtype_code: int) -> int:
+    return lib().det_relative_bias_backward_workspace_size(batch, heads, q, k, num_buckets,
+                                                           dtype_code)
+
+
+def det_relative_bias_backward(dout: torch.Tensor, num_buckets: int, max_distance: int = 128,
+                               bidirectional: bool = True, causal: bool = False,
+                               q_offset: Union[int, torch.Tensor] = 0,
+                               lengths: Optional[torch.Tensor] = None,
+                               dscores: Optional[torch.Tensor] = None,
+                               ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The table's gradient [num_buckets, heads]: ``dout`` [batch, heads, q, k] summed by buckets
+    over the unmasked places, in an order fixed by the sizes (arguments as for
+    det_relative_bias).  ``dscores`` (contiguous, dout's shape and type; may be dout itself)
+    receives the scores' gradient: dout with zeros at the masked places."""
+    code = _lm_code(dout)
+    sb, sh, sq = _bias_strides(dout, "dout")
+    heads, q, k = dout.shape[1:]
+    batch, offset, offsets = _bias_masks(q_offset, lengths, dout.shape[0])
+    if dscores is not None:
+        _of(dscores, dout.dtype, dout.shape, "dscores")
+    dev = dout.device
+    dtable = torch.empty((num_buckets, heads), dtype=dout.dtype, device=dev)
+    w = _workspace(det_relative_bias_backward_workspace_size(batch, heads, q, k, num_buckets, code),
+                   dev, ws)
+    _check(lib().det_relative_bias_backward(_dev_ptr(dout), sb, sh, sq, num_buckets, heads,
+                                            max_distance, _bias_flags(bidirectional, causal),
+                                            batch, q, k, offset, _dev_ptr(offsets),
+                                            _dev_ptr(lengths), code, _dev_ptr(dtable),
+                                            _dev_ptr(dscores), _dev_ptr(w),
+                                            w.numel() * w.element_size(), _stream(dev)),
+           "det_relative_bias_backward")
+    return dtable
+
+
+class TokenLogprobs(NamedTuple):
+    """Float32 logp, entropy and lse of every row; top_logp and top_ids (int64) [..., top], None
+    without alternatives."""
+    logp: torch.Tensor
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_logp: Optional[torch.Tensor]
+    top_ids: Optional[torch.Tensor]
+
+
+def det_token_logprobs(logits: torch.Tensor, targets: torch.Tensor, scale: float = 1.0,
+                       top: int = 0) -> TokenLogprobs:
+    """Log probabilities of ``targets`` under softmax(scale * logits), with each row's entropy and
+    its ``top`` likeliest tokens (ties to the lower id).
+
+    logits: [..., vocab], rows contiguous and evenly spaced (a slice of a padded vocabulary is
+    fine); targets: int64 [...]; one outside the vocabulary (such as -100) is not scored and its
+    logp is 0.  A row's bits depend on its logits and the scale alone."""
+    code = _lm_code(logits)
+    if logits.dim() < 1:
+        raise ValueError("logits must have at least one dimension")
+    shape, vocab, dev = logits.shape[:-1], logits.shape[-1], logits.device
+    _of(targets, torch.int64, shape, "targets")
+    stride = _row_stride(logits, "logits")
+    logp = torch.empty(shape, dtype=torch.float32, device=dev)
+    entropy, lse = torch.empty_like(logp), torch.empty_like(logp)
+    top_logp = top_ids = None
+    if top:
+        top_logp = torch.empty((*shape, top), dtype=torch.float32, device=dev)
+        top_ids = torch.empty((*shape, top), dtype=torch.int64, device=dev)
+    _check(lib().det_token_logprobs(_dev_ptr(logits), stride, _dev_ptr(targets), targets.numel(),
+                                    vocab, code, scale, _dev_ptr(logp), _dev_ptr(entropy),
+                                    _dev_ptr(lse), top, _dev_ptr(top_logp), _dev_ptr(top_ids),
+                                    _stream(dev)), "det_token_logprobs")
+    return TokenLogprobs(logp, entropy, lse, top_logp, top_ids)
+
+
+def det_token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                                dlogp: torch.Tensor, entropy: Optional[torch.Tensor] = None,
+                                dentropy: Optional[torch.Tensor] = None, scale: float = 1.0,
+                                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The logits' gradient for ``dlogp`` and, where given, ``dentropy`` (float32 [...]); ``lse``
+    and ``entropy`` as det_token_logprobs returned them for these logits and this scale.  ``out``
+    (logits' shape and type, rows contiguous and evenly spaced) may be logits itself."""
+    code = _lm_code(logits)
+    if logits.dim() < 1:
+        raise ValueError("logits must have at least one dimension")
+    shape, vocab = logits.shape[:-1], logits.shape[-1]
+    _of(targets, torch.int64, shape, "targets")
+    for t, what in ((lse, "lse"), (dlogp, "dlogp"), (entropy, "entropy"), (dentropy, "dentropy")):
+        if t is not None:
+            _of(t, torch.float32, shape, what)
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs entropy")
+    stride = _row_stride(logits, "logits")
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out_stride = vocab
+    else:
+        if _same(out, logits, "out").shape != logits.shape:
+            raise ValueError("out must have the shape of logits")
+        out_stride = _row_stride(out, "out")
+    _check(lib().det_token_logprobs_backward(_dev_ptr(logits), stride, _dev_ptr(targets),
+                                             _dev_ptr(lse), _dev_ptr(dlogp), _dev_ptr(entropy),
+                                             _dev_ptr(dentropy), targets.numel(), vocab, code,
+                                             scale, _dev_ptr(out), out_stride,
+                                             _stream(logits.device)),
+           "det_token_logprobs_backward")
+    return out
+
+
+class _RmsNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        r = det_rms_norm(x, weight, eps, residual)
+        ctx.save_for_backward(r.h, weight, r.rstd)
+        ctx.set_materialize_grads(False)
+        ctx.residual = residual is not None
+        return (r.y, r.h) if ctx.residual else r.y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        if dy is None and dh is None:
+            return None, None, None, None
+        dy = torch.zeros_like(h) if dy is None else dy.contiguous()
+        dx, dweight = det_rms_norm_backward(dy, h, weight, rstd,
+                                            None if dh is None else dh.contiguous())
+        return dx, dweight, dx if ctx.residual else None, None
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+             eps: float = 1e-6):
+    """Differentiable det_rms_norm: y, or (y, h = x + residual) with a residual."""
+    return _RmsNormFn.apply(x, weight, residual, eps)
+
+
+class _RelativeBias(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, scores, q, k, how, q_offset, lengths):
+        out = det_relative_bias(table, q, k, scores, q_offset=q_offset, lengths=lengths, **how)
+        ctx.how, ctx.buckets, ctx.scored = how, table.shape[0], scores is not None
+        tensor = torch.is_tensor(q_offset)
+        ctx.save_for_backward(q_offset if tensor else None, lengths)
+        ctx.q_offset = None if tensor else q_offset
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        offsets, lengths = ctx.saved_tensors
+        dout = dout.contiguous()
+        masked = ctx.how["causal"] or lengths is not None
+        want = ctx.scored and ctx.needs_input_grad[1]
+        dscores = torch.empty_like(dout) if want and masked else dout if want else None
+        dtable = det_relative_bias_backward(
+            dout, ctx.buckets, q_offset=offsets if offsets is not None else ctx.q_offset,
+            lengths=lengths, dscores=dscores if masked else None, **ctx.how)
+        return dtable, dscores, None, None, None, None, None
+
+
+def relative_bias(table: torch.Tensor, q: int, k: int, scores: Optional[torch.Tensor] = None,
+                  max_distance: int = 128, bidirectional: bool = True, causal: bool = False,
+                  q_offset: Union[int, torch.Tensor] = 0,
+                  lengths: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Differentiable det_relative_bias (gradients of the table and the scores)."""
+    how = {"max_distance": max_distance, "bidirectional": bidirectional, "causal": causal}
+    return _RelativeBias.apply(table, scores, q, k, how, q_offset, lengths)
+
+
+class _TokenLogprobsFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets, scale):
+        r = det_token_logprobs(logits, targets, scale)
+        ctx.save_for_backward(logits, targets, r.lse, r.entropy)
+        ctx.set_materialize_grads(False)
+        ctx.scale = scale
+        return r.logp, r.entropy
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dlogp, dentropy):
+        logits, targets, lse, entropy = ctx.saved_tensors
+        if dlogp is None and dentropy is None:
+            return None, None, None
+        dlogp = torch.zeros_like(lse) if dlogp is None else dlogp.contiguous()
+        dlogits = det_token_logprobs_backward(
+            logits, targets, lse, dlogp, entropy,
+            None if dentropy is None else dentropy.contiguous(), ctx.scale)
+        return dlogits, None, None
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, scale: float = 1.0):
+    """Differentiable det_token_logprobs: (logp, entropy)."""
+    return _TokenLogprobsFn.apply(logits, targets, scale)
 
 
 # ------------------------------------------------------------------ introspection
