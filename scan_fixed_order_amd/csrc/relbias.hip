@@ -20,26 +20,29 @@ constexpr int kBlock = 256;
 
 struct Map {
     int starts[kBiasMaxSide];      // first distance of bucket j of a side, ascending
-    int side;                      // buckets a side
+    int side, top;                 // buckets a side, the largest power of two below that
     bool two_sided, causal;
     int64_t q, k, q_offset;
     const int32_t* q_offsets;      // NULL: q_offset for every sequence
     const int32_t* lengths;        // NULL: no padding
 };
 
-__device__ __forceinline__ int bucket_of(const Map& m, const int* starts, int64_t r) {
-    int64_t far = r < 0 ? -r : (m.two_sided ? r : 0);
+// Bucket of a relative position: the last of the side's whose start is not beyond the distance
+// (starts[0] = 0).  top: the largest power of two below the number of buckets a side.
+__device__ __forceinline__ int bucket_of(const Map& m, const int* starts, int top, int64_t r) {
+    const int64_t far = r < 0 ? -r : (m.two_sided ? r : 0);
     int lo = m.side - 1;
-    if (far < starts[m.side - 1]) {
-        // the last bucket whose start is not beyond the distance (starts[0] = 0)
+    if (far < starts[lo]) {
         lo = 0;
-        int hi = m.side - 1;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (starts[mid] <= far) lo = mid; else hi = mid;
-        }
+        for (int step = top; step > 0; step >>= 1)
+            if (lo + step < m.side && starts[lo + step] <= far) lo += step;
     }
     return m.two_sided && r > 0 ? lo + m.side : lo;
+}
+
+// a / b, in 32 bits where both fit
+__device__ __forceinline__ int64_t split(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 __device__ __forceinline__ int64_t offset_of(const Map& m, int64_t b) {
@@ -56,12 +59,34 @@ struct BiasArgs {
     const void* scores;     // NULL: none
     void* out;              // [batch][heads][q][k]
     int64_t sb, sh, sq;     // strides of scores
+    int64_t extent;         // elements from scores' first to behind its last
     int64_t heads, batch;
     int lanes_log2;         // lanes across the keys: 2^lanes_log2 of the workgroup's 256
-    int rows;               // query rows a lane walks
+    int rows;               // query rows a lane walks, a multiple of kRows
+    int buckets;
     float fill;             // what a masked place gets
-    int64_t kt, qt;         // tiles along the keys and the queries
+    int64_t qt;             // tiles along the queries
 };
+
+constexpr int kRows = 8;
+
+// 8 elements from place `at` of a tensor whose elements lie in [0, extent), of which the first n
+// count; the others are unspecified.  Those may lie past the row's end but never outside the
+// tensor, whose two ends alone are read one by one.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8_inside(const T* p, int64_t at, int64_t n, int64_t extent) {
+    Raw8<T> r = {};
+    if (n > 0) {
+        if (at + kVec <= extent) {
+            r = load8(p + at);
+        } else {
+            float v[kVec];
+            load_tail(p + at, n, 0.0f, v);
+            r = pack8<T>(v);
+        }
+    }
+    return r;
+}
 
 // A workgroup covers `width` = 8 * 2^lanes_log2 keys and (256 >> lanes_log2) * rows queries of
 // one head.  The values of all its diagonals are laid out once in LDS; a lane then walks down
@@ -70,20 +95,26 @@ template <typename T, bool SCORES>
 __global__ __launch_bounds__(kBlock) void k_relative_bias(Map m, BiasArgs a) {
     extern __shared__ float s_diag[];           // value of diagonal (first + i)
     __shared__ int s_starts[kBiasMaxSide];
+    __shared__ float s_table[DET_BIAS_MAX_BUCKETS];
+    constexpr int kStep = SCORES ? kRows / 2 : kRows;
     const int lanes = 1 << a.lanes_log2, teams = kBlock >> a.lanes_log2;
     const int width = kVec * lanes, height = teams * a.rows;
     for (int i = threadIdx.x; i < m.side; i += kBlock) s_starts[i] = m.starts[i];
-    for (int64_t tile = blockIdx.x; tile < a.batch * a.heads * a.qt * a.kt; tile += gridDim.x) {
-        const int64_t kt = tile % a.kt, qt = tile / a.kt % a.qt, bh = tile / (a.kt * a.qt);
-        const int64_t b = bh / a.heads, h = bh % a.heads;
+    const int64_t kt = blockIdx.x;
+    for (int64_t bh = blockIdx.z; bh < a.batch * a.heads; bh += gridDim.z)
+    for (int64_t qt = blockIdx.y; qt < a.qt; qt += gridDim.y) {
+        const int64_t b = split(bh, a.heads), h = bh - b * a.heads;
         const int64_t k0 = kt * width, q0 = qt * height;
         const int64_t off = offset_of(m, b), len = length_of(m, b);
         const T* table = static_cast<const T*>(a.table);
-        __syncthreads();      // s_starts is there; the last tile's diagonals are read
+        for (int i = threadIdx.x; i < a.buckets; i += kBlock)
+            s_table[i] = table ? (float)table[(int64_t)i * a.heads + h] : 0.0f;
+        __syncthreads();      // the last tile's diagonals are read
         // diagonal index i holds r = (k0 - (q0 + height - 1)) + i - off
         const int64_t r0 = k0 - (q0 + height - 1) - off;
+#pragma unroll 3
         for (int i = threadIdx.x; i < width + height - 1; i += kBlock)
-            s_diag[i] = table ? (float)table[bucket_of(m, s_starts, r0 + i) * a.heads + h] : 0.0f;
+            s_diag[i] = s_table[bucket_of(m, s_starts, m.top, r0 + i)];
         __syncthreads();
         const int lane = threadIdx.x & (lanes - 1), team = threadIdx.x >> a.lanes_log2;
         const int64_t c = k0 + kVec * lane, row0 = q0 + (int64_t)team * a.rows;
@@ -94,31 +125,99 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias(Map m, BiasArgs a) {
 #pragma unroll
         for (int i = 1; i < kVec; ++i) v[i - 1] = s_diag[at + i];   // moved into place by the first row
         const int64_t end = row0 + a.rows < m.q ? row0 + a.rows : m.q;
-        for (int64_t row = row0; row < end; ++row, --at) {
+        const int64_t base = SCORES ? b * a.sb + h * a.sh + c : 0;
+        const T* scores = static_cast<const T*>(a.scores);
+        // kStep rows at a time, their loads in flight together
+        for (int64_t row = row0; row < end; row += kStep, at -= kStep) {
+            Raw8<T> raw[kStep];
+            int left[kStep];          // of the vector's keys, those that the masks leave
 #pragma unroll
-            for (int i = kVec - 1; i > 0; --i) v[i] = v[i - 1];
-            v[0] = s_diag[at];
-            // keys that the masks leave this row; a masked place is never read
-            int64_t left = row + off < len ? len : 0;
-            if (m.causal && row + off + 1 < left) left = row + off + 1;
-            left -= c;
-            float o[kVec];
-            if constexpr (SCORES) {
-                const T* sc = static_cast<const T*>(a.scores) + b * a.sb + h * a.sh + row * a.sq + c;
-                read8(sc, left < n ? left : n, 0.0f, o);
+            for (int j = 0; j < kStep; ++j) {
+                const int64_t pos = row + j + off;
+                const int64_t keys = (m.causal && pos + 1 < len ? pos + 1 : len) - c;
+                left[j] = pos >= len || row + j >= end || keys < 0 ? 0 : keys < kVec ? (int)keys : kVec;
+                if constexpr (SCORES)
+                    raw[j] = load8_inside(scores, base + (row + j) * a.sq,
+                                          left[j] < n ? left[j] : n, a.extent);
+            }
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) o[i] += v[i];
+            for (int j = 0; j < kStep; ++j) {
+                if (row + j >= end) break;
+#pragma unroll
+                for (int i = kVec - 1; i > 0; --i) v[i] = v[i - 1];
+                v[0] = s_diag[at - j];
+                float o[kVec];
+                if constexpr (SCORES) {
+                    unpack8<T>(raw[j], o);
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) o[i] += v[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) o[i] = v[i];
+                }
+                if (left[j] < kVec) {
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i)
+                        if (i >= left[j]) o[i] = a.fill;
+                }
+                write8(static_cast<T*>(a.out) + (bh * m.q + row + j) * m.k + c, n, o);
+            }
+        }
+    }
+}
+
+// Few queries: nothing to share between rows, so every lane finds its 8 keys' buckets by itself.
+// A workgroup's teams of 2^lanes_log2 lanes take neighbouring rows of the output.
+template <typename T, bool SCORES>
+__global__ __launch_bounds__(kBlock) void k_relative_bias_row(Map m, BiasArgs a) {
+    __shared__ int s_starts[kBiasMaxSide];
+    const int lanes = 1 << a.lanes_log2, teams = kBlock >> a.lanes_log2;
+    for (int i = threadIdx.x; i < m.side; i += kBlock) s_starts[i] = m.starts[i];
+    __syncthreads();
+    const int64_t c = (int64_t)blockIdx.x * kVec * lanes + kVec * (threadIdx.x & (lanes - 1));
+    const int64_t n = m.k - c;
+    if (n <= 0) return;
+    const T* table = static_cast<const T*>(a.table);
+    for (int64_t r = (int64_t)blockIdx.y * teams + (threadIdx.x >> a.lanes_log2);
+         r < a.batch * a.heads * m.q; r += (int64_t)gridDim.y * teams) {
+        const int64_t bh = split(r, m.q), row = r - bh * m.q;
+        const int64_t b = split(bh, a.heads), h = bh - b * a.heads;
+        const int64_t off = offset_of(m, b), len = length_of(m, b);
+        const int64_t keys = (m.causal && row + off + 1 < len ? row + off + 1 : len) - c;
+        const int left = row + off >= len || keys < 0 ? 0 : keys < kVec ? (int)keys : kVec;
+        float o[kVec];
+        Raw8<T> raw;
+        if constexpr (SCORES)
+            raw = load8_inside(static_cast<const T*>(a.scores),
+                               b * a.sb + h * a.sh + row * a.sq + c, left < n ? left : n, a.extent);
+        const int64_t r0 = c - row - off;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) o[i] = a.fill;
+        if (left > 0) {
+            const int first = bucket_of(m, s_starts, m.top, r0);
+            float v[kVec];
+            v[0] = table ? (float)table[first * a.heads + h] : 0.0f;
+            if (first == bucket_of(m, s_starts, m.top, r0 + kVec - 1)) {
+                // buckets are runs of distances: between two places of one bucket lies no other
+#pragma unroll
+                for (int i = 1; i < kVec; ++i) v[i] = v[0];
             } else {
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) o[i] = v[i];
+                for (int i = 1; i < kVec; ++i)
+                    v[i] = table ? (float)table[bucket_of(m, s_starts, m.top, r0 + i) * a.heads + h]
+                                 : 0.0f;
             }
-            if (left < kVec) {
+            if constexpr (SCORES) {
+                float sc[kVec];
+                unpack8<T>(raw, sc);
 #pragma unroll
-                for (int i = 0; i < kVec; ++i)
-                    if (i >= left) o[i] = a.fill;
+                for (int i = 0; i < kVec; ++i) v[i] += sc[i];
             }
-            write8(static_cast<T*>(a.out) + (bh * m.q + row) * m.k + c, n, o);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if (i < left) o[i] = v[i];
         }
+        write8(static_cast<T*>(a.out) + r * m.k + c, n, o);
     }
 }
 
@@ -126,79 +225,106 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias(Map m, BiasArgs a) {
 
 struct BiasBackArgs {
     const void* dout;
-    float* part;              // [batch * heads][row strips][diagonal tiles][buckets]
-    int64_t sb, sh, sq, heads, batch;
+    double* part;             // [batch * heads][tiles / kWaves][buckets]
+    int64_t sb, sh, sq, extent, heads, batch;
     int strip;                // query rows a workgroup walks
     int64_t qt, dt;           // row strips and diagonal tiles
     int buckets;
 };
 
 constexpr int kWaves = kBlock / 64;
+constexpr int kShortRun = 16;              // diagonals
 constexpr int kDiags = 64 * kVec;          // diagonals a wave covers
 
 // A lane owns 8 neighbouring diagonals and walks down the strip's rows: its 8 elements of a row
-// lie together in memory, one place further along with every row.  The wave then adds its
-// diagonals up by buckets, which are runs of neighbouring diagonals.
+// lie together in memory, one place further along with every row.  kRows rows are added in f32,
+// their sums in f64.  The wave then adds its diagonals up by buckets, which are runs of
+// neighbouring diagonals.
 template <typename T>
 __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBackArgs a) {
-    __shared__ float s_sums[kWaves][kDiags];
+    __shared__ double s_sums[kWaves][kDiags];
+    __shared__ double s_part[kWaves][DET_BIAS_MAX_BUCKETS];
     __shared__ int s_starts[kBiasMaxSide];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int i = threadIdx.x; i < m.side; i += kBlock) s_starts[i] = m.starts[i];
-    const int64_t tiles = a.batch * a.heads * a.qt * a.dt;
-    float* s_sum = s_sums[wave];
-    for (int64_t first = (int64_t)blockIdx.x * kWaves; first < tiles;
-         first += (int64_t)gridDim.x * kWaves) {
-        const bool live = first + wave < tiles;
-        const int64_t tile = live ? first + wave : tiles - 1;
-        const int64_t dt = tile % a.dt, qt = tile / a.dt % a.qt, bh = tile / (a.dt * a.qt);
-        const int64_t b = bh / a.heads, h = bh % a.heads;
+    // a workgroup takes kWaves neighbouring tiles (diagonals, then strips) of one head
+    const int64_t per_head = (a.qt * a.dt + kWaves - 1) / kWaves;
+    double* s_sum = s_sums[wave];
+    for (int64_t group = blockIdx.x; group < a.batch * a.heads * per_head; group += gridDim.x) {
+        const int64_t bh = split(group, per_head), tile = (group - bh * per_head) * kWaves + wave;
+        const bool live = tile < a.qt * a.dt;
+        const int64_t qt = split(tile, a.dt), dt = tile - qt * a.dt;
+        const int64_t b = split(bh, a.heads), h = bh - b * a.heads;
         const int64_t off = offset_of(m, b), len = length_of(m, b);
         const int64_t q0 = qt * a.strip;
-        int64_t q1 = q0 + a.strip < m.q ? q0 + a.strip : m.q;
+        int64_t q1 = !live ? q0 : q0 + a.strip < m.q ? q0 + a.strip : m.q;
         if (q1 > len - off) q1 = len - off;               // rows past the sequence hold nothing
         const int64_t keys = len < m.k ? len : m.k;       // keys past it neither
         // diagonal d of the strip, from 0: key = row + d - shift
         const int64_t shift = q0 + a.strip - 1;
         const int64_t d0 = dt * kDiags + kVec * lane - shift;    // key = row + d0 + i
-        float acc[kVec] = {};
-        const T* p = static_cast<const T*>(a.dout) + b * a.sb + h * a.sh + q0 * a.sq + q0 + d0;
+        double acc[kVec] = {};
+        const T* p = static_cast<const T*>(a.dout);
+        const int64_t base = b * a.sb + h * a.sh + d0;
         // a diagonal after the query is masked as a whole when causal
         const bool some = !m.causal || d0 - off <= 0;
-        if (__all(some && q0 + d0 >= 0 && q1 + d0 + kVec - 1 <= keys)) {
-#pragma unroll 8
-            for (int64_t row = q0; row < q1; ++row, p += a.sq + 1) {
-                float v[kVec];
-                unpack8<T>(load8(p), v);
+        const bool whole = some && q0 + d0 >= 0 && q1 + d0 + kVec - 1 <= keys;
+        const bool inner = __all(whole);
+        for (int64_t row = q0; row < q1; row += kRows) {
+            Raw8<T> raw[kRows];
+            float sum[kVec] = {};
+            if (inner && row + kRows <= q1) {
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) acc[i] += v[i];
-            }
-        } else if (some) {
-#pragma unroll 4
-            for (int64_t row = q0; row < q1; ++row, p += a.sq + 1) {
-                const int64_t c = row + d0;
-                if (c >= 0 && c + kVec <= keys) {
+                for (int j = 0; j < kRows; ++j)
+                    raw[j] = load8_once(p + base + (row + j) * (a.sq + 1));
+#pragma unroll
+                for (int j = 0; j < kRows; ++j) {
                     float v[kVec];
-                    unpack8<T>(load8(p), v);
+                    unpack8<T>(raw[j], v);
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) acc[i] += v[i];
-                } else if (c > -kVec && c < keys) {
+                    for (int i = 0; i < kVec; ++i) sum[i] += v[i];
+                }
+            } else {
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i)
-                        if (c + i >= 0 && c + i < keys) acc[i] += (float)p[i];
+                for (int j = 0; j < kRows; ++j) {
+                    const int64_t c = row + j + d0, at = base + (row + j) * (a.sq + 1);
+                    raw[j] = {};
+                    if (some && row + j < q1 && c > -kVec && c < keys) {
+                        if (at >= 0 && at + kVec <= a.extent) {
+                            raw[j] = load8(p + at);
+                        } else {      // at the tensor's very ends
+                            float v[kVec];
+#pragma unroll
+                            for (int i = 0; i < kVec; ++i)
+                                v[i] = c + i >= 0 && c + i < keys ? (float)p[at + i] : 0.0f;
+                            raw[j] = pack8<T>(v);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kRows; ++j) {
+                    const int c = (int)(row + j + d0 > -kVec ? row + j + d0 : -kVec);
+                    const int64_t rest = keys - (row + j + d0);
+                    const int n = rest < kVec ? (int)rest : kVec;
+                    float v[kVec];
+                    unpack8<T>(raw[j], v);
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) sum[i] += c + i >= 0 && i < n ? v[i] : 0.0f;
                 }
             }
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) acc[i] += (double)sum[i];
         }
         __syncthreads();      // s_starts is there; the last tile's sums are read
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-            s_sum[kVec * lane + i] = m.causal && d0 + i - off > 0 ? 0.0f : acc[i];
+            s_sum[kVec * lane + i] = m.causal && d0 + i - off > 0 ? 0.0 : acc[i];
         __syncthreads();
-        if (!live) continue;
         const int64_t r0 = dt * kDiags - shift - off;     // r of the tile's diagonal 0
-        for (int bk = 0; bk < a.buckets; ++bk) {
-            // diagonals r in [lo, hi) of this bucket
-            int64_t lo = 0, hi = 0;
+        // lane by lane the buckets' runs of diagonals, then one run after the other
+        for (int bk0 = 0; bk0 < a.buckets; bk0 += 64) {
+            const int bk = bk0 + lane;
+            int64_t lo = 0, hi = 0;                       // r in [lo, hi)
             if (bk < m.side) {
                 lo = bk + 1 < m.side ? 1 - (int64_t)s_starts[bk + 1] : INT64_MIN / 2;
                 hi = bk == 0 && !m.two_sided ? INT64_MAX / 2 : 1 - (int64_t)s_starts[bk];
@@ -211,35 +337,61 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
             hi -= r0;
             const int from = (int)(lo < 0 ? 0 : lo > kDiags ? kDiags : lo);
             const int to = (int)(hi < 0 ? 0 : hi > kDiags ? kDiags : hi);
-            float v = 0.0f;
-            for (int i = from + lane; i < to; i += 64) v += s_sum[i];
-            if (from < to) v = wave_pw(v);
-            if (lane == 0) a.part[tile * a.buckets + bk] = v;
+            // short runs by their own lane, long ones by the whole wave
+            double mine = 0.0;
+            const bool wide = to - from > kShortRun;
+            if (!wide)
+                for (int i = from; i < to; ++i) mine += s_sum[i];
+            for (uint64_t runs = __ballot(wide); runs; runs &= runs - 1) {
+                const int l = __ffsll((unsigned long long)runs) - 1;
+                const int f = __builtin_amdgcn_readlane(from, l), t = __builtin_amdgcn_readlane(to, l);
+                double v = 0.0;
+                for (int i = f + lane; i < t; i += 64) v += s_sum[i];
+                v = wave_pw(v);
+                if (lane == l) mine = v;
+            }
+            if (bk < a.buckets) s_part[wave][bk] = mine;
+        }
+        __syncthreads();
+        for (int bk = threadIdx.x; bk < a.buckets; bk += kBlock) {
+            double v = s_part[0][bk];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) v += s_part[w][bk];
+            a.part[group * a.buckets + bk] = v;
         }
     }
 }
 
-// dtable[bk][h] = the tiles' sums of every sequence, added in 64 bits: thread t adds items t,
-// t + 256, ... in that order, then the threads join by a halving tree.
+constexpr int kSumBuckets = 8;      // buckets a workgroup of the last sums takes (64 bytes)
+constexpr int kSumBlock = 512;
+
+// dtable[bk][h] = the workgroups' sums of every sequence: row g of 64 adds items g, g + 64, ...
+// (sequence by sequence) in that order, then the rows join by a halving tree.
 template <typename T>
-__global__ __launch_bounds__(kBlock) void k_bias_table_sums(const float* part, int64_t batch,
-                                                            int64_t heads, int64_t per_head,
-                                                            int buckets, T* out) {
-    __shared__ double s[kBlock];
-    const int bk = blockIdx.x % buckets;
-    const int64_t h = blockIdx.x / buckets;
+__global__ __launch_bounds__(kSumBlock) void k_bias_table_sums(const double* part, int64_t batch,
+                                                               int64_t heads, int64_t per_head,
+                                                               int buckets, T* out) {
+    constexpr int kGroups = kSumBlock / kSumBuckets;
+    __shared__ double s[kGroups][kSumBuckets];
+    const int blocks = (buckets + kSumBuckets - 1) / kSumBuckets;
+    const int x = threadIdx.x % kSumBuckets, g = threadIdx.x / kSumBuckets;
+    const int bk = blockIdx.x % blocks * kSumBuckets + x;
+    const int64_t h = blockIdx.x / blocks, items = batch * per_head;
     double v = 0.0;
-    for (int64_t i = threadIdx.x; i < batch * per_head; i += kBlock) {
-        const int64_t b = i / per_head, t = i % per_head;
-        v += (double)part[((b * heads + h) * per_head + t) * buckets + bk];
+    if (bk < buckets) {
+#pragma unroll 4
+        for (int64_t i = g; i < items; i += kGroups) {
+            const int64_t b = i / per_head, t = i - b * per_head;
+            v += part[((b * heads + h) * per_head + t) * buckets + bk];
+        }
     }
-    s[threadIdx.x] = v;
+    s[g][x] = v;
     __syncthreads();
-    for (int n = kBlock / 2; n > 0; n >>= 1) {
-        if ((int)threadIdx.x < n) s[threadIdx.x] += s[threadIdx.x + n];
+    for (int n = kGroups / 2; n > 0; n >>= 1) {
+        if (g < n) s[g][x] += s[g + n][x];
         __syncthreads();
     }
-    if (threadIdx.x == 0) out[bk * heads + h] = (T)s[0];
+    if (g == 0 && bk < buckets) out[bk * heads + h] = (T)s[0][x];
 }
 
 // ---------------------------------------------------------------- the buckets' borders
@@ -305,6 +457,7 @@ Map map_of(const BiasCall& c) {
     m.side = c.bidirectional ? c.buckets / 2 : c.buckets;
     relbias_starts(m.side, c.max_distance, m.starts);
     for (int i = m.side; i < kBiasMaxSide; ++i) m.starts[i] = 0;
+    for (m.top = 1; 2 * m.top < m.side;) m.top *= 2;
     m.two_sided = c.bidirectional;
     m.causal = c.causal;
     m.q = c.q;
@@ -315,23 +468,46 @@ Map map_of(const BiasCall& c) {
     return m;
 }
 
+// elements from the strided tensor's first to behind its last
+int64_t extent_of(const BiasCall& c) {
+    if (c.batch == 0 || c.q == 0 || c.k == 0) return 0;
+    return (c.batch - 1) * c.sb + (c.heads - 1) * c.sh + (c.q - 1) * c.sq + c.k;
+}
+
 unsigned grid_of(int64_t tiles) { return (unsigned)(tiles < (1 << 22) ? tiles : (1 << 22)); }
 
 template <typename T>
 void bias_typed(const BiasCall& c, hipStream_t s) {
     const Map m = map_of(c);
-    BiasArgs a{c.table, c.scores, c.out, c.sb, c.sh, c.sq, c.heads, c.batch, 8, 1, c.fill, 0, 0};
+    BiasArgs a{c.table, c.scores, c.out, c.sb, c.sh, c.sq, extent_of(c), c.heads, c.batch, 8,
+               kRows, c.buckets, c.fill, 0};
     // as many lanes across the keys as the row has vectors (at most the workgroup), the rest of
     // the workgroup on further rows
     while (a.lanes_log2 > 3 && ((int64_t)kVec << (a.lanes_log2 - 1)) >= c.k) --a.lanes_log2;
     const int teams = kBlock >> a.lanes_log2;
-    while (a.rows < 64 && (int64_t)a.rows * teams < c.q) a.rows *= 2;
-    const int64_t width = (int64_t)kVec << a.lanes_log2, height = (int64_t)teams * a.rows;
-    a.kt = (c.k + width - 1) / width;
+    const int64_t width = (int64_t)kVec << a.lanes_log2;
+    const int64_t kt = (c.k + width - 1) / width, bh = a.batch * a.heads;
+    if (c.q < kRows) {
+        const int64_t rows = (bh * c.q + teams - 1) / teams;
+        const dim3 grid((unsigned)kt, (unsigned)(rows < 65535 ? rows : 65535));
+        KernelTimer timer("k_relative_bias_row", s);
+        if (c.scores)
+            k_relative_bias_row<T, true><<<grid, dim3(kBlock), 0, s>>>(m, a);
+        else
+            k_relative_bias_row<T, false><<<grid, dim3(kBlock), 0, s>>>(m, a);
+        return;
+    }
+    // long walks share one layout of the diagonals among more rows, as long as workgroups enough
+    // to fill the GPU are left
+    while (a.rows < 64 && (int64_t)a.rows * teams < c.q &&
+           bh * kt * ((c.q + 2 * a.rows * teams - 1) / (2 * a.rows * teams)) >= 2048)
+        a.rows *= 2;
+    const int64_t height = (int64_t)teams * a.rows;
     a.qt = (c.q + height - 1) / height;
     const int lds = (int)(width + height) * (int)sizeof(float);
-    const dim3 grid(grid_of(a.batch * a.heads * a.kt * a.qt));
-    KernelTimer kt("k_relative_bias", s);
+    const dim3 grid((unsigned)kt, (unsigned)(a.qt < 65535 ? a.qt : 65535),
+                    (unsigned)(bh < 65535 ? bh : 65535));
+    KernelTimer timer("k_relative_bias", s);
     if (c.scores)
         k_relative_bias<T, true><<<grid, dim3(kBlock), lds, s>>>(m, a);
     else
@@ -343,40 +519,44 @@ struct BackShape {
     int64_t qt, dt;
 };
 
-// Rows a strip and the diagonals' tiles, from (q, k) alone: the order of the sums.
-BackShape back_shape(int64_t q, int64_t k) {
+// Rows a strip and the diagonals' tiles, from the sizes alone: the order of the sums.  Strips of
+// 32 rows, halved down to 8 while that leaves fewer than 4096 waves.
+BackShape back_shape(int64_t batch, int64_t heads, int64_t q, int64_t k) {
     BackShape r;
-    r.strip = q < 128 ? (int)(q > 0 ? q : 1) : 128;
-    r.qt = (q + r.strip - 1) / r.strip;
-    r.dt = (k + r.strip - 1 + kDiags - 1) / kDiags;
-    return r;
+    for (r.strip = 32;; r.strip /= 2) {
+        r.qt = (q + r.strip - 1) / r.strip;
+        r.dt = (k + r.strip - 1 + kDiags - 1) / kDiags;
+        if (r.strip == kRows || (double)batch * heads * r.qt * r.dt >= 4096.0) return r;
+    }
 }
 
 template <typename T>
 det_status back_typed(const BiasCall& c, const void* dout, void* dtable, void* ws, hipStream_t s) {
     const Map m = map_of(c);
-    const BackShape sh = back_shape(c.q, c.k);
-    BiasBackArgs a{dout, static_cast<float*>(ws), c.sb, c.sh, c.sq, c.heads, c.batch, sh.strip,
-                   sh.qt, sh.dt, c.buckets};
-    const int64_t tiles = c.q > 0 && c.k > 0 ? c.batch * c.heads * sh.qt * sh.dt : 0;
-    if (tiles > 0) {
+    const BackShape sh = back_shape(c.batch, c.heads, c.q, c.k);
+    BiasBackArgs a{dout, static_cast<double*>(ws), c.sb, c.sh, c.sq, extent_of(c), c.heads,
+                   c.batch, sh.strip, sh.qt, sh.dt, c.buckets};
+    const int64_t per_head = (sh.qt * sh.dt + kWaves - 1) / kWaves;
+    const int64_t groups = c.q > 0 && c.k > 0 ? c.batch * c.heads * per_head : 0;
+    if (groups > 0) {
         KernelTimer kt("k_relative_bias_backward", s);
-        k_relative_bias_backward<T><<<dim3(grid_of((tiles + kWaves - 1) / kWaves)), dim3(kBlock), 0, s>>>(m, a);
+        k_relative_bias_backward<T><<<dim3(grid_of(groups)), dim3(kBlock), 0, s>>>(m, a);
         const det_status st = launch_status();
         if (st != DET_SUCCESS) return st;
     }
     KernelTimer kt("k_bias_table_sums", s);
-    k_bias_table_sums<T><<<dim3((unsigned)(c.heads * c.buckets)), dim3(kBlock), 0, s>>>(
-        a.part, tiles > 0 ? c.batch : 0, c.heads, sh.qt * sh.dt, c.buckets,
-        static_cast<T*>(dtable));
+    const int64_t wgs = c.heads * ((c.buckets + kSumBuckets - 1) / kSumBuckets);
+    k_bias_table_sums<T><<<dim3((unsigned)wgs), dim3(kSumBlock), 0, s>>>(
+        a.part, groups > 0 ? c.batch : 0, c.heads, per_head, c.buckets, static_cast<T*>(dtable));
     return launch_status();
 }
 
 }  // namespace
 
 size_t bias_backward_workspace(int64_t batch, int64_t heads, int64_t q, int64_t k, int buckets) {
-    const BackShape s = back_shape(q, k);
-    return round_up((size_t)batch * heads * s.qt * s.dt * buckets * sizeof(float), 256) + 256;
+    const BackShape s = back_shape(batch, heads, q, k);
+    const int64_t per_head = (s.qt * s.dt + kWaves - 1) / kWaves;
+    return round_up((size_t)batch * heads * per_head * buckets * sizeof(double), 256) + 256;
 }
 
 det_status bias_launch(const BiasCall& c, hipStream_t s) {
