@@ -12,7 +12,7 @@
 //
 // Order: 1024 lanes share a row, lane L holding elements 8 L + 8192 j .. + 8 for j = 0, 1, ...;
 // each adds its own in that order, then 64 neighbouring lanes join by the adjacent-lanes tree,
-// then the 16 groups in ascending order.  How many threads play those lanes does not enter the
+// then the 16 groups by the same tree.  How many threads play those lanes does not enter the
 // order, nor do the other rows: a row's bits depend on its logits and the scale alone.
 #include <float.h>
 
@@ -25,6 +25,7 @@ namespace {
 constexpr int kLanes = 1024;              // lanes that share a row, in the order above
 constexpr int kTile = kLanes * kVec;      // elements they take at a time
 constexpr int kGroup = 32;                // neighbouring elements whose largest is kept for top
+constexpr int kShort = 512;               // candidates of the short way to the top
 // A lane's reference is one of its own values, replaced when a value exceeds it by more than
 // this: sums against it stay far from overflow, terms are off by at most the rounding of a
 // difference of that size, and a lane rarely rescales.
@@ -71,6 +72,14 @@ __device__ __forceinline__ void rebase(Part& p, float ref) {
     p.ref = ref;
 }
 
+// over 16 neighbouring lanes, by the adjacent-lanes tree
+__device__ __forceinline__ float sum16(float v) {
+    v = v + xor_partner<1>(v);
+    v = v + xor_partner<2>(v);
+    v = v + xor_partner<4>(v);
+    return v + xor_partner<8>(v);
+}
+
 // adds 8 logits; `largest`: their maximum (NaN ignored)
 __device__ __forceinline__ void take(Part& p, const float (&x)[kVec], float largest, float scale) {
     const float top = largest * scale;
@@ -113,22 +122,78 @@ __host__ __device__ constexpr int64_t super_len(int64_t vocab) {
     return ((vocab + kGroup - 1) / kGroup + 63) / 64 | 1;
 }
 
-// The `top` largest logits of a row.  On entry s_key holds the order key of every group's
-// largest logit (0 behind the last group).  The top logits lie in the top groups (each of these
-// holds one that beats every logit of the others), so one wave picks the groups through a
-// tournament of 64 super-groups, and the workgroup ranks the picked groups' logits that reach
-// the last picked group's largest.
+// LDS of the top logits' search
+struct Search {
+    uint32_t super[64];                     // largest key of each super-group
+    uint32_t pick[kShort];                  // groups whose logits may be candidates
+    unsigned long long cand[kShort];        // candidates: key, then the lower index first
+    uint32_t bound;                         // a key that at least `top` logits reach
+    int picks, cands;
+};
+
+// Ranks n candidates (their places differ from run to run, their ranks do not) and writes the
+// first `top`; 8 lanes a candidate.
+template <int BLOCK>
+__device__ __forceinline__ void rank_candidates(const LogpArgs& a, int64_t row,
+                                                const unsigned long long* cand, int n, float ref,
+                                                float log_s) {
+    const int part = threadIdx.x & 7;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += BLOCK / 8) {
+        const int i = i0 + (threadIdx.x >> 3);
+        const unsigned long long c = i < n ? cand[i] : 0;
+        uint32_t rank = 0;
+#pragma unroll 2
+        for (int j = part; j < n; j += 8) rank += cand[j] > c;
+        rank += xor_partner<1>(rank);
+        rank += xor_partner<2>(rank);
+        rank += xor_partner<4>(rank);
+        if (part == 0 && i < n && (int)rank < a.top) {
+            const float z = fmaf(key_value((uint32_t)(c >> 32)), a.scale, -ref);
+            a.top_ids[row * a.top + rank] = (int64_t)(uint32_t)~(uint32_t)c;
+            a.top_logp[row * a.top + rank] = z - log_s;
+        }
+    }
+}
+
+// Candidates among the logits of groups pick[0 .. n): those whose key reaches `bound`, as far as
+// `room` goes (*count counts all).
 template <typename T, int BLOCK>
-__device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s_key,
-                         uint32_t* s_super, uint32_t* s_pick, int* s_count, uint32_t* s_least,
+__device__ __forceinline__ void gather_candidates(const LogpArgs& a, const T* x,
+                                                  const uint32_t* pick, int n, uint32_t bound,
+                                                  unsigned long long* cand, int room, int* count) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n * kGroup; i += BLOCK) {
+        const uint32_t id = pick[i / kGroup] * kGroup + i % kGroup;
+        if (id >= a.vocab) continue;
+        const uint32_t k = order_key((float)x[id]);
+        if (k < bound) continue;
+        const int at = atomicAdd(count, 1);
+        if (at < room) cand[at] = (unsigned long long)k << 32 | (uint32_t)~id;
+    }
+}
+
+// The `top` largest logits of a row.  On entry s_key holds the order key of every group's
+// largest logit (0 behind the last group), in 64 super-groups of super_len groups.
+//
+// The top-th largest of the super-groups' maxima is a bound that at least `top` logits reach, and
+// few more do in most rows: these are ranked against each other.  Where too many reach it (long
+// runs of equal logits, logits in ascending order), one wave picks the top groups one by one
+// through a tournament of the super-groups instead, and their logits are the candidates: the
+// top logits lie in the top groups, since each of these holds one that beats every logit of the
+// others.
+template <typename T, int BLOCK>
+__device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s_key, Search& s,
                          float ref, float log_s) {
     const int groups = (int)((a.vocab + kGroup - 1) / kGroup);
     const int len = (int)super_len(a.vocab);
     const int lane = threadIdx.x & 63;
-    constexpr int kParts = BLOCK / 64;
+    // kParts neighbouring lanes a super-group
+    constexpr int kParts = BLOCK / 64, kOthers = 64 / kParts;
+    const int sg = threadIdx.x / kParts, part = threadIdx.x % kParts;
     {
-        const int sg = threadIdx.x / kParts, part = threadIdx.x % kParts;
         uint32_t m = 0;
+#pragma unroll 4
         for (int i = part; i < len; i += kParts) m = umax(m, s_key[sg * len + i]);
         m = umax(m, xor_partner<1>(m));
         m = umax(m, xor_partner<2>(m));
@@ -136,64 +201,86 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
             m = umax(m, xor_partner<4>(m));
             m = umax(m, xor_partner<8>(m));
         }
-        if (part == 0) s_super[sg] = m;
-        if (threadIdx.x == 0) *s_count = 0;
+        if (part == 0) s.super[sg] = m;
+        if (threadIdx.x == 0) s.picks = s.cands = 0;
     }
     __syncthreads();
-    const int picks = a.top < groups ? a.top : groups;
-    if (threadIdx.x < 64) {
-        uint32_t mine = s_super[lane], best = 0;
-        for (int r = 0; r < picks; ++r) {
-            best = wave_max(mine);
-            const int sg = __ffsll((unsigned long long)__ballot(mine == best)) - 1;
-            // the first group of that super-group with this key, and the largest of the others
-            uint32_t rest = 0;
-            int at = -1;
-            for (int i = 0; i < len; i += 64) {
-                uint32_t k = i + lane < len ? s_key[sg * len + i + lane] : 0;
-                const unsigned long long hits = __ballot(k == best);
-                if (at < 0 && hits) {
-                    const int l = __ffsll(hits) - 1;
-                    at = i + l;
-                    if (lane == l) k = 0;
+    {
+        const uint32_t mine = s.super[sg];
+        uint32_t rank = 0;
+#pragma unroll 4
+        for (int i = 0; i < kOthers; ++i) {
+            const int j = part * kOthers + i;
+            const uint32_t k = s.super[j];
+            rank += k > mine || (k == mine && j < sg);
+        }
+        rank += xor_partner<1>(rank);
+        rank += xor_partner<2>(rank);
+        if constexpr (kParts == 16) {
+            rank += xor_partner<4>(rank);
+            rank += xor_partner<8>(rank);
+        }
+        // 0: a super-group behind the row's end, so that every logit counts
+        if (part == 0 && (int)rank == a.top - 1) s.bound = umax(mine, 1u);
+    }
+    __syncthreads();
+    const uint32_t bound = s.bound;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < groups; i += BLOCK)
+        if (s_key[i] >= bound) {
+            const int at = atomicAdd(&s.picks, 1);
+            if (at < kShort) s.pick[at] = (uint32_t)i;
+        }
+    __syncthreads();
+    bool done = s.picks <= kShort;
+    if (done) {
+        gather_candidates<T, BLOCK>(a, x, s.pick, s.picks, bound, s.cand, kShort, &s.cands);
+        __syncthreads();
+        done = s.cands <= kShort;
+        if (done) rank_candidates<BLOCK>(a, row, s.cand, s.cands, ref, log_s);
+    }
+    if (!done) {
+        const int picks = a.top < groups ? a.top : groups;
+        __syncthreads();      // s.picks and s.cands are read
+        if (threadIdx.x < 64) {
+            uint32_t mine = s.super[lane], best = 0;
+            for (int r = 0; r < picks; ++r) {
+                best = wave_max(mine);
+                const int from = __ffsll((unsigned long long)__ballot(mine == best)) - 1;
+                // the first group of that super-group with this key, and the largest other key
+                uint32_t rest = 0;
+                int at = -1;
+                for (int i = 0; i < len; i += 64) {
+                    uint32_t k = i + lane < len ? s_key[from * len + i + lane] : 0;
+                    const unsigned long long hits = __ballot(k == best);
+                    if (at < 0 && hits) {
+                        const int l = __ffsll(hits) - 1;
+                        at = i + l;
+                        if (lane == l) k = 0;
+                    }
+                    rest = umax(rest, k);
                 }
-                rest = umax(rest, k);
+                rest = wave_max(rest);
+                if (lane == from) mine = rest;
+                if (lane == 0) {
+                    s.pick[r] = from * len + at;
+                    s_key[from * len + at] = 0;
+                }
+                wave_sync();
             }
-            rest = wave_max(rest);
-            if (lane == sg) mine = rest;
+            // with fewer groups than places every logit is a candidate
             if (lane == 0) {
-                s_pick[r] = sg * len + at;
-                s_key[sg * len + at] = 0;
+                s.bound = picks < a.top ? 1u : best;
+                s.cands = 0;
             }
-            wave_sync();
         }
-        // with fewer groups than places every logit is a candidate
-        if (lane == 0) *s_least = picks < a.top ? 1u : best;
+        __syncthreads();
+        unsigned long long* cand = reinterpret_cast<unsigned long long*>(s_key);
+        gather_candidates<T, BLOCK>(a, x, s.pick, picks, s.bound, cand, picks * kGroup, &s.cands);
+        __syncthreads();
+        rank_candidates<BLOCK>(a, row, cand, s.cands, ref, log_s);
     }
-    __syncthreads();
-    unsigned long long* s_cand = reinterpret_cast<unsigned long long*>(s_key);
-    const uint32_t least = *s_least;
-    for (int i = threadIdx.x; i < picks * kGroup; i += BLOCK) {
-        const int64_t id = (int64_t)s_pick[i / kGroup] * kGroup + i % kGroup;
-        if (id >= a.vocab) continue;
-        const uint32_t k = order_key((float)x[id]);
-        if (k < least) continue;
-        s_cand[atomicAdd(s_count, 1)] = (unsigned long long)k << 32 | (uint32_t)~(uint32_t)id;
-    }
-    __syncthreads();
-    // the candidates' places differ from run to run, their ranks do not
-    const int n = *s_count;
-    for (int i = threadIdx.x; i < n; i += BLOCK) {
-        const unsigned long long c = s_cand[i];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += s_cand[j] > c;
-        if (rank < a.top) {
-            const float z = fmaf(key_value((uint32_t)(c >> 32)), a.scale, -ref);
-            a.top_ids[row * a.top + rank] = (int64_t)(uint32_t)~(uint32_t)c;
-            a.top_logp[row * a.top + rank] = z - log_s;
-        }
-    }
-    __syncthreads();      // s_key is written again
+    __syncthreads();      // s_key and s are written again
 }
 
 // One row per workgroup, each logit read once.
@@ -202,13 +289,16 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
     constexpr int kSets = kLanes / BLOCK;       // lanes a thread plays
     constexpr int kSteps = 4 / kSets;           // tiles whose loads are in flight together
     extern __shared__ __align__(16) uint32_t s_key[];
-    __shared__ float s_max[BLOCK / 64], s_s[kLanes / 64], s_w[kLanes / 64];
-    __shared__ uint32_t s_super[64], s_pick[DET_LOGPROB_MAX_TOP], s_least;
-    __shared__ int s_count;
+    __shared__ Part s_part[2][kLanes / 64];      // rows take turns: no second barrier a row
+    __shared__ Search s_search;      // not laid out where nothing is searched
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    int parity = 0;
     const int64_t key_slots = TOP ? 64 * super_len(a.vocab) : 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T* x = static_cast<const T*>(a.logits) + row * a.stride;
+        const int64_t target = a.targets[row];
+        const bool scored = target >= 0 && target < a.vocab;
+        const float picked = scored ? (float)x[target] : 0.0f;
         Part p[kSets];
 #pragma unroll
         for (int u = 0; u < kSets; ++u) p[u] = Part{-FLT_MAX, 0.0f, 0.0f};
@@ -254,46 +344,32 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
                 one(c, u, v, c < a.vocab);
             }
         }
-        // the row's reference, then every lane's sums against it
-        float ref = p[0].ref;
-#pragma unroll
-        for (int u = 1; u < kSets; ++u) ref = fmaxf(ref, p[u].ref);
-        ref = wave_max(ref);
-        if (lane == 0) s_max[wave] = ref;
-        __syncthreads();
-        ref = s_max[0];
-#pragma unroll
-        for (int w = 1; w < BLOCK / 64; ++w) ref = fmaxf(ref, s_max[w]);
+        // 64 neighbouring lanes against their own largest reference, then those 16 groups
 #pragma unroll
         for (int u = 0; u < kSets; ++u) {
+            const float ref = wave_max(p[u].ref);
             rebase(p[u], ref);
             const float s = wave_pw(p[u].s), w = wave_pw(p[u].w);
-            if (lane == 0) {
-                s_s[wave + u * (BLOCK / 64)] = s;
-                s_w[wave + u * (BLOCK / 64)] = w;
-            }
+            if (lane == 0) s_part[parity][wave + u * (BLOCK / 64)] = Part{ref, s, w};
         }
         __syncthreads();
-        float s = s_s[0], w = s_w[0];
-#pragma unroll
-        for (int i = 1; i < kLanes / 64; ++i) {
-            s += s_s[i];
-            w += s_w[i];
-        }
-        const float log_s = logf(s);
+        Part g = s_part[parity][lane & 15];      // every wave joins them for itself
+        parity ^= 1;
+        float ref = g.ref;
+        ref = fmaxf(ref, xor_partner<1>(ref));
+        ref = fmaxf(ref, xor_partner<2>(ref));
+        ref = fmaxf(ref, xor_partner<4>(ref));
+        ref = fmaxf(ref, xor_partner<8>(ref));
+        rebase(g, ref);
+        const float s = sum16(g.s), w = sum16(g.w), log_s = logf(s);
+        const bool none = s == 0.0f;
         if (t == 0) {
-            const int64_t at = a.targets[row];
-            const bool none = s == 0.0f;
             a.lse[row] = ref + log_s;
             a.entropy[row] = none ? 0.0f : log_s - w / s;
-            float lp = 0.0f;
-            if (at >= 0 && at < a.vocab)
-                lp = none ? -INFINITY : fmaf((float)x[at], a.scale, -ref) - log_s;
-            a.logp[row] = lp;
+            a.logp[row] = !scored ? 0.0f : none ? -INFINITY : fmaf(picked, a.scale, -ref) - log_s;
         }
         if constexpr (TOP)
-            pick_top<T, BLOCK>(a, row, x, s_key, s_super, s_pick, &s_count, &s_least,
-                               s == 0.0f ? 0.0f : ref, s == 0.0f ? 0.0f : log_s);
+            pick_top<T, BLOCK>(a, row, x, s_key, s_search, none ? 0.0f : ref, none ? 0.0f : log_s);
     }
 }
 
