@@ -1,4 +1,5 @@
-"""ctypes binding of libdet.so (the HIP library), with the C interface's names.
+"""Binding of libdet.so (the HIP library), with the C interface's names: ctypes, and for the
+language-model operators, whose calls are small, an extension (csrc/lm_binding.cpp).
 
 Argument marshalling only: tensors become device pointers and sizes, the workspace is a
 torch uint8 tensor from the caching allocator, and the current torch stream is passed
@@ -363,53 +364,26 @@ def gather(values: torch.Tensor, index: torch.Tensor) -> torch.Tensor:
 
 # ------------------------------------------------------------------ language-model operators
 
-_LM_TYPES = {torch.float32: DET_F32, torch.float16: DET_F16, torch.bfloat16: DET_BF16}
+_lm = None
 
 
-def _lm_code(t: torch.Tensor) -> int:
-    code = _LM_TYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"the language-model operators take float32, float16 and bfloat16, "
-                        f"got {t.dtype}")
-    return code
-
-
-def _same(t: torch.Tensor, like: torch.Tensor, what: str) -> torch.Tensor:
-    if t.dtype != like.dtype:
-        raise TypeError(f"{what} must be {like.dtype}, got {t.dtype}")
-    return t
-
-
-def _of(t: torch.Tensor, dtype: torch.dtype, shape, what: str) -> torch.Tensor:
-    if t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _flat(t)
+def _lm_binding():
+    """The extension that marshals these operators' arguments (raises if it has not been built)."""
+    global _lm
+    if _lm is None:
+        lib()
+        try:
+            from . import _lm_binding as _lm
+        except ImportError as e:
+            raise RuntimeError(f"{os.path.join(_HERE, '_lm_binding.so')} cannot be loaded ({e}): "
+                               "build it with `python __graft_entry__.py`; there is no fallback "
+                               "path") from e
+    return _lm
 
 
 def _row_stride(t: torch.Tensor, what: str) -> int:
     """Elements between neighbouring rows of ``t`` (its last dimension is a row)."""
-    n = t.shape[-1]
-    if t.is_contiguous():
-        return n
-    if t.stride(-1) == 1 or n == 1:
-        stride = None          # of the innermost leading dimension longer than 1, then of all
-        for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-            if size == 1:
-                continue
-            if stride is None:
-                stride, span = st, st * size
-            elif st == span:
-                span = st * size
-            else:
-                break
-        else:
-            if stride is None:
-                return n
-            if stride >= n:
-                return stride
-    raise ValueError(f"det needs the rows of {what} contiguous and evenly spaced")
+    return _lm_binding().row_stride(t, what)
 
 
 class RmsNorm(NamedTuple):
@@ -431,37 +405,9 @@ def det_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     ``quant=torch.float8_e4m3fn``: y holds 8-bit codes and scales [..., ceil(d / group)] their
     scales, one for every ``group`` (32, 64, 128) neighbouring channels, or with ``group=0``
     one a row; y * scale stands for the normed value."""
-    code = _lm_code(x)
-    if x.dim() < 1:
-        raise ValueError("x must have at least one dimension")
-    shape, d = x.shape, x.shape[-1]
-    _of(weight, x.dtype, (d,), "weight")
-    stride = _row_stride(x, "x")
-    h, res_stride = None, 0
-    if residual is not None:
-        if _same(residual, x, "residual").shape != shape:
-            raise ValueError("residual must have the shape of x")
-        res_stride = _row_stride(residual, "residual")
-        h = torch.empty(shape, dtype=x.dtype, device=x.device)
-    rows = x.numel() // d if d else 0
-    y_code, scales, y_type = code, None, x.dtype
-    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
-    if quant is not None:
-        if quant != torch.float8_e4m3fn:
-            raise TypeError(f"quant must be torch.float8_e4m3fn, got {quant}")
-        if group not in (0, 32, 64, 128):
-            raise ValueError("group must be 0, 32, 64 or 128")
-        y_code, y_type = DET_E4M3, quant
-        scales = torch.empty((*shape[:-1], -(-d // group) if group else 1), dtype=torch.float32,
-                             device=x.device)
-    elif group:
-        raise ValueError("group is for an 8-bit output")
-    y = torch.empty(shape, dtype=y_type, device=x.device)
-    _check(lib().det_rms_norm(_dev_ptr(x), stride, _dev_ptr(residual), res_stride,
-                              _dev_ptr(weight), rows, d, code, eps, _dev_ptr(h), _dev_ptr(y),
-                              y_code, group, _dev_ptr(scales), _dev_ptr(rstd),
-                              _stream(x.device)), "det_rms_norm")
-    return RmsNorm(y, x if h is None else h, rstd, scales)
+    if quant is not None and quant != torch.float8_e4m3fn:
+        raise TypeError(f"quant must be torch.float8_e4m3fn, got {quant}")
+    return RmsNorm(*_lm_binding().rms_norm(x, weight, eps, residual, quant is not None, group))
 
 
 @functools.lru_cache(maxsize=256)
@@ -477,53 +423,7 @@ def det_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     ``dh``: the gradient that reaches h from elsewhere (the residual stream), added to dx.  dx is
     also the residual's gradient.  dweight's sum over the rows has an order fixed by their
     number."""
-    code = _lm_code(h)
-    if h.dim() < 1:
-        raise ValueError("h must have at least one dimension")
-    d = h.shape[-1]
-    _of(weight, h.dtype, (d,), "weight")
-    _of(rstd, torch.float32, h.shape[:-1], "rstd")
-    if _same(dy, h, "dy").shape != h.shape:
-        raise ValueError("dy must have the shape of h")
-    dh_stride = 0
-    if dh is not None:
-        if _same(dh, h, "dh").shape != h.shape:
-            raise ValueError("dh must have the shape of h")
-        dh_stride = _row_stride(dh, "dh")
-    rows = h.numel() // d if d else 0
-    dev = h.device
-    dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
-    dweight = torch.empty(d, dtype=h.dtype, device=dev)
-    w = _workspace(det_rms_norm_backward_workspace_size(rows, d, code), dev, ws)
-    _check(lib().det_rms_norm_backward(_dev_ptr(dy), _row_stride(dy, "dy"), _dev_ptr(h),
-                                       _row_stride(h, "h"), _dev_ptr(weight), _dev_ptr(rstd),
-                                       _dev_ptr(dh), dh_stride, rows, d, code, _dev_ptr(dx),
-                                       _dev_ptr(dweight), _dev_ptr(w),
-                                       w.numel() * w.element_size(), _stream(dev)),
-           "det_rms_norm_backward")
-    return dx, dweight
-
-
-def _bias_masks(q_offset, lengths: Optional[torch.Tensor], batch: Optional[int]):
-    """(batch, whole-number offset, its tensor or None); the tensors' own checks."""
-    offsets = q_offset if torch.is_tensor(q_offset) else None
-    for t, what in ((offsets, "q_offset"), (lengths, "lengths")):
-        if t is None:
-            continue
-        if t.dim() != 1:
-            raise ValueError(f"{what} must be one-dimensional")
-        if batch is None:
-            batch = t.shape[0]
-        _of(t, torch.int32, (batch,), what)
-    return 1 if batch is None else batch, 0 if offsets is not None else int(q_offset), offsets
-
-
-def _bias_strides(t: torch.Tensor, what: str):
-    if t.dim() != 4:
-        raise ValueError(f"{what} must be [batch, heads, q, k]")
-    if t.stride(3) != 1 and t.shape[3] > 1:
-        raise ValueError(f"det needs the rows of {what} contiguous")
-    return t.stride()[:3]
+    return _lm_binding().rms_norm_backward(dy, h, weight, rstd, dh, ws)
 
 
 def _bias_flags(bidirectional: bool, causal: bool) -> int:
@@ -545,28 +445,11 @@ def det_relative_bias(table: torch.Tensor, q: int, k: int, scores: Optional[torc
     position among the keys, a whole number or int32 [batch].  Without scores, lengths or a
     tensor of offsets batch is 1: one bias serves every sequence.  ``scores``: [batch, heads,
     q, k] of the table's type, rows contiguous, other strides free; ``out`` may be scores."""
-    code = _lm_code(table)
-    if table.dim() != 2:
-        raise ValueError("table must be [buckets, heads]")
-    buckets, heads = _flat(table).shape
-    sb = sh = sq = 0
-    batch = None
-    if scores is not None:
-        sb, sh, sq = _bias_strides(_same(scores, table, "scores"), "scores")
-        batch = scores.shape[0]
-        if scores.shape[1:] != (heads, q, k):
-            raise ValueError(f"scores must be [batch, {heads}, {q}, {k}]")
-    batch, offset, offsets = _bias_masks(q_offset, lengths, batch)
-    if out is None:
-        out = torch.empty((batch, heads, q, k), dtype=table.dtype, device=table.device)
-    else:
-        _of(out, table.dtype, (batch, heads, q, k), "out")
-    _check(lib().det_relative_bias(_dev_ptr(table), buckets, heads, max_distance,
-                                   _bias_flags(bidirectional, causal), batch, q, k, offset,
-                                   _dev_ptr(offsets), _dev_ptr(lengths), _dev_ptr(scores), sb, sh,
-                                   sq, code, _dev_ptr(out), _stream(table.device)),
-           "det_relative_bias")
-    return out
+    several = torch.is_tensor(q_offset)
+    return _lm_binding().relative_bias(table, q, k, scores, max_distance,
+                                       _bias_flags(bidirectional, causal),
+                                       0 if several else q_offset, q_offset if several else None,
+                                       lengths, out)
 
 
 @functools.lru_cache(maxsize=256)
@@ -586,24 +469,11 @@ def det_relative_bias_backward(dout: torch.Tensor, num_buckets: int, max_distanc
     over the unmasked places, in an order fixed by the sizes (arguments as for
     det_relative_bias).  ``dscores`` (contiguous, dout's shape and type; may be dout itself)
     receives the scores' gradient: dout with zeros at the masked places."""
-    code = _lm_code(dout)
-    sb, sh, sq = _bias_strides(dout, "dout")
-    heads, q, k = dout.shape[1:]
-    batch, offset, offsets = _bias_masks(q_offset, lengths, dout.shape[0])
-    if dscores is not None:
-        _of(dscores, dout.dtype, dout.shape, "dscores")
-    dev = dout.device
-    dtable = torch.empty((num_buckets, heads), dtype=dout.dtype, device=dev)
-    w = _workspace(det_relative_bias_backward_workspace_size(batch, heads, q, k, num_buckets, code),
-                   dev, ws)
-    _check(lib().det_relative_bias_backward(_dev_ptr(dout), sb, sh, sq, num_buckets, heads,
-                                            max_distance, _bias_flags(bidirectional, causal),
-                                            batch, q, k, offset, _dev_ptr(offsets),
-                                            _dev_ptr(lengths), code, _dev_ptr(dtable),
-                                            _dev_ptr(dscores), _dev_ptr(w),
-                                            w.numel() * w.element_size(), _stream(dev)),
-           "det_relative_bias_backward")
-    return dtable
+    several = torch.is_tensor(q_offset)
+    return _lm_binding().relative_bias_backward(dout, num_buckets, max_distance,
+                                                _bias_flags(bidirectional, causal),
+                                                0 if several else q_offset,
+                                                q_offset if several else None, lengths, dscores, ws)
 
 
 class TokenLogprobs(NamedTuple):
@@ -624,23 +494,7 @@ def det_token_logprobs(logits: torch.Tensor, targets: torch.Tensor, scale: float
     logits: [..., vocab], rows contiguous and evenly spaced (a slice of a padded vocabulary is
     fine); targets: int64 [...]; one outside the vocabulary (such as -100) is not scored and its
     logp is 0.  A row's bits depend on its logits and the scale alone."""
-    code = _lm_code(logits)
-    if logits.dim() < 1:
-        raise ValueError("logits must have at least one dimension")
-    shape, vocab, dev = logits.shape[:-1], logits.shape[-1], logits.device
-    _of(targets, torch.int64, shape, "targets")
-    stride = _row_stride(logits, "logits")
-    logp = torch.empty(shape, dtype=torch.float32, device=dev)
-    entropy, lse = torch.empty_like(logp), torch.empty_like(logp)
-    top_logp = top_ids = None
-    if top:
-        top_logp = torch.empty((*shape, top), dtype=torch.float32, device=dev)
-        top_ids = torch.empty((*shape, top), dtype=torch.int64, device=dev)
-    _check(lib().det_token_logprobs(_dev_ptr(logits), stride, _dev_ptr(targets), targets.numel(),
-                                    vocab, code, scale, _dev_ptr(logp), _dev_ptr(entropy),
-                                    _dev_ptr(lse), top, _dev_ptr(top_logp), _dev_ptr(top_ids),
-                                    _stream(dev)), "det_token_logprobs")
-    return TokenLogprobs(logp, entropy, lse, top_logp, top_ids)
+    return TokenLogprobs(*_lm_binding().token_logprobs(logits, targets, scale, top))
 
 
 def det_token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
@@ -650,31 +504,8 @@ def det_token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse
     """The logits' gradient for ``dlogp`` and, where given, ``dentropy`` (float32 [...]); ``lse``
     and ``entropy`` as det_token_logprobs returned them for these logits and this scale.  ``out``
     (logits' shape and type, rows contiguous and evenly spaced) may be logits itself."""
-    code = _lm_code(logits)
-    if logits.dim() < 1:
-        raise ValueError("logits must have at least one dimension")
-    shape, vocab = logits.shape[:-1], logits.shape[-1]
-    _of(targets, torch.int64, shape, "targets")
-    for t, what in ((lse, "lse"), (dlogp, "dlogp"), (entropy, "entropy"), (dentropy, "dentropy")):
-        if t is not None:
-            _of(t, torch.float32, shape, what)
-    if dentropy is not None and entropy is None:
-        raise ValueError("dentropy needs entropy")
-    stride = _row_stride(logits, "logits")
-    if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        out_stride = vocab
-    else:
-        if _same(out, logits, "out").shape != logits.shape:
-            raise ValueError("out must have the shape of logits")
-        out_stride = _row_stride(out, "out")
-    _check(lib().det_token_logprobs_backward(_dev_ptr(logits), stride, _dev_ptr(targets),
-                                             _dev_ptr(lse), _dev_ptr(dlogp), _dev_ptr(entropy),
-                                             _dev_ptr(dentropy), targets.numel(), vocab, code,
-                                             scale, _dev_ptr(out), out_stride,
-                                             _stream(logits.device)),
-           "det_token_logprobs_backward")
-    return out
+    return _lm_binding().token_logprobs_backward(logits, targets, lse, dlogp, entropy, dentropy,
+                                                 scale, out)
 
 
 class _RmsNormFn(torch.autograd.Function):
