@@ -75,6 +75,14 @@ det_status scatter_running_launch(const void* values, const int32_t* index, int6
                                   void* prev, int64_t* n_skipped, void* ws, hipStream_t s);
 
 // ---- language-model operators (arguments checked by the caller)
+// Inputs from this many bytes on are loaded past the caches.  Half of the 256 MB last-level cache:
+// below it the producer's data may still be there, above it the loads only push out what the
+// call writes.  Measured with inputs that change from call to call, plain and past the caches:
+// norm of 8192 x 8192 bf16 with residual (268 MB read) 97 and 85 us, its backward over 16384 x
+// 4096 111 and 99, log probabilities of 2048 x 131072 105 and 98; but norm of 2048 x 4096
+// (34 MB) 12.4 and 14.5, logits' gradient of 1024 x 16384 (34 MB) 12.9 and 16.6.
+constexpr size_t kOnceBytes = (size_t)128 << 20;
+
 inline size_t lm_size(det_dtype d) { return d == DET_F32 ? 4 : d == DET_E4M3 ? 1 : 2; }
 
 struct NormCall {

@@ -34,27 +34,26 @@ struct Raw8<float> {
     f32x4 a, b;
 };
 
-template <typename T>
+// ONCE: past the caches, for data that is read once and would push out what the caches hold
+template <bool ONCE = false, typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* p) {
     Raw8<T> r;
     if constexpr (sizeof(T) == 4) {
-        r.a = *reinterpret_cast<const f32x4_a4*>(p);
-        r.b = *reinterpret_cast<const f32x4_a4*>(p + 4);
+        const f32x4_a4* q = reinterpret_cast<const f32x4_a4*>(p);
+        const f32x4_a4* q1 = reinterpret_cast<const f32x4_a4*>(p + 4);
+        if constexpr (ONCE) {
+            r.a = __builtin_nontemporal_load(q);
+            r.b = __builtin_nontemporal_load(q1);
+        } else {
+            r.a = *q;
+            r.b = *q1;
+        }
     } else {
-        r.a = *reinterpret_cast<const u32x4_a2*>(p);
-    }
-    return r;
-}
-
-// the same past the caches, for data that is read once
-template <typename T>
-__device__ __forceinline__ Raw8<T> load8_once(const T* p) {
-    Raw8<T> r;
-    if constexpr (sizeof(T) == 4) {
-        r.a = __builtin_nontemporal_load(reinterpret_cast<const f32x4_a4*>(p));
-        r.b = __builtin_nontemporal_load(reinterpret_cast<const f32x4_a4*>(p + 4));
-    } else {
-        r.a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
+        const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p);
+        if constexpr (ONCE)
+            r.a = __builtin_nontemporal_load(q);
+        else
+            r.a = *q;
     }
     return r;
 }
@@ -66,16 +65,6 @@ __device__ __forceinline__ void store8(T* p, const Raw8<T>& r) {
         *reinterpret_cast<f32x4_a4*>(p + 4) = r.b;
     } else {
         *reinterpret_cast<u32x4_a2*>(p) = r.a;
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void store8_once(T* p, const Raw8<T>& r) {
-    if constexpr (sizeof(T) == 4) {
-        __builtin_nontemporal_store(r.a, reinterpret_cast<f32x4_a4*>(p));
-        __builtin_nontemporal_store(r.b, reinterpret_cast<f32x4_a4*>(p + 4));
-    } else {
-        __builtin_nontemporal_store(r.a, reinterpret_cast<u32x4_a2*>(p));
     }
 }
 
@@ -139,12 +128,21 @@ __device__ __forceinline__ void store_tail(T* p, int64_t n, const float (&v)[kVe
 }
 
 // 8 elements of which n lie inside the row (unpacked, `fill` behind them)
-template <typename T>
+template <bool ONCE = false, typename T>
 __device__ __forceinline__ void read8(const T* p, int64_t n, float fill, float (&v)[kVec]) {
     if (n >= kVec)
-        unpack8<T>(load8(p), v);
+        unpack8<T>(load8<ONCE>(p), v);
     else
         load_tail(p, n, fill, v);
+}
+
+// the same as it lies in memory, zeros behind them
+template <bool ONCE = false, typename T>
+__device__ __forceinline__ Raw8<T> read_raw8(const T* p, int64_t n) {
+    if (n >= kVec) return load8<ONCE>(p);
+    float v[kVec];
+    load_tail(p, n, 0.0f, v);
+    return pack8<T>(v);
 }
 
 template <typename T>

@@ -284,7 +284,7 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
 }
 
 // One row per workgroup, each logit read once.
-template <typename T, int BLOCK, bool TOP>
+template <typename T, int BLOCK, bool TOP, bool ONCE>
 __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
     constexpr int kSets = kLanes / BLOCK;       // lanes a thread plays
     constexpr int kSteps = 4 / kSets;           // tiles whose loads are in flight together
@@ -325,7 +325,7 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
             for (int q = 0; q < kSteps; ++q)
 #pragma unroll
                 for (int u = 0; u < kSets; ++u)
-                    raw[q][u] = load8(x + (i * kSteps + q) * kTile + kVec * (t + u * BLOCK));
+                    raw[q][u] = load8<ONCE>(x + (i * kSteps + q) * kTile + kVec * (t + u * BLOCK));
 #pragma unroll
             for (int q = 0; q < kSteps; ++q)
 #pragma unroll
@@ -388,7 +388,7 @@ constexpr int kBackVecs = 4;                              // vectors a thread
 constexpr int kBackTile = 256 * kVec * kBackVecs;
 
 // Each logit read once, each gradient written once; nothing is summed.
-template <typename T>
+template <typename T, bool ONCE>
 __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a) {
     for (int64_t tile = blockIdx.x; tile < a.rows * a.tiles; tile += gridDim.x) {
         const int64_t row = tile / a.tiles, c0 = tile % a.tiles * kBackTile;
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a)
             const int64_t c = c0 + kVec * (threadIdx.x + 256 * j), n = a.vocab - c;
             if (n <= 0) continue;
             float v[kVec];
-            read8(x + c, n, 0.0f, v);
+            read8<ONCE>(x + c, n, 0.0f, v);
             const int64_t hit = scored ? at - c : -1;
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
@@ -422,33 +422,43 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a)
     }
 }
 
-template <typename T, int BLOCK>
+template <typename T, int BLOCK, bool ONCE>
 void logp_block(const LogpArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.rows < (1 << 21) ? a.rows : (1 << 21))), block(BLOCK);
     KernelTimer kt("k_token_logprobs", s);
     if (a.top > 0) {
         const int64_t keys = 64 * super_len(a.vocab) * 4, cand = (int64_t)a.top * kGroup * 8;
         const int lds = (int)(keys > cand ? keys : cand);
-        k_token_logprobs<T, BLOCK, true><<<grid, block, lds, s>>>(a);
+        k_token_logprobs<T, BLOCK, true, ONCE><<<grid, block, lds, s>>>(a);
     } else {
-        k_token_logprobs<T, BLOCK, false><<<grid, block, 0, s>>>(a);
+        k_token_logprobs<T, BLOCK, false, ONCE><<<grid, block, 0, s>>>(a);
     }
+}
+
+template <typename T>
+bool once(int64_t rows, int64_t vocab) {
+    return (double)rows * (double)vocab * sizeof(T) >= (double)kOnceBytes;
 }
 
 template <typename T>
 void logp_typed(const LogpArgs& a, hipStream_t s) {
     if (a.rows <= 256 && a.vocab > kTile)
-        logp_block<T, 1024>(a, s);
+        logp_block<T, 1024, false>(a, s);
+    else if (once<T>(a.rows, a.vocab))
+        logp_block<T, 256, true>(a, s);
     else
-        logp_block<T, 256>(a, s);
+        logp_block<T, 256, false>(a, s);
 }
 
 template <typename T>
 void logp_back_typed(const LogpBackArgs& a, hipStream_t s) {
     const int64_t wgs = a.rows * a.tiles;
+    const dim3 grid((unsigned)(wgs < (1 << 22) ? wgs : (1 << 22))), block(256);
     KernelTimer kt("k_token_logprobs_backward", s);
-    k_token_logprobs_backward<T><<<dim3((unsigned)(wgs < (1 << 22) ? wgs : (1 << 22))), dim3(256),
-                                   0, s>>>(a);
+    if (once<T>(a.rows, a.vocab))
+        k_token_logprobs_backward<T, true><<<grid, block, 0, s>>>(a);
+    else
+        k_token_logprobs_backward<T, false><<<grid, block, 0, s>>>(a);
 }
 
 }  // namespace

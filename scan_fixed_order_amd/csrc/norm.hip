@@ -126,7 +126,7 @@ __device__ __forceinline__ void put(const NormArgs& a, int64_t row, int64_t c, i
 
 // One row per team, the row in registers: NV vectors a lane.  Bound by HBM: every element is
 // read once and written once.
-template <typename T, int TEAM, int NV, bool RES, bool Q8>
+template <typename T, int TEAM, int NV, bool RES, bool Q8, bool ONCE>
 __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
     constexpr int kRows = Team<TEAM>::kRows, kWaves = Team<TEAM>::kWaves;
     __shared__ float s_sum[kRows][kWaves];
@@ -145,8 +145,8 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int64_t c = (int64_t)kVec * (t + j * TEAM);
-        read8(x + c, a.d - c, 0.0f, h[j]);
-        if constexpr (RES) read8(res + c, a.d - c, 0.0f, r[j]);
+        read8<ONCE>(x + c, a.d - c, 0.0f, h[j]);
+        if constexpr (RES) read8<ONCE>(res + c, a.d - c, 0.0f, r[j]);
     }
     float sum = 0.0f;
 #pragma unroll
@@ -263,48 +263,84 @@ struct NormBackArgs {
     int64_t dy_stride, h_stride, dh_stride, rows, d, strip;
 };
 
-// A team walks its strip of rows and keeps the strip's column sums in registers.  Bound by HBM.
-template <typename T, int TEAM, int NV, bool DH>
+// Lanes of a team that takes rows of up to d elements in the backward pass, one vector a lane as
+// far as 1024 lanes go.
+constexpr int back_team(int64_t d) { return d <= 512 ? 64 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024; }
+
+// One row's vectors of a lane as they lie in memory
+template <typename T, int NV>
+struct BackRow {
+    Raw8<T> h[NV], dy[NV], dh[NV];
+    float rstd;
+};
+
+// A team walks its strip of rows and keeps the strip's column sums in registers; the next row's
+// loads are in flight while this one's sum goes round the team (two f32 vectors a lane leave no
+// registers for that).  With two vectors a lane the column sums are kept in LDS: 2048 rows of
+// 16384 bf16 take 57 us so, 98 with them in registers (spilled), 67 so without the loads ahead.  The teams of a workgroup join their sums.  Bound by HBM.
+template <typename T, int TEAM, int NV, bool DH, bool ONCE>
 __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBackArgs a) {
     constexpr int kRows = Team<TEAM>::kRows, kWaves = Team<TEAM>::kWaves;
+    constexpr bool kAhead = sizeof(T) == 2 || NV == 1, kLdsSums = NV > 1;
+    extern __shared__ float s_cols[];      // kLdsSums: the lane's column sums, [vector][element][lane]
     __shared__ float s_sum[2][kRows][kWaves];
+    __shared__ float s_acc[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? TEAM * NV * kVec : 1];
     const int team = threadIdx.x / TEAM, t = threadIdx.x % TEAM;
     const int64_t strip = (int64_t)blockIdx.x * kRows + team;
     const int64_t begin = strip * a.strip;
     const T* w = static_cast<const T*>(a.w);
-    float g[NV][kVec], acc[NV][kVec];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int64_t c = (int64_t)kVec * (t + j * TEAM);
-        read8(w + c, a.d - c, 0.0f, g[j]);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) acc[j][i] = 0.0f;
-    }
-    // every team of the workgroup takes the same number of steps (barriers)
-    for (int64_t k = 0; k < a.strip; ++k) {
-        const int64_t row = begin + k < a.rows ? begin + k : a.rows - 1;
-        const bool live = begin + k < a.rows;
-        const T* hp = static_cast<const T*>(a.h) + row * a.h_stride;
-        const T* dyp = static_cast<const T*>(a.dy) + row * a.dy_stride;
-        const T* dhp = static_cast<const T*>(a.dh) + (DH ? row * a.dh_stride : 0);
-        const float rstd = a.rstd[row];
-        float h[NV][kVec], dy[NV][kVec], e[NV][kVec];
+    const auto read = [&](int64_t row, BackRow<T, NV>& r) {
+        if (row >= a.rows) row = a.rows - 1;
+        r.rstd = a.rstd[row];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int64_t c = (int64_t)kVec * (t + j * TEAM);
-            read8(hp + c, a.d - c, 0.0f, h[j]);
-            read8(dyp + c, a.d - c, 0.0f, dy[j]);
-            if constexpr (DH) read8(dhp + c, a.d - c, 0.0f, e[j]);
+            r.h[j] = read_raw8<ONCE>(static_cast<const T*>(a.h) + row * a.h_stride + c, a.d - c);
+            r.dy[j] = read_raw8<ONCE>(static_cast<const T*>(a.dy) + row * a.dy_stride + c, a.d - c);
+            if constexpr (DH && kAhead)
+                r.dh[j] = read_raw8<ONCE>(static_cast<const T*>(a.dh) + row * a.dh_stride + c, a.d - c);
         }
+    };
+    BackRow<T, NV> cur, next;
+    read(begin, cur);
+    Raw8<T> wraw[NV];
+    float acc[NV][kVec];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = (int64_t)kVec * (t + j * TEAM);
+        wraw[j] = read_raw8(w + c, a.d - c);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            acc[j][i] = 0.0f;
+            if constexpr (kLdsSums) s_cols[(j * kVec + i) * TEAM + t] = 0.0f;
+        }
+    }
+    // every team of the workgroup takes the same number of steps (barriers)
+    for (int64_t k = 0; k < a.strip; ++k) {
+        const bool live = begin + k < a.rows;
+        if constexpr (kAhead) {
+            if (k + 1 < a.strip) read(begin + k + 1, next);
+        }
+        const float rstd = cur.rstd;
+        float h[NV][kVec], dy[NV][kVec];
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
+            unpack8<T>(cur.h[j], h[j]);
+            unpack8<T>(cur.dy[j], dy[j]);
+            float g[kVec];
+            unpack8<T>(wraw[j], g);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
                 h[j][i] *= rstd;
                 const float p = dy[j][i] * h[j][i];
-                if (live) acc[j][i] += p;
-                dy[j][i] *= g[j][i];
+                if (live) {
+                    if constexpr (kLdsSums)
+                        s_cols[(j * kVec + i) * TEAM + t] += p;
+                    else
+                        acc[j][i] += p;
+                }
+                dy[j][i] *= g[i];
                 sum = fmaf(dy[j][i], h[j][i], sum);
             }
         }
@@ -312,21 +348,47 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int64_t c = (int64_t)kVec * (t + j * TEAM);
-            float o[kVec];
+            float o[kVec], e[kVec];
+            if constexpr (DH && kAhead) unpack8<T>(cur.dh[j], e);
+            if constexpr (DH && !kAhead)
+                read8<ONCE>(static_cast<const T*>(a.dh) + (live ? begin + k : a.rows - 1) * a.dh_stride + c,
+                      a.d - c, 0.0f, e);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
                 o[i] = rstd * fmaf(-h[j][i], mean, dy[j][i]);
-                if constexpr (DH) o[i] += e[j][i];
+                if constexpr (DH) o[i] += e[i];
             }
-            if (live && a.d > c) write8(static_cast<T*>(a.dx) + row * a.d + c, a.d - c, o);
+            if (live && a.d > c)
+                write8(static_cast<T*>(a.dx) + (begin + k) * a.d + c, a.d - c, o);
         }
+        if constexpr (kAhead)
+            cur = next;
+        else if (k + 1 < a.strip)
+            read(begin + k + 1, cur);
     }
-    if (begin < a.rows) {
+    if constexpr (kRows > 1) {
+        if (team > 0) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int64_t c = (int64_t)kVec * (t + j * TEAM);
-            if (a.d > c) write8(a.part + strip * a.d + c, a.d - c, acc[j]);
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) s_acc[team - 1][kVec * (t + j * TEAM) + i] = acc[j][i];
         }
+        __syncthreads();
+        if (team > 0) return;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                for (int r = 0; r < kRows - 1; ++r) acc[j][i] += s_acc[r][kVec * (t + j * TEAM) + i];
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = (int64_t)kVec * (t + j * TEAM);
+        if constexpr (kLdsSums) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) acc[j][i] = s_cols[(j * kVec + i) * TEAM + t];
+        }
+        if (a.d > c) write8(a.part + blockIdx.x * a.d + c, a.d - c, acc[j]);
     }
 }
 
@@ -400,46 +462,55 @@ __global__ __launch_bounds__(256) void k_rms_norm_strips(NormBackArgs a) {
     write8(a.part + strip * a.d + c, a.d - c, acc);
 }
 
-// dweight[c] = the strips' sums added: lane group k of 64 adds strips k, k + 64, ... in that
-// order, then the 64 groups join by a halving tree.  16 lanes x 4 columns a workgroup.
+// dweight[c] = the strips' sums added: row k of 256 adds strips k, k + 256, ... in that order,
+// then the 256 join by a halving tree.  4 lanes x 4 columns a workgroup: 64 bytes of a strip.
+constexpr int kSumCols = 16, kSumRows = 256;
+
 template <typename T>
 __global__ __launch_bounds__(1024) void k_col_sums(const float* part, int64_t strips, int64_t d,
                                                    T* out) {
-    __shared__ float s[64][64];
-    const int quad = threadIdx.x & 15, grp = threadIdx.x >> 4;
-    const int64_t c = (int64_t)blockIdx.x * 64 + 4 * quad;
+    __shared__ float s[kSumRows][kSumCols];
+    const int quad = threadIdx.x & 3, grp = threadIdx.x >> 2;
+    const int64_t c = (int64_t)blockIdx.x * kSumCols + 4 * quad;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c + 4 <= d) {
 #pragma unroll 4
-        for (int64_t k = grp; k < strips; k += 64) {
+        for (int64_t k = grp; k < strips; k += kSumRows) {
             const f32x4 q = *reinterpret_cast<const f32x4_a4*>(part + k * d + c);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] += q[i];
         }
     } else {
-        for (int64_t k = grp; k < strips; k += 64)
+        for (int64_t k = grp; k < strips; k += kSumRows)
             for (int i = 0; i < 4; ++i)
                 if (c + i < d) v[i] += part[k * d + c + i];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[grp][4 * quad + i] = v[i];
     __syncthreads();
-    for (int n = 32; n > 0; n >>= 1) {
-        for (int i = threadIdx.x; i < n * 64; i += 1024) s[i >> 6][i & 63] += s[(i >> 6) + n][i & 63];
+    const int col = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols;     // 64 rows at a time
+    for (int n = kSumRows / 2; n > 0; n >>= 1) {
+        for (int r = row; r < n; r += 1024 / kSumCols) s[r][col] += s[r + n][col];
         __syncthreads();
     }
-    const int64_t o = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (threadIdx.x < 64 && o < d) out[o] = (T)s[0][threadIdx.x];
+    const int64_t o = (int64_t)blockIdx.x * kSumCols + threadIdx.x;
+    if (threadIdx.x < kSumCols && o < d) out[o] = (T)s[0][threadIdx.x];
 }
 
 // ---------------------------------------------------------------- launches
 
-// Rows a strip: enough strips to fill the GPU (512 teams of 256 lanes at the widest), at least
-// 4 rows each so that the strips' sums stay small beside the rows.
+// Rows a strip: 2^18 lanes at work (1024 a compute unit, or 512 where rows are short and strips
+// many), at least 4 rows each so that the strips' sums stay small beside the rows.
 int64_t strip_rows(int64_t rows, int64_t d) {
-    const int64_t teams = d <= 512 ? 2048 : 512;
+    const int64_t teams = d <= 512 ? 2048 : (1 << 18) / back_team(d);
     const int64_t r = (rows + teams - 1) / teams;
     return r < 4 ? 4 : r;
+}
+
+// strips whose sums reach k_col_sums
+int64_t strip_sums(int64_t rows, int64_t d, int64_t strip) {
+    const int64_t strips = (rows + strip - 1) / strip;
+    return d <= 512 ? (strips + Team<64>::kRows - 1) / Team<64>::kRows : strips;
 }
 
 // workgroups a launch starts at most (a grid holds fewer than 2^32 threads); each walks the rows
@@ -447,108 +518,110 @@ unsigned grid_of(int64_t wgs) { return (unsigned)(wgs < (1 << 21) ? wgs : (1 << 
 
 constexpr int64_t kRowInRegs = 16384;        // forward: up to 2 vectors a lane of 1024
 
-template <typename T, int TEAM, int NV>
-void norm_in_regs(const NormArgs& a, bool q8, hipStream_t s) {
+template <typename T, int TEAM, int NV, bool RES, bool Q8>
+void norm_in_regs(const NormArgs& a, hipStream_t s) {
     const dim3 grid(grid_of((a.rows + Team<TEAM>::kRows - 1) / Team<TEAM>::kRows));
     const dim3 block(Team<TEAM>::kBlock);
     KernelTimer kt("k_rms_norm", s);
-    if (a.res) {
-        if (q8)
-            k_rms_norm<T, TEAM, NV, true, true><<<grid, block, 0, s>>>(a);
-        else
-            k_rms_norm<T, TEAM, NV, true, false><<<grid, block, 0, s>>>(a);
+    if ((size_t)a.rows * a.d * sizeof(T) * (RES ? 2 : 1) >= kOnceBytes)
+        k_rms_norm<T, TEAM, NV, RES, Q8, true><<<grid, block, 0, s>>>(a);
+    else
+        k_rms_norm<T, TEAM, NV, RES, Q8, false><<<grid, block, 0, s>>>(a);
+}
+
+template <typename T, bool RES, bool Q8>
+void norm_sized(const NormArgs& a, hipStream_t s) {
+    if (a.d <= 512) {
+        norm_in_regs<T, 64, 1, RES, Q8>(a, s);
+    } else if (a.d <= 1024) {
+        norm_in_regs<T, 64, 2, RES, Q8>(a, s);
+    } else if (a.d <= 2048) {
+        norm_in_regs<T, 256, 1, RES, Q8>(a, s);
+    } else if (a.d <= 4096) {
+        norm_in_regs<T, 256, 2, RES, Q8>(a, s);
+    } else if (a.d <= 6144) {
+        norm_in_regs<T, 256, 3, RES, Q8>(a, s);
+    } else if (a.d <= 8192) {
+        norm_in_regs<T, 512, 2, RES, Q8>(a, s);
+    } else if (a.d <= kRowInRegs) {
+        norm_in_regs<T, 1024, 2, RES, Q8>(a, s);
     } else {
-        if (q8)
-            k_rms_norm<T, TEAM, NV, false, true><<<grid, block, 0, s>>>(a);
-        else
-            k_rms_norm<T, TEAM, NV, false, false><<<grid, block, 0, s>>>(a);
+        KernelTimer kt("k_rms_norm_long", s);
+        k_rms_norm_long<T, RES, Q8><<<dim3(grid_of(a.rows)), dim3(1024), 0, s>>>(a);
     }
 }
 
 template <typename T>
 void norm_typed(const NormArgs& a, bool q8, hipStream_t s) {
-    if (a.d <= 512) {
-        norm_in_regs<T, 64, 1>(a, q8, s);
-    } else if (a.d <= 1024) {
-        norm_in_regs<T, 64, 2>(a, q8, s);
-    } else if (a.d <= 2048) {
-        norm_in_regs<T, 256, 1>(a, q8, s);
-    } else if (a.d <= 4096) {
-        norm_in_regs<T, 256, 2>(a, q8, s);
-    } else if (a.d <= 6144) {
-        norm_in_regs<T, 256, 3>(a, q8, s);
-    } else if (a.d <= 8192) {
-        norm_in_regs<T, 512, 2>(a, q8, s);
-    } else if (a.d <= kRowInRegs) {
-        norm_in_regs<T, 1024, 2>(a, q8, s);
+    if (a.res) {
+        if (q8)
+            norm_sized<T, true, true>(a, s);
+        else
+            norm_sized<T, true, false>(a, s);
     } else {
-        const dim3 grid(grid_of(a.rows)), block(1024);
-        KernelTimer kt("k_rms_norm_long", s);
-        if (a.res) {
-            if (q8)
-                k_rms_norm_long<T, true, true><<<grid, block, 0, s>>>(a);
-            else
-                k_rms_norm_long<T, true, false><<<grid, block, 0, s>>>(a);
-        } else {
-            if (q8)
-                k_rms_norm_long<T, false, true><<<grid, block, 0, s>>>(a);
-            else
-                k_rms_norm_long<T, false, false><<<grid, block, 0, s>>>(a);
-        }
+        if (q8)
+            norm_sized<T, false, true>(a, s);
+        else
+            norm_sized<T, false, false>(a, s);
     }
 }
 
-template <typename T, int TEAM, int NV>
-void back_in_regs(const NormBackArgs& a, int64_t strips, hipStream_t s) {
-    const dim3 grid((unsigned)((strips + Team<TEAM>::kRows - 1) / Team<TEAM>::kRows));
-    const dim3 block(Team<TEAM>::kBlock);
+template <typename T, int NV, int TEAM, bool DH>
+void back_in_regs(const NormBackArgs& a, int64_t wgs, hipStream_t s) {
+    const dim3 grid((unsigned)wgs), block(Team<TEAM>::kBlock);
+    const int lds = NV > 1 ? TEAM * NV * kVec * 4 : 0;
     KernelTimer kt("k_rms_norm_backward", s);
-    if (a.dh)
-        k_rms_norm_backward<T, TEAM, NV, true><<<grid, block, 0, s>>>(a);
+    if ((size_t)a.rows * a.d * sizeof(T) * (DH ? 3 : 2) >= kOnceBytes)
+        k_rms_norm_backward<T, TEAM, NV, DH, true><<<grid, block, lds, s>>>(a);
     else
-        k_rms_norm_backward<T, TEAM, NV, false><<<grid, block, 0, s>>>(a);
+        k_rms_norm_backward<T, TEAM, NV, DH, false><<<grid, block, lds, s>>>(a);
+}
+
+template <typename T, bool DH>
+void back_sized(const NormBackArgs& a, int64_t sums, hipStream_t s) {
+    if (a.d <= 512) {
+        back_in_regs<T, 1, back_team(512), DH>(a, sums, s);
+    } else if (a.d <= 2048) {
+        back_in_regs<T, 1, back_team(2048), DH>(a, sums, s);
+    } else if (a.d <= 4096) {
+        back_in_regs<T, 1, back_team(4096), DH>(a, sums, s);
+    } else if (a.d <= 8192) {
+        back_in_regs<T, 1, back_team(8192), DH>(a, sums, s);
+    } else if (a.d <= kRowInRegs) {
+        back_in_regs<T, 2, back_team(kRowInRegs), DH>(a, sums, s);
+    } else {
+        {
+            KernelTimer kt("k_rms_norm_backward_long", s);
+            k_rms_norm_backward_long<T, DH><<<dim3(grid_of(a.rows)), dim3(1024), 0, s>>>(a);
+        }
+        KernelTimer kt("k_rms_norm_strips", s);
+        const dim3 grid((unsigned)((a.d + 256 * kVec - 1) / (256 * kVec)), (unsigned)sums);
+        k_rms_norm_strips<T><<<grid, dim3(256), 0, s>>>(a);
+    }
 }
 
 template <typename T>
 det_status back_typed(const NormBackArgs& a, void* dw, hipStream_t s) {
-    const int64_t strips = (a.rows + a.strip - 1) / a.strip;
+    const int64_t sums = strip_sums(a.rows, a.d, a.strip);
     if (a.rows > 0) {
-        if (a.d <= 512) {
-            back_in_regs<T, 64, 1>(a, strips, s);
-        } else if (a.d <= 2048) {
-            back_in_regs<T, 256, 1>(a, strips, s);
-        } else if (a.d <= 4096) {
-            back_in_regs<T, 512, 1>(a, strips, s);
-        } else if (a.d <= 8192) {
-            back_in_regs<T, 1024, 1>(a, strips, s);
-        } else if (a.d <= kRowInRegs) {
-            back_in_regs<T, 1024, 2>(a, strips, s);
-        } else {
-            {
-                KernelTimer kt("k_rms_norm_backward_long", s);
-                if (a.dh)
-                    k_rms_norm_backward_long<T, true><<<dim3(grid_of(a.rows)), dim3(1024), 0, s>>>(a);
-                else
-                    k_rms_norm_backward_long<T, false><<<dim3(grid_of(a.rows)), dim3(1024), 0, s>>>(a);
-            }
-            KernelTimer kt("k_rms_norm_strips", s);
-            const dim3 grid((unsigned)((a.d + 256 * kVec - 1) / (256 * kVec)), (unsigned)strips);
-            k_rms_norm_strips<T><<<grid, dim3(256), 0, s>>>(a);
-        }
+        if (a.dh)
+            back_sized<T, true>(a, sums, s);
+        else
+            back_sized<T, false>(a, sums, s);
         const det_status st = launch_status();
         if (st != DET_SUCCESS) return st;
     }
     KernelTimer kt("k_col_sums", s);
-    k_col_sums<T><<<dim3((unsigned)((a.d + 63) / 64)), dim3(1024), 0, s>>>(
-        a.part, strips, a.d, static_cast<T*>(dw));
+    k_col_sums<T><<<dim3((unsigned)((a.d + kSumCols - 1) / kSumCols)), dim3(1024), 0, s>>>(
+        a.part, sums, a.d, static_cast<T*>(dw));
     return launch_status();
 }
 
 }  // namespace
 
 size_t norm_backward_workspace(int64_t rows, int64_t d) {
-    const int64_t r = strip_rows(rows, d), strips = (rows + r - 1) / r;
-    return round_up((size_t)strips * (size_t)d * sizeof(float), 256) + 256;
+    const int64_t sums = strip_sums(rows, d, strip_rows(rows, d));
+    return round_up((size_t)sums * (size_t)d * sizeof(float), 256) + 256;
 }
 
 det_status norm_launch(const NormCall& c, hipStream_t s) {

@@ -240,7 +240,7 @@ constexpr int kDiags = 64 * kVec;          // diagonals a wave covers
 // lie together in memory, one place further along with every row.  kRows rows are added in f32,
 // their sums in f64.  The wave then adds its diagonals up by buckets, which are runs of
 // neighbouring diagonals.
-template <typename T>
+template <typename T, bool ONCE>
 __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBackArgs a) {
     __shared__ double s_sums[kWaves][kDiags];
     __shared__ double s_part[kWaves][DET_BIAS_MAX_BUCKETS];
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
             if (inner && row + kRows <= q1) {
 #pragma unroll
                 for (int j = 0; j < kRows; ++j)
-                    raw[j] = load8_once(p + base + (row + j) * (a.sq + 1));
+                    raw[j] = load8<ONCE>(p + base + (row + j) * (a.sq + 1));
 #pragma unroll
                 for (int j = 0; j < kRows; ++j) {
                     float v[kVec];
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
                     raw[j] = {};
                     if (some && row + j < q1 && c > -kVec && c < keys) {
                         if (at >= 0 && at + kVec <= a.extent) {
-                            raw[j] = load8(p + at);
+                            raw[j] = load8<ONCE>(p + at);
                         } else {      // at the tensor's very ends
                             float v[kVec];
 #pragma unroll
@@ -540,7 +540,10 @@ det_status back_typed(const BiasCall& c, const void* dout, void* dtable, void* w
     const int64_t groups = c.q > 0 && c.k > 0 ? c.batch * c.heads * per_head : 0;
     if (groups > 0) {
         KernelTimer kt("k_relative_bias_backward", s);
-        k_relative_bias_backward<T><<<dim3(grid_of(groups)), dim3(kBlock), 0, s>>>(m, a);
+        if ((double)c.batch * c.heads * c.q * c.k * sizeof(T) >= (double)kOnceBytes)
+            k_relative_bias_backward<T, true><<<dim3(grid_of(groups)), dim3(kBlock), 0, s>>>(m, a);
+        else
+            k_relative_bias_backward<T, false><<<dim3(grid_of(groups)), dim3(kBlock), 0, s>>>(m, a);
         const det_status st = launch_status();
         if (st != DET_SUCCESS) return st;
     }
