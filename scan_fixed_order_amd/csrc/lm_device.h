@@ -176,6 +176,12 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return umax(readlane(v, 0), readlane(v, 32));
 }
 
+// orders LDS accesses of one wave's lanes among each other
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // e^x with the hardware's 2^x (about 1 ulp; results below 2^-126 become 0)

@@ -110,12 +110,6 @@ __device__ __forceinline__ float max8(const float (&x)[kVec]) {
     return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max3(x[6], x[7], -INFINITY));
 }
 
-// orders LDS accesses of one wave's lanes among each other
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // groups of a super-group: 64 of them cover the row; odd, so that lanes that read one group of
 // each fall on different LDS banks
 __host__ __device__ constexpr int64_t super_len(int64_t vocab) {

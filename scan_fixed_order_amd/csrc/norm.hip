@@ -499,10 +499,9 @@ __global__ __launch_bounds__(1024) void k_col_sums(const float* part, int64_t st
 
 // ---------------------------------------------------------------- launches
 
-// Rows a strip: 2^18 lanes at work (1024 a compute unit, or 512 where rows are short and strips
-// many), at least 4 rows each so that the strips' sums stay small beside the rows.
+// Rows a strip: 2^17 lanes at work (512 a compute unit), 256 teams at least; at least 4 rows each so that the strips' sums stay small beside the rows.
 int64_t strip_rows(int64_t rows, int64_t d) {
-    const int64_t teams = d <= 512 ? 2048 : (1 << 18) / back_team(d);
+    const int64_t teams = d <= 4096 ? (1 << 17) / back_team(d) : 256;
     const int64_t r = (rows + teams - 1) / teams;
     return r < 4 ? 4 : r;
 }
@@ -538,13 +537,13 @@ void norm_sized(const NormArgs& a, hipStream_t s) {
     } else if (a.d <= 2048) {
         norm_in_regs<T, 256, 1, RES, Q8>(a, s);
     } else if (a.d <= 4096) {
-        norm_in_regs<T, 256, 2, RES, Q8>(a, s);
+        norm_in_regs<T, 512, 1, RES, Q8>(a, s);
     } else if (a.d <= 6144) {
         norm_in_regs<T, 256, 3, RES, Q8>(a, s);
     } else if (a.d <= 8192) {
         norm_in_regs<T, 512, 2, RES, Q8>(a, s);
     } else if (a.d <= kRowInRegs) {
-        norm_in_regs<T, 1024, 2, RES, Q8>(a, s);
+        norm_in_regs<T, 512, 4, RES, Q8>(a, s);
     } else {
         KernelTimer kt("k_rms_norm_long", s);
         k_rms_norm_long<T, RES, Q8><<<dim3(grid_of(a.rows)), dim3(1024), 0, s>>>(a);

@@ -239,7 +239,7 @@ constexpr int kDiags = 64 * kVec;          // diagonals a wave covers
 // A lane owns 8 neighbouring diagonals and walks down the strip's rows: its 8 elements of a row
 // lie together in memory, one place further along with every row.  kRows rows are added in f32,
 // their sums in f64.  The wave then adds its diagonals up by buckets, which are runs of
-// neighbouring diagonals.
+// neighbouring diagonals, and the workgroup its waves.
 template <typename T, bool ONCE>
 __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBackArgs a) {
     __shared__ double s_sums[kWaves][kDiags];
@@ -250,6 +250,7 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
     // a workgroup takes kWaves neighbouring tiles (diagonals, then strips) of one head
     const int64_t per_head = (a.qt * a.dt + kWaves - 1) / kWaves;
     double* s_sum = s_sums[wave];
+    __syncthreads();
     for (int64_t group = blockIdx.x; group < a.batch * a.heads * per_head; group += gridDim.x) {
         const int64_t bh = split(group, per_head), tile = (group - bh * per_head) * kWaves + wave;
         const bool live = tile < a.qt * a.dt;
@@ -266,7 +267,6 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
         double acc[kVec] = {};
         const T* p = static_cast<const T*>(a.dout);
         const int64_t base = b * a.sb + h * a.sh + d0;
-        // a diagonal after the query is masked as a whole when causal
         const bool some = !m.causal || d0 - off <= 0;
         const bool whole = some && q0 + d0 >= 0 && q1 + d0 + kVec - 1 <= keys;
         const bool inner = __all(whole);
@@ -315,13 +315,13 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
 #pragma unroll
             for (int i = 0; i < kVec; ++i) acc[i] += (double)sum[i];
         }
-        __syncthreads();      // s_starts is there; the last tile's sums are read
+        // a diagonal after the query is masked as a whole when causal
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-            s_sum[kVec * lane + i] = m.causal && d0 + i - off > 0 ? 0.0 : acc[i];
-        __syncthreads();
+            if (m.causal && d0 + i - off > 0) acc[i] = 0.0;
         const int64_t r0 = dt * kDiags - shift - off;     // r of the tile's diagonal 0
-        // lane by lane the buckets' runs of diagonals, then one run after the other
+        // lane by lane the buckets' runs of diagonals [from, to)
+        bool laid_out = false;
         for (int bk0 = 0; bk0 < a.buckets; bk0 += 64) {
             const int bk = bk0 + lane;
             int64_t lo = 0, hi = 0;                       // r in [lo, hi)
@@ -337,18 +337,33 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
             hi -= r0;
             const int from = (int)(lo < 0 ? 0 : lo > kDiags ? kDiags : lo);
             const int to = (int)(hi < 0 ? 0 : hi > kDiags ? kDiags : hi);
-            // short runs by their own lane, long ones by the whole wave
-            double mine = 0.0;
             const bool wide = to - from > kShortRun;
-            if (!wide)
-                for (int i = from; i < to; ++i) mine += s_sum[i];
+            double mine = 0.0;
+            // long runs (far from the diagonal one covers the tile): by the whole wave
             for (uint64_t runs = __ballot(wide); runs; runs &= runs - 1) {
                 const int l = __ffsll((unsigned long long)runs) - 1;
-                const int f = __builtin_amdgcn_readlane(from, l), t = __builtin_amdgcn_readlane(to, l);
+                const int f = __builtin_amdgcn_readlane(from, l) - kVec * lane;
+                const int t = __builtin_amdgcn_readlane(to, l) - kVec * lane;
                 double v = 0.0;
-                for (int i = f + lane; i < t; i += 64) v += s_sum[i];
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+                    if (i >= f && i < t) v += acc[i];
                 v = wave_pw(v);
                 if (lane == l) mine = v;
+            }
+            // short ones: each by one lane, the diagonals laid out in LDS
+            if (__ballot(!wide && from < to)) {
+                if (!laid_out) {
+                    wave_sync();
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) s_sum[kVec * lane + i] = acc[i];
+                    wave_sync();
+                    laid_out = true;
+                }
+                if (!wide) {
+#pragma unroll 4
+                    for (int i = from; i < to; ++i) mine += s_sum[i];
+                }
             }
             if (bk < a.buckets) s_part[wave][bk] = mine;
         }
@@ -359,6 +374,7 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
             for (int w = 1; w < kWaves; ++w) v += s_part[w][bk];
             a.part[group * a.buckets + bk] = v;
         }
+        __syncthreads();      // s_part is written again
     }
 }
 
