@@ -167,8 +167,8 @@ __device__ __forceinline__ void gather_candidates(const LogpArgs& a, const T* x,
     }
 }
 
-// The `top` largest logits of a row.  On entry s_key holds the order key of every group's
-// largest logit (0 behind the last group), in 64 super-groups of super_len groups.
+// The `top` largest logits of a row.  On entry s_key holds every group's largest logit; they are
+// replaced by their order keys (0 behind the last group), in 64 super-groups of super_len groups.
 //
 // The top-th largest of the super-groups' maxima is a bound that at least `top` logits reach, and
 // few more do in most rows: these are ranked against each other.  Where too many reach it (long
@@ -188,7 +188,12 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
     {
         uint32_t m = 0;
 #pragma unroll 4
-        for (int i = part; i < len; i += kParts) m = umax(m, s_key[sg * len + i]);
+        for (int i = part; i < len; i += kParts) {
+            const int at = sg * len + i;
+            const uint32_t k = at < groups ? order_key(__uint_as_float(s_key[at])) : 0;
+            s_key[at] = k;
+            m = umax(m, k);
+        }
         m = umax(m, xor_partner<1>(m));
         m = umax(m, xor_partner<2>(m));
         if constexpr (kParts == 16) {
@@ -287,7 +292,6 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
     __shared__ Search s_search;      // not laid out where nothing is searched
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     int parity = 0;
-    const int64_t key_slots = TOP ? 64 * super_len(a.vocab) : 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T* x = static_cast<const T*>(a.logits) + row * a.stride;
         const int64_t target = a.targets[row];
@@ -296,19 +300,13 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
         Part p[kSets];
 #pragma unroll
         for (int u = 0; u < kSets; ++u) p[u] = Part{-FLT_MAX, 0.0f, 0.0f};
-        if constexpr (TOP) {
-            // slots behind the last whole tile's groups
-            for (int64_t i = a.vocab / kTile * (kTile / kGroup) + t; i < key_slots; i += BLOCK)
-                s_key[i] = 0;
-            __syncthreads();
-        }
         const auto one = [&](int64_t c, int u, const float(&v)[kVec], bool keep) {
             const float largest = max8(v);
             if constexpr (TOP) {
                 float g = largest;
                 g = fmaxf(g, xor_partner<1>(g));
                 g = fmaxf(g, xor_partner<2>(g));
-                if (keep && (lane & 3) == 0) s_key[c / kGroup] = order_key(g);
+                if (keep && (lane & 3) == 0) s_key[c / kGroup] = __float_as_uint(g);
             }
             if (keep) take(p[u], v, largest, a.scale);
         };
@@ -332,6 +330,7 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
         for (int64_t base = whole * kSteps * kTile; base < a.vocab; base += kTile) {
 #pragma unroll
             for (int u = 0; u < kSets; ++u) {
+                if (base + kVec * u * BLOCK >= a.vocab) break;
                 const int64_t c = base + kVec * (t + u * BLOCK);
                 float v[kVec];
                 read8(x + c, a.vocab - c, -INFINITY, v);
