@@ -34,10 +34,42 @@ __device__ __forceinline__ int bucket_of(const Map& m, const int* starts, int to
     int lo = m.side - 1;
     if (far < starts[lo]) {
         lo = 0;
-        for (int step = top; step > 0; step >>= 1)
-            if (lo + step < m.side && starts[lo + step] <= far) lo += step;
+        for (int step = top; step > 0; step >>= 1) {
+            const int next = lo + step, at = next < m.side ? next : m.side - 1;
+            lo = starts[at] <= far ? at : lo;
+        }
     }
     return m.two_sided && r > 0 ? lo + m.side : lo;
+}
+
+// Buckets of kVec neighbouring relative positions from r on, their searches side by side.
+__device__ __forceinline__ void buckets_of(const Map& m, const int* starts, int64_t r,
+                                           int (&bucket)[kVec]) {
+    const int border = starts[m.side - 1];
+    int far[kVec];
+    bool near = false;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int64_t a = r + i < 0 ? -(r + i) : (m.two_sided ? r + i : 0);
+        far[i] = a < border ? (int)a : border;
+        near |= far[i] < border;
+        bucket[i] = m.side - 1;
+    }
+    if (near) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) bucket[i] = 0;
+        for (int step = m.top; step > 0; step >>= 1) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                // read in any case: a branch around the load would make the searches take turns
+                const int next = bucket[i] + step, at = next < m.side ? next : m.side - 1;
+                bucket[i] = starts[at] <= far[i] ? at : bucket[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+        if (m.two_sided && r + i > 0) bucket[i] += m.side;
 }
 
 // a / b, in 32 bits where both fit
@@ -194,19 +226,12 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_row(Map m, BiasArgs a)
 #pragma unroll
         for (int i = 0; i < kVec; ++i) o[i] = a.fill;
         if (left > 0) {
-            const int first = bucket_of(m, s_starts, m.top, r0);
+            int bucket[kVec];
+            buckets_of(m, s_starts, r0, bucket);
             float v[kVec];
-            v[0] = table ? (float)table[first * a.heads + h] : 0.0f;
-            if (first == bucket_of(m, s_starts, m.top, r0 + kVec - 1)) {
-                // buckets are runs of distances: between two places of one bucket lies no other
 #pragma unroll
-                for (int i = 1; i < kVec; ++i) v[i] = v[0];
-            } else {
-#pragma unroll
-                for (int i = 1; i < kVec; ++i)
-                    v[i] = table ? (float)table[bucket_of(m, s_starts, m.top, r0 + i) * a.heads + h]
-                                 : 0.0f;
-            }
+            for (int i = 0; i < kVec; ++i)
+                v[i] = table ? (float)table[(int64_t)bucket[i] * a.heads + h] : 0.0f;
             if constexpr (SCORES) {
                 float sc[kVec];
                 unpack8<T>(raw, sc);
@@ -270,7 +295,12 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
         const bool some = !m.causal || d0 - off <= 0;
         const bool whole = some && q0 + d0 >= 0 && q1 + d0 + kVec - 1 <= keys;
         const bool inner = __all(whole);
-        for (int64_t row = q0; row < q1; row += kRows) {
+        // the blocks of rows that meet the wave's diagonals
+        const int64_t w0 = dt * kDiags - shift;
+        const int64_t lo = -(w0 + kDiags - 1), hi = keys - w0;
+        const int64_t from = lo > q0 ? q0 + (lo - q0) / kRows * kRows : q0;
+        const int64_t to = m.causal && w0 - off > 0 ? from : hi < q1 ? hi : q1;
+        for (int64_t row = from; row < to; row += kRows) {
             Raw8<T> raw[kRows];
             float sum[kVec] = {};
             if (inner && row + kRows <= q1) {
@@ -320,7 +350,7 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
         for (int i = 0; i < kVec; ++i)
             if (m.causal && d0 + i - off > 0) acc[i] = 0.0;
         const int64_t r0 = dt * kDiags - shift - off;     // r of the tile's diagonal 0
-        // lane by lane the buckets' runs of diagonals [from, to)
+        // lane by lane the buckets' runs of diagonals [first, last)
         bool laid_out = false;
         for (int bk0 = 0; bk0 < a.buckets; bk0 += 64) {
             const int bk = bk0 + lane;
@@ -335,15 +365,15 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
             }
             lo -= r0;
             hi -= r0;
-            const int from = (int)(lo < 0 ? 0 : lo > kDiags ? kDiags : lo);
-            const int to = (int)(hi < 0 ? 0 : hi > kDiags ? kDiags : hi);
-            const bool wide = to - from > kShortRun;
+            const int first = (int)(lo < 0 ? 0 : lo > kDiags ? kDiags : lo);
+            const int last = (int)(hi < 0 ? 0 : hi > kDiags ? kDiags : hi);
+            const bool wide = last - first > kShortRun;
             double mine = 0.0;
             // long runs (far from the diagonal one covers the tile): by the whole wave
             for (uint64_t runs = __ballot(wide); runs; runs &= runs - 1) {
                 const int l = __ffsll((unsigned long long)runs) - 1;
-                const int f = __builtin_amdgcn_readlane(from, l) - kVec * lane;
-                const int t = __builtin_amdgcn_readlane(to, l) - kVec * lane;
+                const int f = __builtin_amdgcn_readlane(first, l) - kVec * lane;
+                const int t = __builtin_amdgcn_readlane(last, l) - kVec * lane;
                 double v = 0.0;
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
@@ -352,7 +382,7 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
                 if (lane == l) mine = v;
             }
             // short ones: each by one lane, the diagonals laid out in LDS
-            if (__ballot(!wide && from < to)) {
+            if (__ballot(!wide && first < last)) {
                 if (!laid_out) {
                     wave_sync();
 #pragma unroll
@@ -362,7 +392,7 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
                 }
                 if (!wide) {
 #pragma unroll 4
-                    for (int i = from; i < to; ++i) mine += s_sum[i];
+                    for (int i = first; i < last; ++i) mine += s_sum[i];
                 }
             }
             if (bk < a.buckets) s_part[wave][bk] = mine;
