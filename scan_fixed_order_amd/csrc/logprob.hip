@@ -56,7 +56,7 @@ struct LogpArgs {
     int64_t* top_ids;
     int64_t stride, rows, vocab;
     int top;
-    float scale;
+    float scale, unscale;      // unscale = 1 / scale
 };
 
 // One lane's running sums against its reference
@@ -80,10 +80,14 @@ __device__ __forceinline__ float sum16(float v) {
     return v + xor_partner<8>(v);
 }
 
-// adds 8 logits; `largest`: their maximum (NaN ignored)
-__device__ __forceinline__ void take(Part& p, const float (&x)[kVec], float largest, float scale) {
-    const float top = largest * scale;
-    if (top > p.ref + kSlack) rebase(p, top);
+// adds 8 logits; `largest`: their maximum (NaN ignored); `limit`: the logit that passes the
+// reference by kSlack
+__device__ __forceinline__ void take(Part& p, float& limit, const float (&x)[kVec], float largest,
+                                     float scale, float unscale) {
+    if (largest > limit) {
+        rebase(p, largest * scale);
+        limit = (p.ref + kSlack) * unscale;
+    }
     float e[kVec], d[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
@@ -298,17 +302,23 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
         const bool scored = target >= 0 && target < a.vocab;
         const float picked = scored ? (float)x[target] : 0.0f;
         Part p[kSets];
+        float limit[kSets];
 #pragma unroll
-        for (int u = 0; u < kSets; ++u) p[u] = Part{-FLT_MAX, 0.0f, 0.0f};
+        for (int u = 0; u < kSets; ++u) {
+            p[u] = Part{-FLT_MAX, 0.0f, 0.0f};
+            limit[u] = -FLT_MAX * a.unscale;
+        }
         const auto one = [&](int64_t c, int u, const float(&v)[kVec], bool keep) {
             const float largest = max8(v);
             if constexpr (TOP) {
-                float g = largest;
-                g = fmaxf(g, xor_partner<1>(g));
-                g = fmaxf(g, xor_partner<2>(g));
+                // (fmaxf would quiet its operands first, an instruction each)
+                float g = largest, other = xor_partner<1>(g);
+                g = max3(g, other, other);
+                other = xor_partner<2>(g);
+                g = max3(g, other, other);
                 if (keep && (lane & 3) == 0) s_key[c / kGroup] = __float_as_uint(g);
             }
-            if (keep) take(p[u], v, largest, a.scale);
+            if (keep) take(p[u], limit[u], v, largest, a.scale, a.unscale);
         };
         const int64_t whole = a.vocab / (kTile * kSteps);
         for (int64_t i = 0; i < whole; ++i) {
@@ -458,7 +468,7 @@ void logp_back_typed(const LogpBackArgs& a, hipStream_t s) {
 
 det_status logprob_launch(const LogpCall& c, hipStream_t s) {
     const LogpArgs a{c.logits, c.targets, c.logp, c.entropy, c.lse, c.top_logp, c.top_ids,
-                     c.stride, c.rows, c.vocab, c.top, c.scale};
+                     c.stride, c.rows, c.vocab, c.top, c.scale, 1.0f / c.scale};
     switch (c.dtype) {
         case DET_F32: logp_typed<float>(a, s); break;
         case DET_F16: logp_typed<_Float16>(a, s); break;
