@@ -27,6 +27,10 @@
  *  - Sizes: 0 <= n <= DET_MAX_N (2^31 - 1), as scatter record slots are signed 32-bit
  *    (Warp "Deterministic Execution", section "Limitations", large launches).
  *  - No C++ exception crosses this interface.
+ *
+ * The language-model operators further down (norm, relative position bias, token log
+ * probabilities) keep these conventions; their arithmetic and the order of their sums are stated
+ * there.
  */
 #ifndef DET_H
 #define DET_H
@@ -299,7 +303,7 @@ det_status det_rms_norm_backward(const void* dy, int64_t dy_stride, const void* 
  * scores:    NULL, or [batch, heads, q, k] with strides (stride_b, stride_h, stride_q, 1); a
  *            stride may be 0.
  * out:       [batch * heads * q * k].  May be scores itself where that is contiguous.
- * 2 <= n per side, num_buckets <= DET_BIAS_MAX_BUCKETS, n/2 < max_distance < 2^31, 1 <= heads < 65536,
+ * 2 <= n <= 128 per side, n/2 < max_distance < 2^31, 1 <= heads < 65536,
  * |q_offset| < 2^40.  Nothing is summed but the score and its bias. */
 det_status det_relative_bias(const void* table, int64_t num_buckets, int64_t heads,
                              int64_t max_distance, unsigned flags, int64_t batch, int64_t q,

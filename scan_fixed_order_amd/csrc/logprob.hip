@@ -286,7 +286,11 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
     __syncthreads();      // s_key and s are written again
 }
 
-// One row per workgroup, each logit read once.
+// One row per workgroup, each logit read once; 1024 threads for few rows, where a compute unit's
+// vector rate bounds (about 17 logits a nanosecond), 256 for many.  2048 x 131072 bf16: 88 us
+// (6.1 TB/s, bound by HBM), with 5 alternatives 97 us (5.6 TB/s: 10 vector instructions and an
+// exponential a logit fill the vector units, and a row's search runs for 2 us).  256 x 131072 with 5
+// alternatives 16.7 us with 1024 threads a row; 300 rows 31 us with 256.
 template <typename T, int BLOCK, bool TOP, bool ONCE>
 __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
     constexpr int kSets = kLanes / BLOCK;       // lanes a thread plays
@@ -390,7 +394,8 @@ struct LogpBackArgs {
 constexpr int kBackVecs = 4;                              // vectors a thread
 constexpr int kBackTile = 256 * kVec * kBackVecs;
 
-// Each logit read once, each gradient written once; nothing is summed.
+// Each logit read once, each gradient written once; nothing is summed.  Bound by HBM: 4096 x
+// 65536 bf16 188 us (5.7 TB/s).
 template <typename T, bool ONCE>
 __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a) {
     for (int64_t tile = blockIdx.x; tile < a.rows * a.tiles; tile += gridDim.x) {
@@ -443,6 +448,8 @@ bool once(int64_t rows, int64_t vocab) {
     return (double)rows * (double)vocab * sizeof(T) >= (double)kOnceBytes;
 }
 
+// Up to a workgroup a compute unit, 1024 threads: 256 x 131072 bf16 with 5 alternatives 16.5 us
+// against 28 with 256 threads; 700 rows 47 us with 1024, 42 with 256.  (The order is the same.)
 template <typename T>
 void logp_typed(const LogpArgs& a, hipStream_t s) {
     if (a.rows <= 256 && a.vocab > kTile)
