@@ -121,7 +121,8 @@ struct BiasCall {
 // first distance of each of a side's n buckets
 void relbias_starts(int n, int64_t distance, int* starts);
 det_status bias_launch(const BiasCall& c, hipStream_t s);
-size_t bias_backward_workspace(int64_t batch, int64_t heads, int64_t q, int64_t k, int buckets);
+size_t bias_backward_workspace(int64_t batch, int64_t heads, int64_t q, int64_t k, int buckets,
+                               det_dtype dtype);
 det_status bias_backward_launch(const BiasCall& c, const void* dout, void* dtable, void* ws,
                                 hipStream_t s);
 

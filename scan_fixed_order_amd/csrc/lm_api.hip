@@ -217,7 +217,7 @@ size_t det_relative_bias_backward_workspace_size(int64_t batch, int64_t heads, i
         num_buckets > DET_BIAS_MAX_BUCKETS ||
         (double)batch * heads * (double)q * (double)k * lm_size(dtype) > kMaxBytes)
         return 0;
-    return bias_backward_workspace(batch, heads, q, k, (int)num_buckets);
+    return bias_backward_workspace(batch, heads, q, k, (int)num_buckets, dtype);
 }
 
 det_status det_relative_bias_backward(const void* dout, int64_t stride_b, int64_t stride_h,
@@ -238,7 +238,7 @@ det_status det_relative_bias_backward(const void* dout, int64_t stride_b, int64_
         (!dout || overlap(dtable, tbytes, dout, strided_bytes(c)) ||
          (dscores && (!bias_out_ok(c, dscores, obytes) || overlap(dscores, obytes, dtable, tbytes)))))
         return DET_ERROR_INVALID_VALUE;
-    st = ws_status(ws, ws_bytes, bias_backward_workspace(batch, heads, q, k, (int)num_buckets));
+    st = ws_status(ws, ws_bytes, bias_backward_workspace(batch, heads, q, k, (int)num_buckets, dtype));
     if (st != DET_SUCCESS) return st;
     st = bias_backward_launch(c, dout, dtable, ws, static_cast<hipStream_t>(stream));
     if (st != DET_SUCCESS || !dscores || obytes == 0) return st;

@@ -1,11 +1,13 @@
-// lm_device.h -- device helpers of the language-model operators: 8-element vectors of the three
+// lm_device.h -- device helpers of the language-model operators: 16-byte vectors of the three
 // storage types, their conversion to and from f32, and fixed-order reductions over a wave.
 //
-// Every lane owns 8 consecutive elements at a time, whatever the type (16 bytes of f16 or bf16,
-// two 16-byte loads of f32), so which lane sums which element depends on the element's position
-// alone.  The vectors are declared with the element's alignment: gfx950 takes 16-byte global
-// loads and stores at any address, so rows of odd length and views with an offset run the same
-// code and the same order as aligned ones.
+// Every lane owns 16 bytes of consecutive elements at a time (8 of f16 or bf16, 4 of f32), and
+// neighbouring lanes neighbouring vectors, so a wave's load or store covers 1024 bytes without a
+// gap, and which lane sums which element depends on the element's position and the type alone.
+// (8 elements of f32 a lane, two loads apart by 32 bytes a lane, took 231 us where this takes 192:
+// gradient of 8192 x 16385 f32 logits.)  The vectors are declared with the element's alignment:
+// gfx950 takes 16-byte global loads and stores at any address, so rows of odd length and views
+// with an offset run the same code and the same order as aligned ones.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -15,142 +17,128 @@
 
 namespace det {
 
-constexpr int kVec = 8;   // elements a lane loads or stores at a time
+template <typename T>
+constexpr int kVec = 16 / sizeof(T);   // elements a lane loads or stores at a time
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// 8 elements as they lie in memory
+// a vector at any address of an element
 template <typename T>
-struct Raw8 {
-    u32x4 a;
+struct VecAt {
+    typedef u32x4_a2 type;
 };
 template <>
-struct Raw8<float> {
-    f32x4 a, b;
+struct VecAt<float> {
+    typedef u32x4_a4 type;
 };
 
-// ONCE: past the caches, for data that is read once and would push out what the caches hold
+// A vector as it lies in memory.  ONCE: past the caches, for data that is read once and would push
+// out what the caches hold.
 template <bool ONCE = false, typename T>
-__device__ __forceinline__ Raw8<T> load8(const T* p) {
-    Raw8<T> r;
-    if constexpr (sizeof(T) == 4) {
-        const f32x4_a4* q = reinterpret_cast<const f32x4_a4*>(p);
-        const f32x4_a4* q1 = reinterpret_cast<const f32x4_a4*>(p + 4);
-        if constexpr (ONCE) {
-            r.a = __builtin_nontemporal_load(q);
-            r.b = __builtin_nontemporal_load(q1);
-        } else {
-            r.a = *q;
-            r.b = *q1;
-        }
-    } else {
-        const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p);
-        if constexpr (ONCE)
-            r.a = __builtin_nontemporal_load(q);
-        else
-            r.a = *q;
-    }
-    return r;
+__device__ __forceinline__ u32x4 load_vec(const T* p) {
+    const auto* q = reinterpret_cast<const typename VecAt<T>::type*>(p);
+    if constexpr (ONCE)
+        return __builtin_nontemporal_load(q);
+    else
+        return *q;
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const Raw8<T>& r) {
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<f32x4_a4*>(p) = r.a;
-        *reinterpret_cast<f32x4_a4*>(p + 4) = r.b;
-    } else {
-        *reinterpret_cast<u32x4_a2*>(p) = r.a;
-    }
+__device__ __forceinline__ void store_vec(T* p, u32x4 r) {
+    *reinterpret_cast<typename VecAt<T>::type*>(p) = r;
 }
 
 template <typename T>
-__device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&v)[kVec]) {
+__device__ __forceinline__ void unpack(u32x4 r, float (&v)[kVec<T>]) {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = r.a[i];
-            v[4 + i] = r.b[i];
-        }
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
     } else if constexpr (__is_same(T, _Float16)) {
-        const f16x8 h = __builtin_bit_cast(f16x8, r.a);
+        const f16x8 h = __builtin_bit_cast(f16x8, r);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] = (float)h[i];
+        for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(r.a[i] << 16);
-            v[2 * i + 1] = __uint_as_float(r.a[i] & 0xFFFF0000u);
+            v[2 * i] = __uint_as_float(r[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
         }
     }
 }
 
 // one rounding to nearest even
 template <typename T>
-__device__ __forceinline__ Raw8<T> pack8(const float (&v)[kVec]) {
-    Raw8<T> r;
+__device__ __forceinline__ u32x4 pack(const float (&v)[kVec<T>]) {
     if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            r.a[i] = v[i];
-            r.b[i] = v[4 + i];
-        }
+        return u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                     __float_as_uint(v[3])};
     } else if constexpr (__is_same(T, _Float16)) {
         f16x8 h;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) h[i] = (_Float16)v[i];
-        r.a = __builtin_bit_cast(u32x4, h);
+        for (int i = 0; i < 8; ++i) h[i] = (_Float16)v[i];
+        return __builtin_bit_cast(u32x4, h);
     } else {
         bf16x8 h;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) h[i] = (__bf16)v[i];
-        r.a = __builtin_bit_cast(u32x4, h);
+        for (int i = 0; i < 8; ++i) h[i] = (__bf16)v[i];
+        return __builtin_bit_cast(u32x4, h);
     }
-    return r;
 }
 
-// The first n (at most 8) elements at p, `fill` behind them.  n < 1 reads nothing.
+// The first n elements at p, `fill` behind them.  n < 1 reads nothing.
 template <typename T>
-__device__ __forceinline__ void load_tail(const T* p, int64_t n, float fill, float (&v)[kVec]) {
+__device__ __forceinline__ void load_tail(const T* p, int64_t n, float fill, float (&v)[kVec<T>]) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = i < n ? (float)p[i] : fill;
+    for (int i = 0; i < kVec<T>; ++i) v[i] = i < n ? (float)p[i] : fill;
 }
 
-template <typename T>
-__device__ __forceinline__ void store_tail(T* p, int64_t n, const float (&v)[kVec]) {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i)
-        if (i < n) p[i] = (T)v[i];
-}
-
-// 8 elements of which n lie inside the row (unpacked, `fill` behind them)
+// a vector of which n elements lie inside the row (unpacked, `fill` behind them)
 template <bool ONCE = false, typename T>
-__device__ __forceinline__ void read8(const T* p, int64_t n, float fill, float (&v)[kVec]) {
-    if (n >= kVec)
-        unpack8<T>(load8<ONCE>(p), v);
+__device__ __forceinline__ void read_vec(const T* p, int64_t n, float fill, float (&v)[kVec<T>]) {
+    if (n >= kVec<T>)
+        unpack<T>(load_vec<ONCE>(p), v);
     else
         load_tail(p, n, fill, v);
 }
 
 // the same as it lies in memory, zeros behind them
 template <bool ONCE = false, typename T>
-__device__ __forceinline__ Raw8<T> read_raw8(const T* p, int64_t n) {
-    if (n >= kVec) return load8<ONCE>(p);
-    float v[kVec];
+__device__ __forceinline__ u32x4 read_raw(const T* p, int64_t n) {
+    if (n >= kVec<T>) return load_vec<ONCE>(p);
+    float v[kVec<T>];
     load_tail(p, n, 0.0f, v);
-    return pack8<T>(v);
+    return pack<T>(v);
 }
 
 template <typename T>
-__device__ __forceinline__ void write8(T* p, int64_t n, const float (&v)[kVec]) {
-    if (n >= kVec)
-        store8<T>(p, pack8<T>(v));
-    else
-        store_tail(p, n, v);
+__device__ __forceinline__ void write_vec(T* p, int64_t n, const float (&v)[kVec<T>]) {
+    if (n >= kVec<T>) {
+        store_vec(p, pack<T>(v));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i)
+            if (i < n) p[i] = (T)v[i];
+    }
+}
+
+// the first n of N floats
+template <int N>
+__device__ __forceinline__ void write_floats(float* p, int64_t n, const float (&v)[N]) {
+    if (n >= N) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<f32x4_a4*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) p[i] = v[i];
+    }
 }
 
 // ---------------------------------------------------------------- reductions over a wave

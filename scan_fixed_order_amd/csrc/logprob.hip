@@ -10,7 +10,8 @@
 // the entropy also where its logit is -inf.  A row without any mass (all logits -inf) has
 // lse = -inf, entropy 0, logp -inf and gradient 0.
 //
-// Order: 1024 lanes share a row, lane L holding elements 8 L + 8192 j .. + 8 for j = 0, 1, ...;
+// Order: 1024 lanes share a row, lane L holding elements V (L + 1024 j) .. + V for j = 0, 1, ...
+// (V = 8, 4 of f32);
 // each adds its own in that order, then 64 neighbouring lanes join by the adjacent-lanes tree,
 // then the 16 groups by the same tree.  How many threads play those lanes does not enter the
 // order, nor do the other rows: a row's bits depend on its logits and the scale alone.
@@ -23,7 +24,8 @@ namespace det {
 namespace {
 
 constexpr int kLanes = 1024;              // lanes that share a row, in the order above
-constexpr int kTile = kLanes * kVec;      // elements they take at a time
+template <typename T>
+constexpr int kTile = kLanes * kVec<T>;   // elements they take at a time
 constexpr int kGroup = 32;                // neighbouring elements whose largest is kept for top
 constexpr int kShort = 512;               // candidates of the short way to the top
 // A lane's reference is one of its own values, replaced when a value exceeds it by more than
@@ -80,23 +82,24 @@ __device__ __forceinline__ float sum16(float v) {
     return v + xor_partner<8>(v);
 }
 
-// adds 8 logits; `largest`: their maximum (NaN ignored); `limit`: the logit that passes the
+// adds a vector of N logits; `largest`: their maximum (NaN ignored); `limit`: the logit that passes the
 // reference by kSlack
-__device__ __forceinline__ void take(Part& p, float& limit, const float (&x)[kVec], float largest,
+template <int N>
+__device__ __forceinline__ void take(Part& p, float& limit, const float (&x)[N], float largest,
                                      float scale, float unscale) {
     if (largest > limit) {
         rebase(p, largest * scale);
         limit = (p.ref + kSlack) * unscale;
     }
-    float e[kVec], d[kVec];
+    float e[N], d[N];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < N; ++i) {
         d[i] = fmaf(x[i], scale, -p.ref);
         e[i] = exp_fast(d[i]);
     }
     float w0 = e[0] * d[0], w1 = e[1] * d[1];
 #pragma unroll
-    for (int i = 2; i < kVec; i += 2) {
+    for (int i = 2; i < N; i += 2) {
         w0 = fmaf(e[i], d[i], w0);
         w1 = fmaf(e[i + 1], d[i + 1], w1);
     }
@@ -104,14 +107,18 @@ __device__ __forceinline__ void take(Part& p, float& limit, const float (&x)[kVe
     if (w != w) {      // 0 * -inf among them: such a term counts as 0
         w = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) w += e[i] == 0.0f ? 0.0f : e[i] * d[i];
+        for (int i = 0; i < N; ++i) w += e[i] == 0.0f ? 0.0f : e[i] * d[i];
     }
-    p.s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    float s = (e[0] + e[1]) + (e[2] + e[3]);
+    if constexpr (N == 8) s += (e[4] + e[5]) + (e[6] + e[7]);
+    p.s += s;
     p.w += w;
 }
 
-__device__ __forceinline__ float max8(const float (&x)[kVec]) {
-    return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max3(x[6], x[7], -INFINITY));
+template <int N>
+__device__ __forceinline__ float largest_of(const float (&x)[N]) {
+    if constexpr (N == 4) return max3(max3(x[0], x[1], x[2]), x[3], -INFINITY);
+    else return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max3(x[6], x[7], -INFINITY));
 }
 
 // groups of a super-group: 64 of them cover the row; odd, so that lanes that read one group of
@@ -294,7 +301,7 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
 template <typename T, int BLOCK, bool TOP, bool ONCE>
 __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
     constexpr int kSets = kLanes / BLOCK;       // lanes a thread plays
-    constexpr int kSteps = 4 / kSets;           // tiles whose loads are in flight together
+    constexpr int kSteps = 32 / kVec<T> / kSets;   // tiles whose loads are in flight together
     extern __shared__ __align__(16) uint32_t s_key[];
     __shared__ Part s_part[2][kLanes / 64];      // rows take turns: no second barrier a row
     __shared__ Search s_search;      // not laid out where nothing is searched
@@ -312,42 +319,46 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
             p[u] = Part{-FLT_MAX, 0.0f, 0.0f};
             limit[u] = -FLT_MAX * a.unscale;
         }
-        const auto one = [&](int64_t c, int u, const float(&v)[kVec], bool keep) {
-            const float largest = max8(v);
+        const auto one = [&](int64_t c, int u, const float(&v)[kVec<T>], bool keep) {
+            const float largest = largest_of(v);
             if constexpr (TOP) {
                 // (fmaxf would quiet its operands first, an instruction each)
                 float g = largest, other = xor_partner<1>(g);
                 g = max3(g, other, other);
                 other = xor_partner<2>(g);
                 g = max3(g, other, other);
-                if (keep && (lane & 3) == 0) s_key[c / kGroup] = __float_as_uint(g);
+                if constexpr (kGroup / kVec<T> == 8) {
+                    other = xor_partner<4>(g);
+                    g = max3(g, other, other);
+                }
+                if (keep && lane % (kGroup / kVec<T>) == 0) s_key[c / kGroup] = __float_as_uint(g);
             }
             if (keep) take(p[u], limit[u], v, largest, a.scale, a.unscale);
         };
-        const int64_t whole = a.vocab / (kTile * kSteps);
+        const int64_t whole = a.vocab / (kTile<T> * kSteps);
         for (int64_t i = 0; i < whole; ++i) {
-            Raw8<T> raw[kSteps][kSets];
+            u32x4 raw[kSteps][kSets];
 #pragma unroll
             for (int q = 0; q < kSteps; ++q)
 #pragma unroll
                 for (int u = 0; u < kSets; ++u)
-                    raw[q][u] = load8<ONCE>(x + (i * kSteps + q) * kTile + kVec * (t + u * BLOCK));
+                    raw[q][u] = load_vec<ONCE>(x + (i * kSteps + q) * kTile<T> + kVec<T> * (t + u * BLOCK));
 #pragma unroll
             for (int q = 0; q < kSteps; ++q)
 #pragma unroll
                 for (int u = 0; u < kSets; ++u) {
-                    float v[kVec];
-                    unpack8<T>(raw[q][u], v);
-                    one((i * kSteps + q) * kTile + kVec * (t + u * BLOCK), u, v, true);
+                    float v[kVec<T>];
+                    unpack<T>(raw[q][u], v);
+                    one((i * kSteps + q) * kTile<T> + kVec<T> * (t + u * BLOCK), u, v, true);
                 }
         }
-        for (int64_t base = whole * kSteps * kTile; base < a.vocab; base += kTile) {
+        for (int64_t base = whole * kSteps * kTile<T>; base < a.vocab; base += kTile<T>) {
 #pragma unroll
             for (int u = 0; u < kSets; ++u) {
-                if (base + kVec * u * BLOCK >= a.vocab) break;
-                const int64_t c = base + kVec * (t + u * BLOCK);
-                float v[kVec];
-                read8(x + c, a.vocab - c, -INFINITY, v);
+                if (base + kVec<T> * u * BLOCK >= a.vocab) break;
+                const int64_t c = base + kVec<T> * (t + u * BLOCK);
+                float v[kVec<T>];
+                read_vec(x + c, a.vocab - c, -INFINITY, v);
                 one(c, u, v, c < a.vocab);
             }
         }
@@ -391,8 +402,7 @@ struct LogpBackArgs {
     float scale;
 };
 
-constexpr int kBackVecs = 4;                              // vectors a thread
-constexpr int kBackTile = 256 * kVec * kBackVecs;
+constexpr int kBackTile = 8192;                           // elements a workgroup takes at a time
 
 // Each logit read once, each gradient written once; nothing is summed.  Bound by HBM: 4096 x
 // 65536 bf16 188 us (5.7 TB/s).
@@ -410,14 +420,14 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a)
         const float both = a.dentropy ? fmaf(dent, a.entropy[row], dlogp) : dlogp;
         const bool none = lse == -INFINITY;
 #pragma unroll
-        for (int j = 0; j < kBackVecs; ++j) {
-            const int64_t c = c0 + kVec * (threadIdx.x + 256 * j), n = a.vocab - c;
+        for (int j = 0; j < kBackTile / (256 * kVec<T>); ++j) {
+            const int64_t c = c0 + kVec<T> * (threadIdx.x + 256 * j), n = a.vocab - c;
             if (n <= 0) continue;
-            float v[kVec];
-            read8<ONCE>(x + c, n, 0.0f, v);
+            float v[kVec<T>];
+            read_vec<ONCE>(x + c, n, 0.0f, v);
             const int64_t hit = scored ? at - c : -1;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
+            for (int i = 0; i < kVec<T>; ++i) {
                 const float log = fmaf(v[i], a.scale, -lse);
                 const float p = exp_fast(log);
                 // below -1000 p is 0 and -inf must not meet it
@@ -425,7 +435,7 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a)
                 if (i == hit) d += dlogp;
                 v[i] = none ? 0.0f : d * a.scale;
             }
-            write8(out + c, n, v);
+            write_vec(out + c, n, v);
         }
     }
 }
@@ -452,7 +462,7 @@ bool once(int64_t rows, int64_t vocab) {
 // against 28 with 256 threads; 700 rows 47 us with 1024, 42 with 256.  (The order is the same.)
 template <typename T>
 void logp_typed(const LogpArgs& a, hipStream_t s) {
-    if (a.rows <= 256 && a.vocab > kTile)
+    if (a.rows <= 256 && a.vocab > kTile<T>)
         logp_block<T, 1024, false>(a, s);
     else if (once<T>(a.rows, a.vocab))
         logp_block<T, 256, true>(a, s);

@@ -7,7 +7,8 @@
 //   dx = rstd * (dy w - xhat * sum(dy w xhat) / d) + dh,  xhat = h * rstd;  dweight = sum of
 //   dy * xhat over the rows.
 //
-// Order: lane t of the row's team holds elements 8 (t + j * team) .. + 8 for j = 0, 1, ...; it
+// Order: lane t of the row's team holds elements V (t + j * team) .. + V for j = 0, 1, ... (V = 8,
+// 4 of f32); it
 // adds its own in that order, the wave adds its lanes by the adjacent-lanes tree, and the wave
 // sums are added in wave order.  The team's size depends on d alone, so a row's bits depend
 // neither on the other rows nor on their number.  dweight: strips of rows in ascending order,
@@ -60,29 +61,35 @@ __device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t* slots) {
     return v;
 }
 
-// Largest |y| of 8 elements as its bits: they order like the magnitudes, and a NaN's lie above
+// Largest |y| of a vector as its bits: they order like the magnitudes, and a NaN's lie above
 // infinity's, so a NaN reaches its group's scale.
-__device__ __forceinline__ uint32_t max_bits(const float (&y)[kVec]) {
+template <int N>
+__device__ __forceinline__ uint32_t max_bits(const float (&y)[N]) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) m = umax(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < N; ++i) m = umax(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
     return m;
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t n, const float (&y)[kVec], float f) {
-    uint32_t lo = 0, hi = 0;
-    lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0] * f, y[1] * f, (int)lo, false);
-    lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2] * f, y[3] * f, (int)lo, true);
-    hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4] * f, y[5] * f, (int)hi, false);
-    hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[6] * f, y[7] * f, (int)hi, true);
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
-    if (n >= kVec) {
-        *reinterpret_cast<u32x2_a1*>(p) = u32x2{lo, hi};
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t n, const float (&y)[N], float f) {
+    uint32_t code[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i] * f, y[4 * i + 1] * f, 0, false);
+        c = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2] * f, y[4 * i + 3] * f, c, true);
+        code[i] = (uint32_t)c;
+    }
+    if (n >= N) {
+        typedef uint32_t codes __attribute__((ext_vector_type(N / 4), aligned(1)));
+        codes v;
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) v[i] = code[i];
+        *reinterpret_cast<codes*>(p) = v;
     } else {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            if (i < n) p[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+        for (int i = 0; i < N; ++i)
+            if (i < n) p[i] = (uint8_t)(code[i / 4] >> (8 * (i & 3)));
     }
 }
 
@@ -102,16 +109,18 @@ struct NormArgs {
 // y or codes of one vector; m: the row's largest |y| bits where the group is the row
 template <typename T, bool Q8>
 __device__ __forceinline__ void put(const NormArgs& a, int64_t row, int64_t c, int64_t n,
-                                    const float (&y)[kVec], uint32_t m) {
+                                    const float (&y)[kVec<T>], uint32_t m) {
     if constexpr (!Q8) {
-        if (n > 0) write8(static_cast<T*>(a.y) + row * a.d + c, n, y);
+        if (n > 0) write_vec(static_cast<T*>(a.y) + row * a.d + c, n, y);
     } else {
         if (a.group) {
             m = max_bits(y);      // every lane of the wave takes part; lanes past the row hold 0
             m = umax(m, xor_partner<1>(m));
             m = umax(m, xor_partner<2>(m));
-            if (a.group >= 64) m = umax(m, xor_partner<4>(m));
-            if (a.group >= 128) m = umax(m, xor_partner<8>(m));
+            const int lanes = a.group / kVec<T>;      // 4 or more
+            if (lanes >= 8) m = umax(m, xor_partner<4>(m));
+            if (lanes >= 16) m = umax(m, xor_partner<8>(m));
+            if (lanes >= 32) m = umax(m, xor_partner<16>(m));
         }
         const float top = __uint_as_float(umax(m, __float_as_uint(kTinyMax)));
         if (n > 0) {
@@ -144,25 +153,25 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
     const T* res = static_cast<const T*>(a.res) + (RES ? row * a.res_stride : 0);
     const T* w = static_cast<const T*>(a.w);
 
-    float h[NV][kVec];
-    float r[NV][kVec];
+    float h[NV][kVec<T>];
+    float r[NV][kVec<T>];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t c = (int64_t)kVec * (t + j * TEAM);
-        read8<ONCE>(x + c, a.d - c, 0.0f, h[j]);
-        if constexpr (RES) read8<ONCE>(res + c, a.d - c, 0.0f, r[j]);
+        const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
+        read_vec<ONCE>(x + c, a.d - c, 0.0f, h[j]);
+        if constexpr (RES) read_vec<ONCE>(res + c, a.d - c, 0.0f, r[j]);
     }
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if constexpr (RES) {
-            const int64_t c = (int64_t)kVec * (t + j * TEAM);
+            const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) h[j][i] += r[j][i];
-            if (live && a.d > c) write8(static_cast<T*>(a.h) + row * a.d + c, a.d - c, h[j]);
+            for (int i = 0; i < kVec<T>; ++i) h[j][i] += r[j][i];
+            if (live && a.d > c) write_vec(static_cast<T*>(a.h) + row * a.d + c, a.d - c, h[j]);
         }
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sum = fmaf(h[j][i], h[j][i], sum);
+        for (int i = 0; i < kVec<T>; ++i) sum = fmaf(h[j][i], h[j][i], sum);
     }
     sum = team_sum<TEAM>(sum, s_sum[team % kRows]);
     const float rstd = 1.0f / sqrtf(sum / (float)a.d + a.eps);
@@ -171,11 +180,11 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t c = (int64_t)kVec * (t + j * TEAM);
-        float g[kVec];
-        read8(w + c, a.d - c, 0.0f, g);
+        const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
+        float g[kVec<T>];
+        read_vec(w + c, a.d - c, 0.0f, g);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) h[j][i] = (h[j][i] * rstd) * g[i];
+        for (int i = 0; i < kVec<T>; ++i) h[j][i] = (h[j][i] * rstd) * g[i];
         if constexpr (Q8) m = umax(m, max_bits(h[j]));
     }
     if constexpr (Q8) {
@@ -183,7 +192,7 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t c = (int64_t)kVec * (t + j * TEAM);
+        const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
         put<T, Q8>(a, row, c, live ? a.d - c : 0, h[j], m);
     }
     if constexpr (TEAM > 64) __syncthreads();      // the LDS slots are written again
@@ -201,52 +210,52 @@ __global__ __launch_bounds__(1024) void k_rms_norm_long(NormArgs a) {
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
     const T* res = static_cast<const T*>(a.res) + (RES ? row * a.res_stride : 0);
     const T* w = static_cast<const T*>(a.w);
-    const int64_t steps = (a.d + TEAM * kVec - 1) / (TEAM * kVec);
-    const auto sums = [&](int64_t c, float (&h)[kVec]) {
-        read8(x + c, a.d - c, 0.0f, h);
+    const int64_t steps = (a.d + TEAM * kVec<T> - 1) / (TEAM * kVec<T>);
+    const auto sums = [&](int64_t c, float (&h)[kVec<T>]) {
+        read_vec(x + c, a.d - c, 0.0f, h);
         if constexpr (RES) {
-            float r[kVec];
-            read8(res + c, a.d - c, 0.0f, r);
+            float r[kVec<T>];
+            read_vec(res + c, a.d - c, 0.0f, r);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) h[i] += r[i];
+            for (int i = 0; i < kVec<T>; ++i) h[i] += r[i];
         }
     };
     float sum = 0.0f;
     for (int64_t j = 0; j < steps; ++j) {
-        const int64_t c = kVec * (threadIdx.x + j * TEAM);
-        float h[kVec];
+        const int64_t c = kVec<T> * (threadIdx.x + j * TEAM);
+        float h[kVec<T>];
         sums(c, h);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sum = fmaf(h[i], h[i], sum);
+        for (int i = 0; i < kVec<T>; ++i) sum = fmaf(h[i], h[i], sum);
     }
     sum = team_sum<TEAM>(sum, s_sum);
     const float rstd = 1.0f / sqrtf(sum / (float)a.d + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-    const auto outputs = [&](int64_t c, float (&h)[kVec], bool last) {
+    const auto outputs = [&](int64_t c, float (&h)[kVec<T>], bool last) {
         sums(c, h);
-        float g[kVec];
-        read8(w + c, a.d - c, 0.0f, g);
+        float g[kVec<T>];
+        read_vec(w + c, a.d - c, 0.0f, g);
         if constexpr (RES) {
             // only now: h may be x itself
-            if (last && a.d > c) write8(static_cast<T*>(a.h) + row * a.d + c, a.d - c, h);
+            if (last && a.d > c) write_vec(static_cast<T*>(a.h) + row * a.d + c, a.d - c, h);
         }
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) h[i] = (h[i] * rstd) * g[i];
+        for (int i = 0; i < kVec<T>; ++i) h[i] = (h[i] * rstd) * g[i];
     };
     uint32_t m = 0;
     if constexpr (Q8) {
         if (!a.group) {
             for (int64_t j = 0; j < steps; ++j) {
-                float h[kVec];
-                outputs(kVec * (threadIdx.x + j * TEAM), h, false);
+                float h[kVec<T>];
+                outputs(kVec<T> * (threadIdx.x + j * TEAM), h, false);
                 m = umax(m, max_bits(h));
             }
             m = team_max<TEAM>(m, s_max);
         }
     }
     for (int64_t j = 0; j < steps; ++j) {
-        const int64_t c = kVec * (threadIdx.x + j * TEAM);
-        float h[kVec];
+        const int64_t c = kVec<T> * (threadIdx.x + j * TEAM);
+        float h[kVec<T>];
         outputs(c, h, true);
         put<T, Q8>(a, row, c, a.d - c, h, m);
     }
@@ -274,7 +283,7 @@ constexpr int back_team(int64_t d) { return d <= 512 ? 64 : d <= 2048 ? 256 : d 
 // One row's vectors of a lane as they lie in memory
 template <typename T, int NV>
 struct BackRow {
-    Raw8<T> h[NV], dy[NV], dh[NV];
+    u32x4 h[NV], dy[NV], dh[NV];
     float rstd;
 };
 
@@ -287,10 +296,11 @@ struct BackRow {
 template <typename T, int TEAM, int NV, bool DH, bool ONCE>
 __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBackArgs a) {
     constexpr int kRows = Team<TEAM>::kRows, kWaves = Team<TEAM>::kWaves;
-    constexpr bool kAhead = sizeof(T) == 2 || NV == 1, kLdsSums = NV > 1;
+    constexpr int kElems = NV * kVec<T>;      // a lane's share of a row
+    constexpr bool kAhead = sizeof(T) == 2 || kElems <= 8, kLdsSums = kElems > 8;
     extern __shared__ float s_cols[];      // kLdsSums: the lane's column sums, [vector][element][lane]
     __shared__ float s_sum[2][kRows][kWaves];
-    __shared__ float s_acc[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? TEAM * NV * kVec : 1];
+    __shared__ float s_acc[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? TEAM * NV * kVec<T> : 1];
     const int team = threadIdx.x / TEAM, t = threadIdx.x % TEAM;
     const int64_t strip = (int64_t)blockIdx.x * kRows + team;
     const int64_t begin = strip * a.strip;
@@ -300,25 +310,25 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
         r.rstd = a.rstd[row];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t c = (int64_t)kVec * (t + j * TEAM);
-            r.h[j] = read_raw8<ONCE>(static_cast<const T*>(a.h) + row * a.h_stride + c, a.d - c);
-            r.dy[j] = read_raw8<ONCE>(static_cast<const T*>(a.dy) + row * a.dy_stride + c, a.d - c);
+            const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
+            r.h[j] = read_raw<ONCE>(static_cast<const T*>(a.h) + row * a.h_stride + c, a.d - c);
+            r.dy[j] = read_raw<ONCE>(static_cast<const T*>(a.dy) + row * a.dy_stride + c, a.d - c);
             if constexpr (DH && kAhead)
-                r.dh[j] = read_raw8<ONCE>(static_cast<const T*>(a.dh) + row * a.dh_stride + c, a.d - c);
+                r.dh[j] = read_raw<ONCE>(static_cast<const T*>(a.dh) + row * a.dh_stride + c, a.d - c);
         }
     };
     BackRow<T, NV> cur, next;
     read(begin, cur);
-    Raw8<T> wraw[NV];
-    float acc[NV][kVec];
+    u32x4 wraw[NV];
+    float acc[NV][kVec<T>];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t c = (int64_t)kVec * (t + j * TEAM);
-        wraw[j] = read_raw8(w + c, a.d - c);
+        const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
+        wraw[j] = read_raw(w + c, a.d - c);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
+        for (int i = 0; i < kVec<T>; ++i) {
             acc[j][i] = 0.0f;
-            if constexpr (kLdsSums) s_cols[(j * kVec + i) * TEAM + t] = 0.0f;
+            if constexpr (kLdsSums) s_cols[(j * kVec<T> + i) * TEAM + t] = 0.0f;
         }
     }
     // every team of the workgroup takes the same number of steps (barriers)
@@ -328,21 +338,21 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
             if (k + 1 < a.strip) read(begin + k + 1, next);
         }
         const float rstd = cur.rstd;
-        float h[NV][kVec], dy[NV][kVec];
+        float h[NV][kVec<T>], dy[NV][kVec<T>];
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            unpack8<T>(cur.h[j], h[j]);
-            unpack8<T>(cur.dy[j], dy[j]);
-            float g[kVec];
-            unpack8<T>(wraw[j], g);
+            unpack<T>(cur.h[j], h[j]);
+            unpack<T>(cur.dy[j], dy[j]);
+            float g[kVec<T>];
+            unpack<T>(wraw[j], g);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
+            for (int i = 0; i < kVec<T>; ++i) {
                 h[j][i] *= rstd;
                 const float p = dy[j][i] * h[j][i];
                 if (live) {
                     if constexpr (kLdsSums)
-                        s_cols[(j * kVec + i) * TEAM + t] += p;
+                        s_cols[(j * kVec<T> + i) * TEAM + t] += p;
                     else
                         acc[j][i] += p;
                 }
@@ -353,19 +363,19 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
         const float mean = team_sum<TEAM>(sum, s_sum[k & 1][team % kRows]) / (float)a.d;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t c = (int64_t)kVec * (t + j * TEAM);
-            float o[kVec], e[kVec];
-            if constexpr (DH && kAhead) unpack8<T>(cur.dh[j], e);
+            const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
+            float o[kVec<T>], e[kVec<T>];
+            if constexpr (DH && kAhead) unpack<T>(cur.dh[j], e);
             if constexpr (DH && !kAhead)
-                read8<ONCE>(static_cast<const T*>(a.dh) + (live ? begin + k : a.rows - 1) * a.dh_stride + c,
+                read_vec<ONCE>(static_cast<const T*>(a.dh) + (live ? begin + k : a.rows - 1) * a.dh_stride + c,
                       a.d - c, 0.0f, e);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
+            for (int i = 0; i < kVec<T>; ++i) {
                 o[i] = rstd * fmaf(-h[j][i], mean, dy[j][i]);
                 if constexpr (DH) o[i] += e[i];
             }
             if (live && a.d > c)
-                write8(static_cast<T*>(a.dx) + (begin + k) * a.d + c, a.d - c, o);
+                write_vec(static_cast<T*>(a.dx) + (begin + k) * a.d + c, a.d - c, o);
         }
         if constexpr (kAhead)
             cur = next;
@@ -377,24 +387,24 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) s_acc[team - 1][kVec * (t + j * TEAM) + i] = acc[j][i];
+                for (int i = 0; i < kVec<T>; ++i) s_acc[team - 1][kVec<T> * (t + j * TEAM) + i] = acc[j][i];
         }
         __syncthreads();
         if (team > 0) return;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < kVec; ++i)
-                for (int r = 0; r < kRows - 1; ++r) acc[j][i] += s_acc[r][kVec * (t + j * TEAM) + i];
+            for (int i = 0; i < kVec<T>; ++i)
+                for (int r = 0; r < kRows - 1; ++r) acc[j][i] += s_acc[r][kVec<T> * (t + j * TEAM) + i];
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t c = (int64_t)kVec * (t + j * TEAM);
+        const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
         if constexpr (kLdsSums) {
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) acc[j][i] = s_cols[(j * kVec + i) * TEAM + t];
+            for (int i = 0; i < kVec<T>; ++i) acc[j][i] = s_cols[(j * kVec<T> + i) * TEAM + t];
         }
-        if (a.d > c) write8(a.part + blockIdx.x * a.d + c, a.d - c, acc[j]);
+        if (a.d > c) write_floats(a.part + blockIdx.x * a.d + c, a.d - c, acc[j]);
     }
 }
 
@@ -410,37 +420,37 @@ __global__ __launch_bounds__(1024) void k_rms_norm_backward_long(NormBackArgs a)
     const T* dyp = static_cast<const T*>(a.dy) + row * a.dy_stride;
     const T* dhp = static_cast<const T*>(a.dh) + (DH ? row * a.dh_stride : 0);
     const float rstd = a.rstd[row];
-    const int64_t steps = (a.d + TEAM * kVec - 1) / (TEAM * kVec);
-    const auto both = [&](int64_t c, float (&h)[kVec], float (&dy)[kVec]) {
-        float g[kVec];
-        read8(hp + c, a.d - c, 0.0f, h);
-        read8(dyp + c, a.d - c, 0.0f, dy);
-        read8(w + c, a.d - c, 0.0f, g);
+    const int64_t steps = (a.d + TEAM * kVec<T> - 1) / (TEAM * kVec<T>);
+    const auto both = [&](int64_t c, float (&h)[kVec<T>], float (&dy)[kVec<T>]) {
+        float g[kVec<T>];
+        read_vec(hp + c, a.d - c, 0.0f, h);
+        read_vec(dyp + c, a.d - c, 0.0f, dy);
+        read_vec(w + c, a.d - c, 0.0f, g);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
+        for (int i = 0; i < kVec<T>; ++i) {
             h[i] *= rstd;
             dy[i] *= g[i];
         }
     };
     float sum = 0.0f;
     for (int64_t j = 0; j < steps; ++j) {
-        float h[kVec], dy[kVec];
-        both(kVec * (threadIdx.x + j * TEAM), h, dy);
+        float h[kVec<T>], dy[kVec<T>];
+        both(kVec<T> * (threadIdx.x + j * TEAM), h, dy);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sum = fmaf(dy[i], h[i], sum);
+        for (int i = 0; i < kVec<T>; ++i) sum = fmaf(dy[i], h[i], sum);
     }
     const float mean = team_sum<TEAM>(sum, s_sum) / (float)a.d;
     for (int64_t j = 0; j < steps; ++j) {
-        const int64_t c = kVec * (threadIdx.x + j * TEAM);
-        float h[kVec], dy[kVec], e[kVec];
+        const int64_t c = kVec<T> * (threadIdx.x + j * TEAM);
+        float h[kVec<T>], dy[kVec<T>], e[kVec<T>];
         both(c, h, dy);
-        if constexpr (DH) read8(dhp + c, a.d - c, 0.0f, e);
+        if constexpr (DH) read_vec(dhp + c, a.d - c, 0.0f, e);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
+        for (int i = 0; i < kVec<T>; ++i) {
             dy[i] = rstd * fmaf(-h[i], mean, dy[i]);
             if constexpr (DH) dy[i] += e[i];
         }
-        if (a.d > c) write8(static_cast<T*>(a.dx) + row * a.d + c, a.d - c, dy);
+        if (a.d > c) write_vec(static_cast<T*>(a.dx) + row * a.d + c, a.d - c, dy);
     }
     __syncthreads();      // the LDS slots are written again
     }
@@ -449,23 +459,23 @@ __global__ __launch_bounds__(1024) void k_rms_norm_backward_long(NormBackArgs a)
 // The strips' sums of dy * xhat for long rows: a lane owns 8 columns of one strip.
 template <typename T>
 __global__ __launch_bounds__(256) void k_rms_norm_strips(NormBackArgs a) {
-    const int64_t c = kVec * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    const int64_t c = kVec<T> * ((int64_t)blockIdx.x * 256 + threadIdx.x);
     const int64_t strip = blockIdx.y, begin = strip * a.strip;
     if (c >= a.d) return;
     const int64_t end = begin + a.strip < a.rows ? begin + a.strip : a.rows;
-    float acc[kVec] = {};
+    float acc[kVec<T>] = {};
     for (int64_t row = begin; row < end; ++row) {
-        float h[kVec], dy[kVec];
-        read8(static_cast<const T*>(a.h) + row * a.h_stride + c, a.d - c, 0.0f, h);
-        read8(static_cast<const T*>(a.dy) + row * a.dy_stride + c, a.d - c, 0.0f, dy);
+        float h[kVec<T>], dy[kVec<T>];
+        read_vec(static_cast<const T*>(a.h) + row * a.h_stride + c, a.d - c, 0.0f, h);
+        read_vec(static_cast<const T*>(a.dy) + row * a.dy_stride + c, a.d - c, 0.0f, dy);
         const float rstd = a.rstd[row];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
+        for (int i = 0; i < kVec<T>; ++i) {
             const float p = dy[i] * (h[i] * rstd);
             acc[i] += p;
         }
     }
-    write8(a.part + strip * a.d + c, a.d - c, acc);
+    write_floats(a.part + strip * a.d + c, a.d - c, acc);
 }
 
 // dweight[c] = the strips' sums added: row k of 256 adds strips k, k + 256, ... in that order,
@@ -523,15 +533,16 @@ unsigned grid_of(int64_t wgs) { return (unsigned)(wgs < (1 << 21) ? wgs : (1 << 
 
 constexpr int64_t kRowInRegs = 16384;        // forward: up to 2 vectors a lane of 1024
 
+// NV: 8 elements of a row a lane
 template <typename T, int TEAM, int NV, bool RES, bool Q8>
 void norm_in_regs(const NormArgs& a, hipStream_t s) {
     const dim3 grid(grid_of((a.rows + Team<TEAM>::kRows - 1) / Team<TEAM>::kRows));
     const dim3 block(Team<TEAM>::kBlock);
     KernelTimer kt("k_rms_norm", s);
     if ((size_t)a.rows * a.d * sizeof(T) * (RES ? 2 : 1) >= kOnceBytes)
-        k_rms_norm<T, TEAM, NV, RES, Q8, true><<<grid, block, 0, s>>>(a);
+        k_rms_norm<T, TEAM, NV * 8 / kVec<T>, RES, Q8, true><<<grid, block, 0, s>>>(a);
     else
-        k_rms_norm<T, TEAM, NV, RES, Q8, false><<<grid, block, 0, s>>>(a);
+        k_rms_norm<T, TEAM, NV * 8 / kVec<T>, RES, Q8, false><<<grid, block, 0, s>>>(a);
 }
 
 template <typename T, bool RES, bool Q8>
@@ -574,12 +585,12 @@ void norm_typed(const NormArgs& a, bool q8, hipStream_t s) {
 template <typename T, int NV, int TEAM, bool DH>
 void back_in_regs(const NormBackArgs& a, int64_t wgs, hipStream_t s) {
     const dim3 grid((unsigned)wgs), block(Team<TEAM>::kBlock);
-    const int lds = NV > 1 ? TEAM * NV * kVec * 4 : 0;
+    const int lds = NV > 1 ? TEAM * NV * 8 * 4 : 0;      // NV vectors of 8 (f32: twice as many of 4)
     KernelTimer kt("k_rms_norm_backward", s);
     if ((size_t)a.rows * a.d * sizeof(T) * (DH ? 3 : 2) >= kOnceBytes)
-        k_rms_norm_backward<T, TEAM, NV, DH, true><<<grid, block, lds, s>>>(a);
+        k_rms_norm_backward<T, TEAM, NV * 8 / kVec<T>, DH, true><<<grid, block, lds, s>>>(a);
     else
-        k_rms_norm_backward<T, TEAM, NV, DH, false><<<grid, block, lds, s>>>(a);
+        k_rms_norm_backward<T, TEAM, NV * 8 / kVec<T>, DH, false><<<grid, block, lds, s>>>(a);
 }
 
 template <typename T, bool DH>
@@ -600,7 +611,7 @@ void back_sized(const NormBackArgs& a, int64_t sums, hipStream_t s) {
             k_rms_norm_backward_long<T, DH><<<dim3(grid_of(a.rows)), dim3(1024), 0, s>>>(a);
         }
         KernelTimer kt("k_rms_norm_strips", s);
-        const dim3 grid((unsigned)((a.d + 256 * kVec - 1) / (256 * kVec)), (unsigned)sums);
+        const dim3 grid((unsigned)((a.d + 256 * kVec<T> - 1) / (256 * kVec<T>)), (unsigned)sums);
         k_rms_norm_strips<T><<<grid, dim3(256), 0, s>>>(a);
     }
 }

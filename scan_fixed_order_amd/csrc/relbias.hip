@@ -42,14 +42,15 @@ __device__ __forceinline__ int bucket_of(const Map& m, const int* starts, int to
     return m.two_sided && r > 0 ? lo + m.side : lo;
 }
 
-// Buckets of kVec neighbouring relative positions from r on, their searches side by side.
+// Buckets of N neighbouring relative positions from r on, their searches side by side.
+template <int N>
 __device__ __forceinline__ void buckets_of(const Map& m, const int* starts, int64_t r,
-                                           int (&bucket)[kVec]) {
+                                           int (&bucket)[N]) {
     const int border = starts[m.side - 1];
-    int far[kVec];
+    int far[N];
     bool near = false;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < N; ++i) {
         const int64_t a = r + i < 0 ? -(r + i) : (m.two_sided ? r + i : 0);
         far[i] = a < border ? (int)a : border;
         near |= far[i] < border;
@@ -57,10 +58,10 @@ __device__ __forceinline__ void buckets_of(const Map& m, const int* starts, int6
     }
     if (near) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) bucket[i] = 0;
+        for (int i = 0; i < N; ++i) bucket[i] = 0;
         for (int step = m.top; step > 0; step >>= 1) {
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
+            for (int i = 0; i < N; ++i) {
                 // read in any case: a branch around the load would make the searches take turns
                 const int next = bucket[i] + step, at = next < m.side ? next : m.side - 1;
                 bucket[i] = starts[at] <= far[i] ? at : bucket[i];
@@ -68,7 +69,7 @@ __device__ __forceinline__ void buckets_of(const Map& m, const int* starts, int6
         }
     }
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
+    for (int i = 0; i < N; ++i)
         if (m.two_sided && r + i > 0) bucket[i] += m.side;
 }
 
@@ -102,25 +103,25 @@ struct BiasArgs {
 
 constexpr int kRows = 8;
 
-// 8 elements from place `at` of a tensor whose elements lie in [0, extent), of which the first n
+// A vector from place `at` of a tensor whose elements lie in [0, extent), of which the first n
 // count; the others are unspecified.  Those may lie past the row's end but never outside the
 // tensor, whose two ends alone are read one by one.
 template <typename T>
-__device__ __forceinline__ Raw8<T> load8_inside(const T* p, int64_t at, int64_t n, int64_t extent) {
-    Raw8<T> r = {};
+__device__ __forceinline__ u32x4 load_inside(const T* p, int64_t at, int64_t n, int64_t extent) {
+    u32x4 r = {};
     if (n > 0) {
-        if (at + kVec <= extent) {
-            r = load8(p + at);
+        if (at + kVec<T> <= extent) {
+            r = load_vec(p + at);
         } else {
-            float v[kVec];
+            float v[kVec<T>];
             load_tail(p + at, n, 0.0f, v);
-            r = pack8<T>(v);
+            r = pack<T>(v);
         }
     }
     return r;
 }
 
-// A workgroup covers `width` = 8 * 2^lanes_log2 keys and (256 >> lanes_log2) * rows queries of
+// A workgroup covers `width` = 2^lanes_log2 vectors of keys and (256 >> lanes_log2) * rows queries of
 // one head.  The values of all its diagonals are laid out once in LDS; a lane then walks down
 // its rows, and each next row is the last one moved by one element, with one new element read.
 // Bound by HBM's writes: 16 x 4096 x 4096 bf16 alone 97 us (5.5 TB/s; any height, width or order of
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias(Map m, BiasArgs a) {
     __shared__ float s_table[DET_BIAS_MAX_BUCKETS];
     constexpr int kStep = SCORES ? kRows / 2 : kRows;
     const int lanes = 1 << a.lanes_log2, teams = kBlock >> a.lanes_log2;
-    const int width = kVec * lanes, height = teams * a.rows;
+    const int width = kVec<T> * lanes, height = teams * a.rows;
     for (int i = threadIdx.x; i < m.side; i += kBlock) s_starts[i] = m.starts[i];
     const int64_t kt = blockIdx.x;
     for (int64_t bh = blockIdx.z; bh < a.batch * a.heads; bh += gridDim.z)
@@ -152,50 +153,50 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias(Map m, BiasArgs a) {
             s_diag[i] = s_table[bucket_of(m, s_starts, m.top, r0 + i)];
         __syncthreads();
         const int lane = threadIdx.x & (lanes - 1), team = threadIdx.x >> a.lanes_log2;
-        const int64_t c = k0 + kVec * lane, row0 = q0 + (int64_t)team * a.rows;
+        const int64_t c = k0 + kVec<T> * lane, row0 = q0 + (int64_t)team * a.rows;
         const int64_t n = m.k - c;                       // keys from c on
         if (n <= 0) continue;
-        float v[kVec];
-        int at = kVec * lane + (height - 1 - team * a.rows);   // diagonal of (row0, c)
+        float v[kVec<T>];
+        int at = kVec<T> * lane + (height - 1 - team * a.rows);   // diagonal of (row0, c)
 #pragma unroll
-        for (int i = 1; i < kVec; ++i) v[i - 1] = s_diag[at + i];   // moved into place by the first row
+        for (int i = 1; i < kVec<T>; ++i) v[i - 1] = s_diag[at + i];   // moved into place by the first row
         const int64_t end = row0 + a.rows < m.q ? row0 + a.rows : m.q;
         const int64_t base = SCORES ? b * a.sb + h * a.sh + c : 0;
         const T* scores = static_cast<const T*>(a.scores);
         // kStep rows at a time, their loads in flight together
         for (int64_t row = row0; row < end; row += kStep, at -= kStep) {
-            Raw8<T> raw[kStep];
+            u32x4 raw[kStep];
             int left[kStep];          // of the vector's keys, those that the masks leave
 #pragma unroll
             for (int j = 0; j < kStep; ++j) {
                 const int64_t pos = row + j + off;
                 const int64_t keys = (m.causal && pos + 1 < len ? pos + 1 : len) - c;
-                left[j] = pos >= len || row + j >= end || keys < 0 ? 0 : keys < kVec ? (int)keys : kVec;
+                left[j] = pos >= len || row + j >= end || keys < 0 ? 0 : keys < kVec<T> ? (int)keys : kVec<T>;
                 if constexpr (SCORES)
-                    raw[j] = load8_inside(scores, base + (row + j) * a.sq,
+                    raw[j] = load_inside(scores, base + (row + j) * a.sq,
                                           left[j] < n ? left[j] : n, a.extent);
             }
 #pragma unroll
             for (int j = 0; j < kStep; ++j) {
                 if (row + j >= end) break;
 #pragma unroll
-                for (int i = kVec - 1; i > 0; --i) v[i] = v[i - 1];
+                for (int i = kVec<T> - 1; i > 0; --i) v[i] = v[i - 1];
                 v[0] = s_diag[at - j];
-                float o[kVec];
+                float o[kVec<T>];
                 if constexpr (SCORES) {
-                    unpack8<T>(raw[j], o);
+                    unpack<T>(raw[j], o);
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) o[i] += v[i];
+                    for (int i = 0; i < kVec<T>; ++i) o[i] += v[i];
                 } else {
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) o[i] = v[i];
+                    for (int i = 0; i < kVec<T>; ++i) o[i] = v[i];
                 }
-                if (left[j] < kVec) {
+                if (left[j] < kVec<T>) {
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i)
+                    for (int i = 0; i < kVec<T>; ++i)
                         if (i >= left[j]) o[i] = a.fill;
                 }
-                write8(static_cast<T*>(a.out) + (bh * m.q + row + j) * m.k + c, n, o);
+                write_vec(static_cast<T*>(a.out) + (bh * m.q + row + j) * m.k + c, n, o);
             }
         }
     }
@@ -211,7 +212,7 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_row(Map m, BiasArgs a)
     const int lanes = 1 << a.lanes_log2, teams = kBlock >> a.lanes_log2;
     for (int i = threadIdx.x; i < m.side; i += kBlock) s_starts[i] = m.starts[i];
     __syncthreads();
-    const int64_t c = (int64_t)blockIdx.x * kVec * lanes + kVec * (threadIdx.x & (lanes - 1));
+    const int64_t c = (int64_t)blockIdx.x * kVec<T> * lanes + kVec<T> * (threadIdx.x & (lanes - 1));
     const int64_t n = m.k - c;
     if (n <= 0) return;
     const T* table = static_cast<const T*>(a.table);
@@ -221,33 +222,33 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_row(Map m, BiasArgs a)
         const int64_t b = split(bh, a.heads), h = bh - b * a.heads;
         const int64_t off = offset_of(m, b), len = length_of(m, b);
         const int64_t keys = (m.causal && row + off + 1 < len ? row + off + 1 : len) - c;
-        const int left = row + off >= len || keys < 0 ? 0 : keys < kVec ? (int)keys : kVec;
-        float o[kVec];
-        Raw8<T> raw;
+        const int left = row + off >= len || keys < 0 ? 0 : keys < kVec<T> ? (int)keys : kVec<T>;
+        float o[kVec<T>];
+        u32x4 raw;
         if constexpr (SCORES)
-            raw = load8_inside(static_cast<const T*>(a.scores),
+            raw = load_inside(static_cast<const T*>(a.scores),
                                b * a.sb + h * a.sh + row * a.sq + c, left < n ? left : n, a.extent);
         const int64_t r0 = c - row - off;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) o[i] = a.fill;
+        for (int i = 0; i < kVec<T>; ++i) o[i] = a.fill;
         if (left > 0) {
-            int bucket[kVec];
+            int bucket[kVec<T>];
             buckets_of(m, s_starts, r0, bucket);
-            float v[kVec];
+            float v[kVec<T>];
 #pragma unroll
-            for (int i = 0; i < kVec; ++i)
+            for (int i = 0; i < kVec<T>; ++i)
                 v[i] = table ? (float)table[(int64_t)bucket[i] * a.heads + h] : 0.0f;
             if constexpr (SCORES) {
-                float sc[kVec];
-                unpack8<T>(raw, sc);
+                float sc[kVec<T>];
+                unpack<T>(raw, sc);
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) v[i] += sc[i];
+                for (int i = 0; i < kVec<T>; ++i) v[i] += sc[i];
             }
 #pragma unroll
-            for (int i = 0; i < kVec; ++i)
+            for (int i = 0; i < kVec<T>; ++i)
                 if (i < left) o[i] = v[i];
         }
-        write8(static_cast<T*>(a.out) + r * m.k + c, n, o);
+        write_vec(static_cast<T*>(a.out) + r * m.k + c, n, o);
     }
 }
 
@@ -264,18 +265,19 @@ struct BiasBackArgs {
 
 constexpr int kWaves = kBlock / 64;
 constexpr int kShortRun = 16;              // diagonals
-constexpr int kDiags = 64 * kVec;          // diagonals a wave covers
+template <typename T>
+constexpr int kDiags = 64 * kVec<T>;       // diagonals a wave covers
 
-// A lane owns 8 neighbouring diagonals and walks down the strip's rows: its 8 elements of a row
+// A lane owns a vector's neighbouring diagonals and walks down the strip's rows: its elements of a row
 // lie together in memory, one place further along with every row.  kRows rows are added in f32,
 // their sums in f64.  The wave then adds its diagonals up by buckets, which are runs of
 // neighbouring diagonals, and the workgroup its waves.  Bound by HBM: 4 x 16 x 2048 x 2048 bf16
-// 107 us with the last sums (5.0 TB/s; 102 without the buckets' sums).  Its loads start at any
-// element, which fetches a tenth more than the tensor holds.  Strips of 32 rows: 64 took 114 us,
-// 128 took 123 (fewer waves than fill the GPU evenly).
+// 98 us with the last sums (5.5 TB/s); 107 while the edges' rows were masked in 64 bits.  Its loads
+// start at any element, which fetches a tenth more than the tensor holds.  Strips of 32 rows: 64
+// took 4 % longer, 128 12 % (fewer waves than fill the GPU evenly).
 template <typename T, bool ONCE>
 __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBackArgs a) {
-    __shared__ double s_sums[kWaves][kDiags];
+    __shared__ double s_sums[kWaves][kDiags<T>];
     __shared__ double s_part[kWaves][DET_BIAS_MAX_BUCKETS];
     __shared__ int s_starts[kBiasMaxSide];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -296,68 +298,78 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
         const int64_t keys = len < m.k ? len : m.k;       // keys past it neither
         // diagonal d of the strip, from 0: key = row + d - shift
         const int64_t shift = q0 + a.strip - 1;
-        const int64_t d0 = dt * kDiags + kVec * lane - shift;    // key = row + d0 + i
-        double acc[kVec] = {};
+        const int64_t d0 = dt * kDiags<T> + kVec<T> * lane - shift;    // key = row + d0 + i
+        double acc[kVec<T>] = {};
         const T* p = static_cast<const T*>(a.dout);
         const int64_t base = b * a.sb + h * a.sh + d0;
         const bool some = !m.causal || d0 - off <= 0;
-        const bool whole = some && q0 + d0 >= 0 && q1 + d0 + kVec - 1 <= keys;
+        const bool whole = some && q0 + d0 >= 0 && q1 + d0 + kVec<T> - 1 <= keys;
         const bool inner = __all(whole);
         // the blocks of rows that meet the wave's diagonals
-        const int64_t w0 = dt * kDiags - shift;
-        const int64_t lo = -(w0 + kDiags - 1), hi = keys - w0;
+        const int64_t w0 = dt * kDiags<T> - shift;
+        const int64_t lo = -(w0 + kDiags<T> - 1), hi = keys - w0;
         const int64_t from = lo > q0 ? q0 + (lo - q0) / kRows * kRows : q0;
         const int64_t to = m.causal && w0 - off > 0 ? from : hi < q1 ? hi : q1;
         for (int64_t row = from; row < to; row += kRows) {
-            Raw8<T> raw[kRows];
-            float sum[kVec] = {};
-            if (inner && row + kRows <= q1) {
+            u32x4 raw[kRows];
+            float sum[kVec<T>] = {};
+            // of the vector in the first row: its place, its key, clipped, and the keys from it on
+            const int64_t at = base + row * (a.sq + 1), key = row + d0, rest = keys - key;
+            const int c = key < -64 ? -64 : key > 0 ? 0 : (int)key;
+            const int n = rest < 0 ? 0 : rest > 64 ? 64 : (int)rest;
+            const int rows = q1 - row < kRows ? (int)(q1 - row) : kRows;
+            if (inner && rows == kRows) {
 #pragma unroll
-                for (int j = 0; j < kRows; ++j)
-                    raw[j] = load8<ONCE>(p + base + (row + j) * (a.sq + 1));
+                for (int j = 0; j < kRows; ++j) raw[j] = load_vec<ONCE>(p + at + j * (a.sq + 1));
 #pragma unroll
                 for (int j = 0; j < kRows; ++j) {
-                    float v[kVec];
-                    unpack8<T>(raw[j], v);
+                    float v[kVec<T>];
+                    unpack<T>(raw[j], v);
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) sum[i] += v[i];
+                    for (int i = 0; i < kVec<T>; ++i) sum[i] += v[i];
+                }
+            } else if (!some || c + kRows + kVec<T> <= 1 || n == 0) {
+                // none of these rows has a place on the lane's diagonals
+            } else if (at >= 0 && at + (kRows - 1) * (a.sq + 1) + kVec<T> <= a.extent) {
+                // whole vectors inside the tensor, what lies outside the row dropped
+#pragma unroll
+                for (int j = 0; j < kRows; ++j) {
+                    raw[j] = u32x4{};
+                    if (j < rows && c + j + kVec<T> > 0 && j < n)
+                        raw[j] = load_vec<ONCE>(p + at + j * (a.sq + 1));
+                }
+#pragma unroll
+                for (int j = 0; j < kRows; ++j) {
+                    float v[kVec<T>];
+                    unpack<T>(raw[j], v);
+#pragma unroll
+                    for (int i = 0; i < kVec<T>; ++i) sum[i] += i + j >= -c && i + j < n ? v[i] : 0.0f;
                 }
             } else {
+                // at the tensor's very ends, one by one; what does not count is read from the
+                // nearest place inside (branches would make the loads wait for each other)
+#pragma unroll 2
+                for (int j = 0; j < rows; ++j) {
+                    T v[kVec<T>];
 #pragma unroll
-                for (int j = 0; j < kRows; ++j) {
-                    const int64_t c = row + j + d0, at = base + (row + j) * (a.sq + 1);
-                    raw[j] = {};
-                    if (some && row + j < q1 && c > -kVec && c < keys) {
-                        if (at >= 0 && at + kVec <= a.extent) {
-                            raw[j] = load8<ONCE>(p + at);
-                        } else {      // at the tensor's very ends
-                            float v[kVec];
-#pragma unroll
-                            for (int i = 0; i < kVec; ++i)
-                                v[i] = c + i >= 0 && c + i < keys ? (float)p[at + i] : 0.0f;
-                            raw[j] = pack8<T>(v);
-                        }
+                    for (int i = 0; i < kVec<T>; ++i) {
+                        int64_t place = at + j * (a.sq + 1) + i;
+                        place = place < 0 ? 0 : place < a.extent ? place : a.extent - 1;
+                        v[i] = p[place];
                     }
-                }
 #pragma unroll
-                for (int j = 0; j < kRows; ++j) {
-                    const int c = (int)(row + j + d0 > -kVec ? row + j + d0 : -kVec);
-                    const int64_t rest = keys - (row + j + d0);
-                    const int n = rest < kVec ? (int)rest : kVec;
-                    float v[kVec];
-                    unpack8<T>(raw[j], v);
-#pragma unroll
-                    for (int i = 0; i < kVec; ++i) sum[i] += c + i >= 0 && i < n ? v[i] : 0.0f;
+                    for (int i = 0; i < kVec<T>; ++i)
+                        sum[i] += i + j >= -c && i + j < n ? (float)v[i] : 0.0f;
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) acc[i] += (double)sum[i];
+            for (int i = 0; i < kVec<T>; ++i) acc[i] += (double)sum[i];
         }
         // a diagonal after the query is masked as a whole when causal
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
+        for (int i = 0; i < kVec<T>; ++i)
             if (m.causal && d0 + i - off > 0) acc[i] = 0.0;
-        const int64_t r0 = dt * kDiags - shift - off;     // r of the tile's diagonal 0
+        const int64_t r0 = dt * kDiags<T> - shift - off;     // r of the tile's diagonal 0
         // lane by lane the buckets' runs of diagonals [first, last)
         bool laid_out = false;
         for (int bk0 = 0; bk0 < a.buckets; bk0 += 64) {
@@ -373,18 +385,18 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
             }
             lo -= r0;
             hi -= r0;
-            const int first = (int)(lo < 0 ? 0 : lo > kDiags ? kDiags : lo);
-            const int last = (int)(hi < 0 ? 0 : hi > kDiags ? kDiags : hi);
+            const int first = (int)(lo < 0 ? 0 : lo > kDiags<T> ? kDiags<T> : lo);
+            const int last = (int)(hi < 0 ? 0 : hi > kDiags<T> ? kDiags<T> : hi);
             const bool wide = last - first > kShortRun;
             double mine = 0.0;
             // long runs (far from the diagonal one covers the tile): by the whole wave
             for (uint64_t runs = __ballot(wide); runs; runs &= runs - 1) {
                 const int l = __ffsll((unsigned long long)runs) - 1;
-                const int f = __builtin_amdgcn_readlane(first, l) - kVec * lane;
-                const int t = __builtin_amdgcn_readlane(last, l) - kVec * lane;
+                const int f = __builtin_amdgcn_readlane(first, l) - kVec<T> * lane;
+                const int t = __builtin_amdgcn_readlane(last, l) - kVec<T> * lane;
                 double v = 0.0;
 #pragma unroll
-                for (int i = 0; i < kVec; ++i)
+                for (int i = 0; i < kVec<T>; ++i)
                     if (i >= f && i < t) v += acc[i];
                 v = wave_pw(v);
                 if (lane == l) mine = v;
@@ -394,7 +406,7 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
                 if (!laid_out) {
                     wave_sync();
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) s_sum[kVec * lane + i] = acc[i];
+                    for (int i = 0; i < kVec<T>; ++i) s_sum[kVec<T> * lane + i] = acc[i];
                     wave_sync();
                     laid_out = true;
                 }
@@ -537,9 +549,9 @@ void bias_typed(const BiasCall& c, hipStream_t s) {
                kRows, c.buckets, c.fill, 0};
     // as many lanes across the keys as the row has vectors (at most the workgroup), the rest of
     // the workgroup on further rows
-    while (a.lanes_log2 > 3 && ((int64_t)kVec << (a.lanes_log2 - 1)) >= c.k) --a.lanes_log2;
+    while (a.lanes_log2 > 3 && ((int64_t)kVec<T> << (a.lanes_log2 - 1)) >= c.k) --a.lanes_log2;
     const int teams = kBlock >> a.lanes_log2;
-    const int64_t width = (int64_t)kVec << a.lanes_log2;
+    const int64_t width = (int64_t)kVec<T> << a.lanes_log2;
     const int64_t kt = (c.k + width - 1) / width, bh = a.batch * a.heads;
     if (c.q < kRows) {
         const int64_t rows = (bh * c.q + teams - 1) / teams;
@@ -575,11 +587,11 @@ struct BackShape {
 
 // Rows a strip and the diagonals' tiles, from the sizes alone: the order of the sums.  Strips of
 // 32 rows, halved down to 8 while that leaves fewer than 4096 waves.
-BackShape back_shape(int64_t batch, int64_t heads, int64_t q, int64_t k) {
+BackShape back_shape(int64_t batch, int64_t heads, int64_t q, int64_t k, int64_t diags) {
     BackShape r;
     for (r.strip = 32;; r.strip /= 2) {
         r.qt = (q + r.strip - 1) / r.strip;
-        r.dt = (k + r.strip - 1 + kDiags - 1) / kDiags;
+        r.dt = (k + r.strip - 1 + diags - 1) / diags;
         if (r.strip == kRows || (double)batch * heads * r.qt * r.dt >= 4096.0) return r;
     }
 }
@@ -587,7 +599,7 @@ BackShape back_shape(int64_t batch, int64_t heads, int64_t q, int64_t k) {
 template <typename T>
 det_status back_typed(const BiasCall& c, const void* dout, void* dtable, void* ws, hipStream_t s) {
     const Map m = map_of(c);
-    const BackShape sh = back_shape(c.batch, c.heads, c.q, c.k);
+    const BackShape sh = back_shape(c.batch, c.heads, c.q, c.k, kDiags<T>);
     BiasBackArgs a{dout, static_cast<double*>(ws), c.sb, c.sh, c.sq, extent_of(c), c.heads,
                    c.batch, sh.strip, sh.qt, sh.dt, c.buckets};
     const int64_t per_head = (sh.qt * sh.dt + kWaves - 1) / kWaves;
@@ -610,8 +622,10 @@ det_status back_typed(const BiasCall& c, const void* dout, void* dtable, void* w
 
 }  // namespace
 
-size_t bias_backward_workspace(int64_t batch, int64_t heads, int64_t q, int64_t k, int buckets) {
-    const BackShape s = back_shape(batch, heads, q, k);
+size_t bias_backward_workspace(int64_t batch, int64_t heads, int64_t q, int64_t k, int buckets,
+                               det_dtype dtype) {
+    const BackShape s = back_shape(batch, heads, q, k,
+                                   dtype == DET_F32 ? kDiags<float> : kDiags<_Float16>);
     const int64_t per_head = (s.qt * s.dt + kWaves - 1) / kWaves;
     return round_up((size_t)batch * heads * per_head * buckets * sizeof(double), 256) + 256;
 }

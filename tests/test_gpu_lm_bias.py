@@ -1,7 +1,7 @@
 """det_relative_bias and its table's gradient on the GPU against 64-bit statements whose buckets
 are found in whole numbers.  Without scores the output is the table's own values, bit for bit;
-with them one f32 addition and the type's rounding; the table's gradient sums n terms in f32 along
-at most 128 rows, 512 diagonals in 8 steps and 6 levels, and the rest in f64."""
+with them one f32 addition and the type's rounding; the table's gradient sums in f32 along at most
+128 rows and 512 diagonals in 8 steps and 6 levels (in fact along 8 rows), and the rest in f64."""
 import math
 
 import pytest

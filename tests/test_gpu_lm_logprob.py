@@ -3,7 +3,7 @@ have to be equal.
 
 Tolerances: U = 2^-24.  A term exp(z - ref) is off by 2 U (1 + |z - ref|) and the hardware's unit;
 terms count by their weight, so with weights p the sums s and w / s are off by U (40 + vocab /
-8192 * 8 + 4 sum p |z - ref|) relative to s, and by as much times sum p |z - ref| more for w / s.
+1024 + 4 sum p |z - ref|) relative to s, and by as much times sum p |z - ref| more for w / s.
 z - ref and the last additions are rounded once each relative to their sizes."""
 import math
 

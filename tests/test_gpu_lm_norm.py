@@ -18,7 +18,7 @@ E4M3 = torch.float8_e4m3fn
 
 
 def chain(d):
-    return 8 * max(3, -(-d // 8192)) + 6 + 16
+    return 8 * max(4, -(-d // 8192)) + 6 + 16
 
 
 def inputs(rows, d, t, dev, seed, residual=True):
@@ -190,7 +190,8 @@ def test_norm_backward(dev, rows, d, t, stream):
     if stream:
         bound += 2 * U32 * dh.double().abs()
     assert ((dx.double() - want).abs() <= bound).all()
-    # the rows' sum: a strip of at most 8 rows here, the strips of a lane, 6 levels
+    # the rows' sum: a strip of at most 8 rows here, the strips of a workgroup and of a lane, the
+    # levels above
     depth = 8 + -(-rows // 64) + 6 + 4
     mags = (dy.double() * xhat).abs().sum(0)
     assert ((dw.double() - dwant).abs()
