@@ -243,7 +243,7 @@ det_status det_scatter_add_running(const void* values, const int32_t* index, int
  *   rstd = 1 / sqrt(sum(h^2) / d + eps);  y = (h * rstd) * weight
  *   y_dtype DET_E4M3: for every group of neighbouring elements of a row, m = max(|y|, 2^-100),
  *   code = round(y * (448 / m)), scale = m / 448.
- * Order of the row's sum: fixed by d.
+ * Order of the row's sum: fixed by (d, dtype).
  * x, residual:  [rows] rows of d elements, x_stride and residual_stride apart (>= d when
  *               rows > 1).  residual may be NULL.
  * weight:       [d].
@@ -273,7 +273,7 @@ size_t det_rms_norm_backward_workspace_size(int64_t rows, int64_t d, det_dtype d
  * dh:       NULL, or the gradient that reaches h from elsewhere, dh_stride apart.
  * dx:       [rows * d]; may be dy, h or dh itself where that is contiguous and d <= 16384.
  * dweight:  [d], written (zero for no rows).
- * Order: a row's sum fixed by d; dweight's fixed by (rows, d): strips of rows in ascending
+ * Order: a row's sum fixed by (d, dtype); dweight's by (rows, d): strips of rows in ascending
  * order, then the strips. */
 det_status det_rms_norm_backward(const void* dy, int64_t dy_stride, const void* h,
                                  int64_t h_stride, const void* weight, const float* rstd,
@@ -323,7 +323,7 @@ size_t det_relative_bias_backward_workspace_size(int64_t batch, int64_t heads, i
  * dscores:  NULL, or [batch * heads * q * k]: dout with zeros at the masked places (the gradient
  *           of the scores).  May be dout itself where that is contiguous.
  * The other arguments as for det_relative_bias.
- * Order, fixed by (batch, heads, q, k): every diagonal of a strip of query rows in row order, the
+ * Order, fixed by (batch, heads, q, k, dtype): every diagonal of a strip of query rows in row order, the
  * diagonals of a bucket, then the strips in f64. */
 det_status det_relative_bias_backward(const void* dout, int64_t stride_b, int64_t stride_h,
                                       int64_t stride_q, int64_t num_buckets, int64_t heads,
@@ -347,7 +347,7 @@ det_status det_relative_bias_backward(const void* dout, int64_t stride_b, int64_
  *            DET_LOGPROB_MAX_TOP_VOCAB (DET_ERROR_TOO_LARGE).
  * top_logp, top_ids:  float and int64 [rows * top], NULL when top is 0.
  * A row of -inf alone has lse -inf, entropy 0, logp -inf.  vocab >= 1 when rows > 0; scale > 0
- * and finite.  Order of a row's sums: fixed by vocab. */
+ * and finite.  Order of a row's sums: fixed by (vocab, dtype). */
 det_status det_token_logprobs(const void* logits, int64_t row_stride, const int64_t* targets,
                               int64_t rows, int64_t vocab, det_dtype dtype, double scale,
                               float* logp, float* entropy, float* lse, int64_t top,

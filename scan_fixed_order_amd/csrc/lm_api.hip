@@ -59,7 +59,8 @@ det_status det_rms_norm(const void* x, int64_t x_stride, const void* residual,
     if (!lm_dtype(dtype)) return DET_ERROR_UNSUPPORTED;
     const bool codes = y_dtype == DET_E4M3;
     if (!codes && y_dtype != dtype) return DET_ERROR_UNSUPPORTED;
-    if (rows < 0 || d < 0 || !(eps >= 0.0) || !isfinite(eps)) return DET_ERROR_INVALID_VALUE;
+    if (rows < 0 || d < 0 || !(eps >= 0.0) || !isfinite((float)eps))
+        return DET_ERROR_INVALID_VALUE;
     if (rows > DET_MAX_N || d > DET_MAX_N) return DET_ERROR_TOO_LARGE;
     if (codes ? group != 0 && group != 32 && group != 64 && group != 128 : group != 0)
         return DET_ERROR_INVALID_VALUE;

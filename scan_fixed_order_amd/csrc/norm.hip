@@ -23,9 +23,9 @@ constexpr float kE4m3Max = 448.0f;
 constexpr float kTinyMax = 0x1p-100f;
 
 // A team of lanes per row, the row in registers between the sum and the output.  Teams by
-// measurement (norm_sized): 8192 x 4096 bf16 44.4 us with 512 lanes of one vector, 45.9 with 256
-// of two, 52.1 with 128 of four; 2048 x 16384 with codes 50 us with 512 of four, 55 with 1024 of
-// two, 71 with 256 of eight.
+// measurement (norm_sized): 8192 x 8192 bf16 with codes 78 us with 512 lanes of two vectors, 122
+// with 1024 of one; 8192 x 5000 f16 55 us with 256 of three, 60 with 768 of one; 2048 x 16384 with
+// codes 46 us with 512 of four, 58 with 1024 of two.
 template <int TEAM>
 struct Team {
     static constexpr int kBlock = TEAM < 256 ? 256 : TEAM;
@@ -136,12 +136,13 @@ __device__ __forceinline__ void put(const NormArgs& a, int64_t row, int64_t c, i
 }
 
 // One row per team, the row in registers: NV vectors a lane.  Bound by HBM: every element is
-// read once and written once.  8192 x 8192 bf16 with residual: 85 us (6.3 TB/s), with 8-bit codes
-// 87 us (5.4 TB/s); one row of 4096 2.4 us.  Rows that start off 16 bytes cost more: 4096 x 5001
-// f16 with codes 40 us (3.6 TB/s).
+// read once and written once.  8192 x 8192 bf16 with residual: 79 us (6.8 TB/s), with 8-bit codes
+// 78 us (6.0 TB/s); one row of 4096 2.4 us.  Rows that start off 16 bytes cost more: 8192 x 5001
+// f16 64 us (5.1 TB/s), 8192 x 5000 55 us.
 template <typename T, int TEAM, int NV, bool RES, bool Q8, bool ONCE>
 __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
     constexpr int kRows = Team<TEAM>::kRows, kWaves = Team<TEAM>::kWaves;
+    constexpr bool kWeightAhead = NV * kVec<T> <= 16;      // registers for it
     __shared__ float s_sum[kRows][kWaves];
     __shared__ uint32_t s_max[kRows][kWaves];
     const int team = threadIdx.x / TEAM, t = threadIdx.x % TEAM;
@@ -153,21 +154,28 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
     const T* res = static_cast<const T*>(a.res) + (RES ? row * a.res_stride : 0);
     const T* w = static_cast<const T*>(a.w);
 
-    float h[NV][kVec<T>];
-    float r[NV][kVec<T>];
+    u32x4 raw[NV], raw_res[NV], raw_w[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
-        read_vec<ONCE>(x + c, a.d - c, 0.0f, h[j]);
-        if constexpr (RES) read_vec<ONCE>(res + c, a.d - c, 0.0f, r[j]);
+        raw[j] = load_row<ONCE>(x, c, a.d);
+        if constexpr (RES) raw_res[j] = load_row<ONCE>(res, c, a.d);
     }
+    if constexpr (kWeightAhead) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) raw_w[j] = load_row(w, (int64_t)kVec<T> * (t + j * TEAM), a.d);
+    }
+    float h[NV][kVec<T>];
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+        const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
+        unpack<T>(settle<T>(raw[j], c, a.d), h[j]);
         if constexpr (RES) {
-            const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
+            float r[kVec<T>];
+            unpack<T>(settle<T>(raw_res[j], c, a.d), r);
 #pragma unroll
-            for (int i = 0; i < kVec<T>; ++i) h[j][i] += r[j][i];
+            for (int i = 0; i < kVec<T>; ++i) h[j][i] += r[i];
             if (live && a.d > c) write_vec(static_cast<T*>(a.h) + row * a.d + c, a.d - c, h[j]);
         }
 #pragma unroll
@@ -182,7 +190,8 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
     for (int j = 0; j < NV; ++j) {
         const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
         float g[kVec<T>];
-        read_vec(w + c, a.d - c, 0.0f, g);
+        if constexpr (!kWeightAhead) raw_w[j] = load_row(w, c, a.d);
+        unpack<T>(settle<T>(raw_w[j], c, a.d), g);
 #pragma unroll
         for (int i = 0; i < kVec<T>; ++i) h[j][i] = (h[j][i] * rstd) * g[i];
         if constexpr (Q8) m = umax(m, max_bits(h[j]));
@@ -311,10 +320,10 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
-            r.h[j] = read_raw<ONCE>(static_cast<const T*>(a.h) + row * a.h_stride + c, a.d - c);
-            r.dy[j] = read_raw<ONCE>(static_cast<const T*>(a.dy) + row * a.dy_stride + c, a.d - c);
+            r.h[j] = load_row<ONCE>(static_cast<const T*>(a.h) + row * a.h_stride, c, a.d);
+            r.dy[j] = load_row<ONCE>(static_cast<const T*>(a.dy) + row * a.dy_stride, c, a.d);
             if constexpr (DH && kAhead)
-                r.dh[j] = read_raw<ONCE>(static_cast<const T*>(a.dh) + row * a.dh_stride + c, a.d - c);
+                r.dh[j] = load_row<ONCE>(static_cast<const T*>(a.dh) + row * a.dh_stride, c, a.d);
         }
     };
     BackRow<T, NV> cur, next;
@@ -324,7 +333,7 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
-        wraw[j] = read_raw(w + c, a.d - c);
+        wraw[j] = settle<T>(load_row(w, c, a.d), c, a.d);
 #pragma unroll
         for (int i = 0; i < kVec<T>; ++i) {
             acc[j][i] = 0.0f;
@@ -342,8 +351,9 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            unpack<T>(cur.h[j], h[j]);
-            unpack<T>(cur.dy[j], dy[j]);
+            const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
+            unpack<T>(settle<T>(cur.h[j], c, a.d), h[j]);
+            unpack<T>(settle<T>(cur.dy[j], c, a.d), dy[j]);
             float g[kVec<T>];
             unpack<T>(wraw[j], g);
 #pragma unroll
@@ -365,7 +375,7 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
         for (int j = 0; j < NV; ++j) {
             const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
             float o[kVec<T>], e[kVec<T>];
-            if constexpr (DH && kAhead) unpack<T>(cur.dh[j], e);
+            if constexpr (DH && kAhead) unpack<T>(settle<T>(cur.dh[j], c, a.d), e);
             if constexpr (DH && !kAhead)
                 read_vec<ONCE>(static_cast<const T*>(a.dh) + (live ? begin + k : a.rows - 1) * a.dh_stride + c,
                       a.d - c, 0.0f, e);
