@@ -127,16 +127,23 @@ __device__ __forceinline__ u32x4 load_row(const T* row, int64_t c, int64_t d) {
     return load_vec<ONCE>(row + (c + kVec<T> <= d ? c : d - kVec<T>));
 }
 
+// (In 32-bit words.  A 64-bit shift whose amount the compiler had put in the last register that a
+// wave owns gave wrong elements now and then, in the gradient of f32 logits.)
 template <typename T>
 __device__ __forceinline__ u32x4 settle(u32x4 r, int64_t c, int64_t d) {
     const int64_t past = c + kVec<T> - d;      // elements past the end
     if (d >= kVec<T> && __any(past > 0)) {
-        const int bits = (past <= 0 ? 0 : past < kVec<T> ? (int)past : kVec<T>) * (int)sizeof(T) * 8;
-        const uint64_t lo = (uint64_t)r[1] << 32 | r[0], hi = (uint64_t)r[3] << 32 | r[2];
-        const uint64_t carry = bits == 0 ? 0 : hi << (64 - bits & 63);
-        const uint64_t l = bits < 64 ? lo >> (bits & 63) | carry : bits < 128 ? hi >> (bits & 63) : 0;
-        const uint64_t h = bits < 64 ? hi >> (bits & 63) : 0;
-        r = u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+        const uint32_t n = past <= 0 ? 0 : past < kVec<T> ? (uint32_t)past : kVec<T>;
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t half = n % 2 * 16;
+            r = u32x4{__builtin_amdgcn_alignbit(r[1], r[0], half),
+                      __builtin_amdgcn_alignbit(r[2], r[1], half),
+                      __builtin_amdgcn_alignbit(r[3], r[2], half), r[3] >> half};
+        }
+        const uint32_t words = sizeof(T) == 2 ? n / 2 : n;
+        if (words & 1) r = u32x4{r[1], r[2], r[3], 0};
+        if (words & 2) r = u32x4{r[2], r[3], 0, 0};
+        if (words & 4) r = u32x4{0, 0, 0, 0};
     }
     return r;
 }
