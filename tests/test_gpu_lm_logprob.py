@@ -210,6 +210,32 @@ def test_backward(dev, rows, vocab, t, scale, dent):
                                                      scale), got)
 
 
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("vocab", [1000, 1003, 9001])
+def test_gradient_of_many_rows_keeps_its_bits(dev, vocab, t):
+    # enough rows for many waves on each unit, and rows that end inside a wave and a vector
+    rows = 1500
+    x, at = inputs(rows, vocab, t, dev, 18)
+    f = det.det_token_logprobs(x, at)
+    d = randn((rows,), torch.float32, dev, 19)
+    want = ref.logprobs_backward(x.double() - f.lse.double()[:, None], at, f.entropy.double(), d,
+                                 None, 1.0)
+    p = (x.double() - f.lse.double()[:, None]).exp()
+    hit = torch.zeros_like(p).scatter_(1, at.clamp_min(0)[:, None], 1.0)
+    size = (x.double() - f.lse.double()[:, None]).abs()
+    got = det.det_token_logprobs_backward(x, at, f.lse, d)
+    bound = (8 + 4 * size) * U32 * d.double().abs()[:, None] * (hit + p)
+    bound += half(t) * want.abs() * 1.001 + floor_of(t)
+    bound += 2.0 ** -126 * (d.double().abs()[:, None] + 1) * (1 + size.clamp_max(200.0))
+    assert ((got.double() - want).abs() <= bound).all()
+    for _ in range(5):
+        assert same_bits(det.det_token_logprobs_backward(x, at, f.lse, d), got)
+    for r in range(0, rows, 100):
+        part = det.det_token_logprobs_backward(x[r:r + 100], at[r:r + 100], f.lse[r:r + 100],
+                                               d[r:r + 100])
+        assert same_bits(part, got[r:r + 100].contiguous())
+
+
 def test_empty(dev):
     x, at = torch.empty(0, 50, device=dev), torch.empty(0, dtype=torch.int64, device=dev)
     got = det.det_token_logprobs(x, at, top=3)
