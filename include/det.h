@@ -323,8 +323,8 @@ size_t det_relative_bias_backward_workspace_size(int64_t batch, int64_t heads, i
  * dscores:  NULL, or [batch * heads * q * k]: dout with zeros at the masked places (the gradient
  *           of the scores).  May be dout itself where that is contiguous.
  * The other arguments as for det_relative_bias.
- * Order, fixed by (batch, heads, q, k, dtype): every diagonal of a strip of query rows in row order, the
- * diagonals of a bucket, then the strips in f64. */
+ * Order, fixed by (batch, heads, q, k, dtype): every diagonal of a strip of query rows in row
+ * order, the diagonals of a bucket, then the strips in f64. */
 det_status det_relative_bias_backward(const void* dout, int64_t stride_b, int64_t stride_h,
                                       int64_t stride_q, int64_t num_buckets, int64_t heads,
                                       int64_t max_distance, unsigned flags, int64_t batch,

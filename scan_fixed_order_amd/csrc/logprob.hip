@@ -295,9 +295,9 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
 
 // One row per workgroup, each logit read once; 1024 threads for few rows, where a compute unit's
 // vector rate bounds (about 17 logits a nanosecond), 256 for many.  2048 x 131072 bf16: 88 us
-// (6.1 TB/s, bound by HBM), with 5 alternatives 97 us (5.6 TB/s: 10 vector instructions and an
-// exponential a logit fill the vector units, and a row's search runs for 2 us).  256 x 131072 with 5
-// alternatives 16.7 us with 1024 threads a row; 300 rows 31 us with 256.
+// (6.1 TB/s, bound by HBM), with 5 alternatives 96 us (5.6 TB/s: 10 vector instructions and an
+// exponential a logit fill the vector units, and a row's search runs for 2 us).  256 x 131072 with
+// 5 alternatives 16.7 us with 1024 threads a row; 300 rows 31 us with 256.
 template <typename T, int BLOCK, bool TOP, bool ONCE>
 __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
     constexpr int kSets = kLanes / BLOCK;       // lanes a thread plays

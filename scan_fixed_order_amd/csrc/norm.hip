@@ -8,8 +8,7 @@
 //   dy * xhat over the rows.
 //
 // Order: lane t of the row's team holds elements V (t + j * team) .. + V for j = 0, 1, ... (V = 8,
-// 4 of f32); it
-// adds its own in that order, the wave adds its lanes by the adjacent-lanes tree, and the wave
+// 4 of f32); it adds its own in that order, the wave adds its lanes by the adjacent-lanes tree, and the wave
 // sums are added in wave order.  The team's size depends on d alone, so a row's bits depend
 // neither on the other rows nor on their number.  dweight: strips of rows in ascending order,
 // then the strips (k_col_sums); the strip length depends on (rows, d) alone.
@@ -307,7 +306,8 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
     constexpr int kRows = Team<TEAM>::kRows, kWaves = Team<TEAM>::kWaves;
     constexpr int kElems = NV * kVec<T>;      // a lane's share of a row
     constexpr bool kAhead = sizeof(T) == 2 || kElems <= 8, kLdsSums = kElems > 8;
-    extern __shared__ float s_cols[];      // kLdsSums: the lane's column sums, [vector][element][lane]
+    // kLdsSums: the lane's column sums, [vector][element][lane]
+    extern __shared__ float s_cols[];
     __shared__ float s_sum[2][kRows][kWaves];
     __shared__ float s_acc[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? TEAM * NV * kVec<T> : 1];
     const int team = threadIdx.x / TEAM, t = threadIdx.x % TEAM;
@@ -525,7 +525,8 @@ __global__ __launch_bounds__(1024) void k_col_sums(const float* part, int64_t st
 
 // ---------------------------------------------------------------- launches
 
-// Rows a strip: 2^17 lanes at work (512 a compute unit), 256 teams at least; at least 4 rows each so that the strips' sums stay small beside the rows.
+// Rows a strip: 2^17 lanes at work (512 a compute unit), 256 teams at least; at least 4 rows each
+// so that the strips' sums stay small beside the rows.
 int64_t strip_rows(int64_t rows, int64_t d) {
     const int64_t teams = d <= 4096 ? (1 << 17) / back_team(d) : 256;
     const int64_t r = (rows + teams - 1) / teams;

@@ -268,8 +268,8 @@ constexpr int kShortRun = 16;              // diagonals
 template <typename T>
 constexpr int kDiags = 64 * kVec<T>;       // diagonals a wave covers
 
-// A lane owns a vector's neighbouring diagonals and walks down the strip's rows: its elements of a row
-// lie together in memory, one place further along with every row.  kRows rows are added in f32,
+// A lane owns a vector's neighbouring diagonals and walks down the strip's rows: its elements of
+// a row lie together in memory, one place further along with every row.  kRows rows are added in f32,
 // their sums in f64.  The wave then adds its diagonals up by buckets, which are runs of
 // neighbouring diagonals, and the workgroup its waves.  Bound by HBM: 4 x 16 x 2048 x 2048 bf16
 // 98 us with the last sums (5.5 TB/s); 107 while the edges' rows were masked in 64 bits.  Its loads
