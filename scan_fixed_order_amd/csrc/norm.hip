@@ -101,8 +101,9 @@ struct NormArgs {
     float* scales;
     float* rstd;          // NULL: not written
     int64_t x_stride, res_stride, rows, d;
-    int group;            // 8 bits: 32, 64, 128, or 0 for the row
-    float eps;
+    int64_t groups;       // scales a row
+    int group_log2;       // 8 bits: 5, 6, 7, or 0 for the row
+    float len, eps;       // d
 };
 
 // y or codes of one vector; m: the row's largest |y| bits where the group is the row
@@ -112,11 +113,11 @@ __device__ __forceinline__ void put(const NormArgs& a, int64_t row, int64_t c, i
     if constexpr (!Q8) {
         if (n > 0) write_vec(static_cast<T*>(a.y) + row * a.d + c, n, y);
     } else {
-        if (a.group) {
+        if (a.group_log2) {
             m = max_bits(y);      // every lane of the wave takes part; lanes past the row hold 0
             m = umax(m, xor_partner<1>(m));
             m = umax(m, xor_partner<2>(m));
-            const int lanes = a.group / kVec<T>;      // 4 or more
+            const int lanes = (1 << a.group_log2) / kVec<T>;      // 4 or more
             if (lanes >= 8) m = umax(m, xor_partner<4>(m));
             if (lanes >= 16) m = umax(m, xor_partner<8>(m));
             if (lanes >= 32) m = umax(m, xor_partner<16>(m));
@@ -124,12 +125,8 @@ __device__ __forceinline__ void put(const NormArgs& a, int64_t row, int64_t c, i
         const float top = __uint_as_float(umax(m, __float_as_uint(kTinyMax)));
         if (n > 0) {
             store_codes(static_cast<uint8_t*>(a.y) + row * a.d + c, n, y, kE4m3Max / top);
-            if (a.group) {
-                if (c % a.group == 0)
-                    a.scales[row * ((a.d + a.group - 1) / a.group) + c / a.group] = top / kE4m3Max;
-            } else if (c == 0) {
-                a.scales[row] = top / kE4m3Max;
-            }
+            const int64_t g = a.group_log2 ? c >> a.group_log2 : 0;
+            if (g << a.group_log2 == c) a.scales[row * a.groups + g] = top / kE4m3Max;
         }
     }
 }
@@ -181,7 +178,7 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
         for (int i = 0; i < kVec<T>; ++i) sum = fmaf(h[j][i], h[j][i], sum);
     }
     sum = team_sum<TEAM>(sum, s_sum[team % kRows]);
-    const float rstd = 1.0f / sqrtf(sum / (float)a.d + a.eps);
+    const float rstd = 1.0f / sqrtf(sum / a.len + a.eps);
     if (a.rstd && live && t == 0) a.rstd[row] = rstd;
 
     uint32_t m = 0;
@@ -196,7 +193,7 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
         if constexpr (Q8) m = umax(m, max_bits(h[j]));
     }
     if constexpr (Q8) {
-        if (!a.group) m = team_max<TEAM>(m, s_max[team % kRows]);
+        if (!a.group_log2) m = team_max<TEAM>(m, s_max[team % kRows]);
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -237,7 +234,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm_long(NormArgs a) {
         for (int i = 0; i < kVec<T>; ++i) sum = fmaf(h[i], h[i], sum);
     }
     sum = team_sum<TEAM>(sum, s_sum);
-    const float rstd = 1.0f / sqrtf(sum / (float)a.d + a.eps);
+    const float rstd = 1.0f / sqrtf(sum / a.len + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     const auto outputs = [&](int64_t c, float (&h)[kVec<T>], bool last) {
         sums(c, h);
@@ -252,7 +249,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm_long(NormArgs a) {
     };
     uint32_t m = 0;
     if constexpr (Q8) {
-        if (!a.group) {
+        if (!a.group_log2) {
             for (int64_t j = 0; j < steps; ++j) {
                 float h[kVec<T>];
                 outputs(kVec<T> * (threadIdx.x + j * TEAM), h, false);
@@ -282,6 +279,7 @@ struct NormBackArgs {
     void* dx;
     float* part;          // [strips][d], the strips' sums of dy * xhat
     int64_t dy_stride, h_stride, dh_stride, rows, d, strip;
+    float len;            // d
 };
 
 // Lanes of a team that takes rows of up to d elements in the backward pass, one vector a lane as
@@ -370,7 +368,7 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
                 sum = fmaf(dy[j][i], h[j][i], sum);
             }
         }
-        const float mean = team_sum<TEAM>(sum, s_sum[k & 1][team % kRows]) / (float)a.d;
+        const float mean = team_sum<TEAM>(sum, s_sum[k & 1][team % kRows]) / a.len;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
@@ -449,7 +447,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm_backward_long(NormBackArgs a)
 #pragma unroll
         for (int i = 0; i < kVec<T>; ++i) sum = fmaf(dy[i], h[i], sum);
     }
-    const float mean = team_sum<TEAM>(sum, s_sum) / (float)a.d;
+    const float mean = team_sum<TEAM>(sum, s_sum) / a.len;
     for (int64_t j = 0; j < steps; ++j) {
         const int64_t c = kVec<T> * (threadIdx.x + j * TEAM);
         float h[kVec<T>], dy[kVec<T>], e[kVec<T>];
@@ -653,7 +651,9 @@ size_t norm_backward_workspace(int64_t rows, int64_t d) {
 
 det_status norm_launch(const NormCall& c, hipStream_t s) {
     const NormArgs a{c.x, c.residual, c.weight, c.h, c.y, c.scales, c.rstd, c.x_stride,
-                     c.residual_stride, c.rows, c.d, (int)c.group, c.eps};
+                     c.residual_stride, c.rows, c.d,
+                     c.group ? (c.d + c.group - 1) / c.group : 1,
+                     c.group ? __builtin_ctz((unsigned)c.group) : 0, (float)c.d, c.eps};
     switch (c.dtype) {
         case DET_F32: norm_typed<float>(a, c.codes, s); break;
         case DET_F16: norm_typed<_Float16>(a, c.codes, s); break;
@@ -665,7 +665,7 @@ det_status norm_launch(const NormCall& c, hipStream_t s) {
 det_status norm_backward_launch(const NormBackCall& c, void* ws, hipStream_t s) {
     const NormBackArgs a{c.dy, c.h, c.weight, c.dh, c.rstd, c.dx, static_cast<float*>(ws),
                          c.dy_stride, c.h_stride, c.dh_stride, c.rows, c.d,
-                         strip_rows(c.rows, c.d)};
+                         strip_rows(c.rows, c.d), (float)c.d};
     switch (c.dtype) {
         case DET_F32: return back_typed<float>(a, c.dweight, s);
         case DET_F16: return back_typed<_Float16>(a, c.dweight, s);
