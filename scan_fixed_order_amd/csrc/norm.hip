@@ -22,9 +22,10 @@ constexpr float kE4m3Max = 448.0f;
 constexpr float kTinyMax = 0x1p-100f;
 
 // A team of lanes per row, the row in registers between the sum and the output.  Teams by
-// measurement (norm_sized): 8192 x 8192 bf16 with codes 78 us with 512 lanes of two vectors, 122
-// with 1024 of one; 8192 x 5000 f16 55 us with 256 of three, 60 with 768 of one; 2048 x 16384 with
-// codes 46 us with 512 of four, 58 with 1024 of two.
+// measurement (norm_sized): 8192 x 8192 bf16 with codes 76 us with 512 lanes of two vectors, 122
+// with 1024 of one; 8192 x 2914 with codes 33 us with 256 of two, 39 with 512 of one, 37 with 128
+// of four, 48 with 64 of eight; 8192 x 5000 f16 55 us with 256 of three, 60 with 768 of one; 2048 x
+// 16384 with codes 46 us with 512 of four, 58 with 1024 of two.
 template <int TEAM>
 struct Team {
     static constexpr int kBlock = TEAM < 256 ? 256 : TEAM;
@@ -38,7 +39,7 @@ template <int TEAM>
 __device__ __forceinline__ float team_sum(float v, float* slots) {
     v = wave_pw(v);
     if constexpr (TEAM > 64) {
-        if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
+        if ((threadIdx.x & 63) == 0) slots[threadIdx.x % TEAM >> 6] = v;
         __syncthreads();
         v = slots[0];
 #pragma unroll
@@ -51,13 +52,24 @@ template <int TEAM>
 __device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t* slots) {
     v = wave_max(v);
     if constexpr (TEAM > 64) {
-        if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
+        if ((threadIdx.x & 63) == 0) slots[threadIdx.x % TEAM >> 6] = v;
         __syncthreads();
         v = slots[0];
 #pragma unroll
         for (int w = 1; w < TEAM / 64; ++w) v = umax(v, slots[w]);
     }
     return v;
+}
+
+// 1 / sqrt(x) within 2^-23: the hardware's estimate and a Newton step, a quarter of the
+// instructions of a rounded root and division, which every wave of a row runs.
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const bool tiny = x < 0x1p-100f;      // the estimate takes no subnormal numbers
+    const float s = tiny ? x * 0x1p100f : x;
+    const float r = __builtin_amdgcn_rsqf(s);
+    const float y = fmaf(0.5f * r, fmaf(-(s * r), r, 1.0f), r);
+    const float z = s > 0.0f && s < INFINITY ? y : r;      // 0, infinity and NaN need no step
+    return tiny ? z * 0x1p50f : z;
 }
 
 // Largest |y| of a vector as its bits: they order like the magnitudes, and a NaN's lie above
@@ -133,7 +145,7 @@ __device__ __forceinline__ void put(const NormArgs& a, int64_t row, int64_t c, i
 
 // One row per team, the row in registers: NV vectors a lane.  Bound by HBM: every element is
 // read once and written once.  8192 x 8192 bf16 with residual: 79 us (6.8 TB/s), with 8-bit codes
-// 78 us (6.0 TB/s); one row of 4096 2.4 us.  Rows that start off 16 bytes cost more: 8192 x 5001
+// 76 us (6.2 TB/s); one row of 4096 2.4 us.  Rows that start off 16 bytes cost more: 8192 x 5001
 // f16 64 us (5.1 TB/s), 8192 x 5000 55 us.
 template <typename T, int TEAM, int NV, bool RES, bool Q8, bool ONCE>
 __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
@@ -178,7 +190,7 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
         for (int i = 0; i < kVec<T>; ++i) sum = fmaf(h[j][i], h[j][i], sum);
     }
     sum = team_sum<TEAM>(sum, s_sum[team % kRows]);
-    const float rstd = 1.0f / sqrtf(sum / a.len + a.eps);
+    const float rstd = inv_sqrt(sum / a.len + a.eps);
     if (a.rstd && live && t == 0) a.rstd[row] = rstd;
 
     uint32_t m = 0;
@@ -234,7 +246,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm_long(NormArgs a) {
         for (int i = 0; i < kVec<T>; ++i) sum = fmaf(h[i], h[i], sum);
     }
     sum = team_sum<TEAM>(sum, s_sum);
-    const float rstd = 1.0f / sqrtf(sum / a.len + a.eps);
+    const float rstd = inv_sqrt(sum / a.len + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     const auto outputs = [&](int64_t c, float (&h)[kVec<T>], bool last) {
         sums(c, h);
@@ -282,9 +294,14 @@ struct NormBackArgs {
     float len;            // d
 };
 
-// Lanes of a team that takes rows of up to d elements in the backward pass, one vector a lane as
-// far as 1024 lanes go.
-constexpr int back_team(int64_t d) { return d <= 512 ? 64 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024; }
+// Lanes of a team that takes rows of up to d elements in the backward pass: one vector of 8 a lane
+// to 512 elements, then two (11093 rows without dh, f32: 518 elements 19 us, 31 with 256 lanes of
+// one; 2560 elements 65 us, 78 with 512 of one), 1024 lanes of one and two past 4096.
+constexpr int back_team(int64_t d) {
+    return d <= 1024 ? 64 : d <= 2048 ? 128 : d <= 4096 ? 256 : 1024;
+}
+// rows that a workgroup of such teams holds at a time
+constexpr int back_rows(int64_t d) { return back_team(d) < 256 ? 256 / back_team(d) : 1; }
 
 // One row's vectors of a lane as they lie in memory
 template <typename T, int NV>
@@ -295,15 +312,15 @@ struct BackRow {
 
 // A team walks its strip of rows and keeps the strip's column sums in registers; the next row's
 // loads are in flight while this one's sum goes round the team (two f32 vectors a lane leave no
-// registers for that).  With two vectors a lane the column sums are kept in LDS: 2048 rows of
-// 16384 bf16 take 58 us so, 98 with them in registers (spilled).  The teams of a workgroup join
+// registers for that).  With 1024 lanes of two vectors the column sums are kept in LDS: 2048 rows
+// of 16384 bf16 take 58 us so, 98 with them in registers (spilled).  The teams of a workgroup join
 // their sums.  Bound by HBM: 16384 x 4096 bf16 with dh 98 us with k_col_sums (5.5 TB/s), 116
 // without the loads ahead and past the caches.
 template <typename T, int TEAM, int NV, bool DH, bool ONCE>
 __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBackArgs a) {
     constexpr int kRows = Team<TEAM>::kRows, kWaves = Team<TEAM>::kWaves;
     constexpr int kElems = NV * kVec<T>;      // a lane's share of a row
-    constexpr bool kAhead = sizeof(T) == 2 || kElems <= 8, kLdsSums = kElems > 8;
+    constexpr bool kAhead = sizeof(T) == 2 || kElems <= 8, kLdsSums = kElems > 8 && TEAM == 1024;
     // kLdsSums: the lane's column sums, [vector][element][lane]
     extern __shared__ float s_cols[];
     __shared__ float s_sum[2][kRows][kWaves];
@@ -534,7 +551,7 @@ int64_t strip_rows(int64_t rows, int64_t d) {
 // strips whose sums reach k_col_sums
 int64_t strip_sums(int64_t rows, int64_t d, int64_t strip) {
     const int64_t strips = (rows + strip - 1) / strip;
-    return d <= 512 ? (strips + Team<64>::kRows - 1) / Team<64>::kRows : strips;
+    return (strips + back_rows(d) - 1) / back_rows(d);
 }
 
 // workgroups a launch starts at most (a grid holds fewer than 2^32 threads); each walks the rows
@@ -563,7 +580,7 @@ void norm_sized(const NormArgs& a, hipStream_t s) {
     } else if (a.d <= 2048) {
         norm_in_regs<T, 256, 1, RES, Q8>(a, s);
     } else if (a.d <= 4096) {
-        norm_in_regs<T, 512, 1, RES, Q8>(a, s);
+        norm_in_regs<T, 256, 2, RES, Q8>(a, s);
     } else if (a.d <= 6144) {
         norm_in_regs<T, 256, 3, RES, Q8>(a, s);
     } else if (a.d <= 8192) {
@@ -594,7 +611,7 @@ void norm_typed(const NormArgs& a, bool q8, hipStream_t s) {
 template <typename T, int NV, int TEAM, bool DH>
 void back_in_regs(const NormBackArgs& a, int64_t wgs, hipStream_t s) {
     const dim3 grid((unsigned)wgs), block(Team<TEAM>::kBlock);
-    const int lds = NV > 1 ? TEAM * NV * 8 * 4 : 0;      // NV vectors of 8 (f32: twice as many of 4)
+    const int lds = NV > 1 && TEAM == 1024 ? TEAM * NV * 8 * 4 : 0;      // NV vectors of 8 (f32: twice as many of 4)
     KernelTimer kt("k_rms_norm_backward", s);
     if ((size_t)a.rows * a.d * sizeof(T) * (DH ? 3 : 2) >= kOnceBytes)
         k_rms_norm_backward<T, TEAM, NV * 8 / kVec<T>, DH, true><<<grid, block, lds, s>>>(a);
@@ -606,10 +623,12 @@ template <typename T, bool DH>
 void back_sized(const NormBackArgs& a, int64_t sums, hipStream_t s) {
     if (a.d <= 512) {
         back_in_regs<T, 1, back_team(512), DH>(a, sums, s);
+    } else if (a.d <= 1024) {
+        back_in_regs<T, 2, back_team(1024), DH>(a, sums, s);
     } else if (a.d <= 2048) {
-        back_in_regs<T, 1, back_team(2048), DH>(a, sums, s);
+        back_in_regs<T, 2, back_team(2048), DH>(a, sums, s);
     } else if (a.d <= 4096) {
-        back_in_regs<T, 1, back_team(4096), DH>(a, sums, s);
+        back_in_regs<T, 2, back_team(4096), DH>(a, sums, s);
     } else if (a.d <= 8192) {
         back_in_regs<T, 1, back_team(8192), DH>(a, sums, s);
     } else if (a.d <= kRowInRegs) {
