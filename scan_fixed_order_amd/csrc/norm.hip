@@ -355,11 +355,13 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
             if constexpr (kLdsSums) s_cols[(j * kVec<T> + i) * TEAM + t] = 0.0f;
         }
     }
-    // every team of the workgroup takes the same number of steps (barriers)
-    for (int64_t k = 0; k < a.strip; ++k) {
+    // every team of the workgroup takes the steps of the first one (barriers)
+    const int64_t rest = a.rows - (int64_t)blockIdx.x * kRows * a.strip;
+    const int64_t steps = rest < a.strip ? rest : a.strip;
+    for (int64_t k = 0; k < steps; ++k) {
         const bool live = begin + k < a.rows;
         if constexpr (kAhead) {
-            if (k + 1 < a.strip) read(begin + k + 1, next);
+            if (k + 1 < steps) read(begin + k + 1, next);
         }
         const float rstd = cur.rstd;
         float h[NV][kVec<T>], dy[NV][kVec<T>];
@@ -404,7 +406,7 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm_backward(NormBa
         }
         if constexpr (kAhead)
             cur = next;
-        else if (k + 1 < a.strip)
+        else if (k + 1 < steps)
             read(begin + k + 1, cur);
     }
     if constexpr (kRows > 1) {
