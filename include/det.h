@@ -273,8 +273,8 @@ size_t det_rms_norm_backward_workspace_size(int64_t rows, int64_t d, det_dtype d
  * dh:       NULL, or the gradient that reaches h from elsewhere, dh_stride apart.
  * dx:       [rows * d]; may be dy, h or dh itself where that is contiguous and d <= 16384.
  * dweight:  [d], written (zero for no rows).
- * Order: a row's sum fixed by (d, dtype); dweight's by (rows, d): strips of rows in ascending
- * order, then the strips. */
+ * Order: a row's sum fixed by (d, dtype); dweight's by (rows, d, dtype): strips of rows in
+ * ascending order, then the strips. */
 det_status det_rms_norm_backward(const void* dy, int64_t dy_stride, const void* h,
                                  int64_t h_stride, const void* weight, const float* rstd,
                                  const void* dh, int64_t dh_stride, int64_t rows, int64_t d,

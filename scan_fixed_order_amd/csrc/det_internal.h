@@ -103,7 +103,7 @@ struct NormBackCall {
     int64_t dy_stride, h_stride, dh_stride, rows, d;
     det_dtype dtype;
 };
-size_t norm_backward_workspace(int64_t rows, int64_t d);
+size_t norm_backward_workspace(int64_t rows, int64_t d, det_dtype dtype);
 det_status norm_backward_launch(const NormBackCall& c, void* ws, hipStream_t s);
 
 constexpr int kBiasMaxSide = 128;      // buckets of one side of the relative position bias

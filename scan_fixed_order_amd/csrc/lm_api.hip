@@ -92,7 +92,7 @@ det_status det_rms_norm(const void* x, int64_t x_stride, const void* residual,
 
 size_t det_rms_norm_backward_workspace_size(int64_t rows, int64_t d, det_dtype dtype) {
     if (rows < 0 || rows > DET_MAX_N || d < 0 || d > DET_MAX_N || !lm_dtype(dtype)) return 0;
-    return norm_backward_workspace(rows, d);
+    return norm_backward_workspace(rows, d, dtype);
 }
 
 det_status det_rms_norm_backward(const void* dy, int64_t dy_stride, const void* h,
@@ -123,7 +123,7 @@ det_status det_rms_norm_backward(const void* dy, int64_t dy_stride, const void* 
             if (r->p && !apart(dweight, wbytes, *r)) return DET_ERROR_INVALID_VALUE;
         if (overlap(weight, wbytes, dweight, wbytes)) return DET_ERROR_INVALID_VALUE;
     }
-    const det_status st = ws_status(ws, ws_bytes, norm_backward_workspace(rows, d));
+    const det_status st = ws_status(ws, ws_bytes, norm_backward_workspace(rows, d, dtype));
     if (st != DET_SUCCESS) return st;
     const NormBackCall c{dy, h, weight, dh, rstd, dx, dweight, dy_stride, h_stride, dh_stride,
                          rows, d, dtype};
