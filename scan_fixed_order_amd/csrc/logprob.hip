@@ -207,10 +207,8 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
         }
         m = umax(m, xor_partner<1>(m));
         m = umax(m, xor_partner<2>(m));
-        if constexpr (kParts == 16) {
-            m = umax(m, xor_partner<4>(m));
-            m = umax(m, xor_partner<8>(m));
-        }
+        if constexpr (kParts >= 8) m = umax(m, xor_partner<4>(m));
+        if constexpr (kParts >= 16) m = umax(m, xor_partner<8>(m));
         if (part == 0) s.super[sg] = m;
         if (threadIdx.x == 0) s.picks = s.cands = 0;
     }
@@ -226,10 +224,8 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
         }
         rank += xor_partner<1>(rank);
         rank += xor_partner<2>(rank);
-        if constexpr (kParts == 16) {
-            rank += xor_partner<4>(rank);
-            rank += xor_partner<8>(rank);
-        }
+        if constexpr (kParts >= 8) rank += xor_partner<4>(rank);
+        if constexpr (kParts >= 16) rank += xor_partner<8>(rank);
         // 0: a super-group behind the row's end, so that every logit counts
         if (part == 0 && (int)rank == a.top - 1) s.bound = umax(mine, 1u);
     }
@@ -293,8 +289,8 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
     __syncthreads();      // s_key and s are written again
 }
 
-// One row per workgroup, each logit read once; 1024 threads for few rows, where a compute unit's
-// vector rate bounds (about 17 logits a nanosecond), 256 for many.  2048 x 131072 bf16: 88 us
+// One row per workgroup, each logit read once; 1024 or 512 threads for few rows, where a compute
+// unit's vector rate bounds (about 17 logits a nanosecond), 256 for many.  2048 x 131072 bf16: 88 us
 // (6.1 TB/s, bound by HBM), with 5 alternatives 96 us (5.6 TB/s: 10 vector instructions and an
 // exponential a logit fill the vector units, and a row's search runs for 2 us).  256 x 131072 with
 // 5 alternatives 16.7 us with 1024 threads a row; 300 rows 31 us with 256.
@@ -468,16 +464,18 @@ bool once(int64_t rows, int64_t vocab) {
     return (double)rows * (double)vocab * sizeof(T) >= (double)kOnceBytes;
 }
 
-// Up to a workgroup a compute unit, 1024 threads: 256 x 131072 bf16 with 5 alternatives 16.5 us
-// against 28 with 256 threads; 700 rows 47 us with 1024, 42 with 256.  (The order is the same.)
+// Threads for the rows at hand, as many as still leave each row a place on the 256 units (the order
+// is the same): 256 x 131072 bf16 with 5 alternatives 16.5 us with 1024, 28 with 256; 512 rows 29
+// with 512, 38 with 256; 700 rows 45 with 512, 42 with 256.
 template <typename T>
 void logp_typed(const LogpArgs& a, hipStream_t s) {
-    if (a.rows <= 256 && a.vocab > kTile<T>)
+    const bool wide = a.vocab > kTile<T>, past = once<T>(a.rows, a.vocab);
+    if (wide && a.rows <= 256)
         logp_block<T, 1024, false>(a, s);
-    else if (once<T>(a.rows, a.vocab))
-        logp_block<T, 256, true>(a, s);
+    else if (wide && a.rows <= 512)
+        past ? logp_block<T, 512, true>(a, s) : logp_block<T, 512, false>(a, s);
     else
-        logp_block<T, 256, false>(a, s);
+        past ? logp_block<T, 256, true>(a, s) : logp_block<T, 256, false>(a, s);
 }
 
 template <typename T>

@@ -160,6 +160,17 @@ def test_rows_views_and_launches_keep_their_bits(dev, vocab, t):
     assert all(same_bits(a, b) for a, b in zip(want, other))
 
 
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("vocab", [9001, 40000])
+def test_workgroups_of_every_size_keep_the_bits(dev, vocab, t):
+    x, at = inputs(600, vocab, t, dev, 20)
+    want = det.det_token_logprobs(x, at, 0.8, 20)
+    check(x, at, 0.8, want, 20)
+    for a, b in ((0, 100), (40, 420), (599, 600)):
+        part = det.det_token_logprobs(x[a:b], at[a:b], 0.8, 20)
+        assert all(same_bits(p, w[a:b].contiguous()) for p, w in zip(part, want))
+
+
 def test_rows_past_32_bit_offsets(dev):
     vocab, far = 5000, (1 << 32) + 24
     buf = torch.empty(far + vocab, dtype=torch.bfloat16, device=dev)
