@@ -145,7 +145,7 @@ __device__ __forceinline__ void put(const NormArgs& a, int64_t row, int64_t c, i
 
 // One row per team, the row in registers: NV vectors a lane.  Bound by HBM: every element is
 // read once and written once.  8192 x 8192 bf16 with residual: 79 us (6.8 TB/s), with 8-bit codes
-// 76 us (6.2 TB/s); one row of 4096 2.4 us.  Rows that start off 16 bytes cost more: 8192 x 5001
+// 76 us (6.2 TB/s); one row of 4096 2.6 us.  Rows that start off 16 bytes cost more: 8192 x 5001
 // f16 64 us (5.1 TB/s), 8192 x 5000 55 us.
 template <typename T, int TEAM, int NV, bool RES, bool Q8, bool ONCE>
 __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_rms_norm(NormArgs a) {
