@@ -109,8 +109,11 @@ using Guard = c10::DeviceGuard;
 
 void* stream(const Tensor& t) { return c10::hip::getCurrentHIPStream(t.get_device()).stream(); }
 
-void rows_of(const Tensor& t, const char* what) {
+// Number of rows (the last dimension is a row).  From the leading dimensions, not numel(): rows of
+// no elements are rows, and the library refuses them.
+int64_t rows_of(const Tensor& t, const char* what) {
     if (t.dim() < 1) wrong_value(std::string(what) + " must have at least one dimension");
+    return c10::multiply_integers(t.sizes().slice(0, t.dim() - 1));
 }
 
 // ---------------------------------------------------------------- norm
@@ -118,8 +121,7 @@ void rows_of(const Tensor& t, const char* what) {
 py::tuple rms_norm(const Tensor& x, const Tensor& weight, double eps, const Optional& residual,
                    bool codes, int64_t group) {
     const det_dtype type = lm_type(x);
-    rows_of(x, "x");
-    const int64_t d = x.size(-1), rows = d ? x.numel() / d : 0;
+    const int64_t rows = rows_of(x, "x"), d = x.size(-1);
     const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
     of(weight, x.scalar_type(), {d}, "weight");
     const int64_t stride = row_stride(x, "x");
@@ -161,8 +163,7 @@ py::tuple rms_norm(const Tensor& x, const Tensor& weight, double eps, const Opti
 py::tuple rms_norm_backward(const Tensor& dy, const Tensor& h, const Tensor& weight,
                             const Tensor& rstd, const Optional& dh, const Optional& ws) {
     const det_dtype type = lm_type(h);
-    rows_of(h, "h");
-    const int64_t d = h.size(-1), rows = d ? h.numel() / d : 0;
+    const int64_t rows = rows_of(h, "h"), d = h.size(-1);
     of(weight, h.scalar_type(), {d}, "weight");
     of(rstd, at::kFloat, h.sizes().slice(0, h.dim() - 1), "rstd");
     same_type(dy, h, "dy");
@@ -308,9 +309,8 @@ Tensor token_logprobs_backward(const Tensor& logits, const Tensor& targets, cons
                                const Tensor& dlogp, const Optional& entropy,
                                const Optional& dentropy, double scale, const Optional& out) {
     const det_dtype type = lm_type(logits);
-    rows_of(logits, "logits");
+    const int64_t rows = rows_of(logits, "logits"), vocab = logits.size(-1);
     const at::IntArrayRef shape = logits.sizes().slice(0, logits.dim() - 1);
-    const int64_t vocab = logits.size(-1);
     of(targets, at::kLong, shape, "targets");
     of(lse, at::kFloat, shape, "lse");
     of(dlogp, at::kFloat, shape, "dlogp");
@@ -335,7 +335,7 @@ Tensor token_logprobs_backward(const Tensor& logits, const Tensor& targets, cons
     check_status(det_token_logprobs_backward(
                      xp, stride, static_cast<const int64_t*>(tp), static_cast<const float*>(lp),
                      static_cast<const float*>(dp), static_cast<const float*>(ep),
-                     static_cast<const float*>(dep), targets.numel(), vocab, type, scale,
+                     static_cast<const float*>(dep), rows, vocab, type, scale,
                      pointer(o, logits), row_stride(o, "out"), stream(logits)),
                  "det_token_logprobs_backward");
     return o;
