@@ -403,10 +403,66 @@ struct LogpBackArgs {
 
 constexpr int kBackTile = 8192;                           // elements a workgroup takes at a time
 
-// Each logit read once, each gradient written once; nothing is summed.  A lane's loads are all
-// on their way before its first value is used.  Bound by HBM: 4096 x 65536 bf16 176 us (6.1 TB/s;
-// 190 with a branch between whole and partial vectors at each load), 517 x 50021 f32 with the
-// forward pass 65 us (4.8 TB/s; rows there start off 16 bytes), 69 with it.
+// lse is a float: beyond this its rounding moves every p = exp(z - lse) by more than 2^-16, and in a
+// row of the type's lowest values nothing of log(sum) is left in it.  Such a row's sum is taken again.
+constexpr float kFarLse = 256.0f;
+
+// What a row's gradient takes besides its logits
+struct BackTerms {
+    int64_t target;               // -1: not scored
+    float dlogp, dent, both;      // both = dlogp + dentropy * entropy
+};
+
+__device__ __forceinline__ float logit_gradient(float log, const BackTerms& r, bool hit) {
+    const float p = exp_fast(log);
+    // below -1000 p is 0 and -inf must not meet it
+    const float d = -p * fmaf(r.dent, fmaxf(log, -1000.0f), r.both);
+    return hit ? d + r.dlogp : d;
+}
+
+// A row whose lse is far from zero, by one workgroup: its maximum, its sum against that, and only
+// then the gradient (which may replace the logits).  Order of the sum: a lane's vectors, the
+// adjacent-lanes tree, the four waves.
+template <typename T>
+__device__ void far_row(const LogpBackArgs& a, const T* x, T* out, const BackTerms& r) {
+    __shared__ float s_max[4], s_sum[4];
+    const int wave = threadIdx.x >> 6;
+    float v[kVec<T>], top = -INFINITY;
+    for (int64_t c = kVec<T> * threadIdx.x; c < a.vocab; c += 256 * kVec<T>) {
+        read_vec(x + c, a.vocab - c, -INFINITY, v);
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) top = fmaxf(top, v[i]);
+    }
+    top = wave_max(top);
+    if ((threadIdx.x & 63) == 0) s_max[wave] = top;
+    __syncthreads();
+    const float m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3])) * a.scale;
+    float sum = 0.0f;
+    for (int64_t c = kVec<T> * threadIdx.x; c < a.vocab; c += 256 * kVec<T>) {
+        read_vec(x + c, a.vocab - c, -INFINITY, v);
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) sum += exp_fast(fmaf(v[i], a.scale, -m));
+    }
+    sum = wave_pw(sum);
+    if ((threadIdx.x & 63) == 0) s_sum[wave] = sum;
+    __syncthreads();
+    const float log_s = logf(((s_sum[0] + s_sum[1]) + s_sum[2]) + s_sum[3]);
+    for (int64_t c = kVec<T> * threadIdx.x; c < a.vocab; c += 256 * kVec<T>) {
+        read_vec(x + c, a.vocab - c, -INFINITY, v);
+        const int64_t hit = r.target - c;
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i)
+            v[i] = logit_gradient(fmaf(v[i], a.scale, -m) - log_s, r, i == hit) * a.scale;
+        write_vec(out + c, a.vocab - c, v);
+    }
+    __syncthreads();      // the LDS slots are written again
+}
+
+// Each logit read once, each gradient written once; nothing is summed (but in far_row).  A lane's
+// loads are all on their way before its first value is used.  Bound by HBM: 4096 x 65536 bf16 180
+// us (6.0 TB/s; 176 without far rows, 182 with them told apart before the loads, 189 after; 190
+// with a branch between whole and partial vectors at each load), 517 x 50021 f32 with the forward
+// pass 65 us (4.8 TB/s; rows there start off 16 bytes), 69 with such a branch.
 template <typename T, bool ONCE>
 __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a) {
     for (int64_t tile = blockIdx.x; tile < a.rows * a.tiles; tile += gridDim.x) {
@@ -416,10 +472,13 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a)
         const float lse = a.lse[row];
         const int64_t at = a.targets[row];
         const bool scored = at >= 0 && at < a.vocab;
-        const float dlogp = scored ? a.dlogp[row] : 0.0f;
-        const float dent = a.dentropy ? a.dentropy[row] : 0.0f;
-        const float both = a.dentropy ? fmaf(dent, a.entropy[row], dlogp) : dlogp;
-        const bool none = lse == -INFINITY;
+        BackTerms r;
+        r.target = scored ? at : -1;
+        r.dlogp = scored ? a.dlogp[row] : 0.0f;
+        r.dent = a.dentropy ? a.dentropy[row] : 0.0f;
+        r.both = a.dentropy ? fmaf(r.dent, a.entropy[row], r.dlogp) : r.dlogp;
+        const bool none = lse == -INFINITY, far = fabsf(lse) > kFarLse && fabsf(lse) < INFINITY;
+        const int64_t end = far ? 0 : a.vocab;      // far rows come below
         constexpr int kVecs = kBackTile / (256 * kVec<T>);
         u32x4 raw[kVecs];
 #pragma unroll
@@ -427,22 +486,19 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a)
             raw[j] = load_row<ONCE>(x, c0 + kVec<T> * (threadIdx.x + 256 * j), a.vocab);
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int64_t c = c0 + kVec<T> * (threadIdx.x + 256 * j), n = a.vocab - c;
+            const int64_t c = c0 + kVec<T> * (threadIdx.x + 256 * j), n = end - c;
             float v[kVec<T>];
             unpack<T>(settle<T>(raw[j], c, a.vocab), v);
             if (n <= 0) continue;
-            const int64_t hit = scored ? at - c : -1;
+            const int64_t hit = r.target - c;
 #pragma unroll
             for (int i = 0; i < kVec<T>; ++i) {
-                const float log = fmaf(v[i], a.scale, -lse);
-                const float p = exp_fast(log);
-                // below -1000 p is 0 and -inf must not meet it
-                float d = -p * fmaf(dent, fmaxf(log, -1000.0f), both);
-                if (i == hit) d += dlogp;
+                const float d = logit_gradient(fmaf(v[i], a.scale, -lse), r, i == hit);
                 v[i] = none ? 0.0f : d * a.scale;
             }
             write_vec(out + c, n, v);
         }
+        if (far && c0 == 0) far_row<T>(a, x, out, r);
     }
 }
 

@@ -1,10 +1,12 @@
 """Edges of the language-model operators on the GPU: rows of no elements, values at the ends of
 their types, sizes at the ends of a launch."""
+import math
 
 import pytest
 import torch
 
-from lm_reference import IDS, TYPES
+import lm_reference as ref
+from lm_reference import IDS, TYPES, U32, floor_of, half, randn, same_bits
 from scan_fixed_order_amd import det
 
 pytestmark = pytest.mark.gpu
@@ -24,3 +26,65 @@ def test_rows_of_no_elements_are_refused(dev, t):
     # no rows at all are no error
     none = det.det_rms_norm(torch.empty(0, 0, dtype=t, device=dev), w, quant=E4M3)
     assert none.y.shape == (0, 0) and none.rstd.shape == (0,) and none.scales.shape == (0, 1)
+
+
+# ------------------------------------------------------------------ rows far from zero
+
+def gradient_bound(x, at, scale, dlogp, dentropy, want, t):
+    """Against the gradient of the logits alone (no lse handed in): log p is off by its own
+    roundings and by the sum's relative error `rel` (chains of vocab / 256 terms and more, each
+    term off by 2 U (1 + |z - max|)), or by the rounding of an lse of at most 256."""
+    _, entropy, lse, log = ref.logprobs(x, at, scale)
+    p, size = log.exp(), torch.where(log > -math.inf, log.abs(), 0.0)
+    far = (p * size).sum(-1, keepdim=True) + 8
+    rel = U32 * (40 + x.shape[-1] / 256 + 4 * far + lse.abs().clamp_max(256.0)[:, None])
+    d, e = dlogp.double().abs()[:, None], dentropy.double().abs()[:, None]
+    hit = torch.zeros_like(p).scatter_(1, at.clamp_min(0)[:, None], 1.0)
+    parts = d * (hit + p) + e * p * (size + entropy[:, None])
+    bound = ((8 + 4 * size) * U32 + rel) * parts + e * p * rel * (2 + far)
+    bound += 2.0 ** -126 * (d + e + 1) * (1 + size.clamp_max(200.0))
+    return bound * scale + half(t) * want.abs() * 1.001 + floor_of(t)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("vocab", [5, 1000, 9001, 20003])
+@pytest.mark.parametrize("scale", [1.0, 0.5])
+def test_gradient_of_rows_far_from_zero(dev, vocab, t, scale):
+    """lse is a float, and log(sum) is lost in it where the logits are large: in a row of the type's
+    lowest values (a mask that leaves nothing) altogether."""
+    low = torch.finfo(t).min
+    x = randn((9, vocab), torch.float32, dev, 31, 2.0)
+    for i, off in enumerate((0.0, 200.0, -300.0, 700.0, -6000.0, 50000.0)):
+        x[i] += off
+    x = x.to(t)
+    x[6] = low
+    x[7, vocab // 2:] = low
+    x[8] = low
+    x[8, 1] = -math.inf
+    x[3, ::2] = -math.inf
+    at = torch.arange(9, device=dev) % vocab
+    at[5] = -100
+    dlogp, dent = randn((9,), torch.float32, dev, 32), randn((9,), torch.float32, dev, 33)
+    dlogp_in = torch.where(at >= 0, dlogp, 0.0)
+    f = det.det_token_logprobs(x, at, scale)
+    got = det.det_token_logprobs_backward(x, at, f.lse, dlogp, f.entropy, dent, scale)
+    _, entropy, _, log = ref.logprobs(x, at, scale)
+    want = ref.logprobs_backward(log, at, entropy, dlogp, dent, scale)
+    assert ((got.double() - want).abs()
+            <= gradient_bound(x, at, scale, dlogp_in, dent, want, t)).all()
+    # each row alone, in place, and among padded columns: the same bits
+    for i in range(9):
+        one = det.det_token_logprobs_backward(x[i:i + 1], at[i:i + 1], f.lse[i:i + 1],
+                                              dlogp[i:i + 1], f.entropy[i:i + 1], dent[i:i + 1], scale)
+        assert same_bits(one, got[i:i + 1])
+    again = x.clone()
+    det.det_token_logprobs_backward(again, at, f.lse, dlogp, f.entropy, dent, scale, out=again)
+    assert same_bits(again, got)
+    wide = torch.zeros(9, vocab + 5, dtype=t, device=dev)
+    wide[:, 2:vocab + 2] = x
+    assert same_bits(det.det_token_logprobs_backward(wide[:, 2:vocab + 2], at, f.lse, dlogp,
+                                                     f.entropy, dent, scale), got)
+    v = x.clone().requires_grad_(True)
+    logp, ent = det.token_logprobs(v, at, scale)
+    ((logp * dlogp).sum() + (ent * dent).sum()).backward()
+    assert same_bits(v.grad, got)
