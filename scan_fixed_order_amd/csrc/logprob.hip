@@ -34,7 +34,8 @@ constexpr int kShort = 512;               // candidates of the short way to the 
 constexpr float kSlack = 8.0f;
 constexpr float kFar = -1e30f;            // differences of references stop here (never -inf)
 
-// the largest of three; a quiet NaN loses
+// the largest of three; a quiet NaN loses (a signalling one takes what it was compared with along:
+// the instruction answers it with a quiet NaN, which the next comparison drops)
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
@@ -178,8 +179,19 @@ __device__ __forceinline__ void gather_candidates(const LogpArgs& a, const T* x,
     }
 }
 
-// The `top` largest logits of a row.  On entry s_key holds every group's largest logit; they are
-// replaced by their order keys (0 behind the last group), in 64 super-groups of super_len groups.
+// largest key of a group's logits, one by one
+template <typename T>
+__device__ __forceinline__ uint32_t group_key(const LogpArgs& a, const T* x, int group) {
+    const int64_t first = (int64_t)group * kGroup, n = a.vocab - first;
+    uint32_t k = 0;
+#pragma unroll 1
+    for (int i = 0; i < kGroup && i < n; ++i) k = umax(k, order_key((float)x[first + i]));
+    return k;
+}
+
+// The `top` largest logits of a row.  On entry s_key holds every group's largest logit, which are
+// not to be trusted where the row holds a NaN (`suspect`); they are replaced by their order keys (0
+// behind the last group), in 64 super-groups of super_len groups.
 //
 // The top-th largest of the super-groups' maxima is a bound that at least `top` logits reach, and
 // few more do in most rows: these are ranked against each other.  Where too many reach it (long
@@ -189,7 +201,7 @@ __device__ __forceinline__ void gather_candidates(const LogpArgs& a, const T* x,
 // others.
 template <typename T, int BLOCK>
 __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s_key, Search& s,
-                         float ref, float log_s) {
+                         float ref, float log_s, bool suspect) {
     const int groups = (int)((a.vocab + kGroup - 1) / kGroup);
     const int len = (int)super_len(a.vocab);
     const int lane = threadIdx.x & 63;
@@ -201,7 +213,9 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
 #pragma unroll 4
         for (int i = part; i < len; i += kParts) {
             const int at = sg * len + i;
-            const uint32_t k = at < groups ? order_key(__uint_as_float(s_key[at])) : 0;
+            const uint32_t k = at >= groups ? 0
+                               : suspect    ? group_key(a, x, at)
+                                            : order_key(__uint_as_float(s_key[at]));
             s_key[at] = k;
             m = umax(m, k);
         }
@@ -386,7 +400,8 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
             a.logp[row] = !scored ? 0.0f : none ? -INFINITY : fmaf(picked, a.scale, -ref) - log_s;
         }
         if constexpr (TOP)
-            pick_top<T, BLOCK>(a, row, x, s_key, s_search, none ? 0.0f : ref, none ? 0.0f : log_s);
+            pick_top<T, BLOCK>(a, row, x, s_key, s_search, none ? 0.0f : ref, none ? 0.0f : log_s,
+                               s != s);
     }
 }
 

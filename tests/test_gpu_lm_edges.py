@@ -88,3 +88,36 @@ def test_gradient_of_rows_far_from_zero(dev, vocab, t, scale):
     logp, ent = det.token_logprobs(v, at, scale)
     ((logp * dlogp).sum() + (ent * dent).sum()).backward()
     assert same_bits(v.grad, got)
+
+
+# ------------------------------------------------------------------ not a number
+
+NANS = {torch.float32: (torch.int32, (0x7F800001, 0x7FA00000, 0x7FC00000, -0x7FFFFF, -1)),
+        torch.float16: (torch.int16, (0x7C01, 0x7D00, 0x7E00, -0x3FF, -1)),
+        torch.bfloat16: (torch.int16, (0x7F81, 0x7FA0, 0x7FC0, -0x7F, -1))}
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("rows,vocab", [(3, 70), (8, 9001), (300, 9001), (600, 9001), (4, 40000)])
+def test_alternatives_beside_a_signalling_nan(dev, rows, vocab, t):
+    """Every kind of NaN counts as -inf among the alternatives, wherever it stands beside the best."""
+    kind, bits = NANS[t]
+    x = randn((rows, vocab), torch.float32, dev, 41).to(t)
+    best = torch.randint(0, vocab, (rows,), generator=torch.Generator().manual_seed(1))
+    for i in range(rows):
+        x[i, best[i]] = 40.0
+    raw = x.view(kind)
+    for i in range(rows):
+        for j, step in enumerate((-31, -9, -4, -1, 1, 2, 3, 7, 16)[:5 + i % 5]):
+            p = int(best[i]) + step
+            if 0 <= p < vocab:
+                raw[i, p] = bits[(i + j) % len(bits)]
+    raw[0] = bits[0]                                  # nothing else at all
+    raw[1, ::2] = bits[1]
+    nan = x.isnan()
+    assert nan[0].all() and nan.any(1).all()
+    at = torch.zeros(rows, dtype=torch.int64, device=dev)
+    got = det.det_token_logprobs(x, at, top=20)
+    want = ref.top_ids(torch.where(nan, -math.inf, x.double()), 20)
+    assert torch.equal(got.top_ids, want)
+    assert got.lse.isnan().all() and got.logp.isnan().all() and got.entropy.isnan().all()
