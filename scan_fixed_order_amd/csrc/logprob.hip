@@ -6,7 +6,7 @@
 //   entropy = -sum p log p, p = exp(z - lse);  top: the largest logits, ties to the lower index;
 //   dlogits = scale * (dlogp (hit - p) - dentropy * p * (log p + entropy)).
 // One pass forward: s = sum exp(z - ref) and w = sum exp(z - ref) (z - ref) against a running
-// reference give lse = ref + log s and entropy = log s - w / s.  A term whose p is 0 adds 0 to
+// maximum give lse = ref + log s and entropy = log s - w / s.  A term whose p is 0 adds 0 to
 // the entropy also where its logit is -inf.  A row without any mass (all logits -inf) has
 // lse = -inf, entropy 0, logp -inf and gradient 0.
 //
@@ -28,10 +28,6 @@ template <typename T>
 constexpr int kTile = kLanes * kVec<T>;   // elements they take at a time
 constexpr int kGroup = 32;                // neighbouring elements whose largest is kept for top
 constexpr int kShort = 512;               // candidates of the short way to the top
-// A lane's reference is one of its own values, replaced when a value exceeds it by more than
-// this: sums against it stay far from overflow, terms are off by at most the rounding of a
-// difference of that size, and a lane rarely rescales.
-constexpr float kSlack = 8.0f;
 constexpr float kFar = -1e30f;            // differences of references stop here (never -inf)
 
 // the largest of three; a quiet NaN loses (a signalling one takes what it was compared with along:
@@ -62,7 +58,10 @@ struct LogpArgs {
     float scale, unscale;      // unscale = 1 / scale
 };
 
-// One lane's running sums against its reference
+// One lane's running sums against its reference, the largest of its values so far.  (A reference
+// that values may pass by 8 spares most lanes the rescaling, 98 us instead of 101 on 2048 x 131072
+// bf16 with alternatives, but then log(sum) and the target cancel in a row of one likely token: its
+// log probability was off by 20 times 2^-24, where 1.4 times is what a float sum costs.)
 struct Part {
     float ref, s, w;
 };
@@ -83,14 +82,14 @@ __device__ __forceinline__ float sum16(float v) {
     return v + xor_partner<8>(v);
 }
 
-// adds a vector of N logits; `largest`: their maximum (NaN ignored); `limit`: the logit that passes the
-// reference by kSlack
+// adds a vector of N logits; `largest`: their maximum (NaN ignored); `limit`: the logit behind the
+// reference
 template <int N>
 __device__ __forceinline__ void take(Part& p, float& limit, const float (&x)[N], float largest,
-                                     float scale, float unscale) {
+                                     float scale) {
     if (largest > limit) {
         rebase(p, largest * scale);
-        limit = (p.ref + kSlack) * unscale;
+        limit = largest;
     }
     float e[N], d[N];
 #pragma unroll
@@ -304,8 +303,8 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
 }
 
 // One row per workgroup, each logit read once; 1024 or 512 threads for few rows, where a compute
-// unit's vector rate bounds (about 17 logits a nanosecond), 256 for many.  2048 x 131072 bf16: 88 us
-// (6.1 TB/s, bound by HBM), with 5 alternatives 96 us (5.6 TB/s: 10 vector instructions and an
+// unit's vector rate bounds (about 17 logits a nanosecond), 256 for many.  2048 x 131072 bf16: 90 us
+// (5.9 TB/s, bound by HBM), with 5 alternatives 101 us (5.3 TB/s: 10 vector instructions and an
 // exponential a logit fill the vector units, and a row's search runs for 2 us).  256 x 131072 with
 // 5 alternatives 16.7 us with 1024 threads a row; 300 rows 31 us with 256.
 template <typename T, int BLOCK, bool TOP, bool ONCE>
@@ -327,7 +326,7 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
 #pragma unroll
         for (int u = 0; u < kSets; ++u) {
             p[u] = Part{-FLT_MAX, 0.0f, 0.0f};
-            limit[u] = -FLT_MAX * a.unscale;
+            limit[u] = -FLT_MAX * a.unscale;      // below it z overflows
         }
         const auto one = [&](int64_t c, int u, const float(&v)[kVec<T>], bool keep) {
             const float largest = largest_of(v);
@@ -343,7 +342,7 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
                 }
                 if (keep && lane % (kGroup / kVec<T>) == 0) s_key[c / kGroup] = __float_as_uint(g);
             }
-            if (keep) take(p[u], limit[u], v, largest, a.scale, a.unscale);
+            if (keep) take(p[u], limit[u], v, largest, a.scale);
         };
         const int64_t whole = a.vocab / (kTile<T> * kSteps);
         for (int64_t i = 0; i < whole; ++i) {

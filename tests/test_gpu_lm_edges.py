@@ -121,3 +121,31 @@ def test_alternatives_beside_a_signalling_nan(dev, rows, vocab, t):
     want = ref.top_ids(torch.where(nan, -math.inf, x.double()), 20)
     assert torch.equal(got.top_ids, want)
     assert got.lse.isnan().all() and got.logp.isnan().all() and got.entropy.isnan().all()
+
+
+# ------------------------------------------------------------------ rows of one likely token
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("first,second", [(0, 40960), (40960, 0), (3, 9), (17, 700), (4999, 33)])
+@pytest.mark.parametrize("top", [0, 2])
+def test_likely_tokens_keep_their_digits(dev, first, second, top, t):
+    """Two tokens, `gap` apart: s = 1 + r with r = exp(-gap).  r is off by (2 gap + 4) U (product
+    with log2 e and its constant, the hardware's unit, one rescaling), the sum by U, the logarithm
+    by two half-steps; the entropy's second term gap r / s by the same and three more roundings."""
+    gap = torch.arange(1, 129, device=dev) / 8
+    x = torch.full((128, 50000), -math.inf, device=dev)
+    x[:, first] = -3.0
+    x[:, second] = gap - 3.0
+    x = x.to(t)
+    gap = x[:, second].double() - x[:, first].double()
+    at = torch.full((128,), second, device=dev)
+    got = det.det_token_logprobs(x, at, top=top)
+    r = (-gap).exp()
+    logp, part = -torch.log1p(r), gap * r / (1 + r)
+    off = (1 + r * (2 * gap + 4)) / (1 + r) + 2 * logp.abs()
+    assert ((got.logp.double() - logp).abs() <= off * U32).all()
+    off = off + part * (2 * gap + 8) + 2 * (part - logp)
+    assert ((got.entropy.double() - (part - logp)).abs() <= off * U32).all()
+    if top:
+        assert torch.equal(got.top_ids, torch.tensor([[second, first]], device=dev).expand(128, 2))
+        assert same_bits(got.top_logp[:, 0].contiguous(), got.logp)
