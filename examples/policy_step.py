@@ -67,6 +67,7 @@ def step(model, tokens, lengths, advantage, lr=0.2, entropy_bonus=1e-3):
     # positions past a sequence's length are not scored
     targets = torch.where(at < lengths[:, None] - 1, tokens[:, 1:].long(), -100)
     logp, entropy = det.token_logprobs(logits, targets)
+    entropy = torch.where(targets >= 0, entropy, 0.0)      # it is returned for every position
     scored = (targets >= 0).sum()
     loss = -((logp * advantage[:, None]).sum() + entropy_bonus * entropy.sum()) / scored
     for p in model.parameters:

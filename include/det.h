@@ -342,6 +342,7 @@ det_status det_relative_bias_backward(const void* dout, int64_t stride_b, int64_
  *   alike, a NaN like -inf).
  * logits:    [rows] rows of vocab elements, row_stride apart (>= vocab when rows > 1).
  * targets:   int64 [rows]; one outside [0, vocab) is not scored: its logp is 0.
+ *            entropy and lse are written for every row, scored or not.
  * logp, entropy, lse:  float [rows].
  * top:       0 .. min(vocab, DET_LOGPROB_MAX_TOP); above 0, vocab is at most
  *            DET_LOGPROB_MAX_TOP_VOCAB (DET_ERROR_TOO_LARGE).

@@ -493,7 +493,8 @@ def det_token_logprobs(logits: torch.Tensor, targets: torch.Tensor, scale: float
 
     logits: [..., vocab], rows contiguous and evenly spaced (a slice of a padded vocabulary is
     fine); targets: int64 [...]; one outside the vocabulary (such as -100) is not scored and its
-    logp is 0.  A row's bits depend on its logits and the scale alone."""
+    logp is 0, but its entropy is returned like any other's: a loss that adds entropies leaves
+    those out itself.  A row's bits depend on its logits and the scale alone."""
     return TokenLogprobs(*_lm_binding().token_logprobs(logits, targets, scale, top))
 
 
@@ -591,7 +592,7 @@ class _TokenLogprobsFn(torch.autograd.Function):
 
 
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, scale: float = 1.0):
-    """Differentiable det_token_logprobs: (logp, entropy)."""
+    """Differentiable det_token_logprobs: (logp, entropy), the entropy of unscored rows too."""
     return _TokenLogprobsFn.apply(logits, targets, scale)
 
 

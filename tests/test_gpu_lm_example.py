@@ -68,3 +68,23 @@ def test_gradients_of_the_block_against_64_bits(dev, example):
         # f32 products and sums of up to 1000 terms, through three layers
         size = want.grad.abs().max()
         assert ((got.grad.double() - want.grad).abs() <= 2e-4 * size).all()
+
+
+def test_a_step_does_not_learn_from_padding(dev, example):
+    """Loss and gradients are the same whatever stands past each length.  Of the embedding's
+    gradient the zeros that padding adds may regroup a row's sum (at most 8 rows of one token here,
+    3 levels of 2^-24 each, relative to 8 times the largest)."""
+    g = torch.Generator().manual_seed(5)
+    tokens, other = (torch.randint(0, example.VOCAB, (5, 33), generator=g, dtype=torch.int32).to(dev)
+                     for _ in range(2))
+    lengths = torch.tensor([33, 9, 2, 20, 1], dtype=torch.int32, device=dev)
+    other = torch.where(torch.arange(33, device=dev) < lengths[:, None], tokens, other)
+    steps = []
+    for t in (tokens, other):
+        model = example.Policy(dev, 0)
+        loss = example.step(model, t, lengths, torch.ones(5, device=dev), entropy_bonus=0.5)
+        steps.append((loss, [p.grad for p in model.parameters]))
+    (loss, grads), (again, same) = steps
+    assert not torch.equal(tokens, other) and torch.equal(loss, again)
+    for a, b in zip(grads, same):
+        assert ((a - b).abs() <= 8 * 3 * 2.0 ** -24 * a.abs().max()).all()
