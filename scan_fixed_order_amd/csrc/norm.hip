@@ -514,7 +514,9 @@ __global__ __launch_bounds__(1024) void k_col_sums(const float* part, int64_t st
                                                    T* out) {
     __shared__ float s[kSumRows][kSumCols];
     const int quad = threadIdx.x & 3, grp = threadIdx.x >> 2;
-    const int64_t c = (int64_t)blockIdx.x * kSumCols + 4 * quad;
+    for (int64_t first = (int64_t)blockIdx.x * kSumCols, step = (int64_t)gridDim.x * kSumCols;;
+         first += step) {
+    const int64_t c = first + 4 * quad;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c + 4 <= d) {
 #pragma unroll 4
@@ -536,8 +538,11 @@ __global__ __launch_bounds__(1024) void k_col_sums(const float* part, int64_t st
         for (int r = row; r < n; r += 1024 / kSumCols) s[r][col] += s[r + n][col];
         __syncthreads();
     }
-    const int64_t o = (int64_t)blockIdx.x * kSumCols + threadIdx.x;
+    const int64_t o = first + threadIdx.x;
     if (threadIdx.x < kSumCols && o < d) out[o] = (T)s[0][threadIdx.x];
+    if (first + step >= d) return;
+    __syncthreads();      // s is written again
+    }
 }
 
 // ---------------------------------------------------------------- launches
@@ -558,7 +563,8 @@ int64_t strip_sums(int64_t rows, int64_t d, int64_t strip) {
     return (strips + back_rows(d) - 1) / back_rows(d);
 }
 
-// workgroups a launch starts at most (a grid holds fewer than 2^32 threads); each walks the rows
+// workgroups a launch starts at most (a grid holds fewer than 2^32 threads); each walks the rows,
+// or the columns
 unsigned grid_of(int64_t wgs) { return (unsigned)(wgs < (1 << 21) ? wgs : (1 << 21)); }
 
 constexpr int64_t kRowInRegs = 16384;        // forward: up to 2 vectors a lane of 1024
@@ -660,7 +666,7 @@ det_status back_typed(const NormBackArgs& a, void* dw, hipStream_t s) {
         if (st != DET_SUCCESS) return st;
     }
     KernelTimer kt("k_col_sums", s);
-    k_col_sums<T><<<dim3((unsigned)((a.d + kSumCols - 1) / kSumCols)), dim3(1024), 0, s>>>(
+    k_col_sums<T><<<dim3(grid_of((a.d + kSumCols - 1) / kSumCols)), dim3(1024), 0, s>>>(
         a.part, sums, a.d, static_cast<T*>(dw));
     return launch_status();
 }

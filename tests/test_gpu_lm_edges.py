@@ -149,3 +149,24 @@ def test_likely_tokens_keep_their_digits(dev, first, second, top, t):
     if top:
         assert torch.equal(got.top_ids, torch.tensor([[second, first]], device=dev).expand(128, 2))
         assert same_bits(got.top_logp[:, 0].contiguous(), got.logp)
+
+
+# ------------------------------------------------------------------ long rows
+
+@pytest.mark.parametrize("rows,d", [(1, (1 << 26) + 17), (2, (1 << 25) + 1)])
+def test_norm_backward_of_the_longest_rows(dev, rows, d):
+    """Columns past what one launch of the column sums covers (2^21 workgroups of 16)."""
+    h, dy = randn((rows, d), torch.float32, dev, 51), randn((rows, d), torch.float32, dev, 52)
+    w = randn((d,), torch.float32, dev, 53)
+    rstd = h.double().square().mean(1).rsqrt().float()
+    dx, dw = det.det_rms_norm_backward(dy, h, w, rstd)
+    # at most two strips of one row each and the tree's zeros: one addition
+    terms = dy * (h * rstd[:, None])
+    assert torch.equal(dw, terms[0] if rows == 1 else terms[0] + terms[1])
+    want, _ = ref.norm_backward(dy, h, w, rstd)
+    # a lane's chain of d / 1024 terms, the tree's 10 levels; xhat's mean is small beside dy w
+    g, xhat = (dy.double() * w.double()).abs(), (h.double() * rstd.double()[:, None]).abs()
+    chain = d / 1024 + 26
+    mean = (g * xhat).mean(1, keepdim=True)
+    bound = U32 * rstd.double()[:, None] * (8 * (g + xhat * mean) + chain * xhat * mean)
+    assert ((dx.double() - want).abs() <= bound).all()
