@@ -104,6 +104,11 @@ Tensor workspace(size_t bytes, const Optional& ws, const Tensor& like) {
     return *ws;
 }
 
+// An expanded view has more bytes than memory: checked before any size is trusted.
+void check_workspace(const Optional& ws) {
+    if (ws && !ws->is_contiguous()) wrong_value("a workspace must be contiguous");
+}
+
 // the device of `t` while the call lasts
 using Guard = c10::DeviceGuard;
 
@@ -172,6 +177,7 @@ py::tuple rms_norm_backward(const Tensor& dy, const Tensor& h, const Tensor& wei
         same_type(*dh, h, "dh");
         if (dh->sizes() != h.sizes()) wrong_value("dh must have the shape of h");
     }
+    check_workspace(ws);
     void* const dyp = pointer(dy, h);
     void* const hp = pointer(h, h);
     void* const wp = pointer(weight, h);
@@ -254,6 +260,7 @@ Tensor relative_bias_backward(const Tensor& dout, int64_t buckets, int64_t max_d
     const int64_t batch = dout.size(0), heads = dout.size(1), q = dout.size(2), k = dout.size(3);
     bias_batch(batch, offsets, lengths);
     if (dscores) of(*dscores, dout.scalar_type(), dout.sizes(), "dscores");
+    check_workspace(ws);
     void* const dp = pointer(dout, dout);
     void* const op = pointer(offsets, dout);
     void* const lp = pointer(lengths, dout);
