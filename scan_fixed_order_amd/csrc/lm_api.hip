@@ -77,7 +77,9 @@ det_status det_rms_norm(const void* x, int64_t x_stride, const void* residual,
     // what is written lies apart from what is read and from each other; h may replace an input
     const size_t wbytes = (size_t)d * es, sbytes = (size_t)rows * 4;
     const size_t cbytes = codes ? sbytes * (group ? (d + group - 1) / group : 1) : 0;
-    if (!apart(in, yo, false) || !apart(weight, wbytes, yo) || overlap(scales, cbytes, rstd, sbytes))
+    if (!apart(in, yo, false) || !apart(weight, wbytes, yo) ||
+        overlap(scales, cbytes, rstd, sbytes) || overlap(scales, cbytes, weight, wbytes) ||
+        overlap(rstd, sbytes, weight, wbytes))
         return DET_ERROR_INVALID_VALUE;
     if (residual && (!apart(res, yo, false) || !apart(in, ho, true) || !apart(res, ho, true) ||
                      !apart(weight, wbytes, ho) || !apart(ho, yo, false)))
@@ -121,7 +123,9 @@ det_status det_rms_norm_backward(const void* dy, int64_t dy_stride, const void* 
             return DET_ERROR_INVALID_VALUE;
         for (const Rows* r : {&a, &b, &e, &o})
             if (r->p && !apart(dweight, wbytes, *r)) return DET_ERROR_INVALID_VALUE;
-        if (overlap(weight, wbytes, dweight, wbytes)) return DET_ERROR_INVALID_VALUE;
+        if (overlap(weight, wbytes, dweight, wbytes) ||
+            overlap(rstd, (size_t)rows * 4, dweight, wbytes))
+            return DET_ERROR_INVALID_VALUE;
     }
     const det_status st = ws_status(ws, ws_bytes, norm_backward_workspace(rows, d, dtype));
     if (st != DET_SUCCESS) return st;
@@ -177,9 +181,13 @@ bool contiguous(const BiasCall& c) {
            (c.sb == c.heads * c.q * c.k || c.batch == 1);
 }
 
-// `out` may be the call's own strided tensor where that is contiguous, else lies apart from it
+// `out` may be the call's own strided tensor where that is contiguous, else lies apart from it;
+// and from the masks' arguments, which every workgroup reads
 bool bias_out_ok(const BiasCall& c, const void* out, size_t obytes) {
-    if (!out || !aligned(out, lm_size(c.dtype))) return false;
+    if (!out || !aligned(out, lm_size(c.dtype)) ||
+        overlap(out, obytes, c.q_offsets, (size_t)c.batch * 4) ||
+        overlap(out, obytes, c.lengths, (size_t)c.batch * 4))
+        return false;
     if (!c.scores || (out == c.scores && contiguous(c))) return true;
     return !overlap(out, obytes, c.scores, strided_bytes(c));
 }
@@ -202,9 +210,7 @@ det_status det_relative_bias(const void* table, int64_t num_buckets, int64_t hea
     if (batch == 0 || q == 0 || k == 0) return DET_SUCCESS;
     const size_t es = lm_size(dtype), obytes = (size_t)batch * heads * q * k * es;
     if (!table || !aligned(table, es) || !bias_out_ok(c, out, obytes) ||
-        overlap(out, obytes, table, (size_t)num_buckets * heads * es) ||
-        overlap(out, obytes, q_offsets, (size_t)batch * 4) ||
-        overlap(out, obytes, lengths, (size_t)batch * 4))
+        overlap(out, obytes, table, (size_t)num_buckets * heads * es))
         return DET_ERROR_INVALID_VALUE;
     c.table = table;
     c.out = out;
@@ -237,6 +243,8 @@ det_status det_relative_bias_backward(const void* dout, int64_t stride_b, int64_
     if (!dtable || !aligned(dtable, es)) return DET_ERROR_INVALID_VALUE;
     if (obytes > 0 &&
         (!dout || overlap(dtable, tbytes, dout, strided_bytes(c)) ||
+         overlap(dtable, tbytes, q_offsets, (size_t)batch * 4) ||
+         overlap(dtable, tbytes, lengths, (size_t)batch * 4) ||
          (dscores && (!bias_out_ok(c, dscores, obytes) || overlap(dscores, obytes, dtable, tbytes)))))
         return DET_ERROR_INVALID_VALUE;
     st = ws_status(ws, ws_bytes, bias_backward_workspace(batch, heads, q, k, (int)num_buckets, dtype));
@@ -262,13 +270,21 @@ det_status det_token_logprobs(const void* logits, int64_t row_stride, const int6
     const Rows in{logits, row_stride, rows, vocab, lm_size(dtype)};
     if (vocab == 0 || !in.ok() || !targets || !aligned(targets, 8)) return DET_ERROR_INVALID_VALUE;
     if (!in.fits()) return DET_ERROR_TOO_LARGE;
-    for (const void* p : {(const void*)logp, (const void*)entropy, (const void*)lse})
-        if (!p || !aligned(p, 4) || !apart(p, (size_t)rows * 4, in)) return DET_ERROR_INVALID_VALUE;
-    if (top > 0 ? !top_logp || !top_ids || !aligned(top_logp, 4) || !aligned(top_ids, 8) ||
-                      !apart(top_logp, (size_t)rows * top * 4, in) ||
-                      !apart(top_ids, (size_t)rows * top * 8, in)
-                : top_logp || top_ids)
+    if (!logp || !entropy || !lse ||
+        (top > 0 ? !top_logp || !top_ids || !aligned(top_ids, 8) : top_logp || top_ids))
         return DET_ERROR_INVALID_VALUE;
+    // what is written lies apart from what is read and from each other
+    const struct { const void* p; size_t bytes; } outs[] = {
+        {logp, (size_t)rows * 4}, {entropy, (size_t)rows * 4}, {lse, (size_t)rows * 4},
+        {top_logp, (size_t)rows * top * 4}, {top_ids, (size_t)rows * top * 8}};
+    for (const auto& o : outs) {
+        if (!aligned(o.p, 4) || !apart(o.p, o.bytes, in) ||
+            overlap(o.p, o.bytes, targets, (size_t)rows * 8))
+            return DET_ERROR_INVALID_VALUE;
+        for (const auto& other : outs)
+            if (&o != &other && overlap(o.p, o.bytes, other.p, other.bytes))
+                return DET_ERROR_INVALID_VALUE;
+    }
     const LogpCall c{logits, targets, logp, entropy, lse, top_logp, top_ids, row_stride, rows,
                      vocab, (int)top, (float)scale, dtype};
     return logprob_launch(c, static_cast<hipStream_t>(stream));
