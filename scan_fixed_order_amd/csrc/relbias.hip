@@ -268,9 +268,21 @@ constexpr int kShortRun = 16;              // diagonals
 template <typename T>
 constexpr int kDiags = 64 * kVec<T>;       // diagonals a wave covers
 
+// What kRows rows of a diagonal are added in.  A gradient of 16 bits does not show the 7 float
+// roundings (2^-24 each, of the summed magnitudes), and sums in double cost it 3 to 20 % (2 x 16 x
+// 1024 x 1024 f16 20.5 us, 25.1 in double); one of f32 shows them, and pays 0.1 to 2.5 %.
+template <typename T>
+struct RowSum {
+    typedef float type;
+};
+template <>
+struct RowSum<float> {
+    typedef double type;
+};
+
 // A lane owns a vector's neighbouring diagonals and walks down the strip's rows: its elements of
-// a row lie together in memory, one place further along with every row.  kRows rows are added in f32,
-// their sums in f64.  The wave then adds its diagonals up by buckets, which are runs of
+// a row lie together in memory, one place further along with every row.  kRows rows are added in
+// RowSum, their sums in f64.  The wave then adds its diagonals up by buckets, which are runs of
 // neighbouring diagonals, and the workgroup its waves.  Bound by HBM: 4 x 16 x 2048 x 2048 bf16
 // 98 us with the last sums (5.5 TB/s); 107 while the edges' rows were masked in 64 bits.  Its loads
 // start at any element, which fetches a tenth more than the tensor holds.  Strips of 32 rows: 64
@@ -312,7 +324,7 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias_backward(Map m, BiasBa
         const int64_t to = m.causal && w0 - off > 0 ? from : hi < q1 ? hi : q1;
         for (int64_t row = from; row < to; row += kRows) {
             u32x4 raw[kRows];
-            float sum[kVec<T>] = {};
+            typename RowSum<T>::type sum[kVec<T>] = {};
             // of the vector in the first row: its place, its key, clipped, and the keys from it on
             const int64_t at = base + row * (a.sq + 1), key = row + d0, rest = keys - key;
             const int c = key < -64 ? -64 : key > 0 ? 0 : (int)key;

@@ -170,3 +170,19 @@ def test_norm_backward_of_the_longest_rows(dev, rows, d):
     mean = (g * xhat).mean(1, keepdim=True)
     bound = U32 * rstd.double()[:, None] * (8 * (g + xhat * mean) + chain * xhat * mean)
     assert ((dx.double() - want).abs() <= bound).all()
+
+
+# ------------------------------------------------------------------ the table's gradient in f32
+
+@pytest.mark.parametrize("shape", [(2, 3, 9, 20), (1, 4, 100, 1000), (3, 5, 777, 1003), (2, 8, 1500, 2100)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_table_gradient_of_f32_is_rounded_once(dev, shape, causal):
+    """Sums in double throughout: chains of less than 2^14 terms of 2^-53 each stay below 2^-38 of
+    the summed magnitudes, and the result is rounded to float."""
+    b, h, q, k = shape
+    lens = torch.tensor([k - 3 * i for i in range(b)], dtype=torch.int32, device=dev)
+    dout = randn(shape, torch.float32, dev, 61)
+    maps = ref.bias_maps(b, q, k, 32, 128, True, causal, k - q, lens.tolist(), dev)
+    got = det.det_relative_bias_backward(dout, 32, causal=causal, q_offset=k - q, lengths=lens)
+    want, sizes, _ = ref.bias_backward(dout, maps, 32)
+    assert ((got.double() - want).abs() <= U32 * want.abs() * 1.001 + 2.0 ** -38 * sizes).all()
