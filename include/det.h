@@ -359,8 +359,8 @@ det_status det_token_logprobs(const void* logits, int64_t row_stride, const int6
  * where hit is 1 at the target; a target outside [0, vocab) takes no dlogp.
  * lse, entropy:  float [rows], as det_token_logprobs wrote them for these logits and scale.  A
  *                float lse has few digits of log(sum) where it is large (none in a row of the
- *                type's lowest values): a row with a finite |lse| > 256 takes log p from its
- *                logits again, in an order fixed by (vocab, dtype).
+ *                type's lowest values): a row with |lse| > 256 takes log p from its logits again,
+ *                in an order fixed by (vocab, dtype).
  * dlogp:         float [rows].
  * dentropy:      NULL (then entropy may be NULL too), or float [rows].
  * dlogits:       [rows] rows of vocab elements, dlogits_stride apart; may be logits itself (with

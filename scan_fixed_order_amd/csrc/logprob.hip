@@ -5,9 +5,11 @@
 //   lse = log(sum exp z);  logp = z[target] - lse (0 where the target is not a token);
 //   entropy = -sum p log p, p = exp(z - lse);  top: the largest logits, ties to the lower index;
 //   dlogits = scale * (dlogp (hit - p) - dentropy * p * (log p + entropy)).
-// One pass forward: s = sum exp(z - ref) and w = sum exp(z - ref) (z - ref) against a running
-// maximum give lse = ref + log s and entropy = log s - w / s.  A term whose p is 0 adds 0 to
-// the entropy also where its logit is -inf.  A row without any mass (all logits -inf) has
+// One pass forward: s = sum exp(d) and w = sum exp(d) d with d = scale * (x - ref) against a running
+// maximum ref of the logits give lse = scale * ref + log s and entropy = log s - w / s.  d is the
+// difference times the scale, not scale * x less a scaled reference: where a mask has put -1e30 into
+// a row, the rounding of that product alone is 1e22, far more than exp takes.  A term whose p is 0
+// adds 0 to the entropy also where its logit is -inf.  A row without any mass (all logits -inf) has
 // lse = -inf, entropy 0, logp -inf and gradient 0.
 //
 // Order: 1024 lanes share a row, lane L holding elements V (L + 1024 j) .. + V for j = 0, 1, ...
@@ -29,6 +31,7 @@ constexpr int kTile = kLanes * kVec<T>;   // elements they take at a time
 constexpr int kGroup = 32;                // neighbouring elements whose largest is kept for top
 constexpr int kShort = 512;               // candidates of the short way to the top
 constexpr float kFar = -1e30f;            // differences of references stop here (never -inf)
+constexpr float kLn2 = 0.69314718055994531f;
 
 // the largest of three; a quiet NaN loses (a signalling one takes what it was compared with along:
 // the instruction answers it with a quiet NaN, which the next comparison drops)
@@ -55,20 +58,20 @@ struct LogpArgs {
     int64_t* top_ids;
     int64_t stride, rows, vocab;
     int top;
-    float scale, unscale;      // unscale = 1 / scale
+    float scale, scale2;       // scale2 = scale * log2(e)
 };
 
 // One lane's running sums against its reference, the largest of its values so far.  (A reference
-// that values may pass by 8 spares most lanes the rescaling, 98 us instead of 101 on 2048 x 131072
-// bf16 with alternatives, but then log(sum) and the target cancel in a row of one likely token: its
-// log probability was off by 20 times 2^-24, where 1.4 times is what a float sum costs.)
+// that values may pass by 8 spares most lanes the rescaling, 3 % of 2048 x 131072 bf16 with
+// alternatives, but then log(sum) and the target cancel in a row of one likely token: its log
+// probability was off by 20 times 2^-24, where 1.4 times is what a float sum costs.)
 struct Part {
-    float ref, s, w;
+    float ref, s, w;      // w in units of 2^x: times log(2) at the end
 };
 
-__device__ __forceinline__ void rebase(Part& p, float ref) {
-    const float dm = fmaxf(p.ref - ref, kFar);
-    const float f = exp_fast(dm);
+__device__ __forceinline__ void rebase(Part& p, float ref, float scale2) {
+    const float dm = fmaxf((p.ref - ref) * scale2, kFar);
+    const float f = __builtin_amdgcn_exp2f(dm);
     p.w = fmaf(p.s, dm, p.w) * f;
     p.s = p.s * f;
     p.ref = ref;
@@ -82,20 +85,15 @@ __device__ __forceinline__ float sum16(float v) {
     return v + xor_partner<8>(v);
 }
 
-// adds a vector of N logits; `largest`: their maximum (NaN ignored); `limit`: the logit behind the
-// reference
+// adds a vector of N logits; `largest`: their maximum (NaN ignored)
 template <int N>
-__device__ __forceinline__ void take(Part& p, float& limit, const float (&x)[N], float largest,
-                                     float scale) {
-    if (largest > limit) {
-        rebase(p, largest * scale);
-        limit = largest;
-    }
+__device__ __forceinline__ void take(Part& p, const float (&x)[N], float largest, float scale2) {
+    if (largest > p.ref) rebase(p, largest, scale2);
     float e[N], d[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        d[i] = fmaf(x[i], scale, -p.ref);
-        e[i] = exp_fast(d[i]);
+        d[i] = (x[i] - p.ref) * scale2;
+        e[i] = __builtin_amdgcn_exp2f(d[i]);
     }
     float w0 = e[0] * d[0], w1 = e[1] * d[1];
 #pragma unroll
@@ -154,9 +152,9 @@ __device__ __forceinline__ void rank_candidates(const LogpArgs& a, int64_t row,
         rank += xor_partner<2>(rank);
         rank += xor_partner<4>(rank);
         if (part == 0 && i < n && (int)rank < a.top) {
-            const float z = fmaf(key_value((uint32_t)(c >> 32)), a.scale, -ref);
             a.top_ids[row * a.top + rank] = (int64_t)(uint32_t)~(uint32_t)c;
-            a.top_logp[row * a.top + rank] = z - log_s;
+            a.top_logp[row * a.top + rank] =
+                fmaf(key_value((uint32_t)(c >> 32)) - ref, a.scale, -log_s);
         }
     }
 }
@@ -303,8 +301,8 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
 }
 
 // One row per workgroup, each logit read once; 1024 or 512 threads for few rows, where a compute
-// unit's vector rate bounds (about 17 logits a nanosecond), 256 for many.  2048 x 131072 bf16: 90 us
-// (5.9 TB/s, bound by HBM), with 5 alternatives 101 us (5.3 TB/s: 10 vector instructions and an
+// unit's vector rate bounds (about 17 logits a nanosecond), 256 for many.  2048 x 131072 bf16: 89 us
+// (6.0 TB/s, bound by HBM), with 5 alternatives 97 us (5.5 TB/s: 10 vector instructions and an
 // exponential a logit fill the vector units, and a row's search runs for 2 us).  256 x 131072 with
 // 5 alternatives 16.7 us with 1024 threads a row; 300 rows 31 us with 256.
 template <typename T, int BLOCK, bool TOP, bool ONCE>
@@ -322,12 +320,8 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
         const bool scored = target >= 0 && target < a.vocab;
         const float picked = scored ? (float)x[target] : 0.0f;
         Part p[kSets];
-        float limit[kSets];
 #pragma unroll
-        for (int u = 0; u < kSets; ++u) {
-            p[u] = Part{-FLT_MAX, 0.0f, 0.0f};
-            limit[u] = -FLT_MAX * a.unscale;      // below it z overflows
-        }
+        for (int u = 0; u < kSets; ++u) p[u] = Part{-FLT_MAX, 0.0f, 0.0f};
         const auto one = [&](int64_t c, int u, const float(&v)[kVec<T>], bool keep) {
             const float largest = largest_of(v);
             if constexpr (TOP) {
@@ -342,7 +336,7 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
                 }
                 if (keep && lane % (kGroup / kVec<T>) == 0) s_key[c / kGroup] = __float_as_uint(g);
             }
-            if (keep) take(p[u], limit[u], v, largest, a.scale);
+            if (keep) take(p[u], v, largest, a.scale2);
         };
         const int64_t whole = a.vocab / (kTile<T> * kSteps);
         for (int64_t i = 0; i < whole; ++i) {
@@ -378,7 +372,7 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
 #pragma unroll
         for (int u = 0; u < kSets; ++u) {
             const float ref = wave_max(p[u].ref);
-            rebase(p[u], ref);
+            rebase(p[u], ref, a.scale2);
             const float s = wave_pw(p[u].s), w = wave_pw(p[u].w);
             if (lane == 0) s_part[parity][wave + u * (BLOCK / 64)] = Part{ref, s, w};
         }
@@ -390,13 +384,13 @@ __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
         ref = fmaxf(ref, xor_partner<2>(ref));
         ref = fmaxf(ref, xor_partner<4>(ref));
         ref = fmaxf(ref, xor_partner<8>(ref));
-        rebase(g, ref);
+        rebase(g, ref, a.scale2);
         const float s = sum16(g.s), w = sum16(g.w), log_s = logf(s);
         const bool none = s == 0.0f;
         if (t == 0) {
-            a.lse[row] = ref + log_s;
-            a.entropy[row] = none ? 0.0f : log_s - w / s;
-            a.logp[row] = !scored ? 0.0f : none ? -INFINITY : fmaf(picked, a.scale, -ref) - log_s;
+            a.lse[row] = fmaf(ref, a.scale, log_s);
+            a.entropy[row] = none ? 0.0f : log_s - w * kLn2 / s;
+            a.logp[row] = !scored ? 0.0f : none ? -INFINITY : fmaf(picked - ref, a.scale, -log_s);
         }
         if constexpr (TOP)
             pick_top<T, BLOCK>(a, row, x, s_key, s_search, none ? 0.0f : ref, none ? 0.0f : log_s,
@@ -417,8 +411,9 @@ struct LogpBackArgs {
 
 constexpr int kBackTile = 8192;                           // elements a workgroup takes at a time
 
-// lse is a float: beyond this its rounding moves every p = exp(z - lse) by more than 2^-16, and in a
-// row of the type's lowest values nothing of log(sum) is left in it.  Such a row's sum is taken again.
+// lse is a float: beyond this its rounding moves every p = exp(z - lse) by more than 2^-16, in a row of
+// the type's lowest values nothing of log(sum) is left in it, and with a scale it may be infinite.
+// Such a row's sum is taken again.
 constexpr float kFarLse = 256.0f;
 
 // What a row's gradient takes besides its logits
@@ -435,8 +430,8 @@ __device__ __forceinline__ float logit_gradient(float log, const BackTerms& r, b
 }
 
 // A row whose lse is far from zero, by one workgroup: its maximum, its sum against that, and only
-// then the gradient (which may replace the logits).  Order of the sum: a lane's vectors, the
-// adjacent-lanes tree, the four waves.
+// then the gradient (which may replace the logits); 0 where all logits are -inf.  Order of the sum:
+// a lane's vectors, the adjacent-lanes tree, the four waves.
 template <typename T>
 __device__ void far_row(const LogpBackArgs& a, const T* x, T* out, const BackTerms& r) {
     __shared__ float s_max[4], s_sum[4];
@@ -450,12 +445,13 @@ __device__ void far_row(const LogpBackArgs& a, const T* x, T* out, const BackTer
     top = wave_max(top);
     if ((threadIdx.x & 63) == 0) s_max[wave] = top;
     __syncthreads();
-    const float m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3])) * a.scale;
+    top = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    const bool none = top == -INFINITY;
     float sum = 0.0f;
     for (int64_t c = kVec<T> * threadIdx.x; c < a.vocab; c += 256 * kVec<T>) {
         read_vec(x + c, a.vocab - c, -INFINITY, v);
 #pragma unroll
-        for (int i = 0; i < kVec<T>; ++i) sum += exp_fast(fmaf(v[i], a.scale, -m));
+        for (int i = 0; i < kVec<T>; ++i) sum += exp_fast((v[i] - top) * a.scale);
     }
     sum = wave_pw(sum);
     if ((threadIdx.x & 63) == 0) s_sum[wave] = sum;
@@ -465,15 +461,17 @@ __device__ void far_row(const LogpBackArgs& a, const T* x, T* out, const BackTer
         read_vec(x + c, a.vocab - c, -INFINITY, v);
         const int64_t hit = r.target - c;
 #pragma unroll
-        for (int i = 0; i < kVec<T>; ++i)
-            v[i] = logit_gradient(fmaf(v[i], a.scale, -m) - log_s, r, i == hit) * a.scale;
+        for (int i = 0; i < kVec<T>; ++i) {
+            const float d = logit_gradient(fmaf(v[i] - top, a.scale, -log_s), r, i == hit);
+            v[i] = none ? 0.0f : d * a.scale;
+        }
         write_vec(out + c, a.vocab - c, v);
     }
     __syncthreads();      // the LDS slots are written again
 }
 
 // Each logit read once, each gradient written once; nothing is summed (but in far_row).  A lane's
-// loads are all on their way before its first value is used.  Bound by HBM: 4096 x 65536 bf16 180
+// loads are all on their way before its first value is used.  Bound by HBM: 4096 x 65536 bf16 178
 // us (6.0 TB/s; 176 without far rows, 182 with them told apart before the loads, 189 after; 190
 // with a branch between whole and partial vectors at each load), 517 x 50021 f32 with the forward
 // pass 65 us (4.8 TB/s; rows there start off 16 bytes), 69 with such a branch.
@@ -491,7 +489,7 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a)
         r.dlogp = scored ? a.dlogp[row] : 0.0f;
         r.dent = a.dentropy ? a.dentropy[row] : 0.0f;
         r.both = a.dentropy ? fmaf(r.dent, a.entropy[row], r.dlogp) : r.dlogp;
-        const bool none = lse == -INFINITY, far = fabsf(lse) > kFarLse && fabsf(lse) < INFINITY;
+        const bool far = fabsf(lse) > kFarLse;
         const int64_t end = far ? 0 : a.vocab;      // far rows come below
         constexpr int kVecs = kBackTile / (256 * kVec<T>);
         u32x4 raw[kVecs];
@@ -506,10 +504,8 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a)
             if (n <= 0) continue;
             const int64_t hit = r.target - c;
 #pragma unroll
-            for (int i = 0; i < kVec<T>; ++i) {
-                const float d = logit_gradient(fmaf(v[i], a.scale, -lse), r, i == hit);
-                v[i] = none ? 0.0f : d * a.scale;
-            }
+            for (int i = 0; i < kVec<T>; ++i)
+                v[i] = logit_gradient(fmaf(v[i], a.scale, -lse), r, i == hit) * a.scale;
             write_vec(out + c, n, v);
         }
         if (far && c0 == 0) far_row<T>(a, x, out, r);
@@ -563,7 +559,8 @@ void logp_back_typed(const LogpBackArgs& a, hipStream_t s) {
 
 det_status logprob_launch(const LogpCall& c, hipStream_t s) {
     const LogpArgs a{c.logits, c.targets, c.logp, c.entropy, c.lse, c.top_logp, c.top_ids,
-                     c.stride, c.rows, c.vocab, c.top, c.scale, 1.0f / c.scale};
+                     c.stride, c.rows, c.vocab, c.top, c.scale,
+                     (float)(c.scale * 1.4426950408889634)};
     switch (c.dtype) {
         case DET_F32: logp_typed<float>(a, s); break;
         case DET_F16: logp_typed<_Float16>(a, s); break;

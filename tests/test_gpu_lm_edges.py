@@ -186,3 +186,44 @@ def test_table_gradient_of_f32_is_rounded_once(dev, shape, causal):
     got = det.det_relative_bias_backward(dout, 32, causal=causal, q_offset=k - q, lengths=lens)
     want, sizes, _ = ref.bias_backward(dout, maps, 32)
     assert ((got.double() - want).abs() <= U32 * want.abs() * 1.001 + 2.0 ** -38 * sizes).all()
+
+
+# ------------------------------------------------------------------ masks that are numbers
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("rows,vocab", [(12, 5), (12, 258), (12, 9001), (12, 40000), (300, 9001),
+                                        (600, 9001)])
+@pytest.mark.parametrize("scale", [1.0, 0.7, 1.25, 3.0, 0.0078125])
+def test_masks_of_large_numbers(dev, rows, vocab, t, scale):
+    """Logits masked by large negative numbers instead of -inf, under a scale: rows keep their
+    values, and rows of nothing else are even."""
+    low = torch.finfo(t).min
+    masks = [low, low / 1.5, -6e4, -3e4] + ([-1e30, -1e9] if t != torch.float16 else [-5e4, -1e4])
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    x = randn((rows, vocab), torch.float32, dev, 71, 2.0).to(t)
+    column = torch.arange(vocab, device=dev)
+    for i, m in enumerate(masks):
+        x[2 * i] = m                                          # nothing is left
+        x[2 * i + 1] = torch.where(column % 5 == i % 5, x[2 * i + 1], m)
+    at = (column[:1] + torch.arange(rows, device=dev)) % vocab
+    top = min(vocab, 7)
+    got = det.det_token_logprobs(x, at, scale, top)
+    logp, entropy, lse, log = ref.logprobs(x, at, scale)
+    p, size = log.exp(), torch.where(log > -math.inf, log.abs(), 0.0)
+    far = (p * torch.where(p > 0, size, 0.0)).sum(-1) + 8
+    rel = U32 * (40 + vocab / 1024 + 4 * far)
+    fits = lse.abs() <= torch.finfo(torch.float32).max
+    assert ((got.lse.double() - lse).abs() <= rel + 2 * U32 * lse.abs())[fits].all()
+    assert (got.lse[~fits] == -math.inf).all()
+    # a masked target's log probability may lie past the floats
+    lost = logp < -1e38
+    assert (got.logp[lost] < -9e37).all()
+    assert ((got.logp.double() - logp).abs() <= rel + 4 * U32 * (logp.abs() + 8))[~lost].all()
+    assert ((got.entropy.double() - entropy).abs() <= rel * (2 + far)).all()
+    assert torch.equal(got.top_ids, ref.top_ids(x, top))
+
+    dlogp, dent = randn((rows,), torch.float32, dev, 72), randn((rows,), torch.float32, dev, 73)
+    grad = det.det_token_logprobs_backward(x, at, got.lse, dlogp, got.entropy, dent, scale)
+    want = ref.logprobs_backward(log, at, entropy, dlogp, dent, scale)
+    assert ((grad.double() - want).abs()
+            <= gradient_bound(x, at, scale, dlogp, dent, want, t)).all()
