@@ -232,9 +232,10 @@ det_status det_scatter_add_running(const void* values, const int32_t* index, int
  * Norm, relative position bias and token log probabilities, forward and backward.  dtype is
  * DET_F32, DET_F16 or DET_BF16 (else DET_ERROR_UNSUPPORTED): the type of every tensor not
  * declared float, int32 or int64 below.  Everything between loading and the one rounding on
- * storing is f32 (the bias table's last sums f64).  Every sum's order is fixed by the sizes
- * that its comment names, never by the launch, so the bits depend on the arguments alone; the
- * results of a row depend on that row alone, not on the rows beside it or their number.
+ * storing is f32 (the bias table's gradient f64, of 16-bit types but for sums over 8 rows).  Every
+ * sum's order is fixed by the arguments that its comment names, never by the launch, so the bits
+ * depend on the arguments alone; the results of a row depend on that row alone, not on the rows
+ * beside it or their number.
  * Strides count elements; the innermost dimension is contiguous.  No wait inside any kernel
  * depends on another workgroup. */
 
@@ -274,7 +275,8 @@ size_t det_rms_norm_backward_workspace_size(int64_t rows, int64_t d, det_dtype d
  * dx:       [rows * d]; may be dy, h or dh itself where that is contiguous and d <= 16384.
  * dweight:  [d], written (zero for no rows).
  * Order: a row's sum fixed by (d, dtype); dweight's by (rows, d, dtype): strips of rows in
- * ascending order, then the strips. */
+ * ascending order; the strips of 1 to 4 neighbours in theirs; of these sums 256 chains (k, k + 256,
+ * ...), which a halving tree joins. */
 det_status det_rms_norm_backward(const void* dy, int64_t dy_stride, const void* h,
                                  int64_t h_stride, const void* weight, const float* rstd,
                                  const void* dh, int64_t dh_stride, int64_t rows, int64_t d,
@@ -323,8 +325,12 @@ size_t det_relative_bias_backward_workspace_size(int64_t batch, int64_t heads, i
  * dscores:  NULL, or [batch * heads * q * k]: dout with zeros at the masked places (the gradient
  *           of the scores).  May be dout itself where that is contiguous.
  * The other arguments as for det_relative_bias.
- * Order, fixed by (batch, heads, q, k, dtype): every diagonal of a strip of query rows in row
- * order, the diagonals of a bucket, then the strips in f64. */
+ * Order, fixed by (batch, heads, q, k, dtype) and, where a bucket's diagonals begin and end, by
+ * (num_buckets, max_distance, direction, offsets): 8 rows of a diagonal in row order (in float for
+ * 16-bit types), a strip's blocks of 8 rows; the diagonals of a bucket inside a tile (512 of them,
+ * 256 of f32): runs of up to 16 in ascending order, longer ones by lanes of a vector each and the
+ * adjacent-lanes tree; four neighbouring tiles; of these sums, sequence by sequence, 64 chains (g, g
+ * + 64, ...), which a halving tree joins.  All but the 8 rows in f64. */
 det_status det_relative_bias_backward(const void* dout, int64_t stride_b, int64_t stride_h,
                                       int64_t stride_q, int64_t num_buckets, int64_t heads,
                                       int64_t max_distance, unsigned flags, int64_t batch,
@@ -347,7 +353,8 @@ det_status det_relative_bias_backward(const void* dout, int64_t stride_b, int64_
  * top:       0 .. min(vocab, DET_LOGPROB_MAX_TOP); above 0, vocab is at most
  *            DET_LOGPROB_MAX_TOP_VOCAB (DET_ERROR_TOO_LARGE).
  * top_logp, top_ids:  float and int64 [rows * top], NULL when top is 0.
- * A row of -inf alone has lse -inf, entropy 0, logp -inf.  vocab >= 1 when rows > 0; scale > 0
+ * A row of -inf alone has lse -inf, entropy 0, logp -inf; a result past float's range is infinite
+ * (lse of a row of the lowest floats with a scale above 1).  vocab >= 1 when rows > 0; scale > 0
  * and finite.  Order of a row's sums: fixed by (vocab, dtype). */
 det_status det_token_logprobs(const void* logits, int64_t row_stride, const int64_t* targets,
                               int64_t rows, int64_t vocab, det_dtype dtype, double scale,

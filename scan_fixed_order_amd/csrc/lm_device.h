@@ -204,7 +204,9 @@ __device__ __forceinline__ void wave_sync() {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// e^x with the hardware's 2^x (about 1 ulp; results below 2^-126 become 0)
+// e^x with the hardware's 2^x, off by up to (1 + |x|) 2^-23: the constant and the product are rounded
+// to float, which moves the exponent by as much relative to it, and 2^x is good to a last place.
+// Results below 2^-126 become 0.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 }  // namespace det

@@ -302,9 +302,9 @@ __device__ void pick_top(const LogpArgs& a, int64_t row, const T* x, uint32_t* s
 
 // One row per workgroup, each logit read once; 1024 or 512 threads for few rows, where a compute
 // unit's vector rate bounds (about 17 logits a nanosecond), 256 for many.  2048 x 131072 bf16: 89 us
-// (6.0 TB/s, bound by HBM), with 5 alternatives 97 us (5.5 TB/s: 10 vector instructions and an
+// (6.0 TB/s, bound by HBM), with 5 alternatives 97 us (5.5 TB/s: 11 vector instructions and an
 // exponential a logit fill the vector units, and a row's search runs for 2 us).  256 x 131072 with
-// 5 alternatives 16.7 us with 1024 threads a row; 300 rows 31 us with 256.
+// 5 alternatives 17 us with 1024 threads a row, 512 rows 31 us with 512.
 template <typename T, int BLOCK, bool TOP, bool ONCE>
 __global__ __launch_bounds__(BLOCK) void k_token_logprobs(LogpArgs a) {
     constexpr int kSets = kLanes / BLOCK;       // lanes a thread plays
@@ -474,7 +474,7 @@ __device__ void far_row(const LogpBackArgs& a, const T* x, T* out, const BackTer
 // loads are all on their way before its first value is used.  Bound by HBM: 4096 x 65536 bf16 178
 // us (6.0 TB/s; 176 without far rows, 182 with them told apart before the loads, 189 after; 190
 // with a branch between whole and partial vectors at each load), 517 x 50021 f32 with the forward
-// pass 65 us (4.8 TB/s; rows there start off 16 bytes), 69 with such a branch.
+// pass 64 us (4.8 TB/s; rows there start off 16 bytes), 69 with such a branch.
 template <typename T, bool ONCE>
 __global__ __launch_bounds__(256) void k_token_logprobs_backward(LogpBackArgs a) {
     for (int64_t tile = blockIdx.x; tile < a.rows * a.tiles; tile += gridDim.x) {
@@ -531,8 +531,8 @@ bool once(int64_t rows, int64_t vocab) {
 }
 
 // Threads for the rows at hand, as many as still leave each row a place on the 256 units (the order
-// is the same): 256 x 131072 bf16 with 5 alternatives 16.5 us with 1024, 28 with 256; 512 rows 29
-// with 512, 38 with 256; 700 rows 45 with 512, 42 with 256.
+// is the same): 256 x 131072 bf16 with 5 alternatives 17 us with 1024, 28 with 256; 512 rows 30
+// with 512, 38 with 256; 700 rows 45 with 512, 41 with 256.
 template <typename T>
 void logp_typed(const LogpArgs& a, hipStream_t s) {
     const bool wide = a.vocab > kTile<T>, past = once<T>(a.rows, a.vocab);

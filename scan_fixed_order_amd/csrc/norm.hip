@@ -10,8 +10,9 @@
 // Order: lane t of the row's team holds elements V (t + j * team) .. + V for j = 0, 1, ... (V = 8,
 // 4 of f32); it adds its own in that order, the wave adds its lanes by the adjacent-lanes tree, and the wave
 // sums are added in wave order.  The team's size depends on d alone, so a row's bits depend
-// neither on the other rows nor on their number.  dweight: strips of rows in ascending order,
-// then the strips (k_col_sums); the strip length depends on (rows, d, dtype) alone.
+// neither on the other rows nor on their number.  dweight: a team's strip of rows in ascending order,
+// the strips of a workgroup's teams in theirs, then the workgroups (k_col_sums); the strip length
+// depends on (rows, d, dtype) alone.
 #include "det_internal.h"
 #include "lm_device.h"
 
@@ -311,8 +312,8 @@ struct BackRow {
 };
 
 // A team walks its strip of rows and keeps the strip's column sums in registers; the next row's
-// loads are in flight while this one's sum goes round the team (two f32 vectors a lane leave no
-// registers for that).  With 1024 lanes of two vectors the column sums are kept in LDS: 2048 rows
+// loads are in flight while this one's sum goes round the team (16 elements of f32 a lane leave no
+// registers for that).  With 1024 lanes of 16 elements the column sums are kept in LDS: 2048 rows
 // of 16384 bf16 take 58 us so, 98 with them in registers (spilled).  The teams of a workgroup join
 // their sums.  Bound by HBM: 16384 x 4096 bf16 with dh 98 us with k_col_sums (5.5 TB/s), 116
 // without the loads ahead and past the caches.
@@ -483,7 +484,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm_backward_long(NormBackArgs a)
     }
 }
 
-// The strips' sums of dy * xhat for long rows: a lane owns 8 columns of one strip.
+// The strips' sums of dy * xhat for long rows: a lane owns a vector of columns of one strip.
 template <typename T>
 __global__ __launch_bounds__(256) void k_rms_norm_strips(NormBackArgs a) {
     const int64_t c = kVec<T> * ((int64_t)blockIdx.x * 256 + threadIdx.x);
@@ -567,7 +568,7 @@ int64_t strip_sums(int64_t rows, int64_t d, int64_t strip) {
 // or the columns
 unsigned grid_of(int64_t wgs) { return (unsigned)(wgs < (1 << 21) ? wgs : (1 << 21)); }
 
-constexpr int64_t kRowInRegs = 16384;        // forward: up to 2 vectors a lane of 1024
+constexpr int64_t kRowInRegs = 16384;        // forward: 512 lanes of 32 elements
 
 // NV: 8 elements of a row a lane
 template <typename T, int TEAM, int NV, bool RES, bool Q8>

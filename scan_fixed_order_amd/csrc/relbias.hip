@@ -204,8 +204,8 @@ __global__ __launch_bounds__(kBlock) void k_relative_bias(Map m, BiasArgs a) {
 
 // Few queries: nothing to share between rows, so every lane finds its 8 keys' buckets by itself.
 // A workgroup's teams of 2^lanes_log2 lanes take neighbouring rows of the output.  A batch of 32
-// x 16 rows of 4097 keys 8.3 us, 14.9 through the diagonals' layout, of which a row uses each
-// value once.  Bound by latency: of those, 5.4 remain without the buckets.
+// x 16 rows of 4097 keys 6.5 us a call; 8.3 between events, 14.9 through the diagonals' layout, of
+// which a row uses each value once.  Bound by latency: of the 8.3, 5.4 remain without the buckets.
 template <typename T, bool SCORES>
 __global__ __launch_bounds__(kBlock) void k_relative_bias_row(Map m, BiasArgs a) {
     __shared__ int s_starts[kBiasMaxSide];
