@@ -28,9 +28,9 @@
  *    (Warp "Deterministic Execution", section "Limitations", large launches).
  *  - No C++ exception crosses this interface.
  *
- * The language-model operators further down (norm, relative position bias, token log
- * probabilities) keep these conventions; their arithmetic and the order of their sums are stated
- * there.
+ * The language-model operators further down (norms, relative position bias, token log
+ * probabilities, embedding, gated recurrence, linear cross entropy) keep these conventions; their
+ * arithmetic and the order of their sums are stated there.
  */
 #ifndef DET_H
 #define DET_H
@@ -47,14 +47,15 @@ extern "C" {
  * sums wrap modulo 2^32 as two's complement, which no association order can change. */
 /* DET_F16, DET_BF16: storage types of the language-model operators only (they compute in f32).
  * DET_E4M3 (8-bit floats: 4 exponent and 3 mantissa bits, largest 448, no infinity): the output
- * type of det_rms_norm only. */
+ * type of det_rms_norm only.  DET_I64 (and DET_I32): token ids of det_embedding. */
 typedef enum {
     DET_F32 = 0,
     DET_F64 = 1,
     DET_I32 = 2,
     DET_F16 = 3,
     DET_BF16 = 4,
-    DET_E4M3 = 5
+    DET_E4M3 = 5,
+    DET_I64 = 6
 } det_dtype;
 
 typedef enum {
@@ -229,13 +230,14 @@ det_status det_scatter_add_running(const void* values, const int32_t* index, int
 
 /* ------------------------------------------------------------------ language-model operators
  *
- * Norm, relative position bias and token log probabilities, forward and backward.  dtype is
+ * Norms, relative position bias, token log probabilities, embedding, gated recurrence and linear
+ * cross entropy, forward and backward.  dtype is
  * DET_F32, DET_F16 or DET_BF16 (else DET_ERROR_UNSUPPORTED): the type of every tensor not
  * declared float, int32 or int64 below.  Everything between loading and the one rounding on
  * storing is f32 (the bias table's gradient f64, of 16-bit types but for sums over 8 rows).  Every
  * sum's order is fixed by the arguments that its comment names, never by the launch, so the bits
  * depend on the arguments alone; the results of a row depend on that row alone, not on the rows
- * beside it or their number.
+ * beside it or (but for the linear cross entropy) their number.
  * Strides count elements; the innermost dimension is contiguous.  No wait inside any kernel
  * depends on another workgroup. */
 
@@ -378,6 +380,141 @@ det_status det_token_logprobs_backward(const void* logits, int64_t row_stride,
                                        const float* dentropy, int64_t rows, int64_t vocab,
                                        det_dtype dtype, double scale, void* dlogits,
                                        int64_t dlogits_stride, void* stream);
+
+/* Layer norm of rows, with the residual's addition before:
+ *   h = x + residual (x where residual is NULL; used unrounded)
+ *   mean = sum(h) / d;  rstd = 1 / sqrt(sum((h - mean)^2) / d + eps)
+ *   y = ((h - mean) * rstd) * weight + bias
+ * The arguments as for det_rms_norm; bias: NULL, or [d]; mean, rstd: NULL, or float [rows] for the
+ * backward pass.  Order of a row's sums: fixed by (d, dtype). */
+det_status det_layer_norm(const void* x, int64_t x_stride, const void* residual,
+                          int64_t residual_stride, const void* weight, const void* bias,
+                          int64_t rows, int64_t d, det_dtype dtype, double eps, void* h, void* y,
+                          float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace det_layer_norm_backward needs (0 when the arguments are invalid). */
+size_t det_layer_norm_backward_workspace_size(int64_t rows, int64_t d, det_dtype dtype);
+
+/* Gradients of det_layer_norm's y in dtype: with xhat = (h - mean) * rstd, g = dy weight,
+ *   dx = rstd * (g - sum(g) / d - xhat * sum(g xhat) / d) (+ dh)
+ *   dweight = sum over the rows of dy * xhat;  dbias = sum over the rows of dy
+ * dbias: NULL, or [d].  The other arguments, where dx may lie, and the order of the sums as for
+ * det_rms_norm_backward. */
+det_status det_layer_norm_backward(const void* dy, int64_t dy_stride, const void* h,
+                                   int64_t h_stride, const void* weight, const float* mean,
+                                   const float* rstd, const void* dh, int64_t dh_stride,
+                                   int64_t rows, int64_t d, det_dtype dtype, void* dx,
+                                   void* dweight, void* dbias, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* Rows of a table by token ids: out[i] = scale * table[tokens[i]]; a token outside [0, vocab) (such
+ * as -1 for padding) has a row of zeros.
+ * table:   [vocab] rows of d elements, table_stride apart (>= d when vocab > 1).
+ * tokens:  [n] of token_type, DET_I32 or DET_I64 (else DET_ERROR_UNSUPPORTED).
+ * out:     [n * d].  scale: finite. */
+det_status det_embedding(const void* table, int64_t table_stride, const void* tokens,
+                         det_dtype token_type, int64_t n, int64_t vocab, int64_t d,
+                         det_dtype dtype, double scale, void* out, void* stream);
+
+/* Bytes of workspace det_embedding_backward needs (0 when the arguments are invalid). */
+size_t det_embedding_backward_workspace_size(int64_t n, int64_t vocab, int64_t d, det_dtype dtype);
+
+/* The table's gradient: dtable[v] = scale * sum of dout[i] over the i with tokens[i] = v, zeros
+ * where there is none; tokens outside [0, vocab) add to nothing.
+ * dout:    [n] rows of d elements, dout_stride apart.
+ * dtable:  [vocab * d], written whole.
+ * Order: ascending i; blocks of 64 from a token's first position on in float, the blocks of a token
+ * that has several in double.  A row's bits depend on the positions of its own token alone.
+ * n <= DET_MAX_N, vocab < DET_MAX_N. */
+det_status det_embedding_backward(const void* dout, int64_t dout_stride, const void* tokens,
+                                  det_dtype token_type, int64_t n, int64_t vocab, int64_t d,
+                                  det_dtype dtype, double scale, void* dtable, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* det_gated_scan flags */
+#define DET_GATE_SIGMOID 1u /* gates pass through a sigmoid and mix the input in */
+
+/* Bytes of workspace det_gated_scan needs (0 when the arguments are invalid). */
+size_t det_gated_scan_workspace_size(int64_t batch, int64_t steps, int64_t d, det_dtype dtype);
+
+/* The gated linear recurrence of every channel of every sequence:
+ *   h[t] = a[t] h[t-1] + b[t],  h[-1] = state0
+ * with a = gate, b = x, or with DET_GATE_SIGMOID a = 1 / (1 + e^-gate), b = (1 - a) x.
+ * gate, x, h: [batch * steps * d], channels innermost.  In f32 between the loads and h's rounding.
+ * state0:     NULL (zeros), or float [batch * d].
+ * state:      float [batch * d]: h behind each sequence's last step, unrounded.  May be state0 itself
+ *             where steps <= 8.
+ * lengths:    NULL, or int32 [batch]: steps at or past a sequence's length keep the state, and their
+ *             h is 0; gate and x there are not used, whatever they hold.  Values above steps mean
+ *             steps, below 0 none.
+ * Without DET_GATE_SIGMOID gates are taken to have |gate| <= 1: products of up to 128 neighbouring
+ * gates are formed, and where one overflows h may be infinite or NaN.
+ * steps >= 1 when batch * d > 0; batch * d <= DET_MAX_N.
+ * Order: fixed by the step's position alone (spans of 8 steps, chunks of 16 spans), so a sequence's
+ * bits depend neither on the other channels nor on the steps that follow. */
+det_status det_gated_scan(const void* gate, const void* x, const float* state0,
+                          const int32_t* lengths, unsigned flags, int64_t batch, int64_t steps,
+                          int64_t d, det_dtype dtype, void* h, float* state, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* Bytes of workspace det_gated_scan_backward needs (0 when the arguments are invalid). */
+size_t det_gated_scan_backward_workspace_size(int64_t batch, int64_t steps, int64_t d,
+                                              det_dtype dtype);
+
+/* Gradients of det_gated_scan, from the last step on:
+ *   G[t] = dh[t] + E[t+1],  E[t] = a[t] G[t],  E behind a sequence's last step = dstate
+ *   dx = G, dgate = G h[t-1];  with DET_GATE_SIGMOID dx = (1 - a) G, dgate = a (h[t-1] - x) dx
+ * dh, h:    [batch * steps * d]; h as det_gated_scan wrote it.  dh past a length is not used.
+ * state0:   as handed to det_gated_scan.  dstate: NULL (zeros), or float [batch * d].
+ * dgate, dx: [batch * steps * d], 0 past a length.
+ * dstate0:  NULL, or float [batch * d]: E[0], the gradient of state0.
+ * Order: fixed by the step's position and the number of steps. */
+det_status det_gated_scan_backward(const void* dh, const void* gate, const void* x, const void* h,
+                                   const float* state0, const float* dstate,
+                                   const int32_t* lengths, unsigned flags, int64_t batch,
+                                   int64_t steps, int64_t d, det_dtype dtype, void* dgate,
+                                   void* dx, float* dstate0, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* Bytes of workspace det_linear_cross_entropy needs (0 when the arguments are invalid). */
+size_t det_linear_cross_entropy_workspace_size(int64_t rows, int64_t vocab, int64_t d,
+                                               det_dtype dtype);
+
+/* Cross entropy behind an output projection, without its logits in memory:
+ *   z = scale * x weight^T;  lse = log(sum exp z);  loss = lse - z[target]
+ * x:        [rows] rows of d elements, x_stride apart.
+ * weight:   [vocab] rows of d elements, weight_stride apart.
+ * targets:  int64 [rows]; one outside [0, vocab) is not scored: its loss is 0.  lse is written for
+ *           every row.
+ * loss, lse: float [rows].
+ * The products are of dtype's matrix instructions with f32 sums; f32 goes through them in three
+ * parts of 8 bits each, with sums that are off by about 2^-23 relative to the sum of the
+ * products' magnitudes.  rows <= 2^20, 1 <= d <= 2^20, vocab >= 1; scale > 0 and finite.
+ * Order: fixed by (rows, vocab, d, dtype). */
+det_status det_linear_cross_entropy(const void* x, int64_t x_stride, const void* weight,
+                                    int64_t weight_stride, const int64_t* targets, int64_t rows,
+                                    int64_t vocab, int64_t d, det_dtype dtype, double scale,
+                                    float* loss, float* lse, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* Bytes of workspace det_linear_cross_entropy_backward needs (0 when the arguments are invalid). */
+size_t det_linear_cross_entropy_backward_workspace_size(int64_t rows, int64_t vocab, int64_t d,
+                                                        det_dtype dtype);
+
+/* Gradients of det_linear_cross_entropy's loss, the logits made again piece by piece:
+ *   D = exp(z - lse) - hit;  dx = scale * dloss * (D weight);  dweight = scale * (dloss D)^T x
+ * D is rounded to dtype once.  A row that is not scored has dx 0 and adds nothing to dweight,
+ * whatever it holds.  exp(z - lse) is off by about |lse| 2^-24 relative to it.
+ * lse:      float [rows], as det_linear_cross_entropy wrote it for these x, weight and scale.
+ * dloss:    float [rows].
+ * dx:       [rows * d].  dweight: [vocab * d].
+ * vocab, d >= 1; no rows: dweight is 0.  Order: fixed as for det_linear_cross_entropy. */
+det_status det_linear_cross_entropy_backward(const void* x, int64_t x_stride, const void* weight,
+                                             int64_t weight_stride, const int64_t* targets,
+                                             const float* lse, const float* dloss, int64_t rows,
+                                             int64_t vocab, int64_t d, det_dtype dtype,
+                                             double scale, void* dx, void* dweight, void* ws,
+                                             size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------ introspection */
 

@@ -74,6 +74,15 @@ det_status scatter_running_launch(const void* values, const int32_t* index, int6
                                   int64_t row_len, det_dtype dt, void* out, int64_t num_out,
                                   void* prev, int64_t* n_skipped, void* ws, hipStream_t s);
 
+// Stable sort of n row indices by destination (entries outside [0, num_out) left out): keys and
+// source rows in ascending (key, source) order, off[b] the first position with key >= b.
+struct SortedRows {
+    const uint32_t *keys, *src, *off;
+};
+size_t sort_rows_workspace(int64_t n, int64_t num_out);
+det_status sort_rows_launch(const int32_t* index, int64_t n, int64_t num_out, void* ws,
+                            SortedRows* out, hipStream_t s);
+
 // ---- language-model operators (arguments checked by the caller)
 // Inputs from this many bytes on are loaded past the caches.  Half of the 256 MB last-level cache:
 // below it the producer's data may still be there, above it the loads only push out what the
@@ -105,6 +114,98 @@ struct NormBackCall {
 };
 size_t norm_backward_workspace(int64_t rows, int64_t d, det_dtype dtype);
 det_status norm_backward_launch(const NormBackCall& c, void* ws, hipStream_t s);
+
+struct LayerCall {
+    const void *x, *residual, *weight, *bias;
+    void *h, *y;
+    float *mean, *rstd;
+    int64_t x_stride, residual_stride, rows, d;
+    float eps;
+    det_dtype dtype;
+};
+det_status layer_norm_launch(const LayerCall& c, hipStream_t s);
+
+struct LayerBackCall {
+    const void *dy, *h, *weight, *dh;
+    const float *mean, *rstd;
+    void *dx, *dweight, *dbias;      // dbias NULL: not wanted
+    int64_t dy_stride, h_stride, dh_stride, rows, d;
+    det_dtype dtype;
+};
+size_t layer_norm_backward_workspace(int64_t rows, int64_t d, det_dtype dtype);
+det_status layer_norm_backward_launch(const LayerBackCall& c, void* ws, hipStream_t s);
+
+struct EmbedCall {
+    const void *table, *tokens;
+    void* out;
+    int64_t table_stride, n, vocab, d;
+    float scale;
+    bool wide;         // tokens are int64, else int32
+    det_dtype dtype;
+};
+det_status embedding_launch(const EmbedCall& c, hipStream_t s);
+
+struct EmbedBackCall {
+    const void *dout, *tokens;
+    void* dtable;
+    int64_t stride, n, vocab, d;
+    float scale;
+    bool wide;
+    det_dtype dtype;
+};
+size_t embedding_backward_workspace(int64_t n, int64_t vocab, int64_t d);
+det_status embedding_backward_launch(const EmbedBackCall& c, void* ws, hipStream_t s);
+
+// h[t] = a[t] h[t-1] + b[t] over [batch][steps][d]
+struct ScanCall {
+    const void *gate, *x;
+    const float* state0;       // NULL: zeros
+    const int32_t* lengths;    // NULL: every sequence has all steps
+    void* h;
+    float* state;
+    int64_t batch, steps, d;
+    bool sigmoid;
+    det_dtype dtype;
+};
+size_t gated_scan_workspace(int64_t batch, int64_t steps, int64_t d, det_dtype dtype);
+det_status gated_scan_launch(const ScanCall& c, void* ws, hipStream_t s);
+
+struct ScanBackCall {
+    const void *dh, *gate, *x, *h;
+    const float *state0, *dstate;      // NULL: zeros
+    const int32_t* lengths;
+    void *dgate, *dx;
+    float* dstate0;                    // NULL: not wanted
+    int64_t batch, steps, d;
+    bool sigmoid;
+    det_dtype dtype;
+};
+size_t gated_scan_backward_workspace(int64_t batch, int64_t steps, int64_t d, det_dtype dtype);
+det_status gated_scan_backward_launch(const ScanBackCall& c, void* ws, hipStream_t s);
+
+// cross entropy of softmax(scale * x weight^T)
+struct XentCall {
+    const void *x, *weight;
+    const int64_t* targets;
+    float *loss, *lse;
+    int64_t x_stride, w_stride, rows, vocab, d;
+    float scale;
+    det_dtype dtype;
+};
+size_t xent_workspace(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype);
+det_status xent_launch(const XentCall& c, void* ws, hipStream_t s);
+
+struct XentBackCall {
+    const void *x, *weight;
+    const int64_t* targets;
+    const float *lse, *dloss;
+    void *dx, *dweight;
+    int64_t x_stride, w_stride, rows, vocab, d;
+    float scale;
+    det_dtype dtype;
+};
+size_t xent_backward_workspace(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype);
+det_status xent_backward_launch(const XentBackCall& c, void* ws, hipStream_t s);
 
 constexpr int kBiasMaxSide = 128;      // buckets of one side of the relative position bias
 struct BiasCall {

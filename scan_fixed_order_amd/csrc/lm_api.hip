@@ -319,3 +319,340 @@ det_status det_token_logprobs_backward(const void* logits, int64_t row_stride,
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- embedding
+
+namespace {
+
+bool token_dtype(det_dtype t) { return t == DET_I32 || t == DET_I64; }
+
+size_t token_size(det_dtype t) { return t == DET_I64 ? 8 : 4; }
+
+}  // namespace
+
+extern "C" {
+
+det_status det_embedding(const void* table, int64_t table_stride, const void* tokens,
+                         det_dtype token_type, int64_t n, int64_t vocab, int64_t d,
+                         det_dtype dtype, double scale, void* out, void* stream) {
+    if (!lm_dtype(dtype) || !token_dtype(token_type)) return DET_ERROR_UNSUPPORTED;
+    if (n < 0 || vocab < 0 || d < 0 || !isfinite((float)scale)) return DET_ERROR_INVALID_VALUE;
+    if (n > DET_MAX_N || vocab > DET_MAX_N || d > DET_MAX_N) return DET_ERROR_TOO_LARGE;
+    if (n == 0 || d == 0) return DET_SUCCESS;
+    const size_t es = lm_size(dtype);
+    const Rows in{table, table_stride, vocab, d, es}, o{out, d, n, d, es};
+    if ((vocab > 0 && !in.ok()) || !o.ok() || !tokens || !aligned(tokens, token_size(token_type)))
+        return DET_ERROR_INVALID_VALUE;
+    if (!in.fits() || !o.fits()) return DET_ERROR_TOO_LARGE;
+    if ((vocab > 0 && !apart(in, o, false)) || !apart(tokens, (size_t)n * token_size(token_type), o))
+        return DET_ERROR_INVALID_VALUE;
+    const EmbedCall c{table, tokens, out, table_stride, n, vocab, d, (float)scale,
+                      token_type == DET_I64, dtype};
+    return embedding_launch(c, static_cast<hipStream_t>(stream));
+}
+
+size_t det_embedding_backward_workspace_size(int64_t n, int64_t vocab, int64_t d, det_dtype dtype) {
+    if (n < 0 || n > DET_MAX_N || vocab < 0 || vocab >= DET_MAX_N || d < 0 || d > DET_MAX_N ||
+        !lm_dtype(dtype) || (double)n * d * 4 > kMaxBytes)
+        return 0;
+    return embedding_backward_workspace(n, vocab, d);
+}
+
+det_status det_embedding_backward(const void* dout, int64_t dout_stride, const void* tokens,
+                                  det_dtype token_type, int64_t n, int64_t vocab, int64_t d,
+                                  det_dtype dtype, double scale, void* dtable, void* ws,
+                                  size_t ws_bytes, void* stream) {
+    if (!lm_dtype(dtype) || !token_dtype(token_type)) return DET_ERROR_UNSUPPORTED;
+    if (n < 0 || vocab < 0 || d < 0 || !isfinite((float)scale)) return DET_ERROR_INVALID_VALUE;
+    if (n > DET_MAX_N || vocab >= DET_MAX_N || d > DET_MAX_N) return DET_ERROR_TOO_LARGE;
+    if (vocab == 0 || d == 0) return DET_SUCCESS;
+    const size_t es = lm_size(dtype), tbytes = (size_t)n * token_size(token_type);
+    const Rows in{dout, dout_stride, n, d, es}, o{dtable, d, vocab, d, es};
+    if (!o.ok()) return DET_ERROR_INVALID_VALUE;
+    if (!o.fits()) return DET_ERROR_TOO_LARGE;
+    if (n > 0) {
+        if (!in.ok() || !tokens || !aligned(tokens, token_size(token_type)))
+            return DET_ERROR_INVALID_VALUE;
+        if (!in.fits() || (double)n * d * 4 > kMaxBytes) return DET_ERROR_TOO_LARGE;
+        if (!apart(in, o, false) || !apart(tokens, tbytes, o)) return DET_ERROR_INVALID_VALUE;
+    }
+    const det_status st = ws_status(ws, ws_bytes, embedding_backward_workspace(n, vocab, d));
+    if (st != DET_SUCCESS) return st;
+    const EmbedBackCall c{dout, tokens, dtable, dout_stride, n, vocab, d, (float)scale,
+                          token_type == DET_I64, dtype};
+    return embedding_backward_launch(c, ws, static_cast<hipStream_t>(stream));
+}
+
+// ---------------------------------------------------------------- layer norm
+
+det_status det_layer_norm(const void* x, int64_t x_stride, const void* residual,
+                          int64_t residual_stride, const void* weight, const void* bias,
+                          int64_t rows, int64_t d, det_dtype dtype, double eps, void* h, void* y,
+                          float* mean, float* rstd, void* stream) {
+    if (!lm_dtype(dtype)) return DET_ERROR_UNSUPPORTED;
+    if (rows < 0 || d < 0 || !(eps >= 0.0) || !isfinite((float)eps))
+        return DET_ERROR_INVALID_VALUE;
+    if (rows > DET_MAX_N || d > DET_MAX_N) return DET_ERROR_TOO_LARGE;
+    if (rows == 0) return DET_SUCCESS;
+    if (d == 0) return DET_ERROR_INVALID_VALUE;
+    const size_t es = lm_size(dtype), wbytes = (size_t)d * es, sbytes = (size_t)rows * 4;
+    const Rows in{x, x_stride, rows, d, es}, res{residual, residual_stride, rows, d, es};
+    const Rows ho{h, d, rows, d, es}, yo{y, d, rows, d, es};
+    if (!in.ok() || !yo.ok() || !weight || !aligned(weight, es) || !aligned(bias, es) ||
+        !aligned(mean, 4) || !aligned(rstd, 4))
+        return DET_ERROR_INVALID_VALUE;
+    if (residual ? !res.ok() || !ho.ok() : h != nullptr) return DET_ERROR_INVALID_VALUE;
+    if (!in.fits() || !yo.fits() || (residual && !res.fits())) return DET_ERROR_TOO_LARGE;
+    // what is written lies apart from what is read and from each other; h may replace an input
+    if (!apart(in, yo, false) || overlap(mean, sbytes, rstd, sbytes)) return DET_ERROR_INVALID_VALUE;
+    if (residual && (!apart(res, yo, false) || !apart(in, ho, true) || !apart(res, ho, true) ||
+                     !apart(ho, yo, false)))
+        return DET_ERROR_INVALID_VALUE;
+    for (const void* w : {weight, bias})
+        if (!apart(w, wbytes, yo) || (residual && !apart(w, wbytes, ho)) ||
+            overlap(w, wbytes, mean, sbytes) || overlap(w, wbytes, rstd, sbytes))
+            return DET_ERROR_INVALID_VALUE;
+    for (const Rows* r : {&in, &res, &ho, &yo})
+        if (r->p && (!apart(mean, sbytes, *r) || !apart(rstd, sbytes, *r)))
+            return DET_ERROR_INVALID_VALUE;
+    const LayerCall c{x, residual, weight, bias, h, y, mean, rstd, x_stride, residual_stride, rows, d,
+                      (float)eps, dtype};
+    return layer_norm_launch(c, static_cast<hipStream_t>(stream));
+}
+
+size_t det_layer_norm_backward_workspace_size(int64_t rows, int64_t d, det_dtype dtype) {
+    if (rows < 0 || rows > DET_MAX_N || d < 0 || d > DET_MAX_N || !lm_dtype(dtype)) return 0;
+    return layer_norm_backward_workspace(rows, d, dtype);
+}
+
+det_status det_layer_norm_backward(const void* dy, int64_t dy_stride, const void* h,
+                                   int64_t h_stride, const void* weight, const float* mean,
+                                   const float* rstd, const void* dh, int64_t dh_stride,
+                                   int64_t rows, int64_t d, det_dtype dtype, void* dx,
+                                   void* dweight, void* dbias, void* ws, size_t ws_bytes,
+                                   void* stream) {
+    if (!lm_dtype(dtype)) return DET_ERROR_UNSUPPORTED;
+    if (rows < 0 || d < 0) return DET_ERROR_INVALID_VALUE;
+    if (rows > DET_MAX_N || d > DET_MAX_N) return DET_ERROR_TOO_LARGE;
+    if (d == 0) return rows == 0 ? DET_SUCCESS : DET_ERROR_INVALID_VALUE;
+    const size_t es = lm_size(dtype), wbytes = (size_t)d * es, sbytes = (size_t)rows * 4;
+    const Rows a{dy, dy_stride, rows, d, es}, b{h, h_stride, rows, d, es};
+    const Rows e{dh, dh_stride, rows, d, es}, o{dx, d, rows, d, es};
+    if (!dweight || !aligned(dweight, es) || !aligned(dbias, es) ||
+        overlap(dweight, wbytes, dbias, wbytes))
+        return DET_ERROR_INVALID_VALUE;
+    if (rows > 0) {
+        if (!a.ok() || !b.ok() || !o.ok() || !weight || !aligned(weight, es) || !mean || !rstd ||
+            !aligned(mean, 4) || !aligned(rstd, 4) || (dh && !e.ok()))
+            return DET_ERROR_INVALID_VALUE;
+        if (!a.fits() || !b.fits() || !o.fits() || (dh && !e.fits())) return DET_ERROR_TOO_LARGE;
+        // rows beyond the registers are read twice, once more for the weights' sums
+        const bool in_place = d <= 16384;
+        if (!apart(a, o, in_place) || !apart(b, o, in_place) || (dh && !apart(e, o, in_place)) ||
+            !apart(weight, wbytes, o) || !apart(mean, sbytes, o) || !apart(rstd, sbytes, o))
+            return DET_ERROR_INVALID_VALUE;
+        for (const void* g : {(const void*)dweight, (const void*)dbias}) {
+            for (const Rows* r : {&a, &b, &e, &o})
+                if (r->p && !apart(g, wbytes, *r)) return DET_ERROR_INVALID_VALUE;
+            if (overlap(g, wbytes, weight, wbytes) || overlap(g, wbytes, mean, sbytes) ||
+                overlap(g, wbytes, rstd, sbytes))
+                return DET_ERROR_INVALID_VALUE;
+        }
+    }
+    const det_status st = ws_status(ws, ws_bytes, layer_norm_backward_workspace(rows, d, dtype));
+    if (st != DET_SUCCESS) return st;
+    const LayerBackCall c{dy, h, weight, dh, mean, rstd, dx, dweight, dbias, dy_stride, h_stride,
+                          dh_stride, rows, d, dtype};
+    return layer_norm_backward_launch(c, ws, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- gated recurrence
+
+namespace {
+
+// what both directions check of the sizes
+det_status scan_sizes(int64_t batch, int64_t steps, int64_t d, det_dtype dtype, unsigned flags) {
+    if (!lm_dtype(dtype)) return DET_ERROR_UNSUPPORTED;
+    if (flags & ~DET_GATE_SIGMOID) return DET_ERROR_INVALID_VALUE;
+    if (batch < 0 || steps < 0 || d < 0) return DET_ERROR_INVALID_VALUE;
+    if (steps > DET_MAX_N || (double)batch * d > (double)DET_MAX_N || batch > DET_MAX_N ||
+        d > DET_MAX_N || (double)batch * d * (double)steps * 4 > kMaxBytes)
+        return DET_ERROR_TOO_LARGE;
+    return DET_SUCCESS;
+}
+
+struct Range {
+    const void* p;
+    size_t bytes, align;
+};
+
+// every output present and aligned, apart from the inputs and from the other outputs; one may be the
+// input that `same` names (exactly)
+template <int NI, int NO>
+bool ranges_ok(const Range (&in)[NI], const Range (&out)[NO], const void* same_in,
+               const void* same_out) {
+    for (const Range& i : in)
+        if (!aligned(i.p, i.align)) return false;
+    for (const Range& o : out) {
+        if (!aligned(o.p, o.align)) return false;
+        for (const Range& i : in)
+            if (!(o.p == same_out && i.p == same_in && o.p == i.p) &&
+                overlap(o.p, o.bytes, i.p, i.bytes))
+                return false;
+        for (const Range& other : out)
+            if (&o != &other && overlap(o.p, o.bytes, other.p, other.bytes)) return false;
+    }
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t det_gated_scan_workspace_size(int64_t batch, int64_t steps, int64_t d, det_dtype dtype) {
+    if (scan_sizes(batch, steps, d, dtype, 0) != DET_SUCCESS) return 0;
+    return batch && steps && d ? gated_scan_workspace(batch, steps, d, dtype) : 256;
+}
+
+det_status det_gated_scan(const void* gate, const void* x, const float* state0,
+                          const int32_t* lengths, unsigned flags, int64_t batch, int64_t steps,
+                          int64_t d, det_dtype dtype, void* h, float* state, void* ws,
+                          size_t ws_bytes, void* stream) {
+    const det_status bad = scan_sizes(batch, steps, d, dtype, flags);
+    if (bad != DET_SUCCESS) return bad;
+    if (batch == 0 || d == 0) return DET_SUCCESS;
+    if (steps == 0) return DET_ERROR_INVALID_VALUE;
+    const size_t es = lm_size(dtype), cells = (size_t)batch * d, n = cells * steps * es;
+    if (!gate || !x || !h || !state) return DET_ERROR_INVALID_VALUE;
+    const Range in[] = {{gate, n, es}, {x, n, es}, {state0, cells * 4, 4}, {lengths, (size_t)batch * 4, 4}};
+    const Range out[] = {{h, n, es}, {state, cells * 4, 4}};
+    // the first state is read before the last is written only by sequences of one workgroup
+    if (!ranges_ok(in, out, steps <= 8 ? state0 : nullptr, state)) return DET_ERROR_INVALID_VALUE;
+    const det_status st = ws_status(ws, ws_bytes, gated_scan_workspace(batch, steps, d, dtype));
+    if (st != DET_SUCCESS) return st;
+    const ScanCall c{gate, x, state0, lengths, h, state, batch, steps, d,
+                     (flags & DET_GATE_SIGMOID) != 0, dtype};
+    return gated_scan_launch(c, ws, static_cast<hipStream_t>(stream));
+}
+
+size_t det_gated_scan_backward_workspace_size(int64_t batch, int64_t steps, int64_t d,
+                                              det_dtype dtype) {
+    if (scan_sizes(batch, steps, d, dtype, 0) != DET_SUCCESS) return 0;
+    return batch && steps && d ? gated_scan_backward_workspace(batch, steps, d, dtype) : 256;
+}
+
+det_status det_gated_scan_backward(const void* dh, const void* gate, const void* x, const void* h,
+                                   const float* state0, const float* dstate,
+                                   const int32_t* lengths, unsigned flags, int64_t batch,
+                                   int64_t steps, int64_t d, det_dtype dtype, void* dgate,
+                                   void* dx, float* dstate0, void* ws, size_t ws_bytes,
+                                   void* stream) {
+    const det_status bad = scan_sizes(batch, steps, d, dtype, flags);
+    if (bad != DET_SUCCESS) return bad;
+    if (batch == 0 || d == 0) return DET_SUCCESS;
+    if (steps == 0) return DET_ERROR_INVALID_VALUE;
+    const size_t es = lm_size(dtype), cells = (size_t)batch * d, n = cells * steps * es;
+    if (!dh || !gate || !x || !h || !dgate || !dx) return DET_ERROR_INVALID_VALUE;
+    const Range in[] = {{dh, n, es}, {gate, n, es}, {x, n, es}, {h, n, es}, {state0, cells * 4, 4},
+                        {dstate, cells * 4, 4}, {lengths, (size_t)batch * 4, 4}};
+    const Range out[] = {{dgate, n, es}, {dx, n, es}, {dstate0, cells * 4, 4}};
+    if (!ranges_ok(in, out, nullptr, nullptr)) return DET_ERROR_INVALID_VALUE;
+    const det_status st = ws_status(ws, ws_bytes, gated_scan_backward_workspace(batch, steps, d, dtype));
+    if (st != DET_SUCCESS) return st;
+    const ScanBackCall c{dh, gate, x, h, state0, dstate, lengths, dgate, dx, dstate0, batch, steps, d,
+                         (flags & DET_GATE_SIGMOID) != 0, dtype};
+    return gated_scan_backward_launch(c, ws, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- linear cross entropy
+
+namespace {
+
+constexpr int64_t kXentMaxRows = 1 << 20, kXentMaxD = 1 << 20;
+
+det_status xent_sizes(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype) {
+    if (!lm_dtype(dtype)) return DET_ERROR_UNSUPPORTED;
+    if (rows < 0 || vocab < 0 || d < 0) return DET_ERROR_INVALID_VALUE;
+    if (rows > kXentMaxRows || vocab > DET_MAX_N || d > kXentMaxD) return DET_ERROR_TOO_LARGE;
+    return DET_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t det_linear_cross_entropy_workspace_size(int64_t rows, int64_t vocab, int64_t d,
+                                               det_dtype dtype) {
+    return xent_sizes(rows, vocab, d, dtype) == DET_SUCCESS ? xent_workspace(rows, vocab, d, dtype) : 0;
+}
+
+det_status det_linear_cross_entropy(const void* x, int64_t x_stride, const void* weight,
+                                    int64_t weight_stride, const int64_t* targets, int64_t rows,
+                                    int64_t vocab, int64_t d, det_dtype dtype, double scale,
+                                    float* loss, float* lse, void* ws, size_t ws_bytes,
+                                    void* stream) {
+    const det_status bad = xent_sizes(rows, vocab, d, dtype);
+    if (bad != DET_SUCCESS) return bad;
+    if (!((float)scale > 0.0f) || !isfinite((float)scale)) return DET_ERROR_INVALID_VALUE;
+    if (rows == 0) return DET_SUCCESS;
+    if (vocab == 0 || d == 0) return DET_ERROR_INVALID_VALUE;
+    const size_t es = lm_size(dtype), rbytes = (size_t)rows * 4;
+    const Rows xr{x, x_stride, rows, d, es}, wr{weight, weight_stride, vocab, d, es};
+    if (!xr.ok() || !wr.ok() || !targets || !aligned(targets, 8) || !loss || !lse ||
+        !aligned(loss, 4) || !aligned(lse, 4))
+        return DET_ERROR_INVALID_VALUE;
+    if (!xr.fits() || !wr.fits()) return DET_ERROR_TOO_LARGE;
+    for (const float* o : {loss, lse})
+        if (!apart(o, rbytes, xr) || !apart(o, rbytes, wr) || overlap(o, rbytes, targets, (size_t)rows * 8))
+            return DET_ERROR_INVALID_VALUE;
+    if (overlap(loss, rbytes, lse, rbytes)) return DET_ERROR_INVALID_VALUE;
+    const det_status st = ws_status(ws, ws_bytes, xent_workspace(rows, vocab, d, dtype));
+    if (st != DET_SUCCESS) return st;
+    const XentCall c{x, weight, targets, loss, lse, x_stride, weight_stride, rows, vocab, d,
+                     (float)scale, dtype};
+    return xent_launch(c, ws, static_cast<hipStream_t>(stream));
+}
+
+size_t det_linear_cross_entropy_backward_workspace_size(int64_t rows, int64_t vocab, int64_t d,
+                                                        det_dtype dtype) {
+    return xent_sizes(rows, vocab, d, dtype) == DET_SUCCESS
+               ? xent_backward_workspace(rows, vocab, d, dtype) : 0;
+}
+
+det_status det_linear_cross_entropy_backward(const void* x, int64_t x_stride, const void* weight,
+                                             int64_t weight_stride, const int64_t* targets,
+                                             const float* lse, const float* dloss, int64_t rows,
+                                             int64_t vocab, int64_t d, det_dtype dtype,
+                                             double scale, void* dx, void* dweight, void* ws,
+                                             size_t ws_bytes, void* stream) {
+    const det_status bad = xent_sizes(rows, vocab, d, dtype);
+    if (bad != DET_SUCCESS) return bad;
+    if (!((float)scale > 0.0f) || !isfinite((float)scale)) return DET_ERROR_INVALID_VALUE;
+    if (vocab == 0 || d == 0) return DET_ERROR_INVALID_VALUE;
+    const size_t es = lm_size(dtype), rbytes = (size_t)rows * 4;
+    const Rows xr{x, x_stride, rows, d, es}, wr{weight, weight_stride, vocab, d, es};
+    const Rows dxr{dx, d, rows, d, es}, dwr{dweight, d, vocab, d, es};
+    if (rows == 0) {
+        if (!dwr.ok()) return DET_ERROR_INVALID_VALUE;
+        if (!dwr.fits()) return DET_ERROR_TOO_LARGE;
+    } else if (!xr.ok() || !wr.ok() || !dxr.ok() || !dwr.ok() || !targets || !aligned(targets, 8) || !lse ||
+        !dloss || !aligned(lse, 4) || !aligned(dloss, 4))
+        return DET_ERROR_INVALID_VALUE;
+    if (!xr.fits() || !wr.fits() || !dwr.fits()) return DET_ERROR_TOO_LARGE;
+    if (!apart(dxr, dwr, false)) return DET_ERROR_INVALID_VALUE;
+    for (const Rows* o : {&dxr, &dwr})
+        if (!apart(xr, *o, false) || !apart(wr, *o, false) || !apart(targets, (size_t)rows * 8, *o) ||
+            !apart(lse, rbytes, *o) || !apart(dloss, rbytes, *o))
+            return DET_ERROR_INVALID_VALUE;
+    const det_status st = ws_status(ws, ws_bytes, xent_backward_workspace(rows, vocab, d, dtype));
+    if (st != DET_SUCCESS) return st;
+    const XentBackCall c{x, weight, targets, lse, dloss, dx, dweight, x_stride, weight_stride, rows,
+                         vocab, d, (float)scale, dtype};
+    return xent_backward_launch(c, ws, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

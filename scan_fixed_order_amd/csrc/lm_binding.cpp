@@ -348,6 +348,258 @@ Tensor token_logprobs_backward(const Tensor& logits, const Tensor& targets, cons
     return o;
 }
 
+// ---------------------------------------------------------------- layer norm
+
+py::tuple layer_norm(const Tensor& x, const Tensor& weight, const Optional& bias, double eps,
+                     const Optional& residual) {
+    const det_dtype type = lm_type(x);
+    const int64_t rows = rows_of(x, "x"), d = x.size(-1);
+    const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
+    of(weight, x.scalar_type(), {d}, "weight");
+    if (bias) of(*bias, x.scalar_type(), {d}, "bias");
+    const int64_t stride = row_stride(x, "x");
+    int64_t res_stride = 0;
+    if (residual) {
+        same_type(*residual, x, "residual");
+        if (residual->sizes() != x.sizes()) wrong_value("residual must have the shape of x");
+        res_stride = row_stride(*residual, "residual");
+    }
+    void* const xp = pointer(x, x);
+    void* const rp = pointer(residual, x);
+    void* const wp = pointer(weight, x);
+    void* const bp = pointer(bias, x);
+    const Guard guard(x.device());
+    Tensor h;
+    if (residual) h = empty(x.sizes(), x.scalar_type(), x);
+    const Tensor y = empty(x.sizes(), x.scalar_type(), x);
+    const Tensor mean = empty(lead, at::kFloat, x);
+    const Tensor rstd = empty(lead, at::kFloat, x);
+    check_status(det_layer_norm(xp, stride, rp, res_stride, wp, bp, rows, d, type, eps,
+                                residual ? h.data_ptr() : nullptr, y.data_ptr(),
+                                mean.data_ptr<float>(), rstd.data_ptr<float>(), stream(x)),
+                 "det_layer_norm");
+    return py::make_tuple(y, residual ? h : x, mean, rstd);
+}
+
+py::tuple layer_norm_backward(const Tensor& dy, const Tensor& h, const Tensor& weight,
+                              const Tensor& mean, const Tensor& rstd, const Optional& dh,
+                              bool bias, const Optional& ws) {
+    const det_dtype type = lm_type(h);
+    const int64_t rows = rows_of(h, "h"), d = h.size(-1);
+    const at::IntArrayRef lead = h.sizes().slice(0, h.dim() - 1);
+    of(weight, h.scalar_type(), {d}, "weight");
+    of(mean, at::kFloat, lead, "mean");
+    of(rstd, at::kFloat, lead, "rstd");
+    same_type(dy, h, "dy");
+    if (dy.sizes() != h.sizes()) wrong_value("dy must have the shape of h");
+    if (dh) {
+        same_type(*dh, h, "dh");
+        if (dh->sizes() != h.sizes()) wrong_value("dh must have the shape of h");
+    }
+    check_workspace(ws);
+    void* const dyp = pointer(dy, h);
+    void* const hp = pointer(h, h);
+    void* const wp = pointer(weight, h);
+    void* const mp = pointer(mean, h);
+    void* const sp = pointer(rstd, h);
+    void* const dhp = pointer(dh, h);
+    const Guard guard(h.device());
+    const Tensor dx = empty(h.sizes(), h.scalar_type(), h);
+    const Tensor dweight = empty({d}, h.scalar_type(), h);
+    Tensor dbias;
+    if (bias) dbias = empty({d}, h.scalar_type(), h);
+    const Tensor w = workspace(det_layer_norm_backward_workspace_size(rows, d, type), ws, h);
+    check_status(det_layer_norm_backward(dyp, row_stride(dy, "dy"), hp, row_stride(h, "h"), wp,
+                                         static_cast<const float*>(mp),
+                                         static_cast<const float*>(sp), dhp,
+                                         dh ? row_stride(*dh, "dh") : 0, rows, d, type,
+                                         dx.data_ptr(), dweight.data_ptr(),
+                                         bias ? dbias.data_ptr() : nullptr, pointer(w, h),
+                                         w.nbytes(), stream(h)),
+                 "det_layer_norm_backward");
+    return py::make_tuple(dx, dweight, bias ? py::cast(dbias) : py::object(py::none()));
+}
+
+// ---------------------------------------------------------------- embedding
+
+det_dtype token_type(const Tensor& tokens) {
+    if (tokens.scalar_type() != at::kInt && tokens.scalar_type() != at::kLong)
+        wrong_type(std::string("tokens must be Int or Long, got ") + c10::toString(tokens.scalar_type()));
+    if (!tokens.is_contiguous()) wrong_value("det needs contiguous tensors (tokens)");
+    return tokens.scalar_type() == at::kInt ? DET_I32 : DET_I64;
+}
+
+Tensor embedding(const Tensor& table, const Tensor& tokens, double scale) {
+    const det_dtype type = lm_type(table), ids = token_type(tokens);
+    if (table.dim() != 2) wrong_value("table must be [vocab, d]");
+    const int64_t stride = row_stride(table, "table");
+    void* const tp = pointer(table, table);
+    void* const ip = pointer(tokens, table);
+    const Guard guard(table.device());
+    at::DimVector shape(tokens.sizes().begin(), tokens.sizes().end());
+    shape.push_back(table.size(1));
+    const Tensor out = empty(shape, table.scalar_type(), table);
+    check_status(det_embedding(tp, stride, ip, ids, tokens.numel(), table.size(0), table.size(1),
+                               type, scale, out.data_ptr(), stream(table)),
+                 "det_embedding");
+    return out;
+}
+
+Tensor embedding_backward(const Tensor& dout, const Tensor& tokens, int64_t vocab, double scale,
+                          const Optional& ws) {
+    const det_dtype type = lm_type(dout), ids = token_type(tokens);
+    rows_of(dout, "dout");
+    if (dout.sizes().slice(0, dout.dim() - 1) != tokens.sizes())
+        wrong_value("dout must be tokens' shape and a row for each");
+    if (vocab < 0) wrong_value("vocab must not be negative");
+    const int64_t stride = row_stride(dout, "dout"), n = tokens.numel(), d = dout.size(-1);
+    check_workspace(ws);
+    void* const dp = pointer(dout, dout);
+    void* const ip = pointer(tokens, dout);
+    const Guard guard(dout.device());
+    const Tensor dtable = empty({vocab, d}, dout.scalar_type(), dout);
+    const Tensor w = workspace(det_embedding_backward_workspace_size(n, vocab, d, type), ws, dout);
+    check_status(det_embedding_backward(dp, stride, ip, ids, n, vocab, d, type, scale,
+                                        dtable.data_ptr(), pointer(w, dout), w.nbytes(), stream(dout)),
+                 "det_embedding_backward");
+    return dtable;
+}
+
+// ---------------------------------------------------------------- gated recurrence
+
+struct ScanShape {
+    int64_t batch, steps, d;
+};
+
+// [batch, steps, d], all contiguous and of one type
+ScanShape scan_shape(const Tensor& gate) {
+    if (gate.dim() != 3) wrong_value("gate must be [batch, steps, d]");
+    of(gate, gate.scalar_type(), gate.sizes(), "gate");
+    return {gate.size(0), gate.size(1), gate.size(2)};
+}
+
+py::tuple gated_scan(const Tensor& gate, const Tensor& x, const Optional& state, bool sigmoid,
+                     const Optional& lengths, const Optional& state_out, const Optional& ws) {
+    const det_dtype type = lm_type(gate);
+    const ScanShape n = scan_shape(gate);
+    of(x, gate.scalar_type(), gate.sizes(), "x");
+    if (state) of(*state, at::kFloat, {n.batch, n.d}, "state");
+    if (lengths) of(*lengths, at::kInt, {n.batch}, "lengths");
+    if (state_out) of(*state_out, at::kFloat, {n.batch, n.d}, "state_out");
+    check_workspace(ws);
+    void* const gp = pointer(gate, gate);
+    void* const xp = pointer(x, gate);
+    void* const sp = pointer(state, gate);
+    void* const lp = pointer(lengths, gate);
+    const Guard guard(gate.device());
+    const Tensor h = empty(gate.sizes(), gate.scalar_type(), gate);
+    const Tensor end = state_out ? *state_out : empty({n.batch, n.d}, at::kFloat, gate);
+    void* const ep = pointer(end, gate);
+    const Tensor w = workspace(det_gated_scan_workspace_size(n.batch, n.steps, n.d, type), ws, gate);
+    check_status(det_gated_scan(gp, xp, static_cast<const float*>(sp), static_cast<const int32_t*>(lp),
+                                sigmoid ? DET_GATE_SIGMOID : 0, n.batch, n.steps, n.d, type,
+                                h.data_ptr(), static_cast<float*>(ep), pointer(w, gate), w.nbytes(),
+                                stream(gate)),
+                 "det_gated_scan");
+    return py::make_tuple(h, end);
+}
+
+py::tuple gated_scan_backward(const Tensor& dh, const Tensor& gate, const Tensor& x, const Tensor& h,
+                              const Optional& state, const Optional& dstate, bool sigmoid,
+                              const Optional& lengths, const Optional& ws) {
+    const det_dtype type = lm_type(gate);
+    const ScanShape n = scan_shape(gate);
+    of(dh, gate.scalar_type(), gate.sizes(), "dh");
+    of(x, gate.scalar_type(), gate.sizes(), "x");
+    of(h, gate.scalar_type(), gate.sizes(), "h");
+    if (state) of(*state, at::kFloat, {n.batch, n.d}, "state");
+    if (dstate) of(*dstate, at::kFloat, {n.batch, n.d}, "dstate");
+    if (lengths) of(*lengths, at::kInt, {n.batch}, "lengths");
+    check_workspace(ws);
+    void* const dp = pointer(dh, gate);
+    void* const gp = pointer(gate, gate);
+    void* const xp = pointer(x, gate);
+    void* const hp = pointer(h, gate);
+    void* const sp = pointer(state, gate);
+    void* const ep = pointer(dstate, gate);
+    void* const lp = pointer(lengths, gate);
+    const Guard guard(gate.device());
+    const Tensor dgate = empty(gate.sizes(), gate.scalar_type(), gate);
+    const Tensor dx = empty(gate.sizes(), gate.scalar_type(), gate);
+    Tensor first;
+    if (state) first = empty({n.batch, n.d}, at::kFloat, gate);
+    const Tensor w =
+        workspace(det_gated_scan_backward_workspace_size(n.batch, n.steps, n.d, type), ws, gate);
+    check_status(det_gated_scan_backward(dp, gp, xp, hp, static_cast<const float*>(sp),
+                                         static_cast<const float*>(ep),
+                                         static_cast<const int32_t*>(lp),
+                                         sigmoid ? DET_GATE_SIGMOID : 0, n.batch, n.steps, n.d, type,
+                                         dgate.data_ptr(), dx.data_ptr(),
+                                         state ? first.data_ptr<float>() : nullptr,
+                                         pointer(w, gate), w.nbytes(), stream(gate)),
+                 "det_gated_scan_backward");
+    return py::make_tuple(dgate, dx, state ? py::cast(first) : py::object(py::none()));
+}
+
+// ---------------------------------------------------------------- linear cross entropy
+
+// x [..., d], weight [vocab, d], targets [...]
+void xent_shapes(const Tensor& x, const Tensor& weight, const Tensor& targets) {
+    rows_of(x, "x");
+    same_type(weight, x, "weight");
+    if (weight.dim() != 2 || weight.size(1) != x.size(-1)) wrong_value("weight must be [vocab, d]");
+    of(targets, at::kLong, x.sizes().slice(0, x.dim() - 1), "targets");
+}
+
+py::tuple linear_cross_entropy(const Tensor& x, const Tensor& weight, const Tensor& targets,
+                               double scale, const Optional& ws) {
+    const det_dtype type = lm_type(x);
+    xent_shapes(x, weight, targets);
+    check_workspace(ws);
+    const int64_t rows = targets.numel(), vocab = weight.size(0), d = x.size(-1);
+    const int64_t xs = row_stride(x, "x"), wst = row_stride(weight, "weight");
+    void* const xp = pointer(x, x);
+    void* const wp = pointer(weight, x);
+    void* const tp = pointer(targets, x);
+    const Guard guard(x.device());
+    const Tensor loss = empty(targets.sizes(), at::kFloat, x);
+    const Tensor lse = empty(targets.sizes(), at::kFloat, x);
+    const Tensor w = workspace(det_linear_cross_entropy_workspace_size(rows, vocab, d, type), ws, x);
+    check_status(det_linear_cross_entropy(xp, xs, wp, wst, static_cast<const int64_t*>(tp), rows, vocab,
+                                          d, type, scale, loss.data_ptr<float>(),
+                                          lse.data_ptr<float>(), pointer(w, x), w.nbytes(), stream(x)),
+                 "det_linear_cross_entropy");
+    return py::make_tuple(loss, lse);
+}
+
+py::tuple linear_cross_entropy_backward(const Tensor& x, const Tensor& weight, const Tensor& targets,
+                                        const Tensor& lse, const Tensor& dloss, double scale,
+                                        const Optional& ws) {
+    const det_dtype type = lm_type(x);
+    xent_shapes(x, weight, targets);
+    of(lse, at::kFloat, targets.sizes(), "lse");
+    of(dloss, at::kFloat, targets.sizes(), "dloss");
+    check_workspace(ws);
+    const int64_t rows = targets.numel(), vocab = weight.size(0), d = x.size(-1);
+    const int64_t xs = row_stride(x, "x"), wst = row_stride(weight, "weight");
+    void* const xp = pointer(x, x);
+    void* const wp = pointer(weight, x);
+    void* const tp = pointer(targets, x);
+    void* const lp = pointer(lse, x);
+    void* const dp = pointer(dloss, x);
+    const Guard guard(x.device());
+    const Tensor dx = empty(x.sizes(), x.scalar_type(), x);
+    const Tensor dweight = empty({vocab, d}, x.scalar_type(), x);
+    const Tensor w =
+        workspace(det_linear_cross_entropy_backward_workspace_size(rows, vocab, d, type), ws, x);
+    check_status(det_linear_cross_entropy_backward(
+                     xp, xs, wp, wst, static_cast<const int64_t*>(tp), static_cast<const float*>(lp),
+                     static_cast<const float*>(dp), rows, vocab, d, type, scale, dx.data_ptr(),
+                     dweight.data_ptr(), pointer(w, x), w.nbytes(), stream(x)),
+                 "det_linear_cross_entropy_backward");
+    return py::make_tuple(dx, dweight);
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_lm_binding, m) {
@@ -360,4 +612,12 @@ PYBIND11_MODULE(_lm_binding, m) {
     m.def("relative_bias_backward", &relative_bias_backward);
     m.def("token_logprobs", &token_logprobs);
     m.def("token_logprobs_backward", &token_logprobs_backward);
+    m.def("layer_norm", &layer_norm);
+    m.def("layer_norm_backward", &layer_norm_backward);
+    m.def("embedding", &embedding);
+    m.def("embedding_backward", &embedding_backward);
+    m.def("gated_scan", &gated_scan);
+    m.def("gated_scan_backward", &gated_scan_backward);
+    m.def("linear_cross_entropy", &linear_cross_entropy);
+    m.def("linear_cross_entropy_backward", &linear_cross_entropy_backward);
 }

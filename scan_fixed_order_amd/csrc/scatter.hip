@@ -2977,6 +2977,29 @@ det_status scatter_running_impl(const T* values, const int32_t* index, int64_t n
 }
 }  // namespace
 
+size_t sort_rows_workspace(int64_t n, int64_t num_out) {
+    return slayout(n, num_out, 1, DET_F32, true).total;
+}
+
+// The sort of the row path alone: keys and sources into the workspace, the offsets behind them.
+det_status sort_rows_launch(const int32_t* index, int64_t n, int64_t num_out, void* ws,
+                            SortedRows* out, hipStream_t s) {
+    const SLayout L = slayout(n, num_out, 1, DET_F32, true);
+    char* w = static_cast<char*>(ws);
+    uint32_t* off = reinterpret_cast<uint32_t*>(w + L.off);
+    const det_status st = sort_by_dest<uint32_t, true>(index, nullptr, n, num_out, L, w, false, s,
+                                                       &out->keys, &out->src);
+    if (st != DET_SUCCESS) return st;
+    int64_t g = cdiv(num_out + 1, 256);
+    if (g > 8192) g = 8192;
+    KernelTimer kt("k_bin_offsets", s);
+    k_bin_offsets<uint32_t><<<dim3((unsigned)g), dim3(256), 0, s>>>(
+        out->keys, reinterpret_cast<const uint32_t*>(w + L.ctrl), num_out, n, off, nullptr,
+        reinterpret_cast<const uint32_t*>(w + L.hist), key_passes(num_out));
+    out->off = off;
+    return launch_status();
+}
+
 size_t scatter_workspace(int64_t n, int64_t num_out, int64_t row_len, det_dtype dt) {
     return slayout(n, num_out, row_len, dt).total;
 }

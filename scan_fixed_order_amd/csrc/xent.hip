@@ -1,0 +1,831 @@
+// xent.hip -- cross entropy of softmax(scale * x weight^T) without keeping the logits, and its
+// gradients, in pieces of the vocabulary.
+//
+// Mathematics, per row of x:  z = scale * x weight^T;  lse = log(sum exp z);  loss = lse - z[target]
+//   D = exp(z - lse) - hit;  dx = scale * dloss * (D weight);  dweight = scale * (dloss D)^T x
+// A row whose target lies outside the vocabulary has loss 0 and adds to no gradient.
+//
+// Every product is C[i][j] = sum over k of A[i][k] B[j][k], one kernel with four endings:
+//   stats    i vocabulary, j rows of x, k width:  largest logit and sum of a tile's logits per row
+//   dlogits  the same product again: D by rows (for dx) and by columns (for dweight), rounded to the
+//            storage type once
+//   dx       i width, j rows, k a piece of the vocabulary: weight transposed, D
+//   dweight  i width, j vocabulary, k rows: x transposed, D's columns
+// f32 goes through the matrix units in three bfloat16 parts of 8 bits each (exact together) and
+// the six products of parts that reach 2^-24 of the result.
+//
+// Order: k ascending in steps of 16 inside the matrix instruction's own order, f32 accumulators; a
+// tile's logits, then the tiles of a row by lanes and the adjacent-lanes tree; dx adds pieces of the
+// vocabulary in ascending order, then the parts that share a piece.  All of it fixed by (rows,
+// vocab, d, dtype).
+#include "det_internal.h"
+#include "lm_device.h"
+
+namespace det {
+namespace {
+
+constexpr int kDepth = 64;                    // elements of k a step: 128 bytes of a row
+constexpr int64_t kTileV = 256;               // vocabulary entries that a tile's statistics cover
+constexpr int64_t kPieceCells = 1 << 26;      // elements of D that a piece holds, about
+constexpr int64_t kPieceMin = 4096;
+constexpr int64_t kPieceMax = 65536;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// one operand: rows of k elements, ld bytes apart, starting on 16 bytes
+struct Operand {
+    const char* p;
+    int64_t rows, ld;
+};
+
+struct GemmArgs {
+    Operand A, B;
+    int64_t k;            // elements of a row that count; a multiple of 8
+    int64_t plane;        // f32: bytes from one part of a row to the next
+    int64_t ni, nj;       // tiles along i and j
+    int64_t per_z;        // steps of k that a workgroup along z takes
+    float scale;
+    // stats, dlogits
+    const int64_t* targets;
+    int64_t v0, vocab, tile0, tiles;      // the piece's first entry, its first of `tiles` tiles
+    u32x2* stats;                         // [row][tile]: largest logit, sum (two floats)
+    float* hit;                           // [row]: the target's logit
+    const float *lse, *dloss, *unit;      // unit: f16, the largest |dloss|
+    char *d, *dt;                         // D by rows and by columns
+    int64_t d_ld, dt_ld, d_plane, dt_plane, rows_up, piece_up;
+    // dx, dweight
+    void* out;
+    int64_t out_ld;       // elements
+    bool add;
+};
+
+template <typename T>
+struct Half {
+    typedef T type;
+    static constexpr int kParts = 1;
+};
+template <>
+struct Half<float> {
+    typedef __bf16 type;
+    static constexpr int kParts = 3;
+};
+constexpr int kPairs = 6;
+
+__device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c, __bf16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c, _Float16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// The parts of a float: 8 bits each, cut off, so that the rest is exact.  What is not finite is its
+// own first part.
+__device__ __forceinline__ void parts_of(float v, uint16_t (&p)[3]) {
+    const uint32_t b = __float_as_uint(v);
+    if ((b & 0x7F800000u) == 0x7F800000u) {
+        p[0] = (uint16_t)((b >> 16) | (b & 0x7FFFFFu ? 0x40u : 0u));
+        p[1] = p[2] = 0;
+        return;
+    }
+    p[0] = (uint16_t)(b >> 16);
+    const float r = v - __uint_as_float(b & 0xFFFF0000u);
+    const uint32_t rb = __float_as_uint(r);
+    p[1] = (uint16_t)(rb >> 16);
+    const float q = r - __uint_as_float(rb & 0xFFFF0000u);
+    p[2] = (uint16_t)(__float_as_uint(q) >> 16);
+}
+
+// D's factor in storage: f16 has few exponents, and |D| <= 1
+template <typename T>
+constexpr float kUnit = __is_same(T, _Float16) ? 16384.0f : 1.0f;
+
+template <typename H>
+__device__ __forceinline__ uint16_t half_bits(float v) {
+    return __builtin_bit_cast(uint16_t, (H)v);
+}
+
+enum Ending { kStats, kLogits, kDx, kDw };
+
+// Wave grid WI x WJ, a wave has MI x MJ tiles of 32 x 32.  A step's rows go from memory straight to
+// LDS, two steps in turn: 8 rows of 128 bytes a load, whose 16-byte chunks lie in the order chunk
+// ^ (row % 8), so that the 8 rows that a read of the operands takes at a time lie in different
+// banks.  What lies past an operand's rows or k reads as zero (the buffer's bounds).
+template <typename T, int WI, int WJ, int MI, int MJ, int END>
+__device__ __forceinline__ void xent_product(const GemmArgs& a) {
+    typedef typename Half<T>::type H;
+    constexpr int kParts = Half<T>::kParts;
+    constexpr int BI = WI * MI * 32, BJ = WJ * MJ * 32, NW = WI * WJ;
+    constexpr int LA = BI / 8 / NW, LB = BJ / 8 / NW;      // loads of a wave a step
+    static_assert(BI % (8 * NW) == 0 && BJ % (8 * NW) == 0, "rows of a step per wave");
+    __shared__ __attribute__((aligned(16))) char s_0[(BI + BJ) * 128];
+    __shared__ __attribute__((aligned(16))) char s_1[(BI + BJ) * 128];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int wi = wave / WJ, wj = wave % WJ;
+
+    // Workgroup b runs on XCD b % 8: each takes a run of tiles, four along j by as many as follow
+    // along i, so that what an XCD holds at a time shares its rows in its L2.
+    const int64_t tiles = a.ni * a.nj, per = (tiles + 7) / 8;
+    const int64_t q = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || q >= tiles) return;
+    const int64_t band = q / (4 * a.ni), in_band = q % (4 * a.ni);
+    const int64_t wide = a.nj - 4 * band < 4 ? a.nj - 4 * band : 4;
+    const int64_t i0 = in_band / wide * BI, j0 = (4 * band + in_band % wide) * BJ;
+
+    const int64_t span = a.k * 2 + (kParts - 1) * a.plane;      // bytes of a row
+    const auto records = [&](const Operand& o, int64_t first, int64_t most) {
+        const int64_t rows = o.rows - first < most ? o.rows - first : most;
+        return (uint32_t)((rows - 1) * o.ld + span);
+    };
+    const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(a.A.p + i0 * a.A.ld), 0,
+                                                      records(a.A, i0, BI), 0x00020000);
+    const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(a.B.p + j0 * a.B.ld), 0,
+                                                      records(a.B, j0, BJ), 0x00020000);
+    const int row8 = lane >> 3, chunk = (lane & 7) ^ row8;
+    const uint32_t lda = (uint32_t)a.A.ld, ldb = (uint32_t)a.B.ld;
+    const uint32_t oa = (uint32_t)(wave * LA * 8 + row8) * lda + chunk * 16;
+    const uint32_t ob = (uint32_t)(wave * LB * 8 + row8) * ldb + chunk * 16;
+    const int steps_k = (int)((a.k + kDepth - 1) / kDepth);      // of one product of parts
+    const int first = (int)(blockIdx.y * a.per_z);
+    const int behind = (int)(first + a.per_z < (int64_t)steps_k * (kParts == 1 ? 1 : kPairs)
+                                 ? first + a.per_z
+                                 : (int64_t)steps_k * (kParts == 1 ? 1 : kPairs));
+    const auto issue = [&](char* s, int step) {
+        uint32_t ka, kb;
+        bool inside;
+        if constexpr (kParts == 1) {
+            ka = kb = (uint32_t)step * 128;
+            inside = step < behind && step * kDepth + chunk * 8 < a.k;
+        } else {
+            const int pair = step / steps_k, at = step % steps_k;
+            // parts (0,0) (0,1) (1,0) (1,1) (0,2) (2,0)
+            const int ia = pair == 2 || pair == 3 ? 1 : pair == 5 ? 2 : 0;
+            const int ib = pair == 1 || pair == 3 ? 1 : pair == 4 ? 2 : 0;
+            ka = (uint32_t)(ia * a.plane) + at * 128;
+            kb = (uint32_t)(ib * a.plane) + at * 128;
+            inside = step < behind && at * kDepth + chunk * 8 < a.k;
+        }
+        constexpr uint32_t kOut = 0x80000000u;
+#pragma unroll
+        for (int u = 0; u < LA; ++u)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(s + (wave * LA + u) * 1024), 16,
+                                                     inside ? oa + u * 8 * lda + ka : kOut, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < LB; ++u)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(s + BI * 128 + (wave * LB + u) * 1024),
+                                                     16, inside ? ob + u * 8 * ldb + kb : kOut, 0, 0, 0);
+    };
+    f32x16 acc[MI][MJ] = {};
+    const auto products = [&](const char* s) {
+        const char* pa = s + (wi * MI * 32 + (lane & 31)) * 128;
+        const char* pb = s + BI * 128 + (wj * MJ * 32 + (lane & 31)) * 128;
+#pragma unroll
+        for (int kk = 0; kk < kDepth / 16; ++kk) {
+            const int slot = ((kk * 2 + (lane >> 5)) ^ (lane & 7)) * 16;
+            u32x4 av[MI], bv[MJ];
+#pragma unroll
+            for (int i = 0; i < MI; ++i) av[i] = *reinterpret_cast<const u32x4*>(pa + i * 4096 + slot);
+#pragma unroll
+            for (int j = 0; j < MJ; ++j) bv[j] = *reinterpret_cast<const u32x4*>(pb + j * 4096 + slot);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < MJ; ++j) acc[i][j] = mma(av[i], bv[j], acc[i][j], H{});
+        }
+    };
+    // a step's loads are done (every wave waits for its own), and nobody reads the other buffer
+    const auto turn = [&] {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    issue(s_0, first);
+#pragma unroll 1
+    for (int step = first; step < behind; step += 2) {
+        turn();
+        issue(s_1, step + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        products(s_0);
+        turn();
+        issue(s_0, step + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        products(s_1);      // past the last step: zeros
+    }
+    turn();
+
+    // a lane's values: column wj.. + lane % 32, rows wi.. + 8 (r / 4) + 4 (lane / 32) + r % 4 of the tile
+    const int row_base = wi * MI * 32 + 4 * (lane >> 5), col_base = wj * MJ * 32 + (lane & 31);
+    const auto row_of = [&](int i, int r) { return row_base + i * 32 + 8 * (r / 4) + r % 4; };
+    const int rows_left = (int)(a.A.rows - i0 < BI ? a.A.rows - i0 : BI);
+    const int cols_left = (int)(a.B.rows - j0 < BJ ? a.B.rows - j0 : BJ);
+    // the place of a column's target among the lane's rows (row_of less row_base), -1 elsewhere
+    const auto target_at = [&](int64_t target) {
+        const int64_t at = target - a.v0 - i0;
+        return at >= 0 && at < rows_left ? (int)at - row_base : -1;
+    };
+
+    if constexpr (END == kStats) {
+        float* s_top = reinterpret_cast<float*>(s_0);      // [WI][BJ], then the sums
+        float* s_sum = s_top + WI * BJ;
+#pragma unroll
+        for (int j = 0; j < MJ; ++j) {
+            const int col = col_base + j * 32;
+            const int at = col < cols_left ? target_at(a.targets[j0 + col]) : -1;
+            float top = -INFINITY;
+            if (rows_left < BI) {
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (row_of(i, r) >= rows_left) acc[i][j][r] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    acc[i][j][r] *= a.scale;
+                    top = fmaxf(top, acc[i][j][r]);
+                }
+            if (at >= 0) {      // the lane may hold it
+                float hit = 0.0f;
+                bool mine = false;
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (at == i * 32 + 8 * (r / 4) + r % 4) {
+                            hit = acc[i][j][r];
+                            mine = true;
+                        }
+                if (mine) a.hit[j0 + col] = hit;
+            }
+            const float ref = top > -INFINITY ? top : 0.0f;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sum += exp_fast(acc[i][j][r] - ref);
+            // the other half of the wave has the same column
+            const float other_top = __shfl_xor(top, 32), other_sum = __shfl_xor(sum, 32);
+            const float both = fmaxf(top, other_top), from = both > -INFINITY ? both : 0.0f;
+            if (lane < 32) {
+                s_top[wi * BJ + col] = both;
+                s_sum[wi * BJ + col] = sum * exp_fast(top - from) + other_sum * exp_fast(other_top - from);
+            }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols_left; c += NW * 64) {
+            float top = s_top[c];
+#pragma unroll
+            for (int w = 1; w < WI; ++w) top = fmaxf(top, s_top[w * BJ + c]);
+            const float from = top > -INFINITY ? top : 0.0f;
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WI; ++w) sum += s_sum[w * BJ + c] * exp_fast(s_top[w * BJ + c] - from);
+            a.stats[(j0 + c) * a.tiles + a.tile0 + i0 / BI] =
+                u32x2{__float_as_uint(top), __float_as_uint(sum)};
+        }
+    } else if constexpr (END == kLogits) {
+        const int d_left = (int)(a.piece_up - i0 < BI ? a.piece_up - i0 : BI);      // of D's rows
+        const int dt_left = (int)(a.rows_up - j0 < BJ ? a.rows_up - j0 : BJ);       // of its columns'
+#pragma unroll
+        for (int j = 0; j < MJ; ++j) {
+            const int col = col_base + j * 32;
+            const bool real = col < cols_left;
+            const int64_t target = real ? a.targets[j0 + col] : -1;
+            const bool scored = target >= 0 && target < a.vocab;
+            const int at = target_at(target);
+            const float lse = scored ? a.lse[j0 + col] : 0.0f;
+            const float unit = scored ? kUnit<T> : 0.0f;
+            float weight = scored ? a.dloss[j0 + col] : 0.0f;
+            if constexpr (__is_same(T, _Float16)) weight = *a.unit > 0.0f ? weight / *a.unit : 0.0f;
+            char* const d_at = a.d + (j0 + col) * a.d_ld + (i0 + row_base) * 2;
+            char* const dt_at = a.dt + (i0 + row_base) * a.dt_ld + (j0 + col) * 2;
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int in_lane = i * 32 + 8 * g, v = row_base + in_lane;      // and three behind it
+                    float d[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float p = exp_fast(acc[i][j][4 * g + r] * a.scale - lse);
+                        d[r] = at == in_lane + r ? p - 1.0f : p;
+                        d[r] = scored && v + r < rows_left ? d[r] * unit : 0.0f;
+                    }
+                    if constexpr (kParts == 1) {
+                        if (real && v < d_left) {
+                            uint32_t w[2];
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                w[r] = half_bits<H>(d[2 * r]) | (uint32_t)half_bits<H>(d[2 * r + 1]) << 16;
+                            *reinterpret_cast<u32x2*>(d_at + in_lane * 2) = u32x2{w[0], w[1]};
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (v + r < rows_left && col < dt_left)
+                                *reinterpret_cast<uint16_t*>(dt_at + (in_lane + r) * a.dt_ld) =
+                                    half_bits<H>(d[r] * weight);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            uint16_t p[3];
+                            parts_of(d[r], p);
+                            if (real && v < d_left)
+#pragma unroll
+                                for (int n = 0; n < 3; ++n)
+                                    *reinterpret_cast<uint16_t*>(d_at + n * a.d_plane +
+                                                                 (in_lane + r) * 2) = p[n];
+                            parts_of(d[r] * weight, p);
+                            if (v + r < rows_left && col < dt_left)
+#pragma unroll
+                                for (int n = 0; n < 3; ++n)
+                                    *reinterpret_cast<uint16_t*>(dt_at + (in_lane + r) * a.dt_ld +
+                                                                 n * a.dt_plane) = p[n];
+                        }
+                    }
+                }
+        }
+    } else {
+        // dx: f32 sums of a part; dweight: the gradient in its type
+#pragma unroll
+        for (int j = 0; j < MJ; ++j) {
+            const int col = col_base + j * 32;
+            if (col >= cols_left) continue;
+            const int64_t row = j0 + col;
+            float f = 1.0f;
+            if constexpr (END == kDw) {
+                f = a.scale / kUnit<T>;
+                if constexpr (__is_same(T, _Float16)) f *= *a.unit;
+            }
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int left = rows_left - row_of(i, 4 * g);
+                    const int64_t c = i0 + row_of(i, 4 * g);
+                    if (left <= 0) continue;
+                    float v[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * g + r] * f;
+                    if constexpr (END == kDx) {
+                        float* at = static_cast<float*>(a.out) + blockIdx.y * a.B.rows * a.out_ld +
+                                    row * a.out_ld + c;      // out_ld: a multiple of 4, room for 4
+                        if (a.add) {
+                            const f32x4 old = *reinterpret_cast<const f32x4*>(at);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) v[r] = old[r] + v[r];
+                        }
+                        *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
+                    } else {
+                        T* at = static_cast<T*>(a.out) + row * a.out_ld + c;
+                        if constexpr (sizeof(T) == 4) {
+                            if (left >= 4)
+                                *reinterpret_cast<f32x4_a4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
+                            else
+                                for (int r = 0; r < 3; ++r)
+                                    if (r < left) at[r] = v[r];
+                        } else {
+                            typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+                            if (left >= 4) {
+                                uint32_t w[2];
+#pragma unroll
+                                for (int r = 0; r < 2; ++r)
+                                    w[r] = half_bits<T>(v[2 * r]) | (uint32_t)half_bits<T>(v[2 * r + 1]) << 16;
+                                *reinterpret_cast<u32x2_a2*>(at) = u32x2{w[0], w[1]};
+                            } else {
+#pragma unroll
+                                for (int r = 0; r < 3; ++r)
+                                    if (r < left) at[r] = (T)v[r];
+                            }
+                        }
+                    }
+                }
+        }
+    }
+}
+
+// (The kernel's body is a device function: it uses types that the host's compiler pass lacks.)
+template <typename T, int WI, int WJ, int MI, int MJ, int END>
+__global__ __launch_bounds__(WI * WJ * 64) void k_xent_product(GemmArgs a) {
+    xent_product<T, WI, WJ, MI, MJ, END>(a);
+}
+
+// ---------------------------------------------------------------- operands laid out
+
+// rows of d elements -> rows of `wide` (d rounded up to a step), zeros behind; f32 in three parts
+template <typename T>
+__global__ __launch_bounds__(256) void k_xent_pack(const T* src, int64_t stride, int64_t rows,
+                                                   int64_t d, int64_t wide, uint16_t* dst) {
+    constexpr int kParts = Half<T>::kParts;
+    const int64_t per = wide / 8, total = rows * per;      // 8 elements a lane
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < total; n += (int64_t)gridDim.x * 256) {
+        const int64_t row = n / per, c = n % per * 8;
+        uint16_t o[kParts][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const T v = c + i < d ? src[row * stride + c + i] : (T)0.0f;
+            if constexpr (kParts == 1) {
+                o[0][i] = __builtin_bit_cast(uint16_t, v);
+            } else {
+                uint16_t p[3];
+                parts_of(v, p);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) o[k][i] = p[k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kParts; ++k)
+            *reinterpret_cast<u32x4*>(dst + (row * kParts + k) * wide + c) =
+                __builtin_bit_cast(u32x4, o[k]);
+    }
+}
+
+// rows of d elements -> d rows of `wide` (the number of rows rounded up to a step), zeros behind and
+// for the rows that have no target in [0, vocab) (targets NULL: none)
+template <typename T>
+__global__ __launch_bounds__(256) void k_xent_transpose(const T* src, int64_t stride, int64_t rows,
+                                                        int64_t d, int64_t wide, uint16_t* dst,
+                                                        const int64_t* targets, int64_t vocab) {
+    constexpr int kParts = Half<T>::kParts, kSide = 64;
+    __shared__ T s[kSide][kSide + 2];
+    const int64_t r0 = (int64_t)blockIdx.x * kSide, c0 = (int64_t)blockIdx.y * kSide;
+    for (int n = threadIdx.x; n < kSide * kSide; n += 256) {
+        const int64_t r = r0 + n / kSide, c = c0 + n % kSide;
+        T v = (T)0.0f;
+        if (r < rows && c < d) {
+            const int64_t t = targets ? targets[r] : 0;
+            if (t >= 0 && t < vocab) v = src[r * stride + c];
+        }
+        s[n % kSide][n / kSide] = v;
+    }
+    __syncthreads();
+    for (int n = threadIdx.x; n < kSide * kSide / 8; n += 256) {
+        const int c = n / (kSide / 8), r = n % (kSide / 8) * 8;
+        if (c0 + c >= d) continue;
+        uint16_t o[kParts][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (kParts == 1) {
+                o[0][i] = __builtin_bit_cast(uint16_t, s[c][r + i]);
+            } else {
+                uint16_t p[3];
+                parts_of(s[c][r + i], p);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) o[k][i] = p[k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kParts; ++k)
+            *reinterpret_cast<u32x4*>(dst + ((c0 + c) * kParts + k) * wide + r0 + r) =
+                __builtin_bit_cast(u32x4, o[k]);
+    }
+}
+
+// ---------------------------------------------------------------- rows' results
+
+// A row's tiles joined: a wave a row, lanes the tiles l, l + 64, ... in that order.
+__global__ __launch_bounds__(256) void k_xent_rows(const u32x2* stats, const float* hit,
+                                                   const int64_t* targets, int64_t rows,
+                                                   int64_t tiles, int64_t vocab, float* loss,
+                                                   float* lse) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < rows;
+         row += (int64_t)gridDim.x * 4) {
+        float top = -INFINITY, sum = 0.0f;
+        for (int64_t t = lane; t < tiles; t += 64) {
+            const u32x2 one = stats[row * tiles + t];
+            const float m = __uint_as_float(one[0]), s = __uint_as_float(one[1]);
+            const float both = fmaxf(top, m), at = both > -INFINITY ? both : 0.0f;
+            sum = sum * exp_fast(top - at) + s * exp_fast(m - at);
+            top = both;
+        }
+        const float most = wave_max(top), at = most > -INFINITY ? most : 0.0f;
+        const float total = wave_pw(sum * exp_fast(top - at));
+        if (lane == 0) {
+            const int64_t target = targets[row];
+            const float log_total = logf(total);
+            const bool none = total == 0.0f;      // every logit is -infinity
+            lse[row] = none ? -INFINITY : most + log_total;
+            loss[row] = target < 0 || target >= vocab ? 0.0f
+                        : none                        ? INFINITY
+                                                      : log_total + (most - hit[row]);
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void k_xent_zero(uint16_t* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        p[i] = 0;
+}
+
+// the largest |dloss| of the rows that count (f16)
+__global__ __launch_bounds__(1024) void k_xent_unit(const float* dloss, const int64_t* targets,
+                                                    int64_t rows, int64_t vocab, float* unit) {
+    __shared__ float s[16];
+    float m = 0.0f;
+    for (int64_t r = threadIdx.x; r < rows; r += 1024)
+        if (targets[r] >= 0 && targets[r] < vocab) m = fmaxf(m, fabsf(dloss[r]));
+    m = wave_max(m);
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 16; ++w) m = fmaxf(m, s[w]);
+        *unit = m;
+    }
+}
+
+// dx of the parts' sums: parts added in their order, times scale and the row's dloss
+template <typename T>
+__global__ __launch_bounds__(256) void k_xent_dx(const float* sums, int64_t parts, int64_t rows,
+                                                 int64_t d, int64_t ld, const int64_t* targets,
+                                                 int64_t vocab, const float* dloss, float scale,
+                                                 T* dx) {
+    const int64_t per = ld / 4, total = rows * per;
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < total; n += (int64_t)gridDim.x * 256) {
+        const int64_t row = n / per, c = n % per * 4;
+        f32x4 v = *reinterpret_cast<const f32x4*>(sums + row * ld + c);
+        for (int64_t p = 1; p < parts; ++p)
+            v += *reinterpret_cast<const f32x4*>(sums + (p * rows + row) * ld + c);
+        const int64_t target = targets[row];
+        const bool scored = target >= 0 && target < vocab;
+        const float f = scored ? scale * dloss[row] / kUnit<T> : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < d) dx[row * d + c + i] = scored ? (T)(v[i] * f) : (T)0.0f;
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+unsigned lanes_grid(int64_t items) {
+    const int64_t g = cdiv(items, 256);
+    return (unsigned)(g < 1 ? 1 : g < 65536 ? g : 65536);
+}
+
+template <typename T, int WI, int WJ, int MI, int MJ, int END>
+void product_as(GemmArgs a, int parts, hipStream_t s) {
+    constexpr int64_t BI = WI * MI * 32, BJ = WJ * MJ * 32;
+    a.ni = cdiv(a.A.rows, BI);
+    a.nj = cdiv(a.B.rows, BJ);
+    const int64_t steps = cdiv(a.k, kDepth) * (Half<T>::kParts == 1 ? 1 : kPairs);
+    a.per_z = cdiv(steps, parts);
+    k_xent_product<T, WI, WJ, MI, MJ, END>
+        <<<dim3((unsigned)(cdiv(a.ni * a.nj, 8) * 8), (unsigned)parts), dim3(WI * WJ * 64), 0, s>>>(a);
+}
+
+// Tiles of 256 x 256 where they fill the compute units, else 256 x 64 (i is the wide side).
+template <typename T, int END>
+void product(const GemmArgs& a, int parts, hipStream_t s) {
+    static const char* const names[] = {"k_xent_stats", "k_xent_logits", "k_xent_dx", "k_xent_dweight"};
+    KernelTimer kt(names[END], s);
+    if (a.B.rows > 64)
+        product_as<T, 2, 4, 4, 2, END>(a, parts, s);
+    else
+        product_as<T, 4, 1, 2, 2, END>(a, parts, s);
+}
+
+struct XentPlan {
+    int64_t piece;
+    int64_t wide_d, wide_v, wide_r;      // d, piece and rows rounded up to a step
+    int64_t parts, dx_ld, tiles;
+};
+
+// Vocabulary entries of a piece: D of a piece takes about kPieceCells elements, twice.
+XentPlan xent_plan(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype) {
+    XentPlan p;
+    int64_t piece = kPieceCells / (rows > 0 ? rows : 1) / kTileV * kTileV;
+    piece = piece < kPieceMin ? kPieceMin : piece > kPieceMax ? kPieceMax : piece;
+    p.piece = piece < vocab ? piece : vocab;
+    p.wide_d = up(d, kDepth);
+    p.wide_v = up(p.piece, kDepth);
+    p.wide_r = up(rows, kDepth);
+    p.dx_ld = up(d, 4);
+    p.tiles = cdiv(vocab, kTileV);
+    // workgroups that share dx's sum over a piece where its tiles are few
+    const int64_t tiles = cdiv(d, 256) * cdiv(rows, rows > 64 ? 256 : 64);
+    p.parts = tiles >= 128 ? 1 : cdiv(256, tiles);
+    const int64_t steps = p.wide_v / kDepth * (dtype == DET_F32 ? kPairs : 1);
+    if (p.parts > cdiv(steps, 8)) p.parts = cdiv(steps, 8);
+    return p;
+}
+
+// Entries whose rows the forward pass lays out at a time: as many as the backward pass where every
+// call lays them out, few where only an address off 16 bytes asks for it (the workspace has to hold
+// them).  Its sums go by tiles, so this moves no bit.
+int64_t forward_piece(const XentPlan& p, int64_t vocab, int64_t d, det_dtype dtype) {
+    const int64_t n = d % 8 || dtype == DET_F32 ? p.piece : kPieceMin;
+    return n < vocab ? n : vocab;
+}
+
+int64_t parts_of_type(det_dtype dtype) { return dtype == DET_F32 ? 3 : 1; }
+
+struct XentLayout {
+    size_t x, w, stats, hit, xt, wt, d, dt, sums, unit, total;
+};
+
+XentLayout xent_layout(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype, bool back) {
+    const XentPlan p = xent_plan(rows, vocab, d, dtype);
+    const int64_t n = parts_of_type(dtype) * 2;      // bytes of an element laid out
+    XentLayout L = {};
+    size_t o = 0;
+    const auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o += round_up(bytes > 0 ? bytes : 1, 256);
+        return at;
+    };
+    L.x = take((size_t)rows * p.wide_d * n);
+    L.w = take((size_t)(back ? p.piece : forward_piece(p, vocab, d, dtype)) * p.wide_d * n);
+    if (!back) {
+        L.stats = take((size_t)rows * p.tiles * 8);
+        L.hit = take((size_t)rows * 4);
+    } else {
+        L.xt = take((size_t)d * p.wide_r * n);
+        L.wt = take((size_t)d * p.wide_v * n);
+        L.d = take((size_t)rows * p.wide_v * n);
+        L.dt = take((size_t)p.piece * p.wide_r * n);
+        L.sums = take((size_t)p.parts * rows * p.dx_ld * 4);
+        L.unit = take(4);
+    }
+    L.total = o;
+    return L;
+}
+
+// whether the product can read the rows as they lie (a tile's 256 rows within 2^30 bytes)
+template <typename T>
+bool as_they_lie(const void* p, int64_t stride, int64_t d) {
+    return sizeof(T) == 2 && d % 8 == 0 && stride % 8 == 0 && stride <= (1 << 21) &&
+           reinterpret_cast<uintptr_t>(p) % 16 == 0;
+}
+
+template <typename T>
+Operand laid_out(const T* p, int64_t stride, int64_t rows, int64_t d, bool lies, char* at,
+                 int64_t wide, hipStream_t s) {
+    if (lies) return Operand{reinterpret_cast<const char*>(p), rows, stride * (int64_t)sizeof(T)};
+    KernelTimer kt("k_xent_pack", s);
+    k_xent_pack<T><<<dim3(lanes_grid(rows * (wide / 8))), dim3(256), 0, s>>>(
+        p, stride, rows, d, wide, reinterpret_cast<uint16_t*>(at));
+    return Operand{at, rows, wide * 2 * Half<T>::kParts};
+}
+
+template <typename T>
+det_status xent_typed(const XentCall& c, char* ws, hipStream_t s) {
+    const T* x = static_cast<const T*>(c.x);
+    const T* w = static_cast<const T*>(c.weight);
+    const bool x_lies = as_they_lie<T>(x, c.x_stride, c.d), w_lies = as_they_lie<T>(w, c.w_stride, c.d);
+    const XentPlan p = xent_plan(c.rows, c.vocab, c.d, c.dtype);
+    const XentLayout L = xent_layout(c.rows, c.vocab, c.d, c.dtype, false);
+    GemmArgs a = {};
+    a.B = laid_out(x, c.x_stride, c.rows, c.d, x_lies, ws + L.x, p.wide_d, s);
+    a.k = x_lies && w_lies ? c.d : p.wide_d;
+    a.plane = p.wide_d * 2;
+    a.scale = c.scale;
+    a.targets = c.targets;
+    a.vocab = c.vocab;
+    a.stats = reinterpret_cast<u32x2*>(ws + L.stats);
+    a.hit = reinterpret_cast<float*>(ws + L.hit);
+    // rows that need no laying out are one piece, up to what a grid holds
+    const int64_t most = up(cdiv((int64_t)1 << 28, up(c.rows, kTileV)), kTileV) * kTileV;
+    const int64_t piece = !w_lies            ? forward_piece(p, c.vocab, c.d, c.dtype)
+                          : c.vocab < most ? c.vocab : most;
+    a.tiles = p.tiles;
+    for (int64_t v0 = 0; v0 < c.vocab; v0 += piece) {
+        const int64_t n = c.vocab - v0 < piece ? c.vocab - v0 : piece;
+        a.A = laid_out(w + v0 * c.w_stride, c.w_stride, n, c.d, w_lies, ws + L.w, p.wide_d, s);
+        if (x_lies != w_lies) a.k = c.d;      // the shorter of the two rows; both are a multiple of 8
+        a.v0 = v0;
+        product<T, kStats>(a, 1, s);
+        a.tile0 += cdiv(n, kTileV);
+    }
+    det_status st = launch_status();
+    if (st != DET_SUCCESS) return st;
+    KernelTimer kt("k_xent_rows", s);
+    int64_t g = cdiv(c.rows, 4);
+    if (g > 65536) g = 65536;
+    k_xent_rows<<<dim3((unsigned)g), dim3(256), 0, s>>>(a.stats, a.hit, c.targets, c.rows, a.tiles,
+                                                        c.vocab, c.loss, c.lse);
+    return launch_status();
+}
+
+template <typename T>
+det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
+    constexpr int kParts = Half<T>::kParts;
+    const T* x = static_cast<const T*>(c.x);
+    const T* w = static_cast<const T*>(c.weight);
+    const bool x_lies = as_they_lie<T>(x, c.x_stride, c.d), w_lies = as_they_lie<T>(w, c.w_stride, c.d);
+    const XentPlan p = xent_plan(c.rows, c.vocab, c.d, c.dtype);
+    const XentLayout L = xent_layout(c.rows, c.vocab, c.d, c.dtype, true);
+    float* unit = reinterpret_cast<float*>(ws + L.unit);
+    if constexpr (__is_same(T, _Float16)) {
+        KernelTimer kt("k_xent_unit", s);
+        k_xent_unit<<<dim3(1), dim3(1024), 0, s>>>(c.dloss, c.targets, c.rows, c.vocab, unit);
+    }
+    const Operand xo = laid_out(x, c.x_stride, c.rows, c.d, x_lies, ws + L.x, p.wide_d, s);
+    uint16_t* xt = reinterpret_cast<uint16_t*>(ws + L.xt);
+    uint16_t* wt = reinterpret_cast<uint16_t*>(ws + L.wt);
+    {
+        KernelTimer kt("k_xent_transpose", s);
+        k_xent_transpose<T><<<dim3((unsigned)(p.wide_r / 64), (unsigned)cdiv(c.d, 64)), dim3(256), 0, s>>>(
+            x, c.x_stride, c.rows, c.d, p.wide_r, xt, c.targets, c.vocab);
+    }
+    for (int64_t v0 = 0; v0 < c.vocab; v0 += p.piece) {
+        const int64_t n = c.vocab - v0 < p.piece ? c.vocab - v0 : p.piece, wide = up(n, kDepth);
+        const T* rows = w + v0 * c.w_stride;
+        GemmArgs a = {};
+        a.scale = c.scale;
+        a.targets = c.targets;
+        a.vocab = c.vocab;
+        a.v0 = v0;
+        a.lse = c.lse;
+        a.dloss = c.dloss;
+        a.unit = unit;
+        // D of the piece
+        a.A = laid_out(rows, c.w_stride, n, c.d, w_lies, ws + L.w, p.wide_d, s);
+        a.B = xo;
+        a.k = x_lies == w_lies && !x_lies ? p.wide_d : c.d;
+        a.plane = p.wide_d * 2;
+        a.d = ws + L.d;
+        a.dt = ws + L.dt;
+        a.d_ld = p.wide_v * 2 * kParts;
+        a.d_plane = p.wide_v * 2;
+        a.dt_ld = p.wide_r * 2 * kParts;
+        a.dt_plane = p.wide_r * 2;
+        a.rows_up = p.wide_r;
+        a.piece_up = wide;
+        product<T, kLogits>(a, 1, s);
+        // dx += D weight
+        {
+            KernelTimer kt("k_xent_transpose", s);
+            k_xent_transpose<T><<<dim3((unsigned)(wide / 64), (unsigned)cdiv(c.d, 64)), dim3(256), 0, s>>>(
+                rows, c.w_stride, n, c.d, p.wide_v, wt, nullptr, 1);
+        }
+        GemmArgs b = a;
+        b.A = Operand{ws + L.wt, c.d, p.wide_v * 2 * kParts};
+        b.B = Operand{ws + L.d, c.rows, a.d_ld};
+        b.k = wide;
+        b.plane = p.wide_v * 2;
+        b.out = ws + L.sums;
+        b.out_ld = p.dx_ld;
+        b.add = v0 > 0;
+        product<T, kDx>(b, (int)p.parts, s);
+        // dweight of the piece
+        b.A = Operand{ws + L.xt, c.d, a.dt_ld};
+        b.B = Operand{ws + L.dt, n, a.dt_ld};
+        b.k = p.wide_r;
+        b.plane = p.wide_r * 2;
+        b.out = static_cast<T*>(c.dweight) + v0 * c.d;
+        b.out_ld = c.d;
+        product<T, kDw>(b, 1, s);
+        const det_status st = launch_status();
+        if (st != DET_SUCCESS) return st;
+    }
+    KernelTimer kt("k_xent_dx_rows", s);
+    k_xent_dx<T><<<dim3(lanes_grid(c.rows * (p.dx_ld / 4))), dim3(256), 0, s>>>(
+        reinterpret_cast<const float*>(ws + L.sums), p.parts, c.rows, c.d, p.dx_ld, c.targets, c.vocab,
+        c.dloss, c.scale, static_cast<T*>(c.dx));
+    return launch_status();
+}
+
+}  // namespace
+
+size_t xent_workspace(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype) {
+    return rows > 0 && vocab > 0 && d > 0 ? xent_layout(rows, vocab, d, dtype, false).total : 256;
+}
+
+size_t xent_backward_workspace(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype) {
+    return rows > 0 && vocab > 0 && d > 0 ? xent_layout(rows, vocab, d, dtype, true).total : 256;
+}
+
+det_status xent_launch(const XentCall& c, void* ws, hipStream_t s) {
+    char* w = static_cast<char*>(ws);
+    switch (c.dtype) {
+        case DET_F32: return xent_typed<float>(c, w, s);
+        case DET_F16: return xent_typed<_Float16>(c, w, s);
+        default: return xent_typed<__bf16>(c, w, s);
+    }
+}
+
+det_status xent_backward_launch(const XentBackCall& c, void* ws, hipStream_t s) {
+    char* w = static_cast<char*>(ws);
+    if (c.rows == 0) {      // no rows: dweight is 0
+        const int64_t n = c.vocab * c.d * (int64_t)lm_size(c.dtype) / 2;
+        KernelTimer kt("k_xent_zero", s);
+        k_xent_zero<<<dim3(lanes_grid(n)), dim3(256), 0, s>>>(static_cast<uint16_t*>(c.dweight), n);
+        return launch_status();
+    }
+    switch (c.dtype) {
+        case DET_F32: return xent_back_typed<float>(c, w, s);
+        case DET_F16: return xent_back_typed<_Float16>(c, w, s);
+        default: return xent_back_typed<__bf16>(c, w, s);
+    }
+}
+
+}  // namespace det

@@ -24,10 +24,12 @@ DET_I32 = 2      # det_scan only
 DET_F16 = 3      # the language-model operators only, like DET_BF16
 DET_BF16 = 4
 DET_E4M3 = 5     # det_rms_norm's 8-bit output only
+DET_I64 = 6      # token ids, like DET_I32
 DET_SCAN_EXCLUSIVE = 1
 DET_SCAN_REVERSE = 2
 DET_BIAS_BIDIRECTIONAL = 1
 DET_BIAS_CAUSAL = 2
+DET_GATE_SIGMOID = 1
 
 _STATUS = {
     0: "DET_SUCCESS",
@@ -96,6 +98,32 @@ def lib() -> ctypes.CDLL:
     L.det_token_logprobs.restype = i
     L.det_token_logprobs_backward.argtypes = [p, i64, p, p, p, p, p, i64, i64, i, d, p, i64, p]
     L.det_token_logprobs_backward.restype = i
+    L.det_layer_norm.argtypes = [p, i64, p, i64, p, p, i64, i64, i, d, p, p, p, p, p]
+    L.det_layer_norm.restype = i
+    L.det_layer_norm_backward_workspace_size.argtypes = [i64, i64, i]
+    L.det_layer_norm_backward_workspace_size.restype = sz
+    L.det_layer_norm_backward.argtypes = [p, i64, p, i64, p, p, p, p, i64, i64, i64, i, p, p, p, p,
+                                          sz, p]
+    L.det_layer_norm_backward.restype = i
+    L.det_embedding.argtypes = [p, i64, p, i, i64, i64, i64, i, d, p, p]
+    L.det_embedding.restype = i
+    L.det_embedding_backward_workspace_size.argtypes = [i64, i64, i64, i]
+    L.det_embedding_backward_workspace_size.restype = sz
+    L.det_embedding_backward.argtypes = [p, i64, p, i, i64, i64, i64, i, d, p, p, sz, p]
+    L.det_embedding_backward.restype = i
+    for size in (L.det_gated_scan_workspace_size, L.det_gated_scan_backward_workspace_size,
+                 L.det_linear_cross_entropy_workspace_size,
+                 L.det_linear_cross_entropy_backward_workspace_size):
+        size.argtypes, size.restype = [i64, i64, i64, i], sz
+    L.det_gated_scan.argtypes = [p, p, p, p, u, i64, i64, i64, i, p, p, p, sz, p]
+    L.det_gated_scan.restype = i
+    L.det_gated_scan_backward.argtypes = [p, p, p, p, p, p, p, u, i64, i64, i64, i, p, p, p, p, sz, p]
+    L.det_gated_scan_backward.restype = i
+    L.det_linear_cross_entropy.argtypes = [p, i64, p, i64, p, i64, i64, i64, i, d, p, p, p, sz, p]
+    L.det_linear_cross_entropy.restype = i
+    L.det_linear_cross_entropy_backward.argtypes = [p, i64, p, i64, p, p, p, i64, i64, i64, i, d, p,
+                                                    p, p, sz, p]
+    L.det_linear_cross_entropy_backward.restype = i
     L.det_spec_version.argtypes, L.det_spec_version.restype = [], i
     L.det_spec_constants.argtypes = [ctypes.POINTER(i64)] * 4
     L.det_spec_constants.restype = None
@@ -594,6 +622,240 @@ class _TokenLogprobsFn(torch.autograd.Function):
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, scale: float = 1.0):
     """Differentiable det_token_logprobs: (logp, entropy), the entropy of unscored rows too."""
     return _TokenLogprobsFn.apply(logits, targets, scale)
+
+
+class LayerNorm(NamedTuple):
+    """y; h = x + residual as stored (x itself without a residual), mean and rstd, which the backward
+    pass takes."""
+    y: torch.Tensor
+    h: torch.Tensor
+    mean: torch.Tensor
+    rstd: torch.Tensor
+
+
+def det_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                   eps: float = 1e-5, residual: Optional[torch.Tensor] = None) -> LayerNorm:
+    """Layer norm of the rows (last dimension) of ``x + residual``, times ``weight``, plus ``bias``.
+
+    x, residual: [..., d] of one type (float32, float16, bfloat16), rows contiguous and evenly
+    spaced; weight, bias: [d].  Computed in f32, the variance about the mean; a row's bits depend on
+    that row alone."""
+    return LayerNorm(*_lm_binding().layer_norm(x, weight, bias, eps, residual))
+
+
+@functools.lru_cache(maxsize=256)
+def det_layer_norm_backward_workspace_size(rows: int, d: int, dtype_code: int) -> int:
+    return lib().det_layer_norm_backward_workspace_size(rows, d, dtype_code)
+
+
+def det_layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                            mean: torch.Tensor, rstd: torch.Tensor,
+                            dh: Optional[torch.Tensor] = None, bias: bool = True,
+                            ws: Optional[torch.Tensor] = None
+                            ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """(dx, dweight, dbias) of det_layer_norm's ``y``; ``h``, ``mean`` and ``rstd`` as det_layer_norm
+    returned them.  ``dh``: the gradient that reaches h from elsewhere (the residual stream), added
+    to dx.  dx is also the residual's gradient.  ``bias=False``: no dbias (None).  The sums over the
+    rows have an order fixed by their number."""
+    return _lm_binding().layer_norm_backward(dy, h, weight, mean, rstd, dh, bias, ws)
+
+
+def det_embedding(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """``scale * table[tokens]``: [..., d] for tokens [...] (int32 or int64), zeros for a token outside
+    the vocabulary (such as -1 for padding).
+
+    table: [vocab, d] (float32, float16, bfloat16), rows contiguous and evenly spaced."""
+    return _lm_binding().embedding(table, tokens, scale)
+
+
+@functools.lru_cache(maxsize=256)
+def det_embedding_backward_workspace_size(n: int, vocab: int, d: int, dtype_code: int) -> int:
+    return lib().det_embedding_backward_workspace_size(n, vocab, d, dtype_code)
+
+
+def det_embedding_backward(dout: torch.Tensor, tokens: torch.Tensor, vocab: int,
+                           scale: float = 1.0, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The table's gradient [vocab, d]: ``scale`` times the sum of ``dout`` [..., d] over each token's
+    places, in their order, in f32 (a token with more than 64 places: blocks of 64, joined in
+    double); zeros for tokens that do not occur."""
+    return _lm_binding().embedding_backward(dout, tokens, vocab, scale, ws)
+
+
+class GatedScan(NamedTuple):
+    """h of every step, and float32 state behind the last one."""
+    h: torch.Tensor
+    state: torch.Tensor
+
+
+def det_gated_scan(gate: torch.Tensor, x: torch.Tensor, state: Optional[torch.Tensor] = None,
+                   sigmoid: bool = False, lengths: Optional[torch.Tensor] = None,
+                   state_out: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None) -> GatedScan:
+    """The gated linear recurrence h[t] = a[t] h[t-1] + b[t] of every channel.
+
+    gate, x: [batch, steps, d], contiguous, of one type (float32, float16, bfloat16).  a = gate (at
+    most 1 in magnitude) and b = x, or with ``sigmoid`` a = sigmoid(gate) and b = (1 - a) x.
+    ``state``: float32 [batch, d], h before the first step (zeros).  ``lengths``: int32 [batch]; steps
+    at or past a sequence's length keep its state and have h = 0.  ``state_out`` receives the state;
+    up to 8 steps it may be ``state`` itself, which a decoding loop then updates in place.  Computed
+    in f32; the bits of a step depend on its own channel and the steps before it alone."""
+    return GatedScan(*_lm_binding().gated_scan(gate, x, state, sigmoid, lengths, state_out, ws))
+
+
+@functools.lru_cache(maxsize=256)
+def det_gated_scan_workspace_size(batch: int, steps: int, d: int, dtype_code: int) -> int:
+    return lib().det_gated_scan_workspace_size(batch, steps, d, dtype_code)
+
+
+@functools.lru_cache(maxsize=256)
+def det_gated_scan_backward_workspace_size(batch: int, steps: int, d: int, dtype_code: int) -> int:
+    return lib().det_gated_scan_backward_workspace_size(batch, steps, d, dtype_code)
+
+
+def det_gated_scan_backward(dh: torch.Tensor, gate: torch.Tensor, x: torch.Tensor, h: torch.Tensor,
+                            state: Optional[torch.Tensor] = None,
+                            dstate: Optional[torch.Tensor] = None, sigmoid: bool = False,
+                            lengths: Optional[torch.Tensor] = None,
+                            ws: Optional[torch.Tensor] = None
+                            ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """(dgate, dx, the first state's gradient or None without ``state``) for ``dh`` and, where given,
+    ``dstate`` (float32 [batch, d], the last state's).  ``h`` as det_gated_scan returned it, the other
+    arguments as they were handed to it; all contiguous."""
+    return _lm_binding().gated_scan_backward(dh, gate, x, h, state, dstate, sigmoid, lengths, ws)
+
+
+class LinearCrossEntropy(NamedTuple):
+    """Float32 loss and lse of every row."""
+    loss: torch.Tensor
+    lse: torch.Tensor
+
+
+@functools.lru_cache(maxsize=256)
+def det_linear_cross_entropy_workspace_size(rows: int, vocab: int, d: int, dtype_code: int) -> int:
+    return lib().det_linear_cross_entropy_workspace_size(rows, vocab, d, dtype_code)
+
+
+@functools.lru_cache(maxsize=256)
+def det_linear_cross_entropy_backward_workspace_size(rows: int, vocab: int, d: int,
+                                                     dtype_code: int) -> int:
+    return lib().det_linear_cross_entropy_backward_workspace_size(rows, vocab, d, dtype_code)
+
+
+def det_linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                             scale: float = 1.0,
+                             ws: Optional[torch.Tensor] = None) -> LinearCrossEntropy:
+    """Cross entropy of softmax(scale * x weight^T) at ``targets``, the logits never in memory.
+
+    x: [..., d]; weight: [vocab, d] of the same type (float32, float16, bfloat16), rows of both
+    contiguous and evenly spaced; targets: int64 [...]; one outside the vocabulary (such as -100) has
+    loss 0.  Matrix instructions with f32 sums, whose order depends on the sizes alone."""
+    return LinearCrossEntropy(*_lm_binding().linear_cross_entropy(x, weight, targets, scale, ws))
+
+
+def det_linear_cross_entropy_backward(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                                      lse: torch.Tensor, dloss: torch.Tensor, scale: float = 1.0,
+                                      ws: Optional[torch.Tensor] = None
+                                      ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dx, dweight) for ``dloss`` (float32 [...]); ``lse`` as det_linear_cross_entropy returned it for
+    these x, weight and scale.  The logits are made again in pieces of the vocabulary."""
+    return _lm_binding().linear_cross_entropy_backward(x, weight, targets, lse, dloss, scale, ws)
+
+
+class _LayerNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps):
+        r = det_layer_norm(x, weight, bias, eps, residual)
+        ctx.save_for_backward(r.h, weight, r.mean, r.rstd)
+        ctx.set_materialize_grads(False)
+        ctx.residual, ctx.bias = residual is not None, bias is not None
+        return (r.y, r.h) if ctx.residual else r.y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, mean, rstd = ctx.saved_tensors
+        if dy is None and dh is None:
+            return None, None, None, None, None
+        dy = torch.zeros_like(h) if dy is None else dy.contiguous()
+        dx, dweight, dbias = det_layer_norm_backward(
+            dy, h, weight, mean, rstd, None if dh is None else dh.contiguous(), ctx.bias)
+        return dx, dweight, dbias, dx if ctx.residual else None, None
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, eps: float = 1e-5):
+    """Differentiable det_layer_norm: y, or (y, h = x + residual) with a residual."""
+    return _LayerNormFn.apply(x, weight, bias, residual, eps)
+
+
+class _EmbeddingFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, tokens, scale):
+        ctx.save_for_backward(tokens)
+        ctx.vocab, ctx.scale = table.shape[0], scale
+        return det_embedding(table, tokens, scale)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        (tokens,) = ctx.saved_tensors
+        return det_embedding_backward(dout.contiguous(), tokens, ctx.vocab, ctx.scale), None, None
+
+
+def embedding(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """Differentiable det_embedding (gradient of the table)."""
+    return _EmbeddingFn.apply(table, tokens, scale)
+
+
+class _GatedScanFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, x, state, sigmoid, lengths):
+        r = det_gated_scan(gate, x, state, sigmoid, lengths)
+        ctx.save_for_backward(gate, x, state, lengths, r.h)
+        ctx.set_materialize_grads(False)
+        ctx.sigmoid = sigmoid
+        return r.h, r.state
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh, dstate):
+        gate, x, state, lengths, h = ctx.saved_tensors
+        if dh is None and dstate is None:
+            return None, None, None, None, None
+        dh = torch.zeros_like(h) if dh is None else dh.contiguous()
+        dgate, dx, first = det_gated_scan_backward(
+            dh, gate, x, h, state, None if dstate is None else dstate.contiguous(), ctx.sigmoid,
+            lengths)
+        return dgate, dx, first, None, None
+
+
+def gated_scan(gate: torch.Tensor, x: torch.Tensor, state: Optional[torch.Tensor] = None,
+               sigmoid: bool = False, lengths: Optional[torch.Tensor] = None):
+    """Differentiable det_gated_scan: (h, state), with gradients of gate, x and the first state."""
+    return _GatedScanFn.apply(gate, x, state, sigmoid, lengths)
+
+
+class _LinearCrossEntropyFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, targets, scale):
+        r = det_linear_cross_entropy(x, weight, targets, scale)
+        ctx.save_for_backward(x, weight, targets, r.lse)
+        ctx.scale = scale
+        return r.loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss):
+        x, weight, targets, lse = ctx.saved_tensors
+        dx, dweight = det_linear_cross_entropy_backward(x, weight, targets, lse, dloss.contiguous(),
+                                                        ctx.scale)
+        return dx, dweight, None, None
+
+
+def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                         scale: float = 1.0) -> torch.Tensor:
+    """Differentiable det_linear_cross_entropy: the loss of every row (gradients of x and weight)."""
+    return _LinearCrossEntropyFn.apply(x, weight, targets, scale)
 
 
 # ------------------------------------------------------------------ introspection
