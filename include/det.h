@@ -433,6 +433,7 @@ det_status det_embedding_backward(const void* dout, int64_t dout_stride, const v
 
 /* det_gated_scan flags */
 #define DET_GATE_SIGMOID 1u /* gates pass through a sigmoid and mix the input in */
+#define DET_SCAN_MAX_CHANNELS 4194303
 
 /* Bytes of workspace det_gated_scan needs (0 when the arguments are invalid). */
 size_t det_gated_scan_workspace_size(int64_t batch, int64_t steps, int64_t d, det_dtype dtype);
@@ -449,7 +450,7 @@ size_t det_gated_scan_workspace_size(int64_t batch, int64_t steps, int64_t d, de
  *             steps, below 0 none.
  * Without DET_GATE_SIGMOID gates are taken to have |gate| <= 1: products of up to 128 neighbouring
  * gates are formed, and where one overflows h may be infinite or NaN.
- * steps >= 1 when batch * d > 0; batch * d <= DET_MAX_N.
+ * steps >= 1 when batch * d > 0; d <= DET_SCAN_MAX_CHANNELS, batch * d <= DET_MAX_N.
  * Order: fixed by the step's position alone (spans of 8 steps, chunks of 16 spans), so a sequence's
  * bits depend neither on the other channels nor on the steps that follow. */
 det_status det_gated_scan(const void* gate, const void* x, const float* state0,

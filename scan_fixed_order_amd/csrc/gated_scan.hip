@@ -8,55 +8,73 @@
 //   dx = G, dgate = G h[t-1];  sigmoid gates: dx = (1 - a) G, dgate = a (1 - a) (h[t-1] - x) G
 // Steps at or past a sequence's length keep the state and have h, dx and dgate 0.
 //
-// Order, fixed by a step's own position: a span of kSteps steps is a chain of fused multiply-adds
-// from its first step's incoming state; kSpans neighbouring spans make a chunk.  A span's
-// effect on a state is (A, H): h -> A h + H, its chain from 0 and its product of a.  The effects of
-// a chunk's spans are composed from the first on, applied to the chunk's incoming state, and give
-// each span's; a chunk's whole effect gives the next chunk's.  (Backwards the same from the last
-// step, span and chunk on.)  The same bits come out whether one workgroup walks all chunks of its
-// channels or several take a part each.
+// Order, fixed by a step's own position: a span of 8 steps is a chain of fused multiply-adds from the
+// state that reaches its first step; 16 neighbouring spans (backwards 8) make a chunk.  A span's effect
+// on a state is (A, H): h -> A h + H, its chain from 0 and its product of a.  The effects of a chunk's
+// spans are composed from the first on, applied to the state that reaches the chunk, and give what
+// reaches each span and the next chunk.  (Backwards the same from the last step, span and chunk on.)
+// The same bits come out whether one workgroup walks all chunks of its channels or several take a
+// part each.
 #include "det_internal.h"
 #include "lm_device.h"
 
 namespace det {
 namespace {
 
-constexpr int kSteps = 8;                     // steps of a span: a wave's share of a chunk
-constexpr int kSpans = 16;                    // spans of a chunk: waves of a workgroup
-constexpr int kChunkSteps = kSteps * kSpans;
+// By measurement, 8 x 2048 x 4096 bf16 forward and backward, then 3 x 10007 x 2500 f32: 90 and 174, 228
+// and 432 us; 8 spans forward 90, 244; 16 backward 378 (spilled registers), 438; spans of 16 steps with
+// 8 of them 132, 208.
+constexpr int kSteps = 8;              // steps of a span: a lane's share of a chunk
+constexpr int kSpans = 16;             // spans of a chunk
+constexpr int kBackSpans = 8;          // the same backwards, where a step has twice the words
 
 // Channels of a lane: one 32-bit word of a row, so a wave's load of a step takes 256 neighbouring bytes.
+// Rows of one 16-bit channel (Lone) have no word of their own.
 template <typename T>
-constexpr int kCh = 4 / sizeof(T);
+struct Lone {};
+template <typename T>
+struct Elem {
+    typedef T type;
+    static constexpr int kCh = 4 / sizeof(T);
+};
+template <typename T>
+struct Elem<Lone<T>> {
+    typedef T type;
+    static constexpr int kCh = 1;
+};
+template <typename T>
+constexpr int kCh = Elem<T>::kCh;
+template <typename T>
+using elem = typename Elem<T>::type;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 typedef uint32_t u32_a2 __attribute__((aligned(2)));
 
-// The word of channels c .. of a row of d: the row's last word where it reaches past the end, whose
-// element `word_of` moves to the front.  Any c.
+// The word at `off` bytes from `base`, which is uniform.
 template <typename T>
-__device__ __forceinline__ uint32_t load_word(const T* row, int64_t c, int64_t d) {
-    if constexpr (sizeof(T) == 4) {
-        return __float_as_uint(row[c < d ? c : d - 1]);
-    } else {
-        if (d < 2) return (uint32_t)__builtin_bit_cast(uint16_t, row[0]);
-        return *reinterpret_cast<const u32_a2*>(row + (c + 2 <= d ? c : d - 2));
-    }
+__device__ __forceinline__ uint32_t load_word(const elem<T>* base, uint32_t off) {
+    const char* at = reinterpret_cast<const char*>(base) + off;
+    if constexpr (sizeof(elem<T>) == 4)
+        return *reinterpret_cast<const uint32_t*>(at);
+    else if constexpr (kCh<T> == 1)
+        return (uint32_t)*reinterpret_cast<const uint16_t*>(at);
+    else
+        return *reinterpret_cast<const u32_a2*>(at);
 }
 
 template <typename T>
 __device__ __forceinline__ void word_of(uint32_t r, bool last, float (&v)[kCh<T>]) {
-    if constexpr (sizeof(T) == 4) {
+    if constexpr (sizeof(elem<T>) == 4) {
         v[0] = __uint_as_float(r);
     } else {
         if (last) r >>= 16;      // the row's last channel, alone
-        if constexpr (__is_same(T, _Float16)) {
+        if constexpr (__is_same(elem<T>, _Float16)) {
             v[0] = (float)__builtin_bit_cast(_Float16, (uint16_t)r);
-            v[1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(r >> 16));
+            if constexpr (kCh<T> == 2) v[1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(r >> 16));
         } else {
             v[0] = __uint_as_float(r << 16);
-            v[1] = __uint_as_float(r & 0xFFFF0000u);
+            if constexpr (kCh<T> == 2) v[1] = __uint_as_float(r & 0xFFFF0000u);
         }
     }
 }
@@ -70,9 +88,9 @@ __device__ __forceinline__ float as_float(float v) {
 
 // n: channels from this one to the row's end
 template <typename T>
-__device__ __forceinline__ void store_word(T* p, int64_t n, const float (&v)[kCh<T>]) {
-    if constexpr (sizeof(T) == 4) {
-        if (n > 0) *p = v[0];
+__device__ __forceinline__ void store_word(elem<T>* p, int n, const float (&v)[kCh<T>]) {
+    if constexpr (kCh<T> == 1) {
+        if (n > 0) *p = (elem<T>)as_float(v[0]);
     } else {
         const T first = (T)as_float(v[0]);
         const uint32_t lo = __builtin_bit_cast(uint16_t, first);
@@ -84,28 +102,54 @@ __device__ __forceinline__ void store_word(T* p, int64_t n, const float (&v)[kCh
     }
 }
 
+// the first n of N floats of a state, zeros behind them
 template <int N>
 __device__ __forceinline__ void load_state(const float* p, int64_t n, float (&v)[N]) {
+    typedef float floats __attribute__((ext_vector_type(N), aligned(4)));
+    if (n >= N) {
+        const floats f = *reinterpret_cast<const floats*>(p);
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = e < n ? p[e] : 0.0f;
+        for (int e = 0; e < N; ++e) v[e] = f[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = e < n ? p[e] : 0.0f;
+    }
 }
 
 template <int N>
 __device__ __forceinline__ void store_state(float* p, int64_t n, const float (&v)[N]) {
+    typedef float floats __attribute__((ext_vector_type(N), aligned(4)));
+    if (n >= N) {
+        floats f;
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-        if (e < n) p[e] = v[e];
+        for (int e = 0; e < N; ++e) f[e] = v[e];
+        *reinterpret_cast<floats*>(p) = f;
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e < n) p[e] = v[e];
+    }
 }
 
-// 1 / (1 + e^-x), within (3 + |x|) 2^-23 relative to it; 0 below -88
-__device__ __forceinline__ float sigmoid_of(float x) {
-    return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x));
+// (1 / (1 + e^-x), 1 / (1 + e^x)) by one exponential and one reciprocal, both within (4 + |x|) 2^-23
+// relative to themselves; the smaller one is 0 past |x| = 88.
+__device__ __forceinline__ void sigmoids(float x, float& keep, float& take) {
+    const float e = exp_fast(-fabsf(x));
+    const float large = __builtin_amdgcn_rcpf(1.0f + e), small = e * large;
+    keep = x >= 0.0f ? large : small;
+    take = x >= 0.0f ? small : large;
 }
 
-// a state c after a span of effect (A, H): a state of 0 leaves H also where A is infinite
+// A state c after a span of effect (A, H).  Linear gates may make A infinite: a state of 0 leaves H.
+template <bool SIG>
 __device__ __forceinline__ float after_span(float A, float c, float H) {
-    return c == 0.0f ? H : fmaf(A, c, H);
+    return !SIG && c == 0.0f ? H : fmaf(A, c, H);
 }
+
+// what a span of steps does to a state: h -> A h + H
+struct Effect {
+    float A, H;
+};
 
 struct ScanArgs {
     const void *gate, *x;
@@ -113,8 +157,9 @@ struct ScanArgs {
     const int32_t* lengths;
     void* h;
     float* state;
-    float* effects;       // [chunk][A, H][batch * d], where several workgroups share a sequence
+    Effect* effects;      // of every chunk, where several workgroups share a sequence
     int64_t batch, steps, d, tiles, chunks, per;      // per: chunks a workgroup walks
+    bool runs;            // item_of's
 };
 
 struct ScanBackArgs {
@@ -123,8 +168,9 @@ struct ScanBackArgs {
     const int32_t* lengths;
     void *dgate, *dx;
     float* dstate0;
-    float* effects;
+    Effect* effects;
     int64_t batch, steps, d, tiles, chunks, per;
+    bool runs;
 };
 
 // steps of sequence b that count
@@ -135,40 +181,84 @@ __device__ __forceinline__ int64_t length_of(const ARGS& a, int64_t b) {
     return n < 0 ? 0 : n < a.steps ? n : a.steps;
 }
 
-// what a workgroup's lane works on
+// The workgroup's tile; -1 past the last one.  Workgroup b runs on XCD b % 8: with `runs` each XCD takes
+// a run of neighbouring tiles, which share lines where a row is no whole number of 128-byte lines
+// (3 x 10007 x 2500 f32 179 us so, 228 tile by tile; where rows are whole lines tile by tile is
+// faster: 32 x 1024 x 2048 f16 88 us, 95 in runs).
+__device__ __forceinline__ int64_t item_of(int64_t items, bool runs) {
+    if (!runs) return blockIdx.x < items ? (int64_t)blockIdx.x : -1;
+    const int64_t per = (items + 7) / 8, at = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    return (blockIdx.x >> 3) < per && at < items ? at : -1;
+}
+
+// the wave's number, known to be uniform
+__device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// What a workgroup's lane works on.  A wave takes 64 words of channels of one span, or (LANES 32) 32
+// words of two neighbouring spans.  The addresses of a step are uniform but for 32-bit offsets.
 struct Place {
-    int64_t b, c, left, row0;      // sequence, first channel, channels to the row's end, first row
-    bool last;                     // the row's last channel, alone in its word
+    int64_t item, b, row0;   // tile and sequence, its first row
+    int64_t load_c, c0;      // where the workgroup's part of a row begins, for loads and for stores
+    uint32_t off, at;        // the lane's word in it (bytes), and its first channel
+    int left;                // channels from there to the row's end
+    int word, sub, span;     // the lane's word, its span in the wave and in the chunk
+    bool last, whole;        // the row's last channel is alone in its word; every lane's word is whole
 };
 
-template <typename T>
+// Lanes at the row's end load its last word, whose element `word_of` moves to the front.
+template <typename T, int LANES>
 __device__ __forceinline__ Place place_of(int64_t item, int64_t tiles, int64_t steps, int64_t d) {
+    constexpr int E = kCh<T>;
     Place p;
+    p.item = item;
     p.b = item / tiles;
-    p.c = (item % tiles * 64 + (threadIdx.x & 63)) * kCh<T>;
-    p.left = d - p.c;
     p.row0 = p.b * steps;
-    p.last = kCh<T> == 2 && p.left == 1 && d >= 2;
+    p.c0 = item % tiles * LANES * E;
+    p.load_c = p.c0 + E <= d ? p.c0 : d < E ? 0 : d - E;
+    p.word = threadIdx.x & (LANES - 1);
+    p.sub = LANES == 64 ? 0 : (threadIdx.x & 63) / LANES;
+    p.span = wave_of() * (64 / LANES) + p.sub;
+    p.at = p.word * E;
+    const int64_t left = d - p.c0 - p.at, most = d - E - p.load_c;      // the last word's place
+    p.left = left < 0 ? 0 : left < E ? (int)left : E;
+    p.off = (most <= 0 ? 0 : p.at < most ? p.at : (uint32_t)most) * (uint32_t)sizeof(elem<T>);
+    p.last = E == 2 && p.left == 1;
+    p.whole = p.c0 + LANES * E <= d;
     return p;
 }
 
 // (a, b) of one step's word
 template <typename T, bool SIG>
-__device__ __forceinline__ void terms(uint32_t g, uint32_t x, bool last, bool inside,
-                                      float (&a)[kCh<T>], float (&b)[kCh<T>]) {
+__device__ __forceinline__ void terms(uint32_t g, uint32_t x, bool last, float (&a)[kCh<T>],
+                                      float (&b)[kCh<T>]) {
     word_of<T>(g, last, a);
     word_of<T>(x, last, b);
+    if constexpr (SIG) {
 #pragma unroll
-    for (int e = 0; e < kCh<T>; ++e) {
-        if constexpr (SIG) {
-            b[e] = sigmoid_of(-a[e]) * b[e];
-            a[e] = sigmoid_of(a[e]);
-        }
-        if (!inside) {
-            a[e] = 1.0f;
-            b[e] = 0.0f;
+        for (int e = 0; e < kCh<T>; ++e) {
+            float keep, take;
+            sigmoids(a[e], keep, take);
+            b[e] *= take;
+            a[e] = keep;
         }
     }
+}
+
+// The terms of a span's steps that lie past the length: they keep the state.  (A branch of its own: a
+// choice a step costs as much as the recurrence.)
+template <int E>
+__device__ __forceinline__ void keep_past(bool full, int64_t inside, float (&a)[kSteps][E],
+                                          float (&b)[kSteps][E]) {
+    if (full) return;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+        if (i >= inside) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                a[i][e] = 1.0f;
+                b[i][e] = 0.0f;
+            }
+        }
 }
 
 // the two words of each of a span's steps
@@ -176,181 +266,235 @@ struct SpanWords {
     uint32_t g[kSteps], x[kSteps];
 };
 
+// Bytes from a span's first row to the row of step i, the row `rest` steps on from where that lies past
+// it: what is loaded there is not used.  (No branch: the words of a chunk ahead would be copied, and
+// waited for, where two paths of loads meet.)
+__device__ __forceinline__ uint32_t row_bytes(const Place& p, int i, int rest, uint32_t pitch) {
+    const int at = p.sub * kSteps + i;
+    return __umul24((uint32_t)(at < rest ? at : rest), pitch);      // at most 15 times less than 2^24
+}
+
+__device__ __forceinline__ int rest_of(int64_t begin, int64_t most) {
+    return most - begin < 2 * kSteps ? (int)(most - begin) : 2 * kSteps;
+}
+
+// at: the first step of the wave's spans; rows past `most` are that row again
 template <typename T>
-__device__ __forceinline__ void read_span(const T* gate, const T* x, const Place& p, int64_t t0,
-                                          int64_t len, int64_t d, SpanWords& r) {
+__device__ __forceinline__ void read_span(const elem<T>* gate, const elem<T>* x, const Place& p,
+                                          int64_t at, int64_t most, int64_t d, SpanWords& r) {
+    if (at > most) at = most;
+    const int rest = rest_of(at, most);
+    const int64_t row = (p.row0 + at) * d + p.load_c;
+    gate += row;
+    x += row;
+    const uint32_t pitch = (uint32_t)d * sizeof(elem<T>);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-        // past the length the last step again: what lies there is not used
-        const int64_t t = t0 + i < len ? t0 + i : len > 0 ? len - 1 : 0;
-        r.g[i] = load_word(gate + (p.row0 + t) * d, p.c, d);
-        r.x[i] = load_word(x + (p.row0 + t) * d, p.c, d);
+        const uint32_t off = p.off + row_bytes(p, i, rest, pitch);
+        r.g[i] = load_word<T>(gate, off);
+        r.x[i] = load_word<T>(x, off);
     }
 }
 
-template <int E>
-struct Effect {
-    float A[E], H[E];
+// The effects of a chunk's spans on CH channels, and the states that reach the spans.
+template <int SPANS, int CH>
+struct ChunkState {
+    Effect eff[SPANS][CH];
+    float in[SPANS][CH];
 };
 
-// the effects of spans in LDS, composed: of the spans before mine, and of all
-template <int E, bool BACK>
-__device__ __forceinline__ void compose(const Effect<E> (*s)[64], int wave, Effect<E>& mine,
-                                        Effect<E>& all) {
-    const int lane = threadIdx.x & 63;
-    all = s[BACK ? kSpans - 1 : 0][lane];
+// One channel's effects composed, from the first span on (backwards from the last): `in` gets the
+// state that reaches each, for the one that reaches the chunk; that becomes the next chunk's.
+template <bool SIG, bool BACK, int SPANS, int CH>
+__device__ __forceinline__ void compose(ChunkState<SPANS, CH>& s, int ch, float& carry) {
+    Effect all = {};
+    float in[SPANS];
 #pragma unroll
-    for (int k = 1; k < kSpans; ++k) {
-        const int v = BACK ? kSpans - 1 - k : k;
-        if (v == wave) mine = all;
-        const Effect<E> one = s[v][lane];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            all.H[e] = after_span(one.A[e], all.H[e], one.H[e]);
-            all.A[e] *= one.A[e];
-        }
+    for (int k = 0; k < SPANS; ++k) {
+        const Effect one = s.eff[BACK ? SPANS - 1 - k : k][ch];
+        in[k] = k ? after_span<SIG>(all.A, carry, all.H) : carry;
+        all.H = k ? after_span<SIG>(one.A, all.H, one.H) : one.H;
+        all.A = k ? all.A * one.A : one.A;
     }
+#pragma unroll
+    for (int k = 0; k < SPANS; ++k) s.in[BACK ? SPANS - 1 - k : k][ch] = in[k];
+    carry = after_span<SIG>(all.A, carry, all.H);
 }
 
-// the state that reaches the workgroup's first chunk
-template <int E, typename ARGS, bool BACK>
-__device__ __forceinline__ void enter(const ARGS& a, const Place& p, const float* from,
-                                      int64_t chunk, float (&carry)[E]) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) carry[e] = 0.0f;
-    if (from) load_state(from + p.b * a.d + p.c, p.left, carry);
-    const int64_t cells = a.batch * a.d;
+// place of a chunk's effect on a channel: [chunk][sequence][tile][channel]
+template <int CH, typename ARGS>
+__device__ __forceinline__ int64_t effect_at(const ARGS& a, int64_t item, int64_t chunk, int ch) {
+    return (chunk * a.batch * a.tiles + item) * CH + ch;
+}
+
+// The state that reaches the workgroup's first chunk on channel ch (of CH, `inside` the row).
+template <int CH, bool SIG, bool BACK, typename ARGS>
+__device__ __forceinline__ float enter(const ARGS& a, const Place& p, const float* from,
+                                       int64_t chunk, int ch, bool inside) {
+    float carry = from && inside ? from[p.b * a.d + p.c0 + ch] : 0.0f;
     const int64_t count = BACK ? a.chunks - 1 - chunk : chunk;
-#pragma unroll 4
+    const Effect* at = a.effects + effect_at<CH>(a, p.item, BACK ? a.chunks - 1 : 0, ch);
+    const int64_t step = (BACK ? -1 : 1) * a.batch * a.tiles * CH;
+#pragma unroll 8
     for (int64_t i = 0; i < count; ++i) {
-        const float* at = a.effects + (BACK ? a.chunks - 1 - i : i) * 2 * cells + p.b * a.d + p.c;
-        Effect<E> one;
-        load_state(at, p.left, one.A);
-        load_state(at + cells, p.left, one.H);
-#pragma unroll
-        for (int e = 0; e < E; ++e) carry[e] = after_span(one.A[e], carry[e], one.H[e]);
+        const Effect one = at[i * step];
+        carry = after_span<SIG>(one.A, carry, one.H);
     }
+    return carry;
 }
 
-// A workgroup walks chunks of 64 words of channels, a wave per span, the next chunk's words in
-// flight while this one's effects go round.  One pass over gate and x: bound by HBM.
-template <typename T, bool SIG>
-__global__ __launch_bounds__(64 * kSpans) void k_gated_scan(ScanArgs a) {
-    constexpr int E = kCh<T>;
-    __shared__ Effect<E> s_eff[2][kSpans][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const Place p = place_of<T>(blockIdx.x, a.tiles, a.steps, a.d);
+// A workgroup walks chunks of 64 (or 32) words of channels, the next two chunks' words in flight while
+// this one's effects go round.  One pass over gate and x: bound by HBM.
+template <typename T, bool SIG, int LANES>
+__global__ __launch_bounds__(LANES * kSpans) void k_gated_scan(ScanArgs a) {
+    constexpr int E = kCh<T>, CH = LANES * E, kChunkSteps = kSteps * kSpans, kMine = kSteps * 64 / LANES;
+    __shared__ ChunkState<kSpans, CH> s;
+    const int wave = wave_of(), ch = threadIdx.x;      // the threads below CH compose a channel each
+    const int64_t item = item_of(a.batch * a.tiles, a.runs);
+    if (item < 0) return;
+    const Place p = place_of<T, LANES>(item, a.tiles, a.steps, a.d);
     const int64_t len = length_of(a, p.b);
-    const T* gate = static_cast<const T*>(a.gate);
-    const T* x = static_cast<const T*>(a.x);
+    const elem<T>* gate = static_cast<const elem<T>*>(a.gate);
+    const elem<T>* x = static_cast<const elem<T>*>(a.x);
     const int64_t first = (int64_t)blockIdx.y * a.per;
     const int64_t behind = first + a.per < a.chunks ? first + a.per : a.chunks;
-    SpanWords cur, next;
-    read_span(gate, x, p, first * kChunkSteps + wave * kSteps, len, a.d, cur);
-    float carry[E];
-    enter<E, ScanArgs, false>(a, p, a.state0, first, carry);
-    if (first == 0 && len == 0 && wave == 0) store_state(a.state + p.b * a.d + p.c, p.left, carry);
-    for (int64_t k = first; k < behind; ++k) {
-        const int64_t t0 = k * kChunkSteps + wave * kSteps;
-        if (k + 1 < behind) read_span(gate, x, p, t0 + kChunkSteps, len, a.d, next);
+    SpanWords even, odd;      // the words of two chunks, both in flight
+    int64_t begin = first * kChunkSteps + wave * kMine;      // the wave's first step
+    const int64_t limit = len < behind * kChunkSteps ? len : behind * kChunkSteps;
+    const int64_t most = limit > 0 ? limit - 1 : 0;      // the last row that is read
+    read_span<T>(gate, x, p, begin, most, a.d, even);
+    read_span<T>(gate, x, p, begin + kChunkSteps, most, a.d, odd);
+    float carry = 0.0f;
+    if (ch < CH) {
+        const bool inside = p.c0 + ch < a.d;
+        carry = enter<CH, SIG, false>(a, p, a.state0, first, ch, inside);
+        if (first == 0 && len == 0 && inside) a.state[p.b * a.d + p.c0 + ch] = carry;
+    }
+    const auto walk = [&](SpanWords& words) {
+        const int64_t t0 = begin + p.sub * kSteps;
         float av[kSteps][E], bv[kSteps][E];
-        Effect<E> own;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            terms<T, SIG>(cur.g[i], cur.x[i], p.last, t0 + i < len, av[i], bv[i]);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                own.H[e] = i ? fmaf(av[i][e], own.H[e], bv[i][e]) : bv[i][e];
-                own.A[e] = i ? own.A[e] * av[i][e] : av[i][e];
-            }
-        }
-        s_eff[k & 1][wave][lane] = own;
-        __syncthreads();
-        Effect<E> mine, all;
-        compose<E, false>(s_eff[k & 1], wave, mine, all);
-        float h[E];
+        for (int i = 0; i < kSteps; ++i) terms<T, SIG>(words.g[i], words.x[i], p.last, av[i], bv[i]);
+        read_span<T>(gate, x, p, begin + 2 * kChunkSteps, most, a.d, words);
+        keep_past(begin + kMine <= len, len - t0, av, bv);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            h[e] = wave ? after_span(mine.A[e], carry[e], mine.H[e]) : carry[e];
-            carry[e] = after_span(all.A[e], carry[e], all.H[e]);
+            Effect own{av[0][e], bv[0][e]};
+#pragma unroll
+            for (int i = 1; i < kSteps; ++i) {
+                own.H = fmaf(av[i][e], own.H, bv[i][e]);
+                own.A *= av[i][e];
+            }
+            s.eff[p.span][p.at + e] = own;
         }
+        __syncthreads();
+        if (ch < CH) compose<SIG, false>(s, ch, carry);
+        __syncthreads();
+        float h[E];
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int64_t t = t0 + i;
+        for (int e = 0; e < E; ++e) h[e] = s.in[p.span][p.at + e];
+        elem<T>* out = static_cast<elem<T>*>(a.h) + (p.row0 + begin) * a.d + p.c0;
+        const uint32_t at = p.at + (uint32_t)(p.sub * kSteps) * (uint32_t)a.d;
+        if (p.whole && begin + kMine < len) {      // not the last step, whose state is kept
 #pragma unroll
-            for (int e = 0; e < E; ++e) h[e] = fmaf(av[i][e], h[e], bv[i][e]);
-            if (t < len) {
-                store_word(static_cast<T*>(a.h) + (p.row0 + t) * a.d + p.c, p.left, h);
-                if (t == len - 1) store_state(a.state + p.b * a.d + p.c, p.left, h);
-            } else if (t < a.steps) {
-                const float zero[E] = {};
-                store_word(static_cast<T*>(a.h) + (p.row0 + t) * a.d + p.c, p.left, zero);
+            for (int i = 0; i < kSteps; ++i) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) h[e] = fmaf(av[i][e], h[e], bv[i][e]);
+                store_word<T>(out + at, E, h);
+                out += a.d;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int64_t t = t0 + i;
+#pragma unroll
+                for (int e = 0; e < E; ++e) h[e] = fmaf(av[i][e], h[e], bv[i][e]);
+                if (t < len) {
+                    store_word<T>(out + at, p.left, h);
+                    if (t == len - 1) store_state(a.state + p.b * a.d + p.c0 + p.at, p.left, h);
+                } else if (t < a.steps) {
+                    const float zero[E] = {};
+                    store_word<T>(out + at, p.left, zero);
+                }
+                out += a.d;
             }
         }
-        cur = next;
+        begin += kChunkSteps;
+    };
+    for (int64_t k = first; k < behind; k += 2) {
+        walk(even);
+        if (k + 1 < behind) walk(odd);
     }
 }
 
 // The effect of every chunk but the last one (backwards: but the first), for workgroups that begin
 // in the middle of a sequence.
-template <typename T, bool SIG, bool BACK, typename ARGS>
-__device__ __forceinline__ void chunk_effect(const ARGS& a, const T* gate, const T* other,
+template <typename T, bool SIG, bool BACK, int LANES, typename ARGS>
+__device__ __forceinline__ void chunk_effect(const ARGS& a, const elem<T>* gate, const elem<T>* other,
                                              int64_t chunk) {
-    constexpr int E = kCh<T>;
-    __shared__ Effect<E> s_eff[kSpans][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const Place p = place_of<T>(blockIdx.x, a.tiles, a.steps, a.d);
-    const int64_t len = length_of(a, p.b), t0 = chunk * kChunkSteps + wave * kSteps;
+    constexpr int E = kCh<T>, SPANS = BACK ? kBackSpans : kSpans;
+    constexpr int CH = LANES * E, kMine = kSteps * 64 / LANES;
+    __shared__ Effect s_eff[SPANS][CH];
+    const int wave = wave_of(), ch = threadIdx.x;
+    const int64_t item = item_of(a.batch * a.tiles, a.runs);
+    if (item < 0) return;
+    const Place p = place_of<T, LANES>(item, a.tiles, a.steps, a.d);
+    const int64_t len = length_of(a, p.b), begin = chunk * SPANS * kSteps + wave * kMine;
     SpanWords r;
-    read_span(gate, other, p, t0, len, a.d, r);
-    Effect<E> own;
+    read_span<T>(gate, other, p, begin, len > 0 ? len - 1 : 0, a.d, r);
+    float av[kSteps][E], bv[kSteps][E];
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-        const int i = BACK ? kSteps - 1 - j : j;
-        float av[E], bv[E];
+    for (int i = 0; i < kSteps; ++i) {
         if constexpr (BACK) {
-            word_of<T>(r.g[i], p.last, av);
-            word_of<T>(r.x[i], p.last, bv);
+            word_of<T>(r.g[i], p.last, av[i]);
+            word_of<T>(r.x[i], p.last, bv[i]);
+            if constexpr (SIG) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if constexpr (SIG) av[e] = sigmoid_of(av[e]);
-                if (t0 + i >= len) {
-                    av[e] = 1.0f;
-                    bv[e] = 0.0f;
+                for (int e = 0; e < E; ++e) {
+                    float take;
+                    sigmoids(av[i][e], av[i][e], take);
                 }
-                // E -> a (dh + E)
-                own.H[e] = av[e] * (j ? bv[e] + own.H[e] : bv[e]);
-                own.A[e] = j ? own.A[e] * av[e] : av[e];
             }
         } else {
-            terms<T, SIG>(r.g[i], r.x[i], p.last, t0 + i < len, av, bv);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                own.H[e] = j ? fmaf(av[e], own.H[e], bv[e]) : bv[e];
-                own.A[e] = j ? own.A[e] * av[e] : av[e];
-            }
+            terms<T, SIG>(r.g[i], r.x[i], p.last, av[i], bv[i]);
         }
     }
-    s_eff[wave][lane] = own;
+    keep_past(begin + kMine <= len, len - begin - p.sub * kSteps, av, bv);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        Effect own;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            const int i = BACK ? kSteps - 1 - j : j;
+            if constexpr (BACK)      // E -> a (dh + E)
+                own.H = av[i][e] * (j ? bv[i][e] + own.H : bv[i][e]);
+            else
+                own.H = j ? fmaf(av[i][e], own.H, bv[i][e]) : bv[i][e];
+            own.A = j ? own.A * av[i][e] : av[i][e];
+        }
+        s_eff[p.span][p.at + e] = own;
+    }
     __syncthreads();
-    if (wave) return;
-    Effect<E> mine, all;
-    compose<E, BACK>(s_eff, -1, mine, all);
-    const int64_t cells = a.batch * a.d;
-    float* at = a.effects + chunk * 2 * cells + p.b * a.d + p.c;
-    store_state(at, p.left, all.A);
-    store_state(at + cells, p.left, all.H);
+    if (ch >= CH) return;
+    Effect all;
+#pragma unroll
+    for (int k = 0; k < SPANS; ++k) {
+        const Effect one = s_eff[BACK ? SPANS - 1 - k : k][ch];
+        all.H = k ? after_span<SIG>(one.A, all.H, one.H) : one.H;
+        all.A = k ? all.A * one.A : one.A;
+    }
+    a.effects[effect_at<CH>(a, item, chunk, ch)] = all;
 }
 
-template <typename T, bool SIG>
-__global__ __launch_bounds__(64 * kSpans) void k_gated_scan_chunks(ScanArgs a) {
-    chunk_effect<T, SIG, false>(a, static_cast<const T*>(a.gate), static_cast<const T*>(a.x),
+template <typename T, bool SIG, int LANES>
+__global__ __launch_bounds__(LANES * kSpans) void k_gated_scan_chunks(ScanArgs a) {
+    chunk_effect<T, SIG, false, LANES>(a, static_cast<const elem<T>*>(a.gate), static_cast<const elem<T>*>(a.x),
                                 blockIdx.y);
 }
 
-template <typename T, bool SIG>
-__global__ __launch_bounds__(64 * kSpans) void k_gated_scan_chunks_back(ScanBackArgs a) {
-    chunk_effect<T, SIG, true>(a, static_cast<const T*>(a.gate), static_cast<const T*>(a.dh),
+template <typename T, bool SIG, int LANES>
+__global__ __launch_bounds__(LANES * kBackSpans) void k_gated_scan_chunks_back(ScanBackArgs a) {
+    chunk_effect<T, SIG, true, LANES>(a, static_cast<const elem<T>*>(a.gate), static_cast<const elem<T>*>(a.dh),
                                blockIdx.y + 1);
 }
 
@@ -373,8 +517,10 @@ __global__ __launch_bounds__(256) void k_gated_scan_steps(ScanArgs a) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             if constexpr (SIG) {
-                x[e] = sigmoid_of(-g[e]) * x[e];
-                g[e] = sigmoid_of(g[e]);
+                float keep, take;
+                sigmoids(g[e], keep, take);
+                x[e] *= take;
+                g[e] = keep;
             }
             if (t < len) h[e] = fmaf(g[e], h[e], x[e]);
             o[e] = t < len ? as_float(h[e]) : 0.0f;
@@ -386,103 +532,154 @@ __global__ __launch_bounds__(256) void k_gated_scan_steps(ScanArgs a) {
 
 // ---------------------------------------------------------------- backward
 
-// the words of each of a span's steps: gate, dh, h one step before, x (sigmoid gates)
+// the words of each of a span's steps: gate and dh; h one step before and x (sigmoid gates)
 struct BackWords {
-    uint32_t g[kSteps], dh[kSteps], h[kSteps], x[kSteps];
+    SpanWords in;      // gate, dh
+    uint32_t h[kSteps], x[kSteps];
 };
 
+// as read_span; of h the rows before (before the sequence's first that itself, which is not used)
 template <typename T, bool SIG>
-__device__ __forceinline__ void read_back(const ScanBackArgs& a, const Place& p, int64_t t0,
-                                          int64_t len, BackWords& r) {
+__device__ __forceinline__ void read_before(const ScanBackArgs& a, const Place& p, int64_t at,
+                                            int64_t most, BackWords& r) {
+    if (at > most) at = most;
+    const int rest = rest_of(at, most), back = at > 0 ? 0 : 1;
+    const int64_t row = (p.row0 + at) * a.d + p.load_c;
+    const elem<T>* x = static_cast<const elem<T>*>(a.x) + row;
+    const elem<T>* h = static_cast<const elem<T>*>(a.h) + (back ? row : row - a.d);
+    const uint32_t pitch = (uint32_t)a.d * sizeof(elem<T>);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-        const int64_t t = t0 + i < len ? t0 + i : len > 0 ? len - 1 : 0;
-        const int64_t row = (p.row0 + t) * a.d;
-        r.g[i] = load_word(static_cast<const T*>(a.gate) + row, p.c, a.d);
-        r.dh[i] = load_word(static_cast<const T*>(a.dh) + row, p.c, a.d);
-        r.h[i] = load_word(static_cast<const T*>(a.h) + (t > 0 ? row - a.d : row), p.c, a.d);
-        if constexpr (SIG) r.x[i] = load_word(static_cast<const T*>(a.x) + row, p.c, a.d);
+        const uint32_t off = row_bytes(p, i, rest, pitch);
+        if constexpr (SIG) r.x[i] = load_word<T>(x, p.off + off);
+        r.h[i] = load_word<T>(h, p.off + (back && off ? off - pitch : off));
     }
 }
 
 // As k_gated_scan from the last step on.
-template <typename T, bool SIG>
-__global__ __launch_bounds__(64 * kSpans) void k_gated_scan_backward(ScanBackArgs a) {
-    constexpr int E = kCh<T>;
-    __shared__ Effect<E> s_eff[2][kSpans][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const Place p = place_of<T>(blockIdx.x, a.tiles, a.steps, a.d);
+template <typename T, bool SIG, int LANES>
+__global__ __launch_bounds__(LANES * kBackSpans) void k_gated_scan_backward(ScanBackArgs a) {
+    constexpr int E = kCh<T>, CH = LANES * E, kChunkSteps = kSteps * kBackSpans;
+    constexpr int kMine = kSteps * 64 / LANES;
+    __shared__ ChunkState<kBackSpans, CH> s;
+    const int wave = wave_of(), ch = threadIdx.x;      // the threads below CH compose a channel each
+    const int64_t item = item_of(a.batch * a.tiles, a.runs);
+    if (item < 0) return;
+    const Place p = place_of<T, LANES>(item, a.tiles, a.steps, a.d);
     const int64_t len = length_of(a, p.b);
     const int64_t first = (int64_t)blockIdx.y * a.per;
     const int64_t behind = first + a.per < a.chunks ? first + a.per : a.chunks;
-    BackWords cur, next;
-    read_back<T, SIG>(a, p, (behind - 1) * kChunkSteps + wave * kSteps, len, cur);
-    float carry[E], start[E] = {};
-    enter<E, ScanBackArgs, true>(a, p, a.dstate, behind - 1, carry);
-    if (a.state0) load_state(a.state0 + p.b * a.d + p.c, p.left, start);
-    for (int64_t k = behind - 1; k >= first; --k) {
-        const int64_t t0 = k * kChunkSteps + wave * kSteps;
-        if (k > first) read_back<T, SIG>(a, p, t0 - kChunkSteps, len, next);
-        float av[kSteps][E], dv[kSteps][E];
-        Effect<E> own;
+    const elem<T>* gate = static_cast<const elem<T>*>(a.gate);
+    const elem<T>* dh = static_cast<const elem<T>*>(a.dh);
+    BackWords even, odd;      // the words of two chunks, both in flight
+    int64_t begin = (behind - 1) * kChunkSteps + wave * kMine;      // the wave's first step
+    const int64_t least = first * kChunkSteps + wave * kMine, most = len > 0 ? len - 1 : 0;
+    // chunks before the workgroup's first: that one again
+    const auto read_in = [&](int64_t at, BackWords& r) {
+        read_span<T>(gate, dh, p, at > least ? at : least, most, a.d, r.in);
+    };
+    const auto read_rest = [&](int64_t at, BackWords& r) {
+        read_before<T, SIG>(a, p, at > least ? at : least, most, r);
+    };
+    read_in(begin, even);
+    read_rest(begin, even);
+    read_in(begin - kChunkSteps, odd);
+    read_rest(begin - kChunkSteps, odd);
+    float carry = 0.0f, start[E] = {};
+    if (ch < CH) carry = enter<CH, SIG, true>(a, p, a.dstate, behind - 1, ch, p.c0 + ch < a.d);
+    if (a.state0) load_state(a.state0 + p.b * a.d + p.c0 + p.at, p.left, start);
+    const auto walk = [&](BackWords& words) {
+        const int64_t t0 = begin + p.sub * kSteps;
+        const bool full = begin + kMine <= len;
+        float av[kSteps][E], dv[kSteps][E], take[kSteps][E];
 #pragma unroll
-        for (int i = kSteps - 1; i >= 0; --i) {
-            word_of<T>(cur.g[i], p.last, av[i]);
-            word_of<T>(cur.dh[i], p.last, dv[i]);
+        for (int i = 0; i < kSteps; ++i) {
+            word_of<T>(words.in.g[i], p.last, av[i]);
+            word_of<T>(words.in.x[i], p.last, dv[i]);
+            if constexpr (SIG) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                float keep = SIG ? sigmoid_of(av[i][e]) : av[i][e];
-                if (t0 + i >= len) {
-                    keep = 1.0f;
-                    dv[i][e] = 0.0f;
-                }
-                const bool begins = i == kSteps - 1;
-                own.H[e] = keep * (begins ? dv[i][e] : dv[i][e] + own.H[e]);
-                own.A[e] = begins ? keep : own.A[e] * keep;
-                if constexpr (!SIG) av[i][e] = keep;
+                for (int e = 0; e < E; ++e) sigmoids(av[i][e], av[i][e], take[i][e]);
             }
         }
-        s_eff[k & 1][wave][lane] = own;
-        __syncthreads();
-        Effect<E> mine, all;
-        compose<E, true>(s_eff[k & 1], wave, mine, all);
-        float back[E];
+        keep_past(full, len - t0, av, dv);
+        read_in(begin - 2 * kChunkSteps, words);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            back[e] = wave < kSpans - 1 ? after_span(mine.A[e], carry[e], mine.H[e]) : carry[e];
-            carry[e] = after_span(all.A[e], carry[e], all.H[e]);
-        }
+            Effect own{av[kSteps - 1][e], av[kSteps - 1][e] * dv[kSteps - 1][e]};
 #pragma unroll
-        for (int i = kSteps - 1; i >= 0; --i) {
-            const int64_t t = t0 + i;
-            float h[E], x[E], dg[E], dx[E];
-            word_of<T>(cur.h[i], p.last, h);
-            if constexpr (SIG) word_of<T>(cur.x[i], p.last, x);
-            const bool inside = t < len;
+            for (int i = kSteps - 2; i >= 0; --i) {
+                own.H = av[i][e] * (dv[i][e] + own.H);
+                own.A *= av[i][e];
+            }
+            s.eff[p.span][p.at + e] = own;
+        }
+        __syncthreads();
+        if (ch < CH) compose<SIG, true>(s, ch, carry);
+        __syncthreads();
+        float back[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) back[e] = s.in[p.span][p.at + e];
+        const auto step = [&](int i, float (&dg)[E], float (&dx)[E], const float (&before)[E]) {
+            float x[E];
+            if constexpr (SIG) word_of<T>(words.x[i], p.last, x);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float before = t > 0 ? h[e] : start[e];
                 const float total = dv[i][e] + back[e];
                 if constexpr (SIG) {
-                    const float keep = sigmoid_of(av[i][e]), take = sigmoid_of(-av[i][e]);
-                    dx[e] = take * total;
-                    dg[e] = keep * (before - x[e]) * dx[e];
-                    if (inside) back[e] = keep * total;
+                    dx[e] = take[i][e] * total;
+                    dg[e] = av[i][e] * (before[e] - x[e]) * dx[e];
                 } else {
                     dx[e] = total;
-                    dg[e] = before * total;
-                    if (inside) back[e] = av[i][e] * total;
+                    dg[e] = before[e] * total;
                 }
-                if (!inside) dx[e] = dg[e] = 0.0f;
+                back[e] = av[i][e] * total;
             }
-            if (t < a.steps) {
-                const int64_t at = (p.row0 + t) * a.d + p.c;
-                store_word(static_cast<T*>(a.dgate) + at, p.left, dg);
-                store_word(static_cast<T*>(a.dx) + at, p.left, dx);
+        };
+        const int64_t row = (p.row0 + begin + kSteps - 1) * a.d + p.c0;
+        elem<T>* dg_at = static_cast<elem<T>*>(a.dgate) + row;
+        elem<T>* dx_at = static_cast<elem<T>*>(a.dx) + row;
+        const uint32_t at = p.at + (uint32_t)(p.sub * kSteps) * (uint32_t)a.d;
+        if (p.whole && begin > 0 && full) {
+#pragma unroll
+            for (int i = kSteps - 1; i >= 0; --i) {
+                float h[E], dg[E], dx[E];
+                word_of<T>(words.h[i], p.last, h);
+                step(i, dg, dx, h);
+                store_word<T>(dg_at + at, E, dg);
+                store_word<T>(dx_at + at, E, dx);
+                dg_at -= a.d;
+                dx_at -= a.d;
             }
-            if (t == 0 && a.dstate0) store_state(a.dstate0 + p.b * a.d + p.c, p.left, back);
+        } else {
+#pragma unroll
+            for (int i = kSteps - 1; i >= 0; --i) {
+                const int64_t t = t0 + i;
+                float h[E], dg[E], dx[E];
+                word_of<T>(words.h[i], p.last, h);
+                if (t == 0) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) h[e] = start[e];
+                }
+                step(i, dg, dx, h);
+                if (t >= len) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) dg[e] = dx[e] = 0.0f;
+                }
+                if (t < a.steps) {
+                    store_word<T>(dg_at + at, p.left, dg);
+                    store_word<T>(dx_at + at, p.left, dx);
+                }
+                if (t == 0 && a.dstate0) store_state(a.dstate0 + p.b * a.d + p.c0 + p.at, p.left, back);
+                dg_at -= a.d;
+                dx_at -= a.d;
+            }
         }
-        cur = next;
+        read_rest(begin - 2 * kChunkSteps, words);
+        begin -= kChunkSteps;
+    };
+    for (int64_t k = behind - 1; k >= first; k -= 2) {
+        walk(even);
+        if (k - 1 >= first) walk(odd);
     }
 }
 
@@ -490,15 +687,23 @@ __global__ __launch_bounds__(64 * kSpans) void k_gated_scan_backward(ScanBackArg
 
 struct ScanPlan {
     int64_t tiles, chunks, parts, per;
+    int lanes;
+    bool runs;
 };
 
-// One workgroup a tile of channels, unless that leaves most compute units without one: then the
-// chunks' effects are taken first (gate and x read twice) and several share a sequence.
-ScanPlan scan_plan(int64_t batch, int64_t steps, int64_t d, det_dtype dtype) {
+// One workgroup a tile of channels: of 64 words, or of 32 where that leaves compute units without one
+// (120 tiles of 64: 342 us for 3 x 10007 x 2500 f32, 240 of 32: 245; 256 tiles of 64: 100 us for 8 x 2048
+// x 4096 bf16, 512 of 32: 105).  Where those are still few, the chunks' effects are taken first (gate
+// and x read twice) and 512 workgroups share the sequences (1 x 32768 x 2048 bf16 131 us; a workgroup a
+// tile 1375; 240 tiles 245 us without it, 350 with it).
+ScanPlan scan_plan(int64_t batch, int64_t steps, int64_t d, det_dtype dtype, int spans) {
     ScanPlan p;
-    p.tiles = cdiv(d, 64 * (4 / (int64_t)lm_size(dtype)));
-    p.chunks = cdiv(steps, kChunkSteps);
+    const int64_t es = (int64_t)lm_size(dtype), ch = 4 / es;
+    p.lanes = d == 1 || cdiv(d, 64 * ch) * batch <= 160 ? 32 : 64;
+    p.tiles = cdiv(d, p.lanes * (d == 1 ? 1 : ch));
+    p.chunks = cdiv(steps, kSteps * spans);
     p.parts = 1;
+    p.runs = d * es % 128 != 0;
     const int64_t wgs = p.tiles * batch;
     if (wgs <= 128 && p.chunks >= 4) {
         p.parts = cdiv(512, wgs);
@@ -509,6 +714,21 @@ ScanPlan scan_plan(int64_t batch, int64_t steps, int64_t d, det_dtype dtype) {
     return p;
 }
 
+template <typename T, bool SIG, int LANES>
+det_status scan_as(const ScanArgs& a, const ScanPlan& p, hipStream_t s) {
+    const unsigned wgs = (unsigned)(cdiv(p.tiles * a.batch, 8) * 8);
+    const dim3 block(LANES * kSpans);
+    if (p.parts > 1) {
+        KernelTimer kt("k_gated_scan_chunks", s);
+        k_gated_scan_chunks<T, SIG, LANES><<<dim3(wgs, (unsigned)(p.chunks - 1)), block, 0, s>>>(a);
+        const det_status st = launch_status();
+        if (st != DET_SUCCESS) return st;
+    }
+    KernelTimer kt("k_gated_scan", s);
+    k_gated_scan<T, SIG, LANES><<<dim3(wgs, (unsigned)p.parts), block, 0, s>>>(a);
+    return launch_status();
+}
+
 template <typename T, bool SIG>
 det_status scan_typed(const ScanArgs& a, const ScanPlan& p, hipStream_t s) {
     if (a.steps <= kSteps) {
@@ -517,47 +737,60 @@ det_status scan_typed(const ScanArgs& a, const ScanPlan& p, hipStream_t s) {
         k_gated_scan_steps<T, SIG><<<dim3((unsigned)cdiv(items, 256)), dim3(256), 0, s>>>(a);
         return launch_status();
     }
-    const unsigned wgs = (unsigned)(p.tiles * a.batch);
+    if constexpr (sizeof(T) == 2) {
+        if (a.d == 1) return scan_as<Lone<T>, SIG, 32>(a, p, s);
+    }
+    return p.lanes == 32 ? scan_as<T, SIG, 32>(a, p, s) : scan_as<T, SIG, 64>(a, p, s);
+}
+
+template <typename T, bool SIG, int LANES>
+det_status scan_back_as(const ScanBackArgs& a, const ScanPlan& p, hipStream_t s) {
+    const unsigned wgs = (unsigned)(cdiv(p.tiles * a.batch, 8) * 8);
+    const dim3 block(LANES * kBackSpans);
     if (p.parts > 1) {
-        KernelTimer kt("k_gated_scan_chunks", s);
-        k_gated_scan_chunks<T, SIG><<<dim3(wgs, (unsigned)(p.chunks - 1)), dim3(64 * kSpans), 0, s>>>(a);
+        KernelTimer kt("k_gated_scan_chunks_back", s);
+        k_gated_scan_chunks_back<T, SIG, LANES><<<dim3(wgs, (unsigned)(p.chunks - 1)), block, 0, s>>>(a);
         const det_status st = launch_status();
         if (st != DET_SUCCESS) return st;
     }
-    KernelTimer kt("k_gated_scan", s);
-    k_gated_scan<T, SIG><<<dim3(wgs, (unsigned)p.parts), dim3(64 * kSpans), 0, s>>>(a);
+    KernelTimer kt("k_gated_scan_backward", s);
+    k_gated_scan_backward<T, SIG, LANES><<<dim3(wgs, (unsigned)p.parts), block, 0, s>>>(a);
     return launch_status();
 }
 
 template <typename T, bool SIG>
 det_status scan_back_typed(const ScanBackArgs& a, const ScanPlan& p, hipStream_t s) {
-    const unsigned wgs = (unsigned)(p.tiles * a.batch);
-    if (p.parts > 1) {
-        KernelTimer kt("k_gated_scan_chunks_back", s);
-        k_gated_scan_chunks_back<T, SIG><<<dim3(wgs, (unsigned)(p.chunks - 1)), dim3(64 * kSpans), 0, s>>>(a);
-        const det_status st = launch_status();
-        if (st != DET_SUCCESS) return st;
+    if constexpr (sizeof(T) == 2) {
+        if (a.d == 1) return scan_back_as<Lone<T>, SIG, 32>(a, p, s);
     }
-    KernelTimer kt("k_gated_scan_backward", s);
-    k_gated_scan_backward<T, SIG><<<dim3(wgs, (unsigned)p.parts), dim3(64 * kSpans), 0, s>>>(a);
-    return launch_status();
+    return p.lanes == 32 ? scan_back_as<T, SIG, 32>(a, p, s) : scan_back_as<T, SIG, 64>(a, p, s);
+}
+
+}  // namespace
+
+namespace {
+
+size_t effect_bytes(const ScanPlan& p, int64_t batch, det_dtype dtype) {
+    const size_t ch = 4 / lm_size(dtype);      // channels of a word
+    return p.parts > 1 ? round_up((size_t)p.chunks * batch * p.tiles * p.lanes * ch * 8, 256) : 256;
 }
 
 }  // namespace
 
 size_t gated_scan_workspace(int64_t batch, int64_t steps, int64_t d, det_dtype dtype) {
-    const ScanPlan p = scan_plan(batch, steps, d, dtype);
-    return p.parts > 1 ? round_up((size_t)p.chunks * 2 * batch * d * 4, 256) : 256;
+    const ScanPlan p = scan_plan(batch, steps, d, dtype, kSpans);
+    return effect_bytes(p, batch, dtype);
 }
 
 size_t gated_scan_backward_workspace(int64_t batch, int64_t steps, int64_t d, det_dtype dtype) {
-    return gated_scan_workspace(batch, steps, d, dtype);
+    const ScanPlan p = scan_plan(batch, steps, d, dtype, kBackSpans);
+    return effect_bytes(p, batch, dtype);
 }
 
 det_status gated_scan_launch(const ScanCall& c, void* ws, hipStream_t s) {
-    const ScanPlan p = scan_plan(c.batch, c.steps, c.d, c.dtype);
-    const ScanArgs a{c.gate, c.x, c.state0, c.lengths, c.h, c.state, static_cast<float*>(ws),
-                     c.batch, c.steps, c.d, p.tiles, p.chunks, p.per};
+    const ScanPlan p = scan_plan(c.batch, c.steps, c.d, c.dtype, kSpans);
+    const ScanArgs a{c.gate, c.x, c.state0, c.lengths, c.h, c.state, static_cast<Effect*>(ws),
+                     c.batch, c.steps, c.d, p.tiles, p.chunks, p.per, p.runs};
     switch (c.dtype) {
         case DET_F32: return c.sigmoid ? scan_typed<float, true>(a, p, s) : scan_typed<float, false>(a, p, s);
         case DET_F16:
@@ -568,10 +801,10 @@ det_status gated_scan_launch(const ScanCall& c, void* ws, hipStream_t s) {
 }
 
 det_status gated_scan_backward_launch(const ScanBackCall& c, void* ws, hipStream_t s) {
-    const ScanPlan p = scan_plan(c.batch, c.steps, c.d, c.dtype);
+    const ScanPlan p = scan_plan(c.batch, c.steps, c.d, c.dtype, kBackSpans);
     const ScanBackArgs a{c.dh, c.gate, c.x, c.h, c.state0, c.dstate, c.lengths, c.dgate, c.dx,
-                         c.dstate0, static_cast<float*>(ws), c.batch, c.steps, c.d, p.tiles,
-                         p.chunks, p.per};
+                         c.dstate0, static_cast<Effect*>(ws), c.batch, c.steps, c.d, p.tiles,
+                         p.chunks, p.per, p.runs};
     switch (c.dtype) {
         case DET_F32:
             return c.sigmoid ? scan_back_typed<float, true>(a, p, s) : scan_back_typed<float, false>(a, p, s);

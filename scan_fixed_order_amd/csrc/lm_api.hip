@@ -478,7 +478,7 @@ det_status scan_sizes(int64_t batch, int64_t steps, int64_t d, det_dtype dtype, 
     if (flags & ~DET_GATE_SIGMOID) return DET_ERROR_INVALID_VALUE;
     if (batch < 0 || steps < 0 || d < 0) return DET_ERROR_INVALID_VALUE;
     if (steps > DET_MAX_N || (double)batch * d > (double)DET_MAX_N || batch > DET_MAX_N ||
-        d > DET_MAX_N || (double)batch * d * (double)steps * 4 > kMaxBytes)
+        d > DET_SCAN_MAX_CHANNELS || (double)batch * d * (double)steps * 4 > kMaxBytes)
         return DET_ERROR_TOO_LARGE;
     return DET_SUCCESS;
 }
