@@ -82,9 +82,41 @@ __global__ __launch_bounds__(256) void k_embedding(EmbedArgs a) {
 
 typedef unsigned long long u64;
 
-// Chunk of 1024 (token, position): a bitonic network, partners within a wave by lane moves, farther
-// ones through LDS.  Positions are part of the key, so equal tokens keep their order.  Behind the
-// last token the chunk holds tokens larger than any.
+// A step of a bitonic network over the chunk: partners STEP apart, runs of SIZE.
+template <int SIZE, int STEP>
+__device__ __forceinline__ void exchange(u64& key, u64* s_key) {
+    const int t = threadIdx.x;
+    u64 other;
+    if constexpr (STEP >= 64) {
+        __syncthreads();
+        s_key[t] = key;
+        __syncthreads();
+        other = s_key[t ^ STEP];
+    } else {
+        uint32_t lo = (uint32_t)key, hi = (uint32_t)(key >> 32);
+        if constexpr (STEP == 32) {
+            lo = (uint32_t)__builtin_amdgcn_ds_bpermute((t ^ 32) << 2, (int)lo);
+            hi = (uint32_t)__builtin_amdgcn_ds_bpermute((t ^ 32) << 2, (int)hi);
+        } else {
+            lo = xor_partner<STEP>(lo);
+            hi = xor_partner<STEP>(hi);
+        }
+        other = (u64)hi << 32 | lo;
+    }
+    const bool up = (t & SIZE) == 0, low = (t & STEP) == 0;
+    if ((up == low) == (other < key)) key = other;
+    if constexpr (STEP > 1) exchange<SIZE, STEP / 2>(key, s_key);
+}
+
+template <int SIZE>
+__device__ __forceinline__ void merge_runs(u64& key, u64* s_key) {
+    if constexpr (SIZE > 2) merge_runs<SIZE / 2>(key, s_key);
+    exchange<SIZE, SIZE / 2>(key, s_key);
+}
+
+// Chunk of 1024 (token, position), sorted: partners within a wave by lane moves, farther ones through
+// LDS.  Positions are part of the key, so equal tokens keep their order.  Behind the last token the
+// chunk holds tokens larger than any.
 __global__ __launch_bounds__(1024) void k_sort_chunks(const void* tokens, bool wide, int64_t n,
                                                       int64_t vocab, uint32_t* tok, uint32_t* pos) {
     __shared__ u64 s_key[kChunk];
@@ -92,44 +124,28 @@ __global__ __launch_bounds__(1024) void k_sort_chunks(const void* tokens, bool w
     const int64_t i = (int64_t)blockIdx.x * kChunk + t;
     const uint32_t id = i < n ? token_at(tokens, wide, i, vocab, (uint32_t)vocab) : 0xFFFFFFFFu;
     u64 key = (u64)id << 32 | (uint32_t)t;
-    for (int size = 2; size <= kChunk; size *= 2)
-        for (int step = size / 2; step > 0; step /= 2) {
-            u64 other;
-            if (step >= 64) {
-                __syncthreads();
-                s_key[t] = key;
-                __syncthreads();
-                other = s_key[t ^ step];
-            } else {
-                const int at = (t ^ step) << 2;
-                const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(at, (int)(uint32_t)key);
-                const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(at, (int)(uint32_t)(key >> 32));
-                other = (u64)hi << 32 | lo;
-            }
-            const bool up = (t & size) == 0, low = (t & step) == 0;
-            if ((up == low) == (other < key)) key = other;
-        }
+    merge_runs<kChunk>(key, s_key);
     tok[i] = (uint32_t)(key >> 32);
     pos[i] = (uint32_t)(i - t) + (uint32_t)key;
 }
 
 // Place of every token among all: its place in its chunk, and the tokens before it in the others:
-// up to its own number in earlier chunks, below it in later ones.
-__global__ __launch_bounds__(256) void k_rank_tokens(const uint32_t* tok, const uint32_t* pos,
-                                                     int64_t n, uint32_t* keys, uint32_t* src) {
+// up to its own number in earlier chunks, below it in later ones.  A wave takes 64 tokens and searches
+// eight chunks at a time in LDS (32768 tokens: XX us, with 256 tokens a workgroup 17).
+__global__ __launch_bounds__(64) void k_rank_tokens(const uint32_t* tok, const uint32_t* pos,
+                                                    int64_t n, uint32_t* keys, uint32_t* src) {
     __shared__ uint32_t s_tok[kSlabChunks * kChunk];
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;      // of the padded length
-    const int64_t chunks = (n + kChunk - 1) / kChunk, own = e / kChunk;
+    const int64_t e = (int64_t)blockIdx.x * 64 + threadIdx.x;      // of the padded length
+    const int chunks = (int)((n + kChunk - 1) / kChunk), own = (int)(e / kChunk);
     const uint32_t id = tok[e];
-    int64_t place = e % kChunk;
-    for (int64_t c0 = 0; c0 < chunks; c0 += kSlabChunks) {
+    uint32_t place = (uint32_t)(e % kChunk);
+    for (int c0 = 0; c0 < chunks; c0 += kSlabChunks) {
+        const int here = chunks - c0 < kSlabChunks ? chunks - c0 : kSlabChunks;
         __syncthreads();
-        for (int64_t k = threadIdx.x; k < kSlabChunks * kChunk / 4; k += 256) {
-            u32x4 v = u32x4{0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-            if (c0 * kChunk + 4 * k < chunks * kChunk)
-                v = *reinterpret_cast<const u32x4*>(tok + c0 * kChunk + 4 * k);
-            *reinterpret_cast<u32x4*>(s_tok + 4 * k) = v;
-        }
+#pragma unroll 8
+        for (int k = threadIdx.x; k < here * (int)kChunk / 4; k += 64)
+            *reinterpret_cast<u32x4*>(s_tok + 4 * k) =
+                *reinterpret_cast<const u32x4*>(tok + (int64_t)c0 * kChunk + 4 * k);
         __syncthreads();
         uint32_t at[kSlabChunks] = {};
 #pragma unroll
@@ -143,7 +159,7 @@ __global__ __launch_bounds__(256) void k_rank_tokens(const uint32_t* tok, const 
         for (int c = 0; c < kSlabChunks; ++c) {
             const uint32_t bound = id + (c0 + c < own ? 1u : 0u);
             if (s_tok[c * kChunk + at[c]] < bound) at[c] += 1;
-            if (c0 + c != own) place += at[c];
+            if (c < here && c0 + c != own) place += at[c];
         }
     }
     if (id != 0xFFFFFFFFu) {
@@ -221,26 +237,32 @@ __device__ __forceinline__ void add_rows(const EmbedBackArgs& a, int64_t begin, 
     }
 }
 
-// Blocks of tokens with more than 64 positions: a wave per range of 64 places and slab of columns.
-template <typename T>
-__global__ __launch_bounds__(256) void k_embedding_blocks(EmbedBackArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t range = item / a.slabs, c = (item % a.slabs * kSlab + lane) * kVec<T>;
-    const int64_t valid = a.off[a.vocab], p = range * kBlockRows + lane;
+// The blocks that begin in a range of 64 places, of tokens with more than 64 positions: bit l of the
+// result is set where one begins at place l; `first` and `end` are the places of its token.
+__device__ __forceinline__ uint64_t blocks_of(const EmbedBackArgs& a, int64_t range, uint32_t& first,
+                                              uint32_t& end) {
+    const int64_t p = range * kBlockRows + (threadIdx.x & 63);
     bool begins = false;
-    int64_t first = 0, end = 0;
-    if (p < valid) {
+    first = end = 0;
+    if (p < (int64_t)a.off[a.vocab]) {
         const uint32_t v = a.keys[p];
         first = a.off[v];
         end = a.off[v + 1];
-        begins = end - first > kBlockRows && (p - first) % kBlockRows == 0;
+        begins = end - first > kBlockRows && ((uint32_t)p - first) % kBlockRows == 0;
     }
-    for (uint64_t left = __ballot(begins); left; left &= left - 1) {
+    return __ballot(begins);
+}
+
+// Sums of the blocks of tokens with more than 64 positions: a wave per range and slab of columns.
+template <typename T>
+__device__ __forceinline__ void sum_blocks(const EmbedBackArgs& a, int64_t item) {
+    const int64_t range = item / a.slabs, c = (item % a.slabs * kSlab + (threadIdx.x & 63)) * kVec<T>;
+    uint32_t first, end;
+    for (uint64_t left = blocks_of(a, range, first, end); left; left &= left - 1) {
         const int at = __builtin_ctzll(left);
         const int64_t begin = range * kBlockRows + at;
-        const int64_t start = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)first, at);
-        const int64_t stop = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)end, at);
+        const int64_t start = (uint32_t)__builtin_amdgcn_readlane((int)first, at);
+        const int64_t stop = (uint32_t)__builtin_amdgcn_readlane((int)end, at);
         float acc[kVec<T>] = {};
         add_rows<T>(a, begin, begin + kBlockRows < stop ? begin + kBlockRows : stop, c, acc);
         if (c < a.d)
@@ -248,41 +270,111 @@ __global__ __launch_bounds__(256) void k_embedding_blocks(EmbedBackArgs a) {
     }
 }
 
-// A wave per kVocabRows rows of the table and slab of columns: zeros, a token's one block, or its
-// blocks joined.  Bound by HBM: dout is read once, the gradient written once.
-constexpr int64_t kVocabRows = 8;
+// A wave per kVocabRows rows of the table and slab of columns: zeros, or the sum of a token's one
+// block.  The rows' positions lie side by side, so the loads run ahead across them.
+constexpr int kVocabRows = 8;
 
 template <typename T>
-__global__ __launch_bounds__(256) void k_embedding_rows(EmbedBackArgs a) {
+__device__ __forceinline__ void sum_rows(const EmbedBackArgs& a, int64_t item) {
+    constexpr int kAhead = 8;      // rows of dout in flight
     const int lane = threadIdx.x & 63;
-    const int64_t items = (a.vocab + kVocabRows - 1) / kVocabRows * a.slabs;
-    for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < items;
-         item += (int64_t)gridDim.x * 4) {
-        const int64_t v0 = item / a.slabs * kVocabRows, c = (item % a.slabs * kSlab + lane) * kVec<T>;
-        const int64_t bound = v0 + lane < a.vocab ? v0 + lane : a.vocab;
-        const uint32_t off = a.off[lane <= kVocabRows ? bound : v0];
-        for (int r = 0; r < kVocabRows && v0 + r < a.vocab; ++r) {
-            const int64_t begin = (uint32_t)__builtin_amdgcn_readlane((int)off, r);
-            const int64_t end = (uint32_t)__builtin_amdgcn_readlane((int)off, r + 1);
-            float acc[kVec<T>] = {};
-            if (end - begin > kBlockRows) {
-                double sum[kVec<T>] = {};
-                if (c < a.d) {
-                    for (int64_t p = begin; p < end; p += kBlockRows) {
-                        const float* part = a.part + block_slot(p, p == begin) * a.d + c;
+    const int64_t v0 = item / a.slabs * kVocabRows, c = (item % a.slabs * kSlab + lane) * kVec<T>;
+    const int64_t bound = v0 + lane < a.vocab ? v0 + lane : a.vocab;
+    const int off = (int)a.off[lane <= kVocabRows ? bound : v0];
+    const auto off_of = [&](int r) { return (uint32_t)__builtin_amdgcn_readlane(off, r); };
+    const int rows = a.vocab - v0 < kVocabRows ? (int)(a.vocab - v0) : kVocabRows;
+    T* out = static_cast<T*>(a.dtable) + v0 * a.d + c;
+    const auto put = [&](int r, float (&acc)[kVec<T>]) {
 #pragma unroll
-                        for (int i = 0; i < kVec<T>; ++i)
-                            if (c + i < a.d) sum[i] += (double)part[i];
-                    }
+        for (int i = 0; i < kVec<T>; ++i) acc[i] *= a.scale;
+        if (c < a.d) write_vec(out + r * a.d, a.d - c, acc);
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) acc[i] = 0.0f;
+    };
+    float acc[kVec<T>] = {};
+    int r = 0;
+    while (r < rows) {
+        // the rows up to the next token of several blocks, whose row is written once they are there
+        int stop = r;
+        while (stop < rows && off_of(stop + 1) - off_of(stop) <= kBlockRows) ++stop;
+        const uint32_t begin = off_of(r), end = off_of(stop);
+        for (uint32_t p0 = begin; p0 < end; p0 += 64) {
+            const uint32_t mine = a.src[p0 + lane < end ? p0 + lane : end - 1];
+            const int count = end - p0 < 64 ? (int)(end - p0) : 64;
+            for (int k = 0; k < count; k += kAhead) {
+                u32x4 raw[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int at = k + u < count ? k + u : count - 1;
+                    const int64_t row = (uint32_t)__builtin_amdgcn_readlane((int)mine, at);
+                    raw[u] = u32x4{0, 0, 0, 0};
+                    if (c < a.d) raw[u] = load_row(static_cast<const T*>(a.dout) + row * a.stride, c, a.d);
                 }
 #pragma unroll
-                for (int i = 0; i < kVec<T>; ++i) acc[i] = (float)sum[i];
-            } else if (end > begin) {
-                add_rows<T>(a, begin, end, c, acc);
-            }
+                for (int u = 0; u < kAhead; ++u) {
+                    if (k + u < count) {
+                        while (p0 + k + u >= off_of(r + 1)) put(r++, acc);
+                        float v[kVec<T>];
+                        unpack<T>(settle<T>(raw[u], c, a.d), v);
 #pragma unroll
-            for (int i = 0; i < kVec<T>; ++i) acc[i] *= a.scale;
-            if (c < a.d) write_vec(static_cast<T*>(a.dtable) + (v0 + r) * a.d + c, a.d - c, acc);
+                        for (int i = 0; i < kVec<T>; ++i) acc[i] += v[i];
+                    }
+                }
+            }
+        }
+        while (r < stop) put(r++, acc);
+        ++r;      // the token of several blocks
+    }
+}
+
+// Both in one launch, the blocks (the longer work) first.  Bound by HBM: dout is read once, the gradient
+// written once.
+template <typename T>
+__global__ __launch_bounds__(256) void k_embedding_sums(EmbedBackArgs a, int64_t blocks) {
+    const int64_t items = blocks + (a.vocab + kVocabRows - 1) / kVocabRows * a.slabs;
+    for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < items;
+         item += (int64_t)gridDim.x * 4) {
+        if (item < blocks)
+            sum_blocks<T>(a, item);
+        else
+            sum_rows<T>(a, item - blocks);
+    }
+}
+
+// The blocks of every token that has several, joined: a wave per range, that its first block begins in.
+template <typename T>
+__global__ __launch_bounds__(256) void k_embedding_join(EmbedBackArgs a, int64_t blocks) {
+    for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < blocks;
+         item += (int64_t)gridDim.x * 4) {
+        const int64_t range = item / a.slabs, c = (item % a.slabs * kSlab + (threadIdx.x & 63)) * kVec<T>;
+        uint32_t first, end;
+        for (uint64_t left = blocks_of(a, range, first, end); left; left &= left - 1) {
+            const int at = __builtin_ctzll(left);
+            const int64_t begin = (uint32_t)__builtin_amdgcn_readlane((int)first, at);
+            const int64_t stop = (uint32_t)__builtin_amdgcn_readlane((int)end, at);
+            if (begin != range * kBlockRows + at || c >= a.d) continue;
+            const uint32_t v = a.keys[begin];
+            double sum[kVec<T>] = {};
+#pragma unroll 8
+            for (int64_t p = begin; p < stop; p += kBlockRows) {
+                const float* part = a.part + block_slot(p, p == begin) * a.d + c;
+                if (c + kVec<T> <= a.d) {
+#pragma unroll
+                    for (int i = 0; i < kVec<T>; i += 4) {
+                        const f32x4 q = *reinterpret_cast<const f32x4_a4*>(part + i);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[i + e] += (double)q[e];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kVec<T>; ++i)
+                        if (c + i < a.d) sum[i] += (double)part[i];
+                }
+            }
+            float acc[kVec<T>];
+#pragma unroll
+            for (int i = 0; i < kVec<T>; ++i) acc[i] = (float)sum[i] * a.scale;
+            write_vec(static_cast<T*>(a.dtable) + (int64_t)v * a.d + c, a.d - c, acc);
         }
     }
 }
@@ -310,15 +402,20 @@ void embed_typed(const EmbedArgs& a, hipStream_t s) {
 template <typename T>
 det_status embed_back_typed(EmbedBackArgs a, hipStream_t s) {
     a.slabs = cdiv(a.d, kSlab * kVec<T>);
-    const int64_t ranges = cdiv(a.n, kBlockRows);
-    if (ranges > 1) {      // else no token has more than 64 positions
-        KernelTimer kt("k_embedding_blocks", s);
-        k_embedding_blocks<T><<<dim3((unsigned)cdiv(ranges * a.slabs, 4)), dim3(256), 0, s>>>(a);
+    // up to 64 positions no token has several blocks
+    const int64_t blocks = a.n > kBlockRows ? cdiv(a.n, kBlockRows) * a.slabs : 0;
+    const auto grid = [](int64_t waves) {
+        const int64_t g = cdiv(waves, 4);
+        return dim3((unsigned)(g < kGridMax ? g : kGridMax));
+    };
+    {
+        KernelTimer kt("k_embedding_sums", s);
+        k_embedding_sums<T><<<grid(blocks + cdiv(a.vocab, kVocabRows) * a.slabs), dim3(256), 0, s>>>(a, blocks);
     }
-    int64_t g = cdiv(cdiv(a.vocab, kVocabRows) * a.slabs, 4);
-    if (g > kGridMax) g = kGridMax;
-    KernelTimer kt("k_embedding_rows", s);
-    k_embedding_rows<T><<<dim3((unsigned)g), dim3(256), 0, s>>>(a);
+    if (blocks > 0) {
+        KernelTimer kt("k_embedding_join", s);
+        k_embedding_join<T><<<grid(blocks), dim3(256), 0, s>>>(a, blocks);
+    }
     return launch_status();
 }
 
@@ -387,7 +484,7 @@ det_status embedding_backward_launch(const EmbedBackCall& c, void* ws, hipStream
                                                                              c.vocab, tok, pos);
             }
             KernelTimer kt("k_rank_tokens", s);
-            k_rank_tokens<<<dim3((unsigned)(chunks * kChunk / 256)), dim3(256), 0, s>>>(
+            k_rank_tokens<<<dim3((unsigned)(chunks * kChunk / 64)), dim3(64), 0, s>>>(
                 tok, pos, c.n, keys, src);
         }
         int64_t g = cdiv(c.vocab + 1, 256);
