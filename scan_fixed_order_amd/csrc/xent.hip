@@ -25,7 +25,7 @@ namespace det {
 namespace {
 
 constexpr int kDepth = 64;                    // elements of k a step: 128 bytes of a row
-constexpr int64_t kTileV = 256;               // vocabulary entries that a tile's statistics cover
+constexpr int64_t kPieceUnit = 256;           // a piece's entries are a multiple of every tile's
 constexpr int64_t kPieceCells = 1 << 26;      // elements of D that a piece holds, about
 constexpr int64_t kPieceMin = 4096;
 constexpr int64_t kPieceMax = 65536;
@@ -45,7 +45,7 @@ struct Operand {
 
 struct GemmArgs {
     Operand A, B;
-    int64_t k;            // elements of a row that count; a multiple of 8
+    int64_t k;            // elements of a row that count; a multiple of 8 unless they are staged
     int64_t plane;        // f32: bytes from one part of a row to the next
     int64_t ni, nj;       // tiles along i and j
     int64_t per_z;        // steps of k that a workgroup along z takes
@@ -115,17 +115,22 @@ enum Ending { kStats, kLogits, kDx, kDw };
 
 // Wave grid WI x WJ, a wave has MI x MJ tiles of 32 x 32.  A step's rows go from memory straight to
 // LDS, two steps in turn: 8 rows of 128 bytes a load, whose 16-byte chunks lie in the order chunk
-// ^ (row % 8), so that the 8 rows that a read of the operands takes at a time lie in different
-// banks.  What lies past an operand's rows or k reads as zero (the buffer's bounds).
-template <typename T, int WI, int WJ, int MI, int MJ, int END>
+// ^ (row / 2 % 8), so that the 16 rows that a read of the operands takes at a time lie in different
+// banks.  What lies past an operand's rows or k reads as zero (the buffer's bounds).  STAGED: rows that
+// do not lie on 16 bytes go through registers instead.
+template <typename T, int WI, int WJ, int MI, int MJ, bool STAGED, int END>
 __device__ __forceinline__ void xent_product(const GemmArgs& a) {
     typedef typename Half<T>::type H;
     constexpr int kParts = Half<T>::kParts;
     constexpr int BI = WI * MI * 32, BJ = WJ * MJ * 32, NW = WI * WJ;
-    constexpr int LA = BI / 8 / NW, LB = BJ / 8 / NW;      // loads of a wave a step
-    static_assert(BI % (8 * NW) == 0 && BJ % (8 * NW) == 0, "rows of a step per wave");
-    __shared__ __attribute__((aligned(16))) char s_0[(BI + BJ) * 128];
-    __shared__ __attribute__((aligned(16))) char s_1[(BI + BJ) * 128];
+    constexpr int kRow = kDepth * 2, kChunks = kDepth / 8, kRows = 64 / kChunks;      // rows of a load
+    constexpr int LA = BI / kRows / NW, LB = BJ / kRows / NW;      // loads of a wave a step
+    static_assert(BI % (kRows * NW) == 0 && BJ % (kRows * NW) == 0, "rows of a step per wave");
+    constexpr int kStage = (BI + BJ) * kRow;
+    __shared__ __attribute__((aligned(16))) char s_0[kStage];
+    __shared__ __attribute__((aligned(16))) char s_1[kStage];
+    // the places of a row's chunks are turned by this much
+    const auto turn_of = [](int row) { return row >> 1 & 7; };
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wi = wave / WJ, wj = wave % WJ;
 
@@ -147,10 +152,13 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
                                                       records(a.A, i0, BI), 0x00020000);
     const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(a.B.p + j0 * a.B.ld), 0,
                                                       records(a.B, j0, BJ), 0x00020000);
-    const int row8 = lane >> 3, chunk = (lane & 7) ^ row8;
+    // A load takes kRows rows; where the turn goes by more rows than that, every other load's differs.
+    const int in_load = lane / kChunks;
+    const int chunk[2] = {(lane & (kChunks - 1)) ^ turn_of(in_load),
+                          (lane & (kChunks - 1)) ^ turn_of(kRows + in_load)};
     const uint32_t lda = (uint32_t)a.A.ld, ldb = (uint32_t)a.B.ld;
-    const uint32_t oa = (uint32_t)(wave * LA * 8 + row8) * lda + chunk * 16;
-    const uint32_t ob = (uint32_t)(wave * LB * 8 + row8) * ldb + chunk * 16;
+    const uint32_t oa = (uint32_t)(wave * LA * kRows + in_load) * lda;
+    const uint32_t ob = (uint32_t)(wave * LB * kRows + in_load) * ldb;
     const int steps_k = (int)((a.k + kDepth - 1) / kDepth);      // of one product of parts
     const int first = (int)(blockIdx.y * a.per_z);
     const int behind = (int)(first + a.per_z < (int64_t)steps_k * (kParts == 1 ? 1 : kPairs)
@@ -158,68 +166,131 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
                                  : (int64_t)steps_k * (kParts == 1 ? 1 : kPairs));
     const auto issue = [&](char* s, int step) {
         uint32_t ka, kb;
-        bool inside;
+        int left;      // elements of k from the step's first on
         if constexpr (kParts == 1) {
-            ka = kb = (uint32_t)step * 128;
-            inside = step < behind && step * kDepth + chunk * 8 < a.k;
+            ka = kb = (uint32_t)step * kRow;
+            left = (int)a.k - step * kDepth;
         } else {
             const int pair = step / steps_k, at = step % steps_k;
             // parts (0,0) (0,1) (1,0) (1,1) (0,2) (2,0)
             const int ia = pair == 2 || pair == 3 ? 1 : pair == 5 ? 2 : 0;
             const int ib = pair == 1 || pair == 3 ? 1 : pair == 4 ? 2 : 0;
-            ka = (uint32_t)(ia * a.plane) + at * 128;
-            kb = (uint32_t)(ib * a.plane) + at * 128;
-            inside = step < behind && at * kDepth + chunk * 8 < a.k;
+            ka = (uint32_t)(ia * a.plane) + at * kRow;
+            kb = (uint32_t)(ib * a.plane) + at * kRow;
+            left = (int)a.k - at * kDepth;
         }
         constexpr uint32_t kOut = 0x80000000u;
+        if (step >= behind) left = 0;
 #pragma unroll
-        for (int u = 0; u < LA; ++u)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(s + (wave * LA + u) * 1024), 16,
-                                                     inside ? oa + u * 8 * lda + ka : kOut, 0, 0, 0);
+        for (int u = 0; u < LA; ++u) {
+            const int c = chunk[(wave * LA + u) & 1];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                ra, (lds_ptr)(s + (wave * LA + u) * 1024), 16,
+                c * 8 < left ? oa + u * kRows * lda + ka + c * 16 : kOut, 0, 0, 0);
+        }
 #pragma unroll
-        for (int u = 0; u < LB; ++u)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(s + BI * 128 + (wave * LB + u) * 1024),
-                                                     16, inside ? ob + u * 8 * ldb + kb : kOut, 0, 0, 0);
+        for (int u = 0; u < LB; ++u) {
+            const int c = chunk[(wave * LB + u) & 1];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rb, (lds_ptr)(s + BI * kRow + (wave * LB + u) * 1024), 16,
+                c * 8 < left ? ob + u * kRows * ldb + kb + c * 16 : kOut, 0, 0, 0);
+        }
     };
     f32x16 acc[MI][MJ] = {};
     const auto products = [&](const char* s) {
-        const char* pa = s + (wi * MI * 32 + (lane & 31)) * 128;
-        const char* pb = s + BI * 128 + (wj * MJ * 32 + (lane & 31)) * 128;
+        const char* pa = s + (wi * MI * 32 + (lane & 31)) * kRow;
+        const char* pb = s + (BI + wj * MJ * 32 + (lane & 31)) * kRow;
 #pragma unroll
         for (int kk = 0; kk < kDepth / 16; ++kk) {
-            const int slot = ((kk * 2 + (lane >> 5)) ^ (lane & 7)) * 16;
+            const int slot = ((kk * 2 + (lane >> 5)) ^ turn_of(lane)) * 16;
             u32x4 av[MI], bv[MJ];
 #pragma unroll
-            for (int i = 0; i < MI; ++i) av[i] = *reinterpret_cast<const u32x4*>(pa + i * 4096 + slot);
+            for (int i = 0; i < MI; ++i) av[i] = *reinterpret_cast<const u32x4*>(pa + i * 32 * kRow + slot);
 #pragma unroll
-            for (int j = 0; j < MJ; ++j) bv[j] = *reinterpret_cast<const u32x4*>(pb + j * 4096 + slot);
+            for (int j = 0; j < MJ; ++j) bv[j] = *reinterpret_cast<const u32x4*>(pb + j * 32 * kRow + slot);
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < MJ; ++j) acc[i][j] = mma(av[i], bv[j], acc[i][j], H{});
         }
     };
-    // a step's loads are done (every wave waits for its own), and nobody reads the other buffer
-    const auto turn = [&] {
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    issue(s_0, first);
+    if constexpr (STAGED) {
+        // Rows that lie at any element: through registers, a step ahead, rows past the last one as that.
+        const int rows_a = (int)(a.A.rows - i0 < BI ? a.A.rows - i0 : BI);
+        const int rows_b = (int)(a.B.rows - j0 < BJ ? a.B.rows - j0 : BJ);
+        const char* at_a[LA];
+        const char* at_b[LB];
+#pragma unroll
+        for (int u = 0; u < LA; ++u) {
+            const int r = (wave * LA + u) * kRows + in_load;
+            at_a[u] = a.A.p + i0 * a.A.ld + (r < rows_a ? r : rows_a - 1) * a.A.ld;
+        }
+#pragma unroll
+        for (int u = 0; u < LB; ++u) {
+            const int r = (wave * LB + u) * kRows + in_load;
+            at_b[u] = a.B.p + j0 * a.B.ld + (r < rows_b ? r : rows_b - 1) * a.B.ld;
+        }
+        u32x4 ga[LA], gb[LB];
+        const auto column = [&](int step, int load) {
+            return (int64_t)step * kDepth + chunk[load & 1] * 8;
+        };
+        const auto fetch = [&](int step) {
+#pragma unroll
+            for (int u = 0; u < LA; ++u)
+                ga[u] = load_row(reinterpret_cast<const H*>(at_a[u]), column(step, wave * LA + u), a.k);
+#pragma unroll
+            for (int u = 0; u < LB; ++u)
+                gb[u] = load_row(reinterpret_cast<const H*>(at_b[u]), column(step, wave * LB + u), a.k);
+        };
+        const auto put = [&](char* s, int step) {
+#pragma unroll
+            for (int u = 0; u < LA; ++u)
+                *reinterpret_cast<u32x4*>(s + (wave * LA + u) * 1024 + lane * 16) =
+                    settle<H>(ga[u], column(step, wave * LA + u), a.k);
+#pragma unroll
+            for (int u = 0; u < LB; ++u)
+                *reinterpret_cast<u32x4*>(s + BI * kRow + (wave * LB + u) * 1024 + lane * 16) =
+                    settle<H>(gb[u], column(step, wave * LB + u), a.k);
+        };
+        fetch(first);
+        put(s_0, first);
+        __syncthreads();
+        // past the last step: zeros (settle)
 #pragma unroll 1
-    for (int step = first; step < behind; step += 2) {
+        for (int step = first; step < behind; step += 2) {
+            fetch(step + 1);
+            products(s_0);
+            put(s_1, step + 1);
+            __syncthreads();
+            fetch(step + 2);
+            products(s_1);
+            put(s_0, step + 2);
+            __syncthreads();
+        }
+    } else {
+        // The step's loads are done (every wave waits for its own), and nobody reads the other buffer.
+        const auto turn = [&] {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        issue(s_0, first);
+        // past the last step: zeros
+#pragma unroll 1
+        for (int step = first; step < behind; step += 2) {
+            turn();
+            issue(s_1, step + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            products(s_0);
+            turn();
+            issue(s_0, step + 2);
+            __builtin_amdgcn_sched_barrier(0);
+            products(s_1);
+        }
         turn();
-        issue(s_1, step + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        products(s_0);
-        turn();
-        issue(s_0, step + 2);
-        __builtin_amdgcn_sched_barrier(0);
-        products(s_1);      // past the last step: zeros
     }
-    turn();
 
     // a lane's values: column wj.. + lane % 32, rows wi.. + 8 (r / 4) + 4 (lane / 32) + r % 4 of the tile
     const int row_base = wi * MI * 32 + 4 * (lane >> 5), col_base = wj * MJ * 32 + (lane & 31);
@@ -414,38 +485,28 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
 }
 
 // (The kernel's body is a device function: it uses types that the host's compiler pass lacks.)
-template <typename T, int WI, int WJ, int MI, int MJ, int END>
+template <typename T, int WI, int WJ, int MI, int MJ, bool STAGED, int END>
 __global__ __launch_bounds__(WI * WJ * 64) void k_xent_product(GemmArgs a) {
-    xent_product<T, WI, WJ, MI, MJ, END>(a);
+    xent_product<T, WI, WJ, MI, MJ, STAGED, END>(a);
 }
 
 // ---------------------------------------------------------------- operands laid out
 
-// rows of d elements -> rows of `wide` (d rounded up to a step), zeros behind; f32 in three parts
-template <typename T>
-__global__ __launch_bounds__(256) void k_xent_pack(const T* src, int64_t stride, int64_t rows,
-                                                   int64_t d, int64_t wide, uint16_t* dst) {
-    constexpr int kParts = Half<T>::kParts;
-    const int64_t per = wide / 8, total = rows * per;      // 8 elements a lane
+// f32 rows of d elements -> rows of three parts of `wide` elements (d rounded up to a step), zeros behind
+__global__ __launch_bounds__(256) void k_xent_split(const float* src, int64_t stride, int64_t rows,
+                                                    int64_t d, int64_t wide, uint16_t* dst) {
+    const int64_t per = wide / 4, total = rows * per;      // a vector a lane
     for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < total; n += (int64_t)gridDim.x * 256) {
-        const int64_t row = n / per, c = n % per * 8;
-        uint16_t o[kParts][8];
+        const int64_t row = n / per, c = n % per * 4;
+        float v[4];
+        unpack<float>(settle<float>(load_row(src + row * stride, c, d), c, d), v);
+        uint16_t p[4][3];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const T v = c + i < d ? src[row * stride + c + i] : (T)0.0f;
-            if constexpr (kParts == 1) {
-                o[0][i] = __builtin_bit_cast(uint16_t, v);
-            } else {
-                uint16_t p[3];
-                parts_of(v, p);
+        for (int i = 0; i < 4; ++i) parts_of(v[i], p[i]);
 #pragma unroll
-                for (int k = 0; k < 3; ++k) o[k][i] = p[k];
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kParts; ++k)
-            *reinterpret_cast<u32x4*>(dst + (row * kParts + k) * wide + c) =
-                __builtin_bit_cast(u32x4, o[k]);
+        for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<u32x2*>(dst + (row * 3 + k) * wide + c) =
+                u32x2{p[0][k] | (uint32_t)p[1][k] << 16, p[2][k] | (uint32_t)p[3][k] << 16};
     }
 }
 
@@ -458,19 +519,34 @@ __global__ __launch_bounds__(256) void k_xent_transpose(const T* src, int64_t st
     constexpr int kParts = Half<T>::kParts, kSide = 64;
     __shared__ T s[kSide][kSide + 2];
     const int64_t r0 = (int64_t)blockIdx.x * kSide, c0 = (int64_t)blockIdx.y * kSide;
-    for (int n = threadIdx.x; n < kSide * kSide; n += 256) {
-        const int64_t r = r0 + n / kSide, c = c0 + n % kSide;
-        T v = (T)0.0f;
-        if (r < rows && c < d) {
-            const int64_t t = targets ? targets[r] : 0;
-            if (t >= 0 && t < vocab) v = src[r * stride + c];
+    constexpr int kPer = kSide / kVec<T>;      // vectors of a row
+    u32x4 raw[kSide * kPer / 256];
+#pragma unroll
+    for (int u = 0; u < kSide * kPer / 256; ++u) {
+        const int n = threadIdx.x + u * 256;
+        const int64_t r = r0 + n / kPer < rows ? r0 + n / kPer : rows - 1;
+        raw[u] = load_row(src + r * stride, c0 + n % kPer * kVec<T>, d);
+    }
+#pragma unroll
+    for (int u = 0; u < kSide * kPer / 256; ++u) {
+        const int n = threadIdx.x + u * 256, c = n % kPer * kVec<T>;
+        const int64_t r = r0 + n / kPer;
+        bool kept = r < rows;
+        if (kept && targets) kept = targets[r] >= 0 && targets[r] < vocab;
+        const u32x4 w = settle<T>(raw[u], c0 + c, d);
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) {
+            if constexpr (sizeof(T) == 4)
+                s[c + i][n / kPer] = kept ? __uint_as_float(w[i]) : 0.0f;
+            else
+                s[c + i][n / kPer] =
+                    __builtin_bit_cast(T, (uint16_t)(kept ? w[i / 2] >> (16 * (i & 1)) : 0));
         }
-        s[n % kSide][n / kSide] = v;
     }
     __syncthreads();
     for (int n = threadIdx.x; n < kSide * kSide / 8; n += 256) {
         const int c = n / (kSide / 8), r = n % (kSide / 8) * 8;
-        if (c0 + c >= d) continue;
+        if (c0 + c >= d || r0 + r >= wide) continue;
         uint16_t o[kParts][8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -571,62 +647,80 @@ unsigned lanes_grid(int64_t items) {
     return (unsigned)(g < 1 ? 1 : g < 65536 ? g : 65536);
 }
 
-template <typename T, int WI, int WJ, int MI, int MJ, int END>
+template <typename T, int WI, int WJ, int MI, int MJ, bool STAGED, int END>
 void product_as(GemmArgs a, int parts, hipStream_t s) {
     constexpr int64_t BI = WI * MI * 32, BJ = WJ * MJ * 32;
     a.ni = cdiv(a.A.rows, BI);
     a.nj = cdiv(a.B.rows, BJ);
     const int64_t steps = cdiv(a.k, kDepth) * (Half<T>::kParts == 1 ? 1 : kPairs);
     a.per_z = cdiv(steps, parts);
-    k_xent_product<T, WI, WJ, MI, MJ, END>
+    k_xent_product<T, WI, WJ, MI, MJ, STAGED, END>
         <<<dim3((unsigned)(cdiv(a.ni * a.nj, 8) * 8), (unsigned)parts), dim3(WI * WJ * 64), 0, s>>>(a);
 }
 
-// Tiles of 256 x 256 where they fill the compute units, else 256 x 64 (i is the wide side).
+// Columns (rows of x) of a tile by their number: few need few, and many the width that leaves least of
+// the last tile unused, the widest of those.
+int tile_columns(int64_t rows) {
+    if (rows <= 32) return 32;
+    if (rows <= 128) return 128;
+    return up(rows, 192) < up(rows, 256) ? 192 : 256;
+}
+
+// Rows (vocabulary entries) of such a tile.
+int64_t tile_rows(int columns) { return columns == 32 ? 64 : 256; }
+
+template <typename T, bool STAGED, int END>
+void product_of(const GemmArgs& a, int columns, int parts, hipStream_t s) {
+    if (columns == 256)
+        product_as<T, 2, 4, 4, 2, STAGED, END>(a, parts, s);
+    else if (columns == 192)
+        product_as<T, 4, 2, 2, 3, STAGED, END>(a, parts, s);
+    else if (columns == 128)
+        product_as<T, 4, 2, 2, 2, STAGED, END>(a, parts, s);
+    else
+        product_as<T, 2, 1, 1, 1, STAGED, END>(a, parts, s);
+}
+
 template <typename T, int END>
-void product(const GemmArgs& a, int parts, hipStream_t s) {
+void product(const GemmArgs& a, int parts, bool lies, hipStream_t s) {
     static const char* const names[] = {"k_xent_stats", "k_xent_logits", "k_xent_dx", "k_xent_dweight"};
     KernelTimer kt(names[END], s);
-    if (a.B.rows > 64)
-        product_as<T, 2, 4, 4, 2, END>(a, parts, s);
-    else
-        product_as<T, 4, 1, 2, 2, END>(a, parts, s);
+    if constexpr (END == kDw) {      // columns are vocabulary entries, of which there are many
+        product_as<T, 2, 4, 4, 2, false, END>(a, parts, s);
+    } else {
+        const int columns = tile_columns(a.B.rows);
+        if constexpr (sizeof(T) == 2 && (END == kStats || END == kLogits)) {
+            if (!lies) return product_of<T, true, END>(a, columns, parts, s);
+        }
+        product_of<T, false, END>(a, columns, parts, s);
+    }
 }
 
 struct XentPlan {
     int64_t piece;
-    int64_t wide_d, wide_v, wide_r;      // d, piece and rows rounded up to a step
+    int64_t wide_d, wide_v, wide_r;      // d, piece and rows rounded up: zeros behind them
     int64_t parts, dx_ld, tiles;
 };
 
 // Vocabulary entries of a piece: D of a piece takes about kPieceCells elements, twice.
 XentPlan xent_plan(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype) {
     XentPlan p;
-    int64_t piece = kPieceCells / (rows > 0 ? rows : 1) / kTileV * kTileV;
+    int64_t piece = kPieceCells / (rows > 0 ? rows : 1) / kPieceUnit * kPieceUnit;
     piece = piece < kPieceMin ? kPieceMin : piece > kPieceMax ? kPieceMax : piece;
     p.piece = piece < vocab ? piece : vocab;
     p.wide_d = up(d, kDepth);
     p.wide_v = up(p.piece, kDepth);
-    p.wide_r = up(rows, kDepth);
+    p.wide_r = up(rows, 32);      // what the narrowest tile writes of D's columns
     p.dx_ld = up(d, 4);
-    p.tiles = cdiv(vocab, kTileV);
+    p.tiles = cdiv(vocab, tile_rows(tile_columns(rows)));
     // workgroups that share dx's sum over a piece where its tiles are few
-    const int64_t tiles = cdiv(d, 256) * cdiv(rows, rows > 64 ? 256 : 64);
+    const int columns = tile_columns(rows);
+    const int64_t tiles = cdiv(d, tile_rows(columns)) * cdiv(rows, columns);
     p.parts = tiles >= 128 ? 1 : cdiv(256, tiles);
     const int64_t steps = p.wide_v / kDepth * (dtype == DET_F32 ? kPairs : 1);
     if (p.parts > cdiv(steps, 8)) p.parts = cdiv(steps, 8);
     return p;
 }
-
-// Entries whose rows the forward pass lays out at a time: as many as the backward pass where every
-// call lays them out, few where only an address off 16 bytes asks for it (the workspace has to hold
-// them).  Its sums go by tiles, so this moves no bit.
-int64_t forward_piece(const XentPlan& p, int64_t vocab, int64_t d, det_dtype dtype) {
-    const int64_t n = d % 8 || dtype == DET_F32 ? p.piece : kPieceMin;
-    return n < vocab ? n : vocab;
-}
-
-int64_t parts_of_type(det_dtype dtype) { return dtype == DET_F32 ? 3 : 1; }
 
 struct XentLayout {
     size_t x, w, stats, hit, xt, wt, d, dt, sums, unit, total;
@@ -634,7 +728,7 @@ struct XentLayout {
 
 XentLayout xent_layout(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype, bool back) {
     const XentPlan p = xent_plan(rows, vocab, d, dtype);
-    const int64_t n = parts_of_type(dtype) * 2;      // bytes of an element laid out
+    const int64_t n = dtype == DET_F32 ? 6 : 2;      // bytes of an element laid out
     XentLayout L = {};
     size_t o = 0;
     const auto take = [&](size_t bytes) {
@@ -642,8 +736,10 @@ XentLayout xent_layout(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype, 
         o += round_up(bytes > 0 ? bytes : 1, 256);
         return at;
     };
-    L.x = take((size_t)rows * p.wide_d * n);
-    L.w = take((size_t)(back ? p.piece : forward_piece(p, vocab, d, dtype)) * p.wide_d * n);
+    if (dtype == DET_F32) {      // the others are read as they lie
+        L.x = take((size_t)rows * p.wide_d * n);
+        L.w = take((size_t)p.piece * p.wide_d * n);
+    }
     if (!back) {
         L.stats = take((size_t)rows * p.tiles * 8);
         L.hit = take((size_t)rows * 4);
@@ -659,51 +755,51 @@ XentLayout xent_layout(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype, 
     return L;
 }
 
-// whether the product can read the rows as they lie (a tile's 256 rows within 2^30 bytes)
-template <typename T>
-bool as_they_lie(const void* p, int64_t stride, int64_t d) {
-    return sizeof(T) == 2 && d % 8 == 0 && stride % 8 == 0 && stride <= (1 << 21) &&
-           reinterpret_cast<uintptr_t>(p) % 16 == 0;
+// whether a 16-bit operand's rows can go straight to LDS (a tile's 256 rows within 2^30 bytes)
+bool lies_on_16(const void* p, int64_t stride, int64_t d) {
+    return d % 8 == 0 && stride % 8 == 0 && stride <= (1 << 21) && reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
+// 16-bit rows as they lie; f32 rows in parts at `at`
 template <typename T>
-Operand laid_out(const T* p, int64_t stride, int64_t rows, int64_t d, bool lies, char* at,
-                 int64_t wide, hipStream_t s) {
-    if (lies) return Operand{reinterpret_cast<const char*>(p), rows, stride * (int64_t)sizeof(T)};
-    KernelTimer kt("k_xent_pack", s);
-    k_xent_pack<T><<<dim3(lanes_grid(rows * (wide / 8))), dim3(256), 0, s>>>(
-        p, stride, rows, d, wide, reinterpret_cast<uint16_t*>(at));
-    return Operand{at, rows, wide * 2 * Half<T>::kParts};
+Operand operand_of(const T* p, int64_t stride, int64_t rows, int64_t d, char* at, int64_t wide,
+                   hipStream_t s) {
+    if constexpr (sizeof(T) == 2) {
+        return Operand{reinterpret_cast<const char*>(p), rows, stride * 2};
+    } else {
+        KernelTimer kt("k_xent_split", s);
+        k_xent_split<<<dim3(lanes_grid(rows * (wide / 4))), dim3(256), 0, s>>>(
+            p, stride, rows, d, wide, reinterpret_cast<uint16_t*>(at));
+        return Operand{at, rows, wide * 6};
+    }
 }
 
 template <typename T>
 det_status xent_typed(const XentCall& c, char* ws, hipStream_t s) {
     const T* x = static_cast<const T*>(c.x);
     const T* w = static_cast<const T*>(c.weight);
-    const bool x_lies = as_they_lie<T>(x, c.x_stride, c.d), w_lies = as_they_lie<T>(w, c.w_stride, c.d);
+    const bool lies = lies_on_16(x, c.x_stride, c.d) && lies_on_16(w, c.w_stride, c.d);
     const XentPlan p = xent_plan(c.rows, c.vocab, c.d, c.dtype);
     const XentLayout L = xent_layout(c.rows, c.vocab, c.d, c.dtype, false);
     GemmArgs a = {};
-    a.B = laid_out(x, c.x_stride, c.rows, c.d, x_lies, ws + L.x, p.wide_d, s);
-    a.k = x_lies && w_lies ? c.d : p.wide_d;
+    a.B = operand_of(x, c.x_stride, c.rows, c.d, ws + L.x, p.wide_d, s);
+    a.k = sizeof(T) == 2 ? c.d : p.wide_d;
     a.plane = p.wide_d * 2;
     a.scale = c.scale;
     a.targets = c.targets;
     a.vocab = c.vocab;
     a.stats = reinterpret_cast<u32x2*>(ws + L.stats);
     a.hit = reinterpret_cast<float*>(ws + L.hit);
-    // rows that need no laying out are one piece, up to what a grid holds
-    const int64_t most = up(cdiv((int64_t)1 << 28, up(c.rows, kTileV)), kTileV) * kTileV;
-    const int64_t piece = !w_lies            ? forward_piece(p, c.vocab, c.d, c.dtype)
-                          : c.vocab < most ? c.vocab : most;
+    // 16-bit rows are one piece, up to what a grid holds
+    const int64_t most = up(cdiv((int64_t)1 << 28, up(c.rows, kPieceUnit)), kPieceUnit) * kPieceUnit;
+    const int64_t piece = sizeof(T) == 4 ? p.piece : c.vocab < most ? c.vocab : most;
     a.tiles = p.tiles;
     for (int64_t v0 = 0; v0 < c.vocab; v0 += piece) {
         const int64_t n = c.vocab - v0 < piece ? c.vocab - v0 : piece;
-        a.A = laid_out(w + v0 * c.w_stride, c.w_stride, n, c.d, w_lies, ws + L.w, p.wide_d, s);
-        if (x_lies != w_lies) a.k = c.d;      // the shorter of the two rows; both are a multiple of 8
+        a.A = operand_of(w + v0 * c.w_stride, c.w_stride, n, c.d, ws + L.w, p.wide_d, s);
         a.v0 = v0;
-        product<T, kStats>(a, 1, s);
-        a.tile0 += cdiv(n, kTileV);
+        product<T, kStats>(a, 1, lies, s);
+        a.tile0 += cdiv(n, tile_rows(tile_columns(c.rows)));
     }
     det_status st = launch_status();
     if (st != DET_SUCCESS) return st;
@@ -720,7 +816,7 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
     constexpr int kParts = Half<T>::kParts;
     const T* x = static_cast<const T*>(c.x);
     const T* w = static_cast<const T*>(c.weight);
-    const bool x_lies = as_they_lie<T>(x, c.x_stride, c.d), w_lies = as_they_lie<T>(w, c.w_stride, c.d);
+    const bool lies = lies_on_16(x, c.x_stride, c.d) && lies_on_16(w, c.w_stride, c.d);
     const XentPlan p = xent_plan(c.rows, c.vocab, c.d, c.dtype);
     const XentLayout L = xent_layout(c.rows, c.vocab, c.d, c.dtype, true);
     float* unit = reinterpret_cast<float*>(ws + L.unit);
@@ -728,12 +824,12 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         KernelTimer kt("k_xent_unit", s);
         k_xent_unit<<<dim3(1), dim3(1024), 0, s>>>(c.dloss, c.targets, c.rows, c.vocab, unit);
     }
-    const Operand xo = laid_out(x, c.x_stride, c.rows, c.d, x_lies, ws + L.x, p.wide_d, s);
+    const Operand xo = operand_of(x, c.x_stride, c.rows, c.d, ws + L.x, p.wide_d, s);
     uint16_t* xt = reinterpret_cast<uint16_t*>(ws + L.xt);
     uint16_t* wt = reinterpret_cast<uint16_t*>(ws + L.wt);
     {
         KernelTimer kt("k_xent_transpose", s);
-        k_xent_transpose<T><<<dim3((unsigned)(p.wide_r / 64), (unsigned)cdiv(c.d, 64)), dim3(256), 0, s>>>(
+        k_xent_transpose<T><<<dim3((unsigned)cdiv(p.wide_r, 64), (unsigned)cdiv(c.d, 64)), dim3(256), 0, s>>>(
             x, c.x_stride, c.rows, c.d, p.wide_r, xt, c.targets, c.vocab);
     }
     for (int64_t v0 = 0; v0 < c.vocab; v0 += p.piece) {
@@ -748,9 +844,9 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         a.dloss = c.dloss;
         a.unit = unit;
         // D of the piece
-        a.A = laid_out(rows, c.w_stride, n, c.d, w_lies, ws + L.w, p.wide_d, s);
+        a.A = operand_of(rows, c.w_stride, n, c.d, ws + L.w, p.wide_d, s);
         a.B = xo;
-        a.k = x_lies == w_lies && !x_lies ? p.wide_d : c.d;
+        a.k = sizeof(T) == 2 ? c.d : p.wide_d;
         a.plane = p.wide_d * 2;
         a.d = ws + L.d;
         a.dt = ws + L.dt;
@@ -760,7 +856,7 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         a.dt_plane = p.wide_r * 2;
         a.rows_up = p.wide_r;
         a.piece_up = wide;
-        product<T, kLogits>(a, 1, s);
+        product<T, kLogits>(a, 1, lies, s);
         // dx += D weight
         {
             KernelTimer kt("k_xent_transpose", s);
@@ -775,7 +871,7 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         b.out = ws + L.sums;
         b.out_ld = p.dx_ld;
         b.add = v0 > 0;
-        product<T, kDx>(b, (int)p.parts, s);
+        product<T, kDx>(b, (int)p.parts, true, s);
         // dweight of the piece
         b.A = Operand{ws + L.xt, c.d, a.dt_ld};
         b.B = Operand{ws + L.dt, n, a.dt_ld};
@@ -783,7 +879,7 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         b.plane = p.wide_r * 2;
         b.out = static_cast<T*>(c.dweight) + v0 * c.d;
         b.out_ld = c.d;
-        product<T, kDw>(b, 1, s);
+        product<T, kDw>(b, 1, true, s);
         const det_status st = launch_status();
         if (st != DET_SUCCESS) return st;
     }
