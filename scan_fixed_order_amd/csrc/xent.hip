@@ -12,7 +12,7 @@
 //   dx       i width, j rows, k a piece of the vocabulary: weight transposed, D
 //   dweight  i width, j vocabulary, k rows: x transposed, D's columns
 // f32 goes through the matrix units in three bfloat16 parts of 8 bits each (exact together) and
-// the six products of parts that reach 2^-24 of the result.
+// the six products of parts that reach 2^-24 of the result; there an infinite factor may give NaN.
 //
 // Order: k ascending in steps of 16 inside the matrix instruction's own order, f32 accumulators; a
 // tile's logits, then the tiles of a row by lanes and the adjacent-lanes tree; dx adds pieces of the
@@ -24,7 +24,7 @@
 namespace det {
 namespace {
 
-constexpr int kDepth = 64;                    // elements of k a step: 128 bytes of a row
+constexpr int kDepth = 64, kDepthF32 = 32;    // elements of k a step: 128 bytes of a row
 constexpr int64_t kPieceUnit = 256;           // a piece's entries are a multiple of every tile's
 constexpr int64_t kPieceCells = 1 << 26;      // elements of D that a piece holds, about
 constexpr int64_t kPieceMin = 4096;
@@ -37,7 +37,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
-// one operand: rows of k elements, ld bytes apart, starting on 16 bytes
+// one operand: rows of k elements, ld bytes apart
 struct Operand {
     const char* p;
     int64_t rows, ld;
@@ -45,8 +45,7 @@ struct Operand {
 
 struct GemmArgs {
     Operand A, B;
-    int64_t k;            // elements of a row that count; a multiple of 8 unless they are staged
-    int64_t plane;        // f32: bytes from one part of a row to the next
+    int64_t k;            // elements of a row that count
     int64_t ni, nj;       // tiles along i and j
     int64_t per_z;        // steps of k that a workgroup along z takes
     float scale;
@@ -57,24 +56,12 @@ struct GemmArgs {
     float* hit;                           // [row]: the target's logit
     const float *lse, *dloss, *unit;      // unit: f16, the largest |dloss|
     char *d, *dt;                         // D by rows and by columns
-    int64_t d_ld, dt_ld, d_plane, dt_plane, rows_up, piece_up;
+    int64_t d_ld, dt_ld, rows_up, piece_up;      // bytes; D's rows and columns with their zeros
     // dx, dweight
     void* out;
     int64_t out_ld;       // elements
     bool add;
 };
-
-template <typename T>
-struct Half {
-    typedef T type;
-    static constexpr int kParts = 1;
-};
-template <>
-struct Half<float> {
-    typedef __bf16 type;
-    static constexpr int kParts = 3;
-};
-constexpr int kPairs = 6;
 
 __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c, __bf16) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
@@ -113,185 +100,12 @@ __device__ __forceinline__ uint16_t half_bits(float v) {
 
 enum Ending { kStats, kLogits, kDx, kDw };
 
-// Wave grid WI x WJ, a wave has MI x MJ tiles of 32 x 32.  A step's rows go from memory straight to
-// LDS, two steps in turn: 8 rows of 128 bytes a load, whose 16-byte chunks lie in the order chunk
-// ^ (row / 2 % 8), so that the 16 rows that a read of the operands takes at a time lie in different
-// banks.  What lies past an operand's rows or k reads as zero (the buffer's bounds).  STAGED: rows that
-// do not lie on 16 bytes go through registers instead.
-template <typename T, int WI, int WJ, int MI, int MJ, bool STAGED, int END>
-__device__ __forceinline__ void xent_product(const GemmArgs& a) {
-    typedef typename Half<T>::type H;
-    constexpr int kParts = Half<T>::kParts;
+// What becomes of a tile at (i0, j0): wave (wi, wj)'s sums.  `lds` is free.
+template <typename T, int WI, int WJ, int MI, int MJ, int END>
+__device__ __forceinline__ void xent_ending(const GemmArgs& a, f32x16 (&acc)[MI][MJ], int64_t i0,
+                                            int64_t j0, int wi, int wj, char* lds) {
     constexpr int BI = WI * MI * 32, BJ = WJ * MJ * 32, NW = WI * WJ;
-    constexpr int kRow = kDepth * 2, kChunks = kDepth / 8, kRows = 64 / kChunks;      // rows of a load
-    constexpr int LA = BI / kRows / NW, LB = BJ / kRows / NW;      // loads of a wave a step
-    static_assert(BI % (kRows * NW) == 0 && BJ % (kRows * NW) == 0, "rows of a step per wave");
-    constexpr int kStage = (BI + BJ) * kRow;
-    __shared__ __attribute__((aligned(16))) char s_0[kStage];
-    __shared__ __attribute__((aligned(16))) char s_1[kStage];
-    // the places of a row's chunks are turned by this much
-    const auto turn_of = [](int row) { return row >> 1 & 7; };
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int wi = wave / WJ, wj = wave % WJ;
-
-    // Workgroup b runs on XCD b % 8: each takes a run of tiles, four along j by as many as follow
-    // along i, so that what an XCD holds at a time shares its rows in its L2.
-    const int64_t tiles = a.ni * a.nj, per = (tiles + 7) / 8;
-    const int64_t q = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || q >= tiles) return;
-    const int64_t band = q / (4 * a.ni), in_band = q % (4 * a.ni);
-    const int64_t wide = a.nj - 4 * band < 4 ? a.nj - 4 * band : 4;
-    const int64_t i0 = in_band / wide * BI, j0 = (4 * band + in_band % wide) * BJ;
-
-    const int64_t span = a.k * 2 + (kParts - 1) * a.plane;      // bytes of a row
-    const auto records = [&](const Operand& o, int64_t first, int64_t most) {
-        const int64_t rows = o.rows - first < most ? o.rows - first : most;
-        return (uint32_t)((rows - 1) * o.ld + span);
-    };
-    const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(a.A.p + i0 * a.A.ld), 0,
-                                                      records(a.A, i0, BI), 0x00020000);
-    const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(a.B.p + j0 * a.B.ld), 0,
-                                                      records(a.B, j0, BJ), 0x00020000);
-    // A load takes kRows rows; where the turn goes by more rows than that, every other load's differs.
-    const int in_load = lane / kChunks;
-    const int chunk[2] = {(lane & (kChunks - 1)) ^ turn_of(in_load),
-                          (lane & (kChunks - 1)) ^ turn_of(kRows + in_load)};
-    const uint32_t lda = (uint32_t)a.A.ld, ldb = (uint32_t)a.B.ld;
-    const uint32_t oa = (uint32_t)(wave * LA * kRows + in_load) * lda;
-    const uint32_t ob = (uint32_t)(wave * LB * kRows + in_load) * ldb;
-    const int steps_k = (int)((a.k + kDepth - 1) / kDepth);      // of one product of parts
-    const int first = (int)(blockIdx.y * a.per_z);
-    const int behind = (int)(first + a.per_z < (int64_t)steps_k * (kParts == 1 ? 1 : kPairs)
-                                 ? first + a.per_z
-                                 : (int64_t)steps_k * (kParts == 1 ? 1 : kPairs));
-    const auto issue = [&](char* s, int step) {
-        uint32_t ka, kb;
-        int left;      // elements of k from the step's first on
-        if constexpr (kParts == 1) {
-            ka = kb = (uint32_t)step * kRow;
-            left = (int)a.k - step * kDepth;
-        } else {
-            const int pair = step / steps_k, at = step % steps_k;
-            // parts (0,0) (0,1) (1,0) (1,1) (0,2) (2,0)
-            const int ia = pair == 2 || pair == 3 ? 1 : pair == 5 ? 2 : 0;
-            const int ib = pair == 1 || pair == 3 ? 1 : pair == 4 ? 2 : 0;
-            ka = (uint32_t)(ia * a.plane) + at * kRow;
-            kb = (uint32_t)(ib * a.plane) + at * kRow;
-            left = (int)a.k - at * kDepth;
-        }
-        constexpr uint32_t kOut = 0x80000000u;
-        if (step >= behind) left = 0;
-#pragma unroll
-        for (int u = 0; u < LA; ++u) {
-            const int c = chunk[(wave * LA + u) & 1];
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                ra, (lds_ptr)(s + (wave * LA + u) * 1024), 16,
-                c * 8 < left ? oa + u * kRows * lda + ka + c * 16 : kOut, 0, 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < LB; ++u) {
-            const int c = chunk[(wave * LB + u) & 1];
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rb, (lds_ptr)(s + BI * kRow + (wave * LB + u) * 1024), 16,
-                c * 8 < left ? ob + u * kRows * ldb + kb + c * 16 : kOut, 0, 0, 0);
-        }
-    };
-    f32x16 acc[MI][MJ] = {};
-    const auto products = [&](const char* s) {
-        const char* pa = s + (wi * MI * 32 + (lane & 31)) * kRow;
-        const char* pb = s + (BI + wj * MJ * 32 + (lane & 31)) * kRow;
-#pragma unroll
-        for (int kk = 0; kk < kDepth / 16; ++kk) {
-            const int slot = ((kk * 2 + (lane >> 5)) ^ turn_of(lane)) * 16;
-            u32x4 av[MI], bv[MJ];
-#pragma unroll
-            for (int i = 0; i < MI; ++i) av[i] = *reinterpret_cast<const u32x4*>(pa + i * 32 * kRow + slot);
-#pragma unroll
-            for (int j = 0; j < MJ; ++j) bv[j] = *reinterpret_cast<const u32x4*>(pb + j * 32 * kRow + slot);
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int j = 0; j < MJ; ++j) acc[i][j] = mma(av[i], bv[j], acc[i][j], H{});
-        }
-    };
-    if constexpr (STAGED) {
-        // Rows that lie at any element: through registers, a step ahead, rows past the last one as that.
-        const int rows_a = (int)(a.A.rows - i0 < BI ? a.A.rows - i0 : BI);
-        const int rows_b = (int)(a.B.rows - j0 < BJ ? a.B.rows - j0 : BJ);
-        const char* at_a[LA];
-        const char* at_b[LB];
-#pragma unroll
-        for (int u = 0; u < LA; ++u) {
-            const int r = (wave * LA + u) * kRows + in_load;
-            at_a[u] = a.A.p + i0 * a.A.ld + (r < rows_a ? r : rows_a - 1) * a.A.ld;
-        }
-#pragma unroll
-        for (int u = 0; u < LB; ++u) {
-            const int r = (wave * LB + u) * kRows + in_load;
-            at_b[u] = a.B.p + j0 * a.B.ld + (r < rows_b ? r : rows_b - 1) * a.B.ld;
-        }
-        u32x4 ga[LA], gb[LB];
-        const auto column = [&](int step, int load) {
-            return (int64_t)step * kDepth + chunk[load & 1] * 8;
-        };
-        const auto fetch = [&](int step) {
-#pragma unroll
-            for (int u = 0; u < LA; ++u)
-                ga[u] = load_row(reinterpret_cast<const H*>(at_a[u]), column(step, wave * LA + u), a.k);
-#pragma unroll
-            for (int u = 0; u < LB; ++u)
-                gb[u] = load_row(reinterpret_cast<const H*>(at_b[u]), column(step, wave * LB + u), a.k);
-        };
-        const auto put = [&](char* s, int step) {
-#pragma unroll
-            for (int u = 0; u < LA; ++u)
-                *reinterpret_cast<u32x4*>(s + (wave * LA + u) * 1024 + lane * 16) =
-                    settle<H>(ga[u], column(step, wave * LA + u), a.k);
-#pragma unroll
-            for (int u = 0; u < LB; ++u)
-                *reinterpret_cast<u32x4*>(s + BI * kRow + (wave * LB + u) * 1024 + lane * 16) =
-                    settle<H>(gb[u], column(step, wave * LB + u), a.k);
-        };
-        fetch(first);
-        put(s_0, first);
-        __syncthreads();
-        // past the last step: zeros (settle)
-#pragma unroll 1
-        for (int step = first; step < behind; step += 2) {
-            fetch(step + 1);
-            products(s_0);
-            put(s_1, step + 1);
-            __syncthreads();
-            fetch(step + 2);
-            products(s_1);
-            put(s_0, step + 2);
-            __syncthreads();
-        }
-    } else {
-        // The step's loads are done (every wave waits for its own), and nobody reads the other buffer.
-        const auto turn = [&] {
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        issue(s_0, first);
-        // past the last step: zeros
-#pragma unroll 1
-        for (int step = first; step < behind; step += 2) {
-            turn();
-            issue(s_1, step + 1);
-            __builtin_amdgcn_sched_barrier(0);
-            products(s_0);
-            turn();
-            issue(s_0, step + 2);
-            __builtin_amdgcn_sched_barrier(0);
-            products(s_1);
-        }
-        turn();
-    }
-
+    const int lane = threadIdx.x & 63;
     // a lane's values: column wj.. + lane % 32, rows wi.. + 8 (r / 4) + 4 (lane / 32) + r % 4 of the tile
     const int row_base = wi * MI * 32 + 4 * (lane >> 5), col_base = wj * MJ * 32 + (lane & 31);
     const auto row_of = [&](int i, int r) { return row_base + i * 32 + 8 * (r / 4) + r % 4; };
@@ -304,7 +118,7 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
     };
 
     if constexpr (END == kStats) {
-        float* s_top = reinterpret_cast<float*>(s_0);      // [WI][BJ], then the sums
+        float* s_top = reinterpret_cast<float*>(lds);      // [WI][BJ], then the sums
         float* s_sum = s_top + WI * BJ;
 #pragma unroll
         for (int j = 0; j < MJ; ++j) {
@@ -378,8 +192,8 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
             const float unit = scored ? kUnit<T> : 0.0f;
             float weight = scored ? a.dloss[j0 + col] : 0.0f;
             if constexpr (__is_same(T, _Float16)) weight = *a.unit > 0.0f ? weight / *a.unit : 0.0f;
-            char* const d_at = a.d + (j0 + col) * a.d_ld + (i0 + row_base) * 2;
-            char* const dt_at = a.dt + (i0 + row_base) * a.dt_ld + (j0 + col) * 2;
+            char* const d_at = a.d + (j0 + col) * a.d_ld + (i0 + row_base) * (int64_t)sizeof(T);
+            char* const dt_at = a.dt + (i0 + row_base) * a.dt_ld + (j0 + col) * (int64_t)sizeof(T);
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -392,36 +206,26 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
                         d[r] = at == in_lane + r ? p - 1.0f : p;
                         d[r] = scored && v + r < rows_left ? d[r] * unit : 0.0f;
                     }
-                    if constexpr (kParts == 1) {
+                    if constexpr (sizeof(T) == 2) {
                         if (real && v < d_left) {
                             uint32_t w[2];
 #pragma unroll
                             for (int r = 0; r < 2; ++r)
-                                w[r] = half_bits<H>(d[2 * r]) | (uint32_t)half_bits<H>(d[2 * r + 1]) << 16;
+                                w[r] = half_bits<T>(d[2 * r]) | (uint32_t)half_bits<T>(d[2 * r + 1]) << 16;
                             *reinterpret_cast<u32x2*>(d_at + in_lane * 2) = u32x2{w[0], w[1]};
                         }
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             if (v + r < rows_left && col < dt_left)
                                 *reinterpret_cast<uint16_t*>(dt_at + (in_lane + r) * a.dt_ld) =
-                                    half_bits<H>(d[r] * weight);
+                                    half_bits<T>(d[r] * weight);
                     } else {
+                        if (real && v < d_left)
+                            *reinterpret_cast<f32x4*>(d_at + in_lane * 4) = f32x4{d[0], d[1], d[2], d[3]};
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            uint16_t p[3];
-                            parts_of(d[r], p);
-                            if (real && v < d_left)
-#pragma unroll
-                                for (int n = 0; n < 3; ++n)
-                                    *reinterpret_cast<uint16_t*>(d_at + n * a.d_plane +
-                                                                 (in_lane + r) * 2) = p[n];
-                            parts_of(d[r] * weight, p);
+                        for (int r = 0; r < 4; ++r)
                             if (v + r < rows_left && col < dt_left)
-#pragma unroll
-                                for (int n = 0; n < 3; ++n)
-                                    *reinterpret_cast<uint16_t*>(dt_at + (in_lane + r) * a.dt_ld +
-                                                                 n * a.dt_plane) = p[n];
-                        }
+                                *reinterpret_cast<float*>(dt_at + (in_lane + r) * a.dt_ld) = d[r] * weight;
                     }
                 }
         }
@@ -484,39 +288,301 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
     }
 }
 
+// Place of the workgroup's tile.  Workgroup b runs on XCD b % 8: each takes a run of tiles, four along j by
+// as many as follow along i, so that what an XCD holds at a time shares its rows in its L2.
+template <int BI, int BJ>
+__device__ __forceinline__ bool tile_of(const GemmArgs& a, int64_t& i0, int64_t& j0) {
+    const int64_t tiles = a.ni * a.nj, per = (tiles + 7) / 8;
+    const int64_t q = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || q >= tiles) return false;
+    const int64_t band = q / (4 * a.ni), in_band = q % (4 * a.ni);
+    const int64_t wide = a.nj - 4 * band < 4 ? a.nj - 4 * band : 4;
+    i0 = in_band / wide * BI;
+    j0 = (4 * band + in_band % wide) * BJ;
+    return true;
+}
+
+// 16-bit types.  Wave grid WI x WJ, a wave has MI x MJ tiles of 32 x 32.  A step's rows go from memory
+// straight to LDS, two steps in turn: 8 rows of 128 bytes a load, whose 16-byte chunks lie in the order
+// chunk ^ (row / 2 % 8), so that the 16 rows that a read of the operands takes at a time lie in
+// different banks.  What lies past an operand's rows or k reads as zero (the buffer's bounds).
+// STAGED: rows that do not lie on 16 bytes go through registers instead.
+template <typename T, int WI, int WJ, int MI, int MJ, bool STAGED, int END>
+__device__ __forceinline__ void xent_product(const GemmArgs& a) {
+    constexpr int BI = WI * MI * 32, BJ = WJ * MJ * 32, NW = WI * WJ;
+    constexpr int kRow = kDepth * 2, kRows = 8;                    // rows of a load
+    constexpr int LA = BI / kRows / NW, LB = BJ / kRows / NW;      // loads of a wave a step
+    static_assert(BI % (kRows * NW) == 0 && BJ % (kRows * NW) == 0, "rows of a step per wave");
+    constexpr int kStage = (BI + BJ) * kRow;
+    __shared__ __attribute__((aligned(16))) char s_0[kStage];
+    __shared__ __attribute__((aligned(16))) char s_1[kStage];
+    // the places of a row's chunks are turned by this much
+    const auto turn_of = [](int row) { return row >> 1 & 7; };
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int wi = wave / WJ, wj = wave % WJ;
+    int64_t i0, j0;
+    if (!tile_of<BI, BJ>(a, i0, j0)) return;
+    // a load's 8 rows are half of what the turn goes by: every other load's chunks differ
+    const int in_load = lane >> 3;
+    const int chunk[2] = {(lane & 7) ^ turn_of(in_load), (lane & 7) ^ turn_of(kRows + in_load)};
+    const int first = (int)(blockIdx.y * a.per_z), steps = (int)((a.k + kDepth - 1) / kDepth);
+    const int behind = first + a.per_z < steps ? (int)(first + a.per_z) : steps;
+    f32x16 acc[MI][MJ] = {};
+    const auto products = [&](const char* s) {
+        const char* pa = s + (wi * MI * 32 + (lane & 31)) * kRow;
+        const char* pb = s + (BI + wj * MJ * 32 + (lane & 31)) * kRow;
+#pragma unroll
+        for (int kk = 0; kk < kDepth / 16; ++kk) {
+            const int slot = ((kk * 2 + (lane >> 5)) ^ turn_of(lane)) * 16;
+            u32x4 av[MI], bv[MJ];
+#pragma unroll
+            for (int i = 0; i < MI; ++i) av[i] = *reinterpret_cast<const u32x4*>(pa + i * 32 * kRow + slot);
+#pragma unroll
+            for (int j = 0; j < MJ; ++j) bv[j] = *reinterpret_cast<const u32x4*>(pb + j * 32 * kRow + slot);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < MJ; ++j) acc[i][j] = mma(av[i], bv[j], acc[i][j], T{});
+        }
+    };
+    if constexpr (STAGED) {
+        // Rows that lie at any element: through registers, a step ahead, rows past the last one as that.
+        const int rows_a = (int)(a.A.rows - i0 < BI ? a.A.rows - i0 : BI);
+        const int rows_b = (int)(a.B.rows - j0 < BJ ? a.B.rows - j0 : BJ);
+        const char* at_a[LA];
+        const char* at_b[LB];
+#pragma unroll
+        for (int u = 0; u < LA; ++u) {
+            const int r = (wave * LA + u) * kRows + in_load;
+            at_a[u] = a.A.p + i0 * a.A.ld + (r < rows_a ? r : rows_a - 1) * a.A.ld;
+        }
+#pragma unroll
+        for (int u = 0; u < LB; ++u) {
+            const int r = (wave * LB + u) * kRows + in_load;
+            at_b[u] = a.B.p + j0 * a.B.ld + (r < rows_b ? r : rows_b - 1) * a.B.ld;
+        }
+        u32x4 ga[LA], gb[LB];
+        const auto column = [&](int step, int load) {      // past the last step: k
+            return step < behind ? (int64_t)step * kDepth + chunk[load & 1] * 8 : a.k;
+        };
+        const auto fetch = [&](int step) {
+#pragma unroll
+            for (int u = 0; u < LA; ++u)
+                ga[u] = load_row(reinterpret_cast<const T*>(at_a[u]), column(step, wave * LA + u), a.k);
+#pragma unroll
+            for (int u = 0; u < LB; ++u)
+                gb[u] = load_row(reinterpret_cast<const T*>(at_b[u]), column(step, wave * LB + u), a.k);
+        };
+        const auto put = [&](char* s, int step) {
+#pragma unroll
+            for (int u = 0; u < LA; ++u)
+                *reinterpret_cast<u32x4*>(s + (wave * LA + u) * 1024 + lane * 16) =
+                    settle<T>(ga[u], column(step, wave * LA + u), a.k);
+#pragma unroll
+            for (int u = 0; u < LB; ++u)
+                *reinterpret_cast<u32x4*>(s + BI * kRow + (wave * LB + u) * 1024 + lane * 16) =
+                    settle<T>(gb[u], column(step, wave * LB + u), a.k);
+        };
+        fetch(first);
+        put(s_0, first);
+        __syncthreads();
+        // past the last step: zeros (settle)
+#pragma unroll 1
+        for (int step = first; step < behind; step += 2) {
+            fetch(step + 1);
+            products(s_0);
+            put(s_1, step + 1);
+            __syncthreads();
+            fetch(step + 2);
+            products(s_1);
+            put(s_0, step + 2);
+            __syncthreads();
+        }
+    } else {
+        const auto records = [&](const Operand& o, int64_t from, int64_t most) {
+            const int64_t rows = o.rows - from < most ? o.rows - from : most;
+            return (uint32_t)((rows - 1) * o.ld + a.k * 2);
+        };
+        const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(a.A.p + i0 * a.A.ld), 0,
+                                                          records(a.A, i0, BI), 0x00020000);
+        const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(a.B.p + j0 * a.B.ld), 0,
+                                                          records(a.B, j0, BJ), 0x00020000);
+        const uint32_t lda = (uint32_t)a.A.ld, ldb = (uint32_t)a.B.ld;
+        const uint32_t oa = (uint32_t)(wave * LA * kRows + in_load) * lda;
+        const uint32_t ob = (uint32_t)(wave * LB * kRows + in_load) * ldb;
+        const auto issue = [&](char* s, int step) {
+            constexpr uint32_t kOut = 0x80000000u;      // past every row
+            const uint32_t at = (uint32_t)step * kRow;
+            const int left = step < behind ? (int)a.k - step * kDepth : 0;      // elements of k
+#pragma unroll
+            for (int u = 0; u < LA; ++u) {
+                const int c = chunk[(wave * LA + u) & 1];
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    ra, (lds_ptr)(s + (wave * LA + u) * 1024), 16,
+                    c * 8 < left ? oa + u * kRows * lda + at + c * 16 : kOut, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < LB; ++u) {
+                const int c = chunk[(wave * LB + u) & 1];
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rb, (lds_ptr)(s + BI * kRow + (wave * LB + u) * 1024), 16,
+                    c * 8 < left ? ob + u * kRows * ldb + at + c * 16 : kOut, 0, 0, 0);
+            }
+        };
+        // The step's loads are done (every wave waits for its own), and nobody reads the other buffer.
+        const auto turn = [&] {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        issue(s_0, first);
+        // past the last step: zeros
+#pragma unroll 1
+        for (int step = first; step < behind; step += 2) {
+            turn();
+            issue(s_1, step + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            products(s_0);
+            turn();
+            issue(s_0, step + 2);
+            __builtin_amdgcn_sched_barrier(0);
+            products(s_1);
+        }
+        turn();
+    }
+    xent_ending<T, WI, WJ, MI, MJ, END>(a, acc, i0, j0, wi, wj, s_0);
+}
+
+// f32.  A step's rows go through registers a step ahead, are cut into their three parts and lie in LDS
+// part by part (64 bytes of a row, chunk ^ (row / 4 % 4)); the product of the first parts has sums of
+// its own, the five smaller ones theirs, so that few of the additions round at the result's size.
+template <int WI, int WJ, int MI, int MJ, int END>
+__device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
+    constexpr int BI = WI * MI * 32, BJ = WJ * MJ * 32, NW = WI * WJ;
+    constexpr int kRow = kDepthF32 * 2, kRows = 8, kPart = (BI + BJ) * kRow;
+    constexpr int LA = BI / kRows / NW, LB = BJ / kRows / NW;
+    static_assert(BI % (kRows * NW) == 0 && BJ % (kRows * NW) == 0, "rows of a step per wave");
+    __shared__ __attribute__((aligned(16))) char s_0[3 * kPart];
+    __shared__ __attribute__((aligned(16))) char s_1[3 * kPart];
+    const auto turn_of = [](int row) { return row >> 2 & 3; };
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int wi = wave / WJ, wj = wave % WJ, in_load = lane >> 3;
+    int64_t i0, j0;
+    if (!tile_of<BI, BJ>(a, i0, j0)) return;
+    const int first = (int)(blockIdx.y * a.per_z), steps = (int)((a.k + kDepthF32 - 1) / kDepthF32);
+    const int behind = first + a.per_z < steps ? (int)(first + a.per_z) : steps;
+    const int rows_a = (int)(a.A.rows - i0 < BI ? a.A.rows - i0 : BI);
+    const int rows_b = (int)(a.B.rows - j0 < BJ ? a.B.rows - j0 : BJ);
+    const char* at_a[LA];
+    const char* at_b[LB];
+#pragma unroll
+    for (int u = 0; u < LA; ++u) {      // rows past the last one as that
+        const int r = (wave * LA + u) * kRows + in_load;
+        at_a[u] = a.A.p + i0 * a.A.ld + (r < rows_a ? r : rows_a - 1) * a.A.ld;
+    }
+#pragma unroll
+    for (int u = 0; u < LB; ++u) {
+        const int r = (wave * LB + u) * kRows + in_load;
+        at_b[u] = a.B.p + j0 * a.B.ld + (r < rows_b ? r : rows_b - 1) * a.B.ld;
+    }
+    u32x4 ga[LA], gb[LB];
+    const auto column = [&](int step) { return (int64_t)step * kDepthF32 + (lane & 7) * 4; };
+    const auto fetch = [&](int step) {
+        const int64_t c = column(step);
+#pragma unroll
+        for (int u = 0; u < LA; ++u) ga[u] = load_row(reinterpret_cast<const float*>(at_a[u]), c, a.k);
+#pragma unroll
+        for (int u = 0; u < LB; ++u) gb[u] = load_row(reinterpret_cast<const float*>(at_b[u]), c, a.k);
+    };
+    const auto put_one = [&](char* s, int row, u32x4 raw, int64_t c) {
+        const u32x4 r = settle<float>(raw, c, a.k);
+        uint16_t p[4][3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) parts_of(__uint_as_float(r[i]), p[i]);
+        char* at = s + row * kRow + (((lane & 7) >> 1) ^ turn_of(row)) * 16 + (lane & 1) * 8;
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+            *reinterpret_cast<u32x2*>(at + n * kPart) =
+                u32x2{p[0][n] | (uint32_t)p[1][n] << 16, p[2][n] | (uint32_t)p[3][n] << 16};
+    };
+    const auto put = [&](char* s, int step) {
+        const int64_t c = step < behind ? column(step) : a.k;      // past the last step: zeros
+#pragma unroll
+        for (int u = 0; u < LA; ++u) put_one(s, (wave * LA + u) * kRows + in_load, ga[u], c);
+#pragma unroll
+        for (int u = 0; u < LB; ++u) put_one(s + BI * kRow, (wave * LB + u) * kRows + in_load, gb[u], c);
+    };
+    f32x16 acc[MI][MJ] = {}, small[MI][MJ] = {};
+    const auto products = [&](const char* s) {
+        const char* pa = s + (wi * MI * 32 + (lane & 31)) * kRow;
+        const char* pb = s + (BI + wj * MJ * 32 + (lane & 31)) * kRow;
+#pragma unroll
+        for (int kk = 0; kk < kDepthF32 / 16; ++kk) {
+            const int slot = ((kk * 2 + (lane >> 5)) ^ turn_of(lane)) * 16;
+            u32x4 av[3][MI], bv[3][MJ];
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+                    av[n][i] = *reinterpret_cast<const u32x4*>(pa + n * kPart + i * 32 * kRow + slot);
+#pragma unroll
+                for (int j = 0; j < MJ; ++j)
+                    bv[n][j] = *reinterpret_cast<const u32x4*>(pb + n * kPart + j * 32 * kRow + slot);
+            }
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < MJ; ++j) {
+                    acc[i][j] = mma(av[0][i], bv[0][j], acc[i][j], __bf16{});
+                    small[i][j] = mma(av[2][i], bv[0][j], small[i][j], __bf16{});
+                    small[i][j] = mma(av[1][i], bv[1][j], small[i][j], __bf16{});
+                    small[i][j] = mma(av[0][i], bv[2][j], small[i][j], __bf16{});
+                    small[i][j] = mma(av[1][i], bv[0][j], small[i][j], __bf16{});
+                    small[i][j] = mma(av[0][i], bv[1][j], small[i][j], __bf16{});
+                }
+        }
+    };
+    fetch(first);
+    put(s_0, first);
+    __syncthreads();
+#pragma unroll 1
+    for (int step = first; step < behind; step += 2) {
+        fetch(step + 1);
+        products(s_0);
+        put(s_1, step + 1);
+        __syncthreads();
+        fetch(step + 2);
+        products(s_1);
+        put(s_0, step + 2);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < MJ; ++j) acc[i][j] += small[i][j];
+    xent_ending<float, WI, WJ, MI, MJ, END>(a, acc, i0, j0, wi, wj, s_0);
+}
+
 // (The kernel's body is a device function: it uses types that the host's compiler pass lacks.)
 template <typename T, int WI, int WJ, int MI, int MJ, bool STAGED, int END>
 __global__ __launch_bounds__(WI * WJ * 64) void k_xent_product(GemmArgs a) {
-    xent_product<T, WI, WJ, MI, MJ, STAGED, END>(a);
+    if constexpr (sizeof(T) == 4)
+        xent_product_f32<WI, WJ, MI, MJ, END>(a);
+    else
+        xent_product<T, WI, WJ, MI, MJ, STAGED, END>(a);
 }
 
 // ---------------------------------------------------------------- operands laid out
 
-// f32 rows of d elements -> rows of three parts of `wide` elements (d rounded up to a step), zeros behind
-__global__ __launch_bounds__(256) void k_xent_split(const float* src, int64_t stride, int64_t rows,
-                                                    int64_t d, int64_t wide, uint16_t* dst) {
-    const int64_t per = wide / 4, total = rows * per;      // a vector a lane
-    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < total; n += (int64_t)gridDim.x * 256) {
-        const int64_t row = n / per, c = n % per * 4;
-        float v[4];
-        unpack<float>(settle<float>(load_row(src + row * stride, c, d), c, d), v);
-        uint16_t p[4][3];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) parts_of(v[i], p[i]);
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-            *reinterpret_cast<u32x2*>(dst + (row * 3 + k) * wide + c) =
-                u32x2{p[0][k] | (uint32_t)p[1][k] << 16, p[2][k] | (uint32_t)p[3][k] << 16};
-    }
-}
-
-// rows of d elements -> d rows of `wide` (the number of rows rounded up to a step), zeros behind and
+// rows of d elements -> d rows of `wide` (the number of rows rounded up), zeros behind and
 // for the rows that have no target in [0, vocab) (targets NULL: none)
 template <typename T>
 __global__ __launch_bounds__(256) void k_xent_transpose(const T* src, int64_t stride, int64_t rows,
-                                                        int64_t d, int64_t wide, uint16_t* dst,
+                                                        int64_t d, int64_t wide, T* dst,
                                                         const int64_t* targets, int64_t vocab) {
-    constexpr int kParts = Half<T>::kParts, kSide = 64;
+    constexpr int kSide = 64;
     __shared__ T s[kSide][kSide + 2];
     const int64_t r0 = (int64_t)blockIdx.x * kSide, c0 = (int64_t)blockIdx.y * kSide;
     constexpr int kPer = kSide / kVec<T>;      // vectors of a row
@@ -544,25 +610,20 @@ __global__ __launch_bounds__(256) void k_xent_transpose(const T* src, int64_t st
         }
     }
     __syncthreads();
-    for (int n = threadIdx.x; n < kSide * kSide / 8; n += 256) {
-        const int c = n / (kSide / 8), r = n % (kSide / 8) * 8;
+#pragma unroll
+    for (int u = 0; u < kSide * kPer / 256; ++u) {
+        const int n = threadIdx.x + u * 256, c = n / kPer, r = n % kPer * kVec<T>;
         if (c0 + c >= d || r0 + r >= wide) continue;
-        uint16_t o[kParts][8];
+        u32x4 w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (kParts == 1) {
-                o[0][i] = __builtin_bit_cast(uint16_t, s[c][r + i]);
-            } else {
-                uint16_t p[3];
-                parts_of(s[c][r + i], p);
-#pragma unroll
-                for (int k = 0; k < 3; ++k) o[k][i] = p[k];
-            }
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4)
+                w[i] = __float_as_uint(s[c][r + i]);
+            else
+                w[i] = __builtin_bit_cast(uint16_t, s[c][r + 2 * i]) |
+                       (uint32_t)__builtin_bit_cast(uint16_t, s[c][r + 2 * i + 1]) << 16;
         }
-#pragma unroll
-        for (int k = 0; k < kParts; ++k)
-            *reinterpret_cast<u32x4*>(dst + ((c0 + c) * kParts + k) * wide + r0 + r) =
-                __builtin_bit_cast(u32x4, o[k]);
+        *reinterpret_cast<u32x4*>(dst + (c0 + c) * wide + r0 + r) = w;
     }
 }
 
@@ -652,17 +713,16 @@ void product_as(GemmArgs a, int parts, hipStream_t s) {
     constexpr int64_t BI = WI * MI * 32, BJ = WJ * MJ * 32;
     a.ni = cdiv(a.A.rows, BI);
     a.nj = cdiv(a.B.rows, BJ);
-    const int64_t steps = cdiv(a.k, kDepth) * (Half<T>::kParts == 1 ? 1 : kPairs);
-    a.per_z = cdiv(steps, parts);
+    a.per_z = cdiv(cdiv(a.k, sizeof(T) == 4 ? kDepthF32 : kDepth), parts);
     k_xent_product<T, WI, WJ, MI, MJ, STAGED, END>
         <<<dim3((unsigned)(cdiv(a.ni * a.nj, 8) * 8), (unsigned)parts), dim3(WI * WJ * 64), 0, s>>>(a);
 }
 
 // Columns (rows of x) of a tile by their number: few need few, and many the width that leaves least of
-// the last tile unused, the widest of those.
-int tile_columns(int64_t rows) {
+// the last tile unused, the widest of those (f32, whose parts take three times the room, 128).
+int tile_columns(int64_t rows, bool f32) {
     if (rows <= 32) return 32;
-    if (rows <= 128) return 128;
+    if (rows <= 128 || f32) return 128;
     return up(rows, 192) < up(rows, 256) ? 192 : 256;
 }
 
@@ -671,25 +731,27 @@ int64_t tile_rows(int columns) { return columns == 32 ? 64 : 256; }
 
 template <typename T, bool STAGED, int END>
 void product_of(const GemmArgs& a, int columns, int parts, hipStream_t s) {
-    if (columns == 256)
-        product_as<T, 2, 4, 4, 2, STAGED, END>(a, parts, s);
-    else if (columns == 192)
-        product_as<T, 4, 2, 2, 3, STAGED, END>(a, parts, s);
-    else if (columns == 128)
-        product_as<T, 4, 2, 2, 2, STAGED, END>(a, parts, s);
-    else
-        product_as<T, 2, 1, 1, 1, STAGED, END>(a, parts, s);
+    if (columns == 32) return product_as<T, 2, 1, 1, 1, STAGED, END>(a, parts, s);
+    if constexpr (sizeof(T) == 2) {
+        if (columns == 256) return product_as<T, 2, 4, 4, 2, STAGED, END>(a, parts, s);
+        if (columns == 192) return product_as<T, 4, 2, 2, 3, STAGED, END>(a, parts, s);
+    }
+    product_as<T, 4, 2, 2, 2, STAGED, END>(a, parts, s);
 }
 
 template <typename T, int END>
 void product(const GemmArgs& a, int parts, bool lies, hipStream_t s) {
     static const char* const names[] = {"k_xent_stats", "k_xent_logits", "k_xent_dx", "k_xent_dweight"};
     KernelTimer kt(names[END], s);
+    constexpr bool f32 = sizeof(T) == 4;
     if constexpr (END == kDw) {      // columns are vocabulary entries, of which there are many
-        product_as<T, 2, 4, 4, 2, false, END>(a, parts, s);
+        if constexpr (f32)
+            product_as<T, 4, 2, 2, 2, false, END>(a, parts, s);
+        else
+            product_as<T, 2, 4, 4, 2, false, END>(a, parts, s);
     } else {
-        const int columns = tile_columns(a.B.rows);
-        if constexpr (sizeof(T) == 2 && (END == kStats || END == kLogits)) {
+        const int columns = tile_columns(a.B.rows, f32);
+        if constexpr (!f32 && (END == kStats || END == kLogits)) {
             if (!lies) return product_of<T, true, END>(a, columns, parts, s);
         }
         product_of<T, false, END>(a, columns, parts, s);
@@ -698,8 +760,8 @@ void product(const GemmArgs& a, int parts, bool lies, hipStream_t s) {
 
 struct XentPlan {
     int64_t piece;
-    int64_t wide_d, wide_v, wide_r;      // d, piece and rows rounded up: zeros behind them
-    int64_t parts, dx_ld, tiles;
+    int64_t wide_v, wide_r;      // piece and rows rounded up: zeros behind them
+    int64_t parts, dx_ld, tile_i, tiles;
 };
 
 // Vocabulary entries of a piece: D of a piece takes about kPieceCells elements, twice.
@@ -708,27 +770,27 @@ XentPlan xent_plan(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype) {
     int64_t piece = kPieceCells / (rows > 0 ? rows : 1) / kPieceUnit * kPieceUnit;
     piece = piece < kPieceMin ? kPieceMin : piece > kPieceMax ? kPieceMax : piece;
     p.piece = piece < vocab ? piece : vocab;
-    p.wide_d = up(d, kDepth);
     p.wide_v = up(p.piece, kDepth);
     p.wide_r = up(rows, 32);      // what the narrowest tile writes of D's columns
     p.dx_ld = up(d, 4);
-    p.tiles = cdiv(vocab, tile_rows(tile_columns(rows)));
+    const int columns = tile_columns(rows, dtype == DET_F32);
+    p.tile_i = tile_rows(columns);
+    p.tiles = cdiv(vocab, p.tile_i);
     // workgroups that share dx's sum over a piece where its tiles are few
-    const int columns = tile_columns(rows);
-    const int64_t tiles = cdiv(d, tile_rows(columns)) * cdiv(rows, columns);
+    const int64_t tiles = cdiv(d, p.tile_i) * cdiv(rows, columns);
     p.parts = tiles >= 128 ? 1 : cdiv(256, tiles);
-    const int64_t steps = p.wide_v / kDepth * (dtype == DET_F32 ? kPairs : 1);
+    const int64_t steps = p.wide_v / (dtype == DET_F32 ? kDepthF32 : kDepth);
     if (p.parts > cdiv(steps, 8)) p.parts = cdiv(steps, 8);
     return p;
 }
 
 struct XentLayout {
-    size_t x, w, stats, hit, xt, wt, d, dt, sums, unit, total;
+    size_t stats, hit, xt, wt, d, dt, sums, unit, total;
 };
 
 XentLayout xent_layout(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype, bool back) {
     const XentPlan p = xent_plan(rows, vocab, d, dtype);
-    const int64_t n = dtype == DET_F32 ? 6 : 2;      // bytes of an element laid out
+    const int64_t n = (int64_t)lm_size(dtype);
     XentLayout L = {};
     size_t o = 0;
     const auto take = [&](size_t bytes) {
@@ -736,10 +798,6 @@ XentLayout xent_layout(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype, 
         o += round_up(bytes > 0 ? bytes : 1, 256);
         return at;
     };
-    if (dtype == DET_F32) {      // the others are read as they lie
-        L.x = take((size_t)rows * p.wide_d * n);
-        L.w = take((size_t)p.piece * p.wide_d * n);
-    }
     if (!back) {
         L.stats = take((size_t)rows * p.tiles * 8);
         L.hit = take((size_t)rows * 4);
@@ -760,20 +818,6 @@ bool lies_on_16(const void* p, int64_t stride, int64_t d) {
     return d % 8 == 0 && stride % 8 == 0 && stride <= (1 << 21) && reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
-// 16-bit rows as they lie; f32 rows in parts at `at`
-template <typename T>
-Operand operand_of(const T* p, int64_t stride, int64_t rows, int64_t d, char* at, int64_t wide,
-                   hipStream_t s) {
-    if constexpr (sizeof(T) == 2) {
-        return Operand{reinterpret_cast<const char*>(p), rows, stride * 2};
-    } else {
-        KernelTimer kt("k_xent_split", s);
-        k_xent_split<<<dim3(lanes_grid(rows * (wide / 4))), dim3(256), 0, s>>>(
-            p, stride, rows, d, wide, reinterpret_cast<uint16_t*>(at));
-        return Operand{at, rows, wide * 6};
-    }
-}
-
 template <typename T>
 det_status xent_typed(const XentCall& c, char* ws, hipStream_t s) {
     const T* x = static_cast<const T*>(c.x);
@@ -782,24 +826,23 @@ det_status xent_typed(const XentCall& c, char* ws, hipStream_t s) {
     const XentPlan p = xent_plan(c.rows, c.vocab, c.d, c.dtype);
     const XentLayout L = xent_layout(c.rows, c.vocab, c.d, c.dtype, false);
     GemmArgs a = {};
-    a.B = operand_of(x, c.x_stride, c.rows, c.d, ws + L.x, p.wide_d, s);
-    a.k = sizeof(T) == 2 ? c.d : p.wide_d;
-    a.plane = p.wide_d * 2;
+    a.B = Operand{reinterpret_cast<const char*>(x), c.rows, c.x_stride * (int64_t)sizeof(T)};
+    a.k = c.d;
     a.scale = c.scale;
     a.targets = c.targets;
     a.vocab = c.vocab;
     a.stats = reinterpret_cast<u32x2*>(ws + L.stats);
     a.hit = reinterpret_cast<float*>(ws + L.hit);
-    // 16-bit rows are one piece, up to what a grid holds
+    // one piece, up to what a grid holds
     const int64_t most = up(cdiv((int64_t)1 << 28, up(c.rows, kPieceUnit)), kPieceUnit) * kPieceUnit;
-    const int64_t piece = sizeof(T) == 4 ? p.piece : c.vocab < most ? c.vocab : most;
+    const int64_t piece = c.vocab < most ? c.vocab : most;
     a.tiles = p.tiles;
     for (int64_t v0 = 0; v0 < c.vocab; v0 += piece) {
         const int64_t n = c.vocab - v0 < piece ? c.vocab - v0 : piece;
-        a.A = operand_of(w + v0 * c.w_stride, c.w_stride, n, c.d, ws + L.w, p.wide_d, s);
+        a.A = Operand{reinterpret_cast<const char*>(w + v0 * c.w_stride), n, c.w_stride * (int64_t)sizeof(T)};
         a.v0 = v0;
         product<T, kStats>(a, 1, lies, s);
-        a.tile0 += cdiv(n, tile_rows(tile_columns(c.rows)));
+        a.tile0 += cdiv(n, p.tile_i);
     }
     det_status st = launch_status();
     if (st != DET_SUCCESS) return st;
@@ -813,7 +856,7 @@ det_status xent_typed(const XentCall& c, char* ws, hipStream_t s) {
 
 template <typename T>
 det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
-    constexpr int kParts = Half<T>::kParts;
+    constexpr int64_t es = sizeof(T);
     const T* x = static_cast<const T*>(c.x);
     const T* w = static_cast<const T*>(c.weight);
     const bool lies = lies_on_16(x, c.x_stride, c.d) && lies_on_16(w, c.w_stride, c.d);
@@ -824,9 +867,8 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         KernelTimer kt("k_xent_unit", s);
         k_xent_unit<<<dim3(1), dim3(1024), 0, s>>>(c.dloss, c.targets, c.rows, c.vocab, unit);
     }
-    const Operand xo = operand_of(x, c.x_stride, c.rows, c.d, ws + L.x, p.wide_d, s);
-    uint16_t* xt = reinterpret_cast<uint16_t*>(ws + L.xt);
-    uint16_t* wt = reinterpret_cast<uint16_t*>(ws + L.wt);
+    T* xt = reinterpret_cast<T*>(ws + L.xt);
+    T* wt = reinterpret_cast<T*>(ws + L.wt);
     {
         KernelTimer kt("k_xent_transpose", s);
         k_xent_transpose<T><<<dim3((unsigned)cdiv(p.wide_r, 64), (unsigned)cdiv(c.d, 64)), dim3(256), 0, s>>>(
@@ -844,16 +886,13 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         a.dloss = c.dloss;
         a.unit = unit;
         // D of the piece
-        a.A = operand_of(rows, c.w_stride, n, c.d, ws + L.w, p.wide_d, s);
-        a.B = xo;
-        a.k = sizeof(T) == 2 ? c.d : p.wide_d;
-        a.plane = p.wide_d * 2;
+        a.A = Operand{reinterpret_cast<const char*>(rows), n, c.w_stride * es};
+        a.B = Operand{reinterpret_cast<const char*>(x), c.rows, c.x_stride * es};
+        a.k = c.d;
         a.d = ws + L.d;
         a.dt = ws + L.dt;
-        a.d_ld = p.wide_v * 2 * kParts;
-        a.d_plane = p.wide_v * 2;
-        a.dt_ld = p.wide_r * 2 * kParts;
-        a.dt_plane = p.wide_r * 2;
+        a.d_ld = p.wide_v * es;
+        a.dt_ld = p.wide_r * es;
         a.rows_up = p.wide_r;
         a.piece_up = wide;
         product<T, kLogits>(a, 1, lies, s);
@@ -864,10 +903,9 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
                 rows, c.w_stride, n, c.d, p.wide_v, wt, nullptr, 1);
         }
         GemmArgs b = a;
-        b.A = Operand{ws + L.wt, c.d, p.wide_v * 2 * kParts};
+        b.A = Operand{ws + L.wt, c.d, p.wide_v * es};
         b.B = Operand{ws + L.d, c.rows, a.d_ld};
         b.k = wide;
-        b.plane = p.wide_v * 2;
         b.out = ws + L.sums;
         b.out_ld = p.dx_ld;
         b.add = v0 > 0;
@@ -876,7 +914,6 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         b.A = Operand{ws + L.xt, c.d, a.dt_ld};
         b.B = Operand{ws + L.dt, n, a.dt_ld};
         b.k = p.wide_r;
-        b.plane = p.wide_r * 2;
         b.out = static_cast<T*>(c.dweight) + v0 * c.d;
         b.out_ld = c.d;
         product<T, kDw>(b, 1, true, s);
