@@ -10,7 +10,7 @@
 //   dlogits  the same product again: D by rows (for dx) and by columns (for dweight), rounded to the
 //            storage type once
 //   dx       i width, j rows, k a piece of the vocabulary: weight transposed, D
-//   dweight  i width, j vocabulary, k rows: x transposed, D's columns
+//   dweight  i width, j vocabulary, k rows: x transposed, D's columns times dloss (f32: x times dloss)
 // f32 goes through the matrix units in three bfloat16 parts of 8 bits each (exact together) and
 // the six products of parts that reach 2^-24 of the result; there an infinite factor may give NaN.
 //
@@ -72,21 +72,15 @@ __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c, _Float16) {
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// The parts of a float: 8 bits each, cut off, so that the rest is exact.  What is not finite is its
-// own first part.
-__device__ __forceinline__ void parts_of(float v, uint16_t (&p)[3]) {
-    const uint32_t b = __float_as_uint(v);
-    if ((b & 0x7F800000u) == 0x7F800000u) {
-        p[0] = (uint16_t)((b >> 16) | (b & 0x7FFFFFu ? 0x40u : 0u));
-        p[1] = p[2] = 0;
-        return;
+// Two floats in three parts each, 8 bits a part, cut off, so that the rest is exact: parts n of a
+// and b side by side in p[n].  The rest of an infinity is NaN.
+__device__ __forceinline__ void parts_of(uint32_t a, uint32_t b, uint32_t (&p)[3]) {
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+        p[n] = __builtin_amdgcn_perm(b, a, 0x07060302u);      // their upper halves
+        a = __float_as_uint(__uint_as_float(a) - __uint_as_float(a & 0xFFFF0000u));
+        b = __float_as_uint(__uint_as_float(b) - __uint_as_float(b & 0xFFFF0000u));
     }
-    p[0] = (uint16_t)(b >> 16);
-    const float r = v - __uint_as_float(b & 0xFFFF0000u);
-    const uint32_t rb = __float_as_uint(r);
-    p[1] = (uint16_t)(rb >> 16);
-    const float q = r - __uint_as_float(rb & 0xFFFF0000u);
-    p[2] = (uint16_t)(__float_as_uint(q) >> 16);
 }
 
 // D's factor in storage: f16 has few exponents, and |D| <= 1
@@ -100,6 +94,53 @@ __device__ __forceinline__ uint16_t half_bits(float v) {
 
 enum Ending { kStats, kLogits, kDx, kDw };
 
+// Columns of a tile on their way to rows in memory: a lane holds four elements of a column, whose rows in
+// memory it would write 8 or 16 bytes at a time; through LDS a row's elements leave side by side.
+// (dweight of 30000 entries x 1000 f32, 8 rows: XX us, in pieces of 16 bytes 306: the rows that the
+// chip has begun and not ended are as large as its caches.)  The 16-byte chunks of a column lie turned by it,
+// so that lanes, a column each, write to different banks.
+template <typename T, int BI>
+__device__ __forceinline__ void column_put(char* lds, int col, int e, const float (&v)[4]) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<f32x4*>(lds + col * BI * 4 + ((e / 4) ^ (col & 15)) * 16) =
+            f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+        uint32_t w[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            w[r] = half_bits<T>(v[2 * r]) | (uint32_t)half_bits<T>(v[2 * r + 1]) << 16;
+        *reinterpret_cast<u32x2*>(lds + col * BI * 2 + ((e / 8) ^ (col & 7)) * 16 + (e & 4) * 2) =
+            u32x2{w[0], w[1]};
+    }
+}
+
+// The columns j * 32 .. of every wave along j, elements below `left`, columns below `cols_left`.
+template <typename T, int BI, int WJ, int MJ, int THREADS>
+__device__ __forceinline__ void columns_out(const char* lds, int j, int left, int cols_left, T* out,
+                                            int64_t ld) {
+    constexpr int kChunks = BI / kVec<T>, kTurn = sizeof(T) == 4 ? 15 : 7;
+    __syncthreads();
+    for (int n = threadIdx.x; n < WJ * 32 * kChunks; n += THREADS) {
+        const int in = n / kChunks, c = n % kChunks, col = (in / 32 * MJ + j) * 32 + in % 32;
+        if (col >= cols_left || c * kVec<T> >= left) continue;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(lds + in * BI * (int)sizeof(T) + (c ^ (in & kTurn)) * 16);
+        T* at = out + (int64_t)col * ld + c * kVec<T>;
+        if (c * kVec<T> + kVec<T> <= left) {
+            store_vec(at, w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVec<T>; ++i)
+                if (c * kVec<T> + i < left) {
+                    if constexpr (sizeof(T) == 4)
+                        at[i] = __uint_as_float(w[i]);
+                    else
+                        at[i] = __builtin_bit_cast(T, (uint16_t)(w[i / 2] >> (16 * (i & 1))));
+                }
+        }
+    }
+    __syncthreads();
+}
+
 // What becomes of a tile at (i0, j0): wave (wi, wj)'s sums.  `lds` is free.
 template <typename T, int WI, int WJ, int MI, int MJ, int END>
 __device__ __forceinline__ void xent_ending(const GemmArgs& a, f32x16 (&acc)[MI][MJ], int64_t i0,
@@ -108,6 +149,7 @@ __device__ __forceinline__ void xent_ending(const GemmArgs& a, f32x16 (&acc)[MI]
     const int lane = threadIdx.x & 63;
     // a lane's values: column wj.. + lane % 32, rows wi.. + 8 (r / 4) + 4 (lane / 32) + r % 4 of the tile
     const int row_base = wi * MI * 32 + 4 * (lane >> 5), col_base = wj * MJ * 32 + (lane & 31);
+    const int col_in = wj * 32 + (lane & 31);      // among the columns of one j
     const auto row_of = [&](int i, int r) { return row_base + i * 32 + 8 * (r / 4) + r % 4; };
     const int rows_left = (int)(a.A.rows - i0 < BI ? a.A.rows - i0 : BI);
     const int cols_left = (int)(a.B.rows - j0 < BJ ? a.B.rows - j0 : BJ);
@@ -192,7 +234,6 @@ __device__ __forceinline__ void xent_ending(const GemmArgs& a, f32x16 (&acc)[MI]
             const float unit = scored ? kUnit<T> : 0.0f;
             float weight = scored ? a.dloss[j0 + col] : 0.0f;
             if constexpr (__is_same(T, _Float16)) weight = *a.unit > 0.0f ? weight / *a.unit : 0.0f;
-            char* const d_at = a.d + (j0 + col) * a.d_ld + (i0 + row_base) * (int64_t)sizeof(T);
             char* const dt_at = a.dt + (i0 + row_base) * a.dt_ld + (j0 + col) * (int64_t)sizeof(T);
 #pragma unroll
             for (int i = 0; i < MI; ++i)
@@ -206,36 +247,24 @@ __device__ __forceinline__ void xent_ending(const GemmArgs& a, f32x16 (&acc)[MI]
                         d[r] = at == in_lane + r ? p - 1.0f : p;
                         d[r] = scored && v + r < rows_left ? d[r] * unit : 0.0f;
                     }
+                    column_put<T, BI>(lds, col_in, v, d);
                     if constexpr (sizeof(T) == 2) {
-                        if (real && v < d_left) {
-                            uint32_t w[2];
-#pragma unroll
-                            for (int r = 0; r < 2; ++r)
-                                w[r] = half_bits<T>(d[2 * r]) | (uint32_t)half_bits<T>(d[2 * r + 1]) << 16;
-                            *reinterpret_cast<u32x2*>(d_at + in_lane * 2) = u32x2{w[0], w[1]};
-                        }
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             if (v + r < rows_left && col < dt_left)
                                 *reinterpret_cast<uint16_t*>(dt_at + (in_lane + r) * a.dt_ld) =
                                     half_bits<T>(d[r] * weight);
-                    } else {
-                        if (real && v < d_left)
-                            *reinterpret_cast<f32x4*>(d_at + in_lane * 4) = f32x4{d[0], d[1], d[2], d[3]};
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (v + r < rows_left && col < dt_left)
-                                *reinterpret_cast<float*>(dt_at + (in_lane + r) * a.dt_ld) = d[r] * weight;
                     }
                 }
+            columns_out<T, BI, WJ, MJ, NW * 64>(lds, j, d_left, cols_left,
+                                                reinterpret_cast<T*>(a.d + j0 * a.d_ld) + i0,
+                                                a.d_ld / (int64_t)sizeof(T));
         }
     } else {
         // dx: f32 sums of a part; dweight: the gradient in its type
 #pragma unroll
         for (int j = 0; j < MJ; ++j) {
             const int col = col_base + j * 32;
-            if (col >= cols_left) continue;
-            const int64_t row = j0 + col;
             float f = 1.0f;
             if constexpr (END == kDw) {
                 f = a.scale / kUnit<T>;
@@ -245,45 +274,26 @@ __device__ __forceinline__ void xent_ending(const GemmArgs& a, f32x16 (&acc)[MI]
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int left = rows_left - row_of(i, 4 * g);
-                    const int64_t c = i0 + row_of(i, 4 * g);
-                    if (left <= 0) continue;
+                    const int e = row_of(i, 4 * g);
                     float v[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * g + r] * f;
-                    if constexpr (END == kDx) {
+                    if constexpr (END == kDw) {
+                        column_put<T, BI>(lds, col_in, e, v);
+                    } else if (col < cols_left && e < rows_left) {
                         float* at = static_cast<float*>(a.out) + blockIdx.y * a.B.rows * a.out_ld +
-                                    row * a.out_ld + c;      // out_ld: a multiple of 4, room for 4
+                                    (j0 + col) * a.out_ld + i0 + e;      // out_ld: a multiple of 4, room for 4
                         if (a.add) {
                             const f32x4 old = *reinterpret_cast<const f32x4*>(at);
 #pragma unroll
                             for (int r = 0; r < 4; ++r) v[r] = old[r] + v[r];
                         }
                         *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
-                    } else {
-                        T* at = static_cast<T*>(a.out) + row * a.out_ld + c;
-                        if constexpr (sizeof(T) == 4) {
-                            if (left >= 4)
-                                *reinterpret_cast<f32x4_a4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
-                            else
-                                for (int r = 0; r < 3; ++r)
-                                    if (r < left) at[r] = v[r];
-                        } else {
-                            typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
-                            if (left >= 4) {
-                                uint32_t w[2];
-#pragma unroll
-                                for (int r = 0; r < 2; ++r)
-                                    w[r] = half_bits<T>(v[2 * r]) | (uint32_t)half_bits<T>(v[2 * r + 1]) << 16;
-                                *reinterpret_cast<u32x2_a2*>(at) = u32x2{w[0], w[1]};
-                            } else {
-#pragma unroll
-                                for (int r = 0; r < 3; ++r)
-                                    if (r < left) at[r] = (T)v[r];
-                            }
-                        }
                     }
                 }
+            if constexpr (END == kDw)
+                columns_out<T, BI, WJ, MJ, NW * 64>(lds, j, rows_left, cols_left,
+                                                    static_cast<T*>(a.out) + j0 * a.out_ld + i0, a.out_ld);
         }
     }
 }
@@ -429,10 +439,10 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
                     c * 8 < left ? ob + u * kRows * ldb + at + c * 16 : kOut, 0, 0, 0);
             }
         };
-        // The step's loads are done (every wave waits for its own), and nobody reads the other buffer.
+        // The step's loads are done (every wave waits for its own) and so are the reads of the other buffer.
         const auto turn = [&] {
             asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
+            __builtin_amdgcn_s_waitcnt(0x0070);      // vmcnt(0) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
@@ -455,81 +465,142 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
     xent_ending<T, WI, WJ, MI, MJ, END>(a, acc, i0, j0, wi, wj, s_0);
 }
 
-// f32.  A step's rows go through registers a step ahead, are cut into their three parts and lie in LDS
-// part by part (64 bytes of a row, chunk ^ (row / 4 % 4)); the product of the first parts has sums of
-// its own, the five smaller ones theirs, so that few of the additions round at the result's size.
-template <int WI, int WJ, int MI, int MJ, int END>
+// f32.  A step's rows go through registers, are cut into their three parts and lie in LDS part by
+// part; the product of the first parts has sums of its own, the five smaller ones theirs, so that few
+// of the additions round at the result's size.
+//
+// An operand may lie with k along its columns (weight for dx, D for dweight): lanes take blocks of
+// elements, H along k by four, and write a row's H side by side.
+//
+// Row r of an operand of B rows has slot r % 4 * (B / 4) + r / 4 of 64 bytes and its chunks turned by r % 4:
+// 16 lanes that read rows one behind the other reach different banks, and so do 8 lanes that write
+// rows r, r + 4, ..., in either form.
+//
+// Cutting a step into parts takes the vector units about as long as its products the matrix units: half
+// of the eight waves do the one while the others do the other.  A tile of few columns waits for
+// memory instead and has two steps on their way.
+template <int WI, int WJ, int MI, int MJ, bool AK, bool BK, int END>
 __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
     constexpr int BI = WI * MI * 32, BJ = WJ * MJ * 32, NW = WI * WJ;
-    constexpr int kRow = kDepthF32 * 2, kRows = 8, kPart = (BI + BJ) * kRow;
-    constexpr int LA = BI / kRows / NW, LB = BJ / kRows / NW;
-    static_assert(BI % (kRows * NW) == 0 && BJ % (kRows * NW) == 0, "rows of a step per wave");
+    constexpr int kRow = kDepthF32 * 2, kPart = (BI + BJ) * kRow;
+    constexpr int LA = BI / 8 / NW, LB = BJ / 8 / NW, kSets = NW == 8 ? 1 : 2;
+    static_assert(!AK || LA == 4, "blocks of four along k");
+    static_assert(!BK || (LB == 2 && NW == 8 && BJ == 128), "blocks of two along k");
     __shared__ __attribute__((aligned(16))) char s_0[3 * kPart];
     __shared__ __attribute__((aligned(16))) char s_1[3 * kPart];
-    const auto turn_of = [](int row) { return row >> 2 & 3; };
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int wi = wave / WJ, wj = wave % WJ, in_load = lane >> 3;
+    const int wi = wave / WJ, wj = wave % WJ, hi = lane >> 3, lo = lane & 7;
     int64_t i0, j0;
     if (!tile_of<BI, BJ>(a, i0, j0)) return;
     const int first = (int)(blockIdx.y * a.per_z), steps = (int)((a.k + kDepthF32 - 1) / kDepthF32);
     const int behind = first + a.per_z < steps ? (int)(first + a.per_z) : steps;
-    const int rows_a = (int)(a.A.rows - i0 < BI ? a.A.rows - i0 : BI);
-    const int rows_b = (int)(a.B.rows - j0 < BJ ? a.B.rows - j0 : BJ);
-    const char* at_a[LA];
-    const char* at_b[LB];
-#pragma unroll
-    for (int u = 0; u < LA; ++u) {      // rows past the last one as that
-        const int r = (wave * LA + u) * kRows + in_load;
-        at_a[u] = a.A.p + i0 * a.A.ld + (r < rows_a ? r : rows_a - 1) * a.A.ld;
-    }
-#pragma unroll
-    for (int u = 0; u < LB; ++u) {
-        const int r = (wave * LB + u) * kRows + in_load;
-        at_b[u] = a.B.p + j0 * a.B.ld + (r < rows_b ? r : rows_b - 1) * a.B.ld;
-    }
-    u32x4 ga[LA], gb[LB];
-    const auto column = [&](int step) { return (int64_t)step * kDepthF32 + (lane & 7) * 4; };
-    const auto fetch = [&](int step) {
-        const int64_t c = column(step);
-#pragma unroll
-        for (int u = 0; u < LA; ++u) ga[u] = load_row(reinterpret_cast<const float*>(at_a[u]), c, a.k);
-#pragma unroll
-        for (int u = 0; u < LB; ++u) gb[u] = load_row(reinterpret_cast<const float*>(at_b[u]), c, a.k);
+    // load u of a wave: rows q / 4 * 32 + q % 4 + 4 hi with q = wave * L + u, four elements of k from 4 lo;
+    // k along the columns: element H hi + u of k (and 16 for the other half of the waves), rows 32 t + 4 lo
+    const auto row_at = [&](const Operand& o, int64_t from, int most, int q) {      // past the last as that
+        const int r = q / 4 * 32 + q % 4 + 4 * hi, rows = (int)(o.rows - from < most ? o.rows - from : most);
+        return o.p + (from + (r < rows ? r : rows - 1)) * o.ld;
     };
-    const auto put_one = [&](char* s, int row, u32x4 raw, int64_t c) {
-        const u32x4 r = settle<float>(raw, c, a.k);
-        uint16_t p[4][3];
+    const char* at_a[AK ? 1 : LA];
+    const char* at_b[BK ? 1 : LB];
+    if constexpr (!AK) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) parts_of(__uint_as_float(r[i]), p[i]);
-        char* at = s + row * kRow + (((lane & 7) >> 1) ^ turn_of(row)) * 16 + (lane & 1) * 8;
+        for (int u = 0; u < LA; ++u) at_a[u] = row_at(a.A, i0, BI, wave * LA + u);
+    }
+    if constexpr (!BK) {
 #pragma unroll
-        for (int n = 0; n < 3; ++n)
-            *reinterpret_cast<u32x2*>(at + n * kPart) =
-                u32x2{p[0][n] | (uint32_t)p[1][n] << 16, p[2][n] | (uint32_t)p[3][n] << 16};
+        for (int u = 0; u < LB; ++u) at_b[u] = row_at(a.B, j0, BJ, wave * LB + u);
+    }
+    const int64_t col_a = i0 + wave * 32 + 4 * lo, col_b = j0 + wave / 2 * 32 + 4 * lo;
+    const int in_a = 4 * hi, in_b = (wave & 1) * 16 + 2 * hi;
+    u32x4 ga[kSets][LA], gb[kSets][LB];
+    const auto load_k = [&](const Operand& o, int64_t col, int64_t k) {
+        const int64_t row = k < a.k ? k : a.k - 1;
+        return load_row(reinterpret_cast<const float*>(o.p + row * o.ld), col < o.rows ? col : o.rows, o.rows);
     };
-    const auto put = [&](char* s, int step) {
-        const int64_t c = step < behind ? column(step) : a.k;      // past the last step: zeros
+    const auto fetch = [&](int set, int step) {
+        const int64_t k = (int64_t)step * kDepthF32;
 #pragma unroll
-        for (int u = 0; u < LA; ++u) put_one(s, (wave * LA + u) * kRows + in_load, ga[u], c);
+        for (int u = 0; u < LA; ++u) {
+            if constexpr (AK)
+                ga[set][u] = load_k(a.A, col_a, k + in_a + u);
+            else
+                ga[set][u] = load_row(reinterpret_cast<const float*>(at_a[u]), k + 4 * lo, a.k);
+        }
 #pragma unroll
-        for (int u = 0; u < LB; ++u) put_one(s + BI * kRow, (wave * LB + u) * kRows + in_load, gb[u], c);
+        for (int u = 0; u < LB; ++u) {
+            if constexpr (BK)
+                gb[set][u] = load_k(a.B, col_b, k + in_b + u);
+            else
+                gb[set][u] = load_row(reinterpret_cast<const float*>(at_b[u]), k + 4 * lo, a.k);
+        }
+    };
+    const auto put_row = [&](char* s, int rows, int q, u32x4 raw, int64_t k) {
+        const u32x4 r = settle<float>(raw, k, a.k);
+        uint32_t p[3], h[3];
+        parts_of(r[0], r[1], p);
+        parts_of(r[2], r[3], h);
+        char* at = s + (q % 4 * (rows / 4) + q / 4 * 8 + hi) * kRow + ((lo >> 1) ^ (q & 3)) * 16 + (lo & 1) * 8;
+#pragma unroll
+        for (int n = 0; n < 3; ++n) *reinterpret_cast<u32x2*>(at + n * kPart) = u32x2{p[n], h[n]};
+    };
+    const auto put = [&](char* s, int set, int step) {      // past the last step: zeros
+        const int64_t k = step < behind ? (int64_t)step * kDepthF32 : a.k;
+        if constexpr (AK) {
+            u32x4 r[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                r[u] = settle<float>(ga[set][u], col_a < a.A.rows ? col_a : a.A.rows, a.A.rows);
+                if (k + in_a + u >= a.k) r[u] = u32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t p[3], h[3];
+                parts_of(r[0][i], r[1][i], p);
+                parts_of(r[2][i], r[3][i], h);
+                char* at = s + (i * (BI / 4) + wave * 8 + lo) * kRow + ((hi >> 1) ^ i) * 16 + (hi & 1) * 8;
+#pragma unroll
+                for (int n = 0; n < 3; ++n) *reinterpret_cast<u32x2*>(at + n * kPart) = u32x2{p[n], h[n]};
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < LA; ++u) put_row(s, BI, wave * LA + u, ga[set][u], k + 4 * lo);
+        }
+        if constexpr (BK) {
+            u32x4 r[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                r[u] = settle<float>(gb[set][u], col_b < a.B.rows ? col_b : a.B.rows, a.B.rows);
+                if (k + in_b + u >= a.k) r[u] = u32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t p[3];
+                parts_of(r[0][i], r[1][i], p);
+                char* at = s + (BI + i * (BJ / 4) + wave / 2 * 8 + lo) * kRow + ((in_b >> 3) ^ i) * 16 + (hi & 3) * 4;
+#pragma unroll
+                for (int n = 0; n < 3; ++n) *reinterpret_cast<uint32_t*>(at + n * kPart) = p[n];
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < LB; ++u) put_row(s + BI * kRow, BJ, wave * LB + u, gb[set][u], k + 4 * lo);
+        }
     };
     f32x16 acc[MI][MJ] = {}, small[MI][MJ] = {};
     const auto products = [&](const char* s) {
-        const char* pa = s + (wi * MI * 32 + (lane & 31)) * kRow;
-        const char* pb = s + (BI + wj * MJ * 32 + (lane & 31)) * kRow;
+        const char* pa = s + ((lane & 3) * (BI / 4) + wi * MI * 8 + (lane & 31) / 4) * kRow;
+        const char* pb = s + (BI + (lane & 3) * (BJ / 4) + wj * MJ * 8 + (lane & 31) / 4) * kRow;
 #pragma unroll
         for (int kk = 0; kk < kDepthF32 / 16; ++kk) {
-            const int slot = ((kk * 2 + (lane >> 5)) ^ turn_of(lane)) * 16;
+            const int slot = ((kk * 2 + (lane >> 5)) ^ (lane & 3)) * 16;
             u32x4 av[3][MI], bv[3][MJ];
 #pragma unroll
             for (int n = 0; n < 3; ++n) {
 #pragma unroll
                 for (int i = 0; i < MI; ++i)
-                    av[n][i] = *reinterpret_cast<const u32x4*>(pa + n * kPart + i * 32 * kRow + slot);
+                    av[n][i] = *reinterpret_cast<const u32x4*>(pa + n * kPart + i * 8 * kRow + slot);
 #pragma unroll
                 for (int j = 0; j < MJ; ++j)
-                    bv[n][j] = *reinterpret_cast<const u32x4*>(pb + n * kPart + j * 32 * kRow + slot);
+                    bv[n][j] = *reinterpret_cast<const u32x4*>(pb + n * kPart + j * 8 * kRow + slot);
             }
 #pragma unroll
             for (int i = 0; i < MI; ++i)
@@ -544,19 +615,28 @@ __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
                 }
         }
     };
-    fetch(first);
-    put(s_0, first);
+    const bool early = NW == 8 && wave < 4;      // of the two waves of a SIMD one
+    const auto one = [&](const char* now, char* next, int set, int step) {
+        if (early) {
+            put(next, set, step + 1);
+            fetch(set, step + 1 + kSets);
+        }
+        products(now);
+        if (!early) {
+            put(next, set, step + 1);
+            fetch(set, step + 1 + kSets);
+        }
+        __syncthreads();
+    };
+    fetch(0, first);
+    put(s_0, 0, first);
+    fetch(1 % kSets, first + 1);
+    if constexpr (kSets == 2) fetch(0, first + 2);
     __syncthreads();
 #pragma unroll 1
     for (int step = first; step < behind; step += 2) {
-        fetch(step + 1);
-        products(s_0);
-        put(s_1, step + 1);
-        __syncthreads();
-        fetch(step + 2);
-        products(s_1);
-        put(s_0, step + 2);
-        __syncthreads();
+        one(s_0, s_1, 1 % kSets, step);
+        one(s_1, s_0, 0, step + 1);
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -569,7 +649,7 @@ __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
 template <typename T, int WI, int WJ, int MI, int MJ, bool STAGED, int END>
 __global__ __launch_bounds__(WI * WJ * 64) void k_xent_product(GemmArgs a) {
     if constexpr (sizeof(T) == 4)
-        xent_product_f32<WI, WJ, MI, MJ, END>(a);
+        xent_product_f32<WI, WJ, MI, MJ, END == kDx, END == kDw, END>(a);
     else
         xent_product<T, WI, WJ, MI, MJ, STAGED, END>(a);
 }
@@ -577,11 +657,12 @@ __global__ __launch_bounds__(WI * WJ * 64) void k_xent_product(GemmArgs a) {
 // ---------------------------------------------------------------- operands laid out
 
 // rows of d elements -> d rows of `wide` (the number of rows rounded up), zeros behind and
-// for the rows that have no target in [0, vocab) (targets NULL: none)
+// for the rows that have no target in [0, vocab) (targets NULL: none); f32: times the row's dloss
 template <typename T>
 __global__ __launch_bounds__(256) void k_xent_transpose(const T* src, int64_t stride, int64_t rows,
                                                         int64_t d, int64_t wide, T* dst,
-                                                        const int64_t* targets, int64_t vocab) {
+                                                        const int64_t* targets, int64_t vocab,
+                                                        const float* dloss) {
     constexpr int kSide = 64;
     __shared__ T s[kSide][kSide + 2];
     const int64_t r0 = (int64_t)blockIdx.x * kSide, c0 = (int64_t)blockIdx.y * kSide;
@@ -600,10 +681,11 @@ __global__ __launch_bounds__(256) void k_xent_transpose(const T* src, int64_t st
         bool kept = r < rows;
         if (kept && targets) kept = targets[r] >= 0 && targets[r] < vocab;
         const u32x4 w = settle<T>(raw[u], c0 + c, d);
+        const float f = sizeof(T) == 4 && kept ? dloss[r] : 1.0f;
 #pragma unroll
         for (int i = 0; i < kVec<T>; ++i) {
             if constexpr (sizeof(T) == 4)
-                s[c + i][n / kPer] = kept ? __uint_as_float(w[i]) : 0.0f;
+                s[c + i][n / kPer] = kept ? __uint_as_float(w[i]) * f : 0.0f;
             else
                 s[c + i][n / kPer] =
                     __builtin_bit_cast(T, (uint16_t)(kept ? w[i / 2] >> (16 * (i & 1)) : 0));
@@ -803,9 +885,9 @@ XentLayout xent_layout(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype, 
         L.hit = take((size_t)rows * 4);
     } else {
         L.xt = take((size_t)d * p.wide_r * n);
-        L.wt = take((size_t)d * p.wide_v * n);
+        if (n == 2) L.wt = take((size_t)d * p.wide_v * n);
         L.d = take((size_t)rows * p.wide_v * n);
-        L.dt = take((size_t)p.piece * p.wide_r * n);
+        if (n == 2) L.dt = take((size_t)p.piece * p.wide_r * n);
         L.sums = take((size_t)p.parts * rows * p.dx_ld * 4);
         L.unit = take(4);
     }
@@ -868,11 +950,10 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         k_xent_unit<<<dim3(1), dim3(1024), 0, s>>>(c.dloss, c.targets, c.rows, c.vocab, unit);
     }
     T* xt = reinterpret_cast<T*>(ws + L.xt);
-    T* wt = reinterpret_cast<T*>(ws + L.wt);
     {
         KernelTimer kt("k_xent_transpose", s);
         k_xent_transpose<T><<<dim3((unsigned)cdiv(p.wide_r, 64), (unsigned)cdiv(c.d, 64)), dim3(256), 0, s>>>(
-            x, c.x_stride, c.rows, c.d, p.wide_r, xt, c.targets, c.vocab);
+            x, c.x_stride, c.rows, c.d, p.wide_r, xt, c.targets, c.vocab, c.dloss);
     }
     for (int64_t v0 = 0; v0 < c.vocab; v0 += p.piece) {
         const int64_t n = c.vocab - v0 < p.piece ? c.vocab - v0 : p.piece, wide = up(n, kDepth);
@@ -897,23 +978,27 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         a.piece_up = wide;
         product<T, kLogits>(a, 1, lies, s);
         // dx += D weight
-        {
-            KernelTimer kt("k_xent_transpose", s);
-            k_xent_transpose<T><<<dim3((unsigned)(wide / 64), (unsigned)cdiv(c.d, 64)), dim3(256), 0, s>>>(
-                rows, c.w_stride, n, c.d, p.wide_v, wt, nullptr, 1);
-        }
         GemmArgs b = a;
-        b.A = Operand{ws + L.wt, c.d, p.wide_v * es};
-        b.B = Operand{ws + L.d, c.rows, a.d_ld};
-        b.k = wide;
         b.out = ws + L.sums;
         b.out_ld = p.dx_ld;
         b.add = v0 > 0;
+        b.B = Operand{ws + L.d, c.rows, a.d_ld};
+        if constexpr (es == 4) {
+            b.A = Operand{reinterpret_cast<const char*>(rows), c.d, c.w_stride * es};
+            b.k = n;
+        } else {
+            T* wt = reinterpret_cast<T*>(ws + L.wt);
+            KernelTimer kt("k_xent_transpose", s);
+            k_xent_transpose<T><<<dim3((unsigned)(wide / 64), (unsigned)cdiv(c.d, 64)), dim3(256), 0, s>>>(
+                rows, c.w_stride, n, c.d, p.wide_v, wt, nullptr, 1, nullptr);
+            b.A = Operand{ws + L.wt, c.d, p.wide_v * es};
+            b.k = wide;
+        }
         product<T, kDx>(b, (int)p.parts, true, s);
         // dweight of the piece
-        b.A = Operand{ws + L.xt, c.d, a.dt_ld};
-        b.B = Operand{ws + L.dt, n, a.dt_ld};
-        b.k = p.wide_r;
+        b.A = Operand{ws + L.xt, c.d, p.wide_r * es};
+        b.B = es == 4 ? Operand{ws + L.d, n, a.d_ld} : Operand{ws + L.dt, n, a.dt_ld};
+        b.k = es == 4 ? c.rows : p.wide_r;
         b.out = static_cast<T*>(c.dweight) + v0 * c.d;
         b.out_ld = c.d;
         product<T, kDw>(b, 1, true, s);
