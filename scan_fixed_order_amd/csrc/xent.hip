@@ -47,7 +47,7 @@ struct GemmArgs {
     Operand A, B;
     int64_t k;            // elements of a row that count
     int64_t ni, nj;       // tiles along i and j
-    int64_t per_z;        // steps of k that a workgroup along z takes
+    int64_t parts, per_part;      // of k, and the steps of one
     float scale;
     // stats, dlogits
     const int64_t* targets;
@@ -144,7 +144,7 @@ __device__ __forceinline__ void columns_out(const char* lds, int j, int left, in
 // What becomes of a tile at (i0, j0): wave (wi, wj)'s sums.  `lds` is free.
 template <typename T, int WI, int WJ, int MI, int MJ, int END>
 __device__ __forceinline__ void xent_ending(const GemmArgs& a, f32x16 (&acc)[MI][MJ], int64_t i0,
-                                            int64_t j0, int wi, int wj, char* lds) {
+                                            int64_t j0, int part, int wi, int wj, char* lds) {
     constexpr int BI = WI * MI * 32, BJ = WJ * MJ * 32, NW = WI * WJ;
     const int lane = threadIdx.x & 63;
     // a lane's values: column wj.. + lane % 32, rows wi.. + 8 (r / 4) + 4 (lane / 32) + r % 4 of the tile
@@ -281,7 +281,7 @@ __device__ __forceinline__ void xent_ending(const GemmArgs& a, f32x16 (&acc)[MI]
                     if constexpr (END == kDw) {
                         column_put<T, BI>(lds, col_in, e, v);
                     } else if (col < cols_left && e < rows_left) {
-                        float* at = static_cast<float*>(a.out) + blockIdx.y * a.B.rows * a.out_ld +
+                        float* at = static_cast<float*>(a.out) + part * a.B.rows * a.out_ld +
                                     (j0 + col) * a.out_ld + i0 + e;      // out_ld: a multiple of 4, room for 4
                         if (a.add) {
                             const f32x4 old = *reinterpret_cast<const f32x4*>(at);
@@ -298,13 +298,16 @@ __device__ __forceinline__ void xent_ending(const GemmArgs& a, f32x16 (&acc)[MI]
     }
 }
 
-// Place of the workgroup's tile.  Workgroup b runs on XCD b % 8: each takes a run of tiles, four along j by
-// as many as follow along i, so that what an XCD holds at a time shares its rows in its L2.
+// Place of the workgroup's tile and its part of k.  Workgroup b runs on XCD b % 8: each takes a run of
+// tiles, four along j by as many as follow along i, of one part of k and then the next, so that what
+// an XCD holds at a time shares its rows in its L2.
 template <int BI, int BJ>
-__device__ __forceinline__ bool tile_of(const GemmArgs& a, int64_t& i0, int64_t& j0) {
-    const int64_t tiles = a.ni * a.nj, per = (tiles + 7) / 8;
-    const int64_t q = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || q >= tiles) return false;
+__device__ __forceinline__ bool tile_of(const GemmArgs& a, int64_t& i0, int64_t& j0, int& part) {
+    const int64_t tiles = a.ni * a.nj, all = tiles * a.parts, per = (all + 7) / 8;
+    int64_t q = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || q >= all) return false;
+    part = a.parts > 1 ? (int)(q / tiles) : 0;
+    q -= part * tiles;
     const int64_t band = q / (4 * a.ni), in_band = q % (4 * a.ni);
     const int64_t wide = a.nj - 4 * band < 4 ? a.nj - 4 * band : 4;
     i0 = in_band / wide * BI;
@@ -331,12 +334,13 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wi = wave / WJ, wj = wave % WJ;
     int64_t i0, j0;
-    if (!tile_of<BI, BJ>(a, i0, j0)) return;
+    int part;
+    if (!tile_of<BI, BJ>(a, i0, j0, part)) return;
     // a load's 8 rows are half of what the turn goes by: every other load's chunks differ
     const int in_load = lane >> 3;
     const int chunk[2] = {(lane & 7) ^ turn_of(in_load), (lane & 7) ^ turn_of(kRows + in_load)};
-    const int first = (int)(blockIdx.y * a.per_z), steps = (int)((a.k + kDepth - 1) / kDepth);
-    const int behind = first + a.per_z < steps ? (int)(first + a.per_z) : steps;
+    const int first = (int)(part * a.per_part), steps = (int)((a.k + kDepth - 1) / kDepth);
+    const int behind = first + a.per_part < steps ? (int)(first + a.per_part) : steps;
     f32x16 acc[MI][MJ] = {};
     const auto products = [&](const char* s) {
         const char* pa = s + (wi * MI * 32 + (lane & 31)) * kRow;
@@ -462,7 +466,7 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
         }
         turn();
     }
-    xent_ending<T, WI, WJ, MI, MJ, END>(a, acc, i0, j0, wi, wj, s_0);
+    xent_ending<T, WI, WJ, MI, MJ, END>(a, acc, i0, j0, part, wi, wj, s_0);
 }
 
 // f32.  A step's rows go through registers, are cut into their three parts and lie in LDS part by
@@ -491,9 +495,10 @@ __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wi = wave / WJ, wj = wave % WJ, hi = lane >> 3, lo = lane & 7;
     int64_t i0, j0;
-    if (!tile_of<BI, BJ>(a, i0, j0)) return;
-    const int first = (int)(blockIdx.y * a.per_z), steps = (int)((a.k + kDepthF32 - 1) / kDepthF32);
-    const int behind = first + a.per_z < steps ? (int)(first + a.per_z) : steps;
+    int part;
+    if (!tile_of<BI, BJ>(a, i0, j0, part)) return;
+    const int first = (int)(part * a.per_part), steps = (int)((a.k + kDepthF32 - 1) / kDepthF32);
+    const int behind = first + a.per_part < steps ? (int)(first + a.per_part) : steps;
     // load u of a wave: rows q / 4 * 32 + q % 4 + 4 hi with q = wave * L + u, four elements of k from 4 lo;
     // k along the columns: element H hi + u of k (and 16 for the other half of the waves), rows 32 t + 4 lo
     const auto row_at = [&](const Operand& o, int64_t from, int most, int q) {      // past the last as that
@@ -642,7 +647,7 @@ __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
     for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < MJ; ++j) acc[i][j] += small[i][j];
-    xent_ending<float, WI, WJ, MI, MJ, END>(a, acc, i0, j0, wi, wj, s_0);
+    xent_ending<float, WI, WJ, MI, MJ, END>(a, acc, i0, j0, part, wi, wj, s_0);
 }
 
 // (The kernel's body is a device function: it uses types that the host's compiler pass lacks.)
@@ -656,11 +661,11 @@ __global__ __launch_bounds__(WI * WJ * 64) void k_xent_product(GemmArgs a) {
 
 // ---------------------------------------------------------------- operands laid out
 
-// rows of d elements -> d rows of `wide` (the number of rows rounded up), zeros behind and
+// rows of d elements -> d rows of `wide` (the number of rows rounded up), ld apart, zeros behind and
 // for the rows that have no target in [0, vocab) (targets NULL: none); f32: times the row's dloss
 template <typename T>
 __global__ __launch_bounds__(256) void k_xent_transpose(const T* src, int64_t stride, int64_t rows,
-                                                        int64_t d, int64_t wide, T* dst,
+                                                        int64_t d, int64_t wide, int64_t ld, T* dst,
                                                         const int64_t* targets, int64_t vocab,
                                                         const float* dloss) {
     constexpr int kSide = 64;
@@ -705,7 +710,7 @@ __global__ __launch_bounds__(256) void k_xent_transpose(const T* src, int64_t st
                 w[i] = __builtin_bit_cast(uint16_t, s[c][r + 2 * i]) |
                        (uint32_t)__builtin_bit_cast(uint16_t, s[c][r + 2 * i + 1]) << 16;
         }
-        *reinterpret_cast<u32x4*>(dst + (c0 + c) * wide + r0 + r) = w;
+        *reinterpret_cast<u32x4*>(dst + (c0 + c) * ld + r0 + r) = w;
     }
 }
 
@@ -720,6 +725,7 @@ __global__ __launch_bounds__(256) void k_xent_rows(const u32x2* stats, const flo
     for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < rows;
          row += (int64_t)gridDim.x * 4) {
         float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
         for (int64_t t = lane; t < tiles; t += 64) {
             const u32x2 one = stats[row * tiles + t];
             const float m = __uint_as_float(one[0]), s = __uint_as_float(one[1]);
@@ -772,6 +778,7 @@ __global__ __launch_bounds__(256) void k_xent_dx(const float* sums, int64_t part
     for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < total; n += (int64_t)gridDim.x * 256) {
         const int64_t row = n / per, c = n % per * 4;
         f32x4 v = *reinterpret_cast<const f32x4*>(sums + row * ld + c);
+#pragma unroll 8
         for (int64_t p = 1; p < parts; ++p)
             v += *reinterpret_cast<const f32x4*>(sums + (p * rows + row) * ld + c);
         const int64_t target = targets[row];
@@ -795,9 +802,10 @@ void product_as(GemmArgs a, int parts, hipStream_t s) {
     constexpr int64_t BI = WI * MI * 32, BJ = WJ * MJ * 32;
     a.ni = cdiv(a.A.rows, BI);
     a.nj = cdiv(a.B.rows, BJ);
-    a.per_z = cdiv(cdiv(a.k, sizeof(T) == 4 ? kDepthF32 : kDepth), parts);
+    a.parts = parts;
+    a.per_part = cdiv(cdiv(a.k, sizeof(T) == 4 ? kDepthF32 : kDepth), parts);
     k_xent_product<T, WI, WJ, MI, MJ, STAGED, END>
-        <<<dim3((unsigned)(cdiv(a.ni * a.nj, 8) * 8), (unsigned)parts), dim3(WI * WJ * 64), 0, s>>>(a);
+        <<<dim3((unsigned)(cdiv(a.ni * a.nj * parts, 8) * 8)), dim3(WI * WJ * 64), 0, s>>>(a);
 }
 
 // Columns (rows of x) of a tile by their number: few need few, and many the width that leaves least of
@@ -842,7 +850,8 @@ void product(const GemmArgs& a, int parts, bool lies, hipStream_t s) {
 
 struct XentPlan {
     int64_t piece;
-    int64_t wide_v, wide_r;      // piece and rows rounded up: zeros behind them
+    int64_t wide_r;              // rows rounded up: zeros behind them
+    int64_t ld_v, ld_r;          // rows of a piece and of the rows, in elements
     int64_t parts, dx_ld, tile_i, tiles;
 };
 
@@ -852,17 +861,22 @@ XentPlan xent_plan(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype) {
     int64_t piece = kPieceCells / (rows > 0 ? rows : 1) / kPieceUnit * kPieceUnit;
     piece = piece < kPieceMin ? kPieceMin : piece > kPieceMax ? kPieceMax : piece;
     p.piece = piece < vocab ? piece : vocab;
-    p.wide_v = up(p.piece, kDepth);
     p.wide_r = up(rows, 32);      // what the narrowest tile writes of D's columns
+    // rows a power of two apart would meet in the same channels of the memory
+    const auto apart = [](int64_t n) { return n % 512 == 0 ? n + kDepth : n; };
+    p.ld_v = apart(up(p.piece, kDepth));
+    p.ld_r = apart(p.wide_r);
     p.dx_ld = up(d, 4);
     const int columns = tile_columns(rows, dtype == DET_F32);
     p.tile_i = tile_rows(columns);
     p.tiles = cdiv(vocab, p.tile_i);
     // workgroups that share dx's sum over a piece where its tiles are few
     const int64_t tiles = cdiv(d, p.tile_i) * cdiv(rows, columns);
-    p.parts = tiles >= 128 ? 1 : cdiv(256, tiles);
-    const int64_t steps = p.wide_v / (dtype == DET_F32 ? kDepthF32 : kDepth);
+    // (256 of them run at a time, of the narrow tiles 1024)
+    p.parts = (columns == 32 ? 1024 : 256) / tiles;
+    const int64_t steps = cdiv(p.piece, dtype == DET_F32 ? kDepthF32 : kDepth);
     if (p.parts > cdiv(steps, 8)) p.parts = cdiv(steps, 8);
+    if (p.parts < 1) p.parts = 1;
     return p;
 }
 
@@ -884,10 +898,10 @@ XentLayout xent_layout(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype, 
         L.stats = take((size_t)rows * p.tiles * 8);
         L.hit = take((size_t)rows * 4);
     } else {
-        L.xt = take((size_t)d * p.wide_r * n);
-        if (n == 2) L.wt = take((size_t)d * p.wide_v * n);
-        L.d = take((size_t)rows * p.wide_v * n);
-        if (n == 2) L.dt = take((size_t)p.piece * p.wide_r * n);
+        L.xt = take((size_t)d * p.ld_r * n);
+        if (n == 2) L.wt = take((size_t)d * p.ld_v * n);
+        L.d = take((size_t)rows * p.ld_v * n);
+        if (n == 2) L.dt = take((size_t)p.piece * p.ld_r * n);
         L.sums = take((size_t)p.parts * rows * p.dx_ld * 4);
         L.unit = take(4);
     }
@@ -953,7 +967,7 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
     {
         KernelTimer kt("k_xent_transpose", s);
         k_xent_transpose<T><<<dim3((unsigned)cdiv(p.wide_r, 64), (unsigned)cdiv(c.d, 64)), dim3(256), 0, s>>>(
-            x, c.x_stride, c.rows, c.d, p.wide_r, xt, c.targets, c.vocab, c.dloss);
+            x, c.x_stride, c.rows, c.d, p.wide_r, p.ld_r, xt, c.targets, c.vocab, c.dloss);
     }
     for (int64_t v0 = 0; v0 < c.vocab; v0 += p.piece) {
         const int64_t n = c.vocab - v0 < p.piece ? c.vocab - v0 : p.piece, wide = up(n, kDepth);
@@ -972,8 +986,8 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         a.k = c.d;
         a.d = ws + L.d;
         a.dt = ws + L.dt;
-        a.d_ld = p.wide_v * es;
-        a.dt_ld = p.wide_r * es;
+        a.d_ld = p.ld_v * es;
+        a.dt_ld = p.ld_r * es;
         a.rows_up = p.wide_r;
         a.piece_up = wide;
         product<T, kLogits>(a, 1, lies, s);
@@ -990,13 +1004,13 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
             T* wt = reinterpret_cast<T*>(ws + L.wt);
             KernelTimer kt("k_xent_transpose", s);
             k_xent_transpose<T><<<dim3((unsigned)(wide / 64), (unsigned)cdiv(c.d, 64)), dim3(256), 0, s>>>(
-                rows, c.w_stride, n, c.d, p.wide_v, wt, nullptr, 1, nullptr);
-            b.A = Operand{ws + L.wt, c.d, p.wide_v * es};
+                rows, c.w_stride, n, c.d, wide, p.ld_v, wt, nullptr, 1, nullptr);
+            b.A = Operand{ws + L.wt, c.d, p.ld_v * es};
             b.k = wide;
         }
         product<T, kDx>(b, (int)p.parts, true, s);
         // dweight of the piece
-        b.A = Operand{ws + L.xt, c.d, p.wide_r * es};
+        b.A = Operand{ws + L.xt, c.d, p.ld_r * es};
         b.B = es == 4 ? Operand{ws + L.d, n, a.d_ld} : Operand{ws + L.dt, n, a.dt_ld};
         b.k = es == 4 ? c.rows : p.wide_r;
         b.out = static_cast<T*>(c.dweight) + v0 * c.d;
