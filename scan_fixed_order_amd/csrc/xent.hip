@@ -96,7 +96,7 @@ enum Ending { kStats, kLogits, kDx, kDw };
 
 // Columns of a tile on their way to rows in memory: a lane holds four elements of a column, whose rows in
 // memory it would write 8 or 16 bytes at a time; through LDS a row's elements leave side by side.
-// (dweight of 30000 entries x 1000 f32, 8 rows: XX us, in pieces of 16 bytes 306: the rows that the
+// (dweight of 30000 entries x 1000 f32, 8 rows: 54 us, in pieces of 16 bytes 306: the rows that the
 // chip has begun and not ended are as large as its caches.)  The 16-byte chunks of a column lie turned by it,
 // so that lanes, a column each, write to different banks.
 template <typename T, int BI>
@@ -360,57 +360,92 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
         }
     };
     if constexpr (STAGED) {
-        // Rows that lie at any element: through registers, a step ahead, rows past the last one as that.
+        // Rows that lie at any element: through registers, a step ahead (a tile of few columns, which waits
+        // for memory, two), rows past the last one as that.  dx reads weight with k along its columns: a
+        // lane takes four elements of k by eight rows of A and writes a row's four side by side.
+        constexpr bool kAcross = END == kDx;
+        constexpr int kSets = NW == 8 ? 1 : 2;
+        static_assert(!kAcross || (BI == 64 && NW == 2), "a wave takes half of a step's k");
         const int rows_a = (int)(a.A.rows - i0 < BI ? a.A.rows - i0 : BI);
         const int rows_b = (int)(a.B.rows - j0 < BJ ? a.B.rows - j0 : BJ);
-        const char* at_a[LA];
+        const char* at_a[kAcross ? 1 : LA];
         const char* at_b[LB];
+        if constexpr (!kAcross) {
 #pragma unroll
-        for (int u = 0; u < LA; ++u) {
-            const int r = (wave * LA + u) * kRows + in_load;
-            at_a[u] = a.A.p + i0 * a.A.ld + (r < rows_a ? r : rows_a - 1) * a.A.ld;
+            for (int u = 0; u < LA; ++u) {
+                const int r = (wave * LA + u) * kRows + in_load;
+                at_a[u] = a.A.p + i0 * a.A.ld + (r < rows_a ? r : rows_a - 1) * a.A.ld;
+            }
         }
 #pragma unroll
         for (int u = 0; u < LB; ++u) {
             const int r = (wave * LB + u) * kRows + in_load;
             at_b[u] = a.B.p + j0 * a.B.ld + (r < rows_b ? r : rows_b - 1) * a.B.ld;
         }
-        u32x4 ga[LA], gb[LB];
+        u32x4 ga[kSets][LA], gb[kSets][LB];
+        const int in_k = (wave * 8 + in_load) * 4, in_a = (lane & 7) * 8;      // kAcross
+        const int64_t col = i0 + in_a < a.A.rows ? i0 + in_a : a.A.rows;
         const auto column = [&](int step, int load) {      // past the last step: k
             return step < behind ? (int64_t)step * kDepth + chunk[load & 1] * 8 : a.k;
         };
-        const auto fetch = [&](int step) {
+        const auto fetch = [&](int set, int step) {
 #pragma unroll
-            for (int u = 0; u < LA; ++u)
-                ga[u] = load_row(reinterpret_cast<const T*>(at_a[u]), column(step, wave * LA + u), a.k);
+            for (int u = 0; u < LA; ++u) {
+                if constexpr (kAcross) {
+                    const int64_t k = (int64_t)step * kDepth + in_k + u, row = k < a.k ? k : a.k - 1;
+                    ga[set][u] = load_row(reinterpret_cast<const T*>(a.A.p + row * a.A.ld), col, a.A.rows);
+                } else {
+                    ga[set][u] = load_row(reinterpret_cast<const T*>(at_a[u]), column(step, wave * LA + u), a.k);
+                }
+            }
 #pragma unroll
             for (int u = 0; u < LB; ++u)
-                gb[u] = load_row(reinterpret_cast<const T*>(at_b[u]), column(step, wave * LB + u), a.k);
+                gb[set][u] = load_row(reinterpret_cast<const T*>(at_b[u]), column(step, wave * LB + u), a.k);
         };
-        const auto put = [&](char* s, int step) {
+        const auto put = [&](char* s, int set, int step) {
+            if constexpr (kAcross) {
+                const int64_t k = step < behind ? (int64_t)step * kDepth + in_k : a.k;
+                u32x4 r[4];
 #pragma unroll
-            for (int u = 0; u < LA; ++u)
-                *reinterpret_cast<u32x4*>(s + (wave * LA + u) * 1024 + lane * 16) =
-                    settle<T>(ga[u], column(step, wave * LA + u), a.k);
+                for (int u = 0; u < 4; ++u) {
+                    r[u] = settle<T>(ga[set][u], col, a.A.rows);
+                    if (k + u >= a.k) r[u] = u32x4{0, 0, 0, 0};
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t half = i & 1 ? 0x07060302u : 0x05040100u;
+                    *reinterpret_cast<u32x2*>(s + (in_a + i) * kRow + ((in_k >> 3) ^ turn_of(in_a + i)) * 16 +
+                                              (in_k & 4) * 2) =
+                        u32x2{__builtin_amdgcn_perm(r[1][i / 2], r[0][i / 2], half),
+                              __builtin_amdgcn_perm(r[3][i / 2], r[2][i / 2], half)};
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < LA; ++u)
+                    *reinterpret_cast<u32x4*>(s + (wave * LA + u) * 1024 + lane * 16) =
+                        settle<T>(ga[set][u], column(step, wave * LA + u), a.k);
+            }
 #pragma unroll
             for (int u = 0; u < LB; ++u)
                 *reinterpret_cast<u32x4*>(s + BI * kRow + (wave * LB + u) * 1024 + lane * 16) =
-                    settle<T>(gb[u], column(step, wave * LB + u), a.k);
+                    settle<T>(gb[set][u], column(step, wave * LB + u), a.k);
         };
-        fetch(first);
-        put(s_0, first);
+        const auto one = [&](const char* now, char* next, int set, int step) {
+            products(now);
+            put(next, set, step + 1);
+            fetch(set, step + 1 + kSets);
+            __syncthreads();
+        };
+        fetch(0, first);
+        put(s_0, 0, first);
+        fetch(1 % kSets, first + 1);
+        if constexpr (kSets == 2) fetch(0, first + 2);
         __syncthreads();
         // past the last step: zeros (settle)
 #pragma unroll 1
         for (int step = first; step < behind; step += 2) {
-            fetch(step + 1);
-            products(s_0);
-            put(s_1, step + 1);
-            __syncthreads();
-            fetch(step + 2);
-            products(s_1);
-            put(s_0, step + 2);
-            __syncthreads();
+            one(s_0, s_1, 1 % kSets, step);
+            one(s_1, s_0, 0, step + 1);
         }
     } else {
         const auto records = [&](const Operand& o, int64_t from, int64_t most) {
@@ -821,7 +856,9 @@ int64_t tile_rows(int columns) { return columns == 32 ? 64 : 256; }
 
 template <typename T, bool STAGED, int END>
 void product_of(const GemmArgs& a, int columns, int parts, hipStream_t s) {
-    if (columns == 32) return product_as<T, 2, 1, 1, 1, STAGED, END>(a, parts, s);
+    if constexpr (sizeof(T) == 4 || END != kDx) {
+        if (columns == 32) return product_as<T, 2, 1, 1, 1, STAGED, END>(a, parts, s);
+    }
     if constexpr (sizeof(T) == 2) {
         if (columns == 256) return product_as<T, 2, 4, 4, 2, STAGED, END>(a, parts, s);
         if (columns == 192) return product_as<T, 4, 2, 2, 3, STAGED, END>(a, parts, s);
@@ -841,7 +878,9 @@ void product(const GemmArgs& a, int parts, bool lies, hipStream_t s) {
             product_as<T, 2, 4, 4, 2, false, END>(a, parts, s);
     } else {
         const int columns = tile_columns(a.B.rows, f32);
-        if constexpr (!f32 && (END == kStats || END == kLogits)) {
+        if constexpr (!f32 && END == kDx) {
+            if (columns == 32) return product_as<T, 2, 1, 1, 1, true, END>(a, parts, s);
+        } else if constexpr (!f32) {
             if (!lies) return product_of<T, true, END>(a, columns, parts, s);
         }
         product_of<T, false, END>(a, columns, parts, s);
@@ -853,6 +892,7 @@ struct XentPlan {
     int64_t wide_r;              // rows rounded up: zeros behind them
     int64_t ld_v, ld_r;          // rows of a piece and of the rows, in elements
     int64_t parts, dx_ld, tile_i, tiles;
+    int64_t wt_rows;             // weight transposed for dx: its d rows, 0: read as it lies
 };
 
 // Vocabulary entries of a piece: D of a piece takes about kPieceCells elements, twice.
@@ -869,6 +909,7 @@ XentPlan xent_plan(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype) {
     p.dx_ld = up(d, 4);
     const int columns = tile_columns(rows, dtype == DET_F32);
     p.tile_i = tile_rows(columns);
+    p.wt_rows = dtype == DET_F32 || columns == 32 ? 0 : d;
     p.tiles = cdiv(vocab, p.tile_i);
     // workgroups that share dx's sum over a piece where its tiles are few
     const int64_t tiles = cdiv(d, p.tile_i) * cdiv(rows, columns);
@@ -899,7 +940,7 @@ XentLayout xent_layout(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype, 
         L.hit = take((size_t)rows * 4);
     } else {
         L.xt = take((size_t)d * p.ld_r * n);
-        if (n == 2) L.wt = take((size_t)d * p.ld_v * n);
+        L.wt = take((size_t)p.wt_rows * p.ld_v * n);
         L.d = take((size_t)rows * p.ld_v * n);
         if (n == 2) L.dt = take((size_t)p.piece * p.ld_r * n);
         L.sums = take((size_t)p.parts * rows * p.dx_ld * 4);
@@ -997,7 +1038,7 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         b.out_ld = p.dx_ld;
         b.add = v0 > 0;
         b.B = Operand{ws + L.d, c.rows, a.d_ld};
-        if constexpr (es == 4) {
+        if (p.wt_rows == 0) {
             b.A = Operand{reinterpret_cast<const char*>(rows), c.d, c.w_stride * es};
             b.k = n;
         } else {
