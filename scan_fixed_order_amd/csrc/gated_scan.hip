@@ -487,15 +487,15 @@ __device__ __forceinline__ void chunk_effect(const ARGS& a, const elem<T>* gate,
 }
 
 template <typename T, bool SIG, int LANES>
-__global__ __launch_bounds__(LANES * kSpans) void k_gated_scan_chunks(ScanArgs a) {
+__global__ __launch_bounds__(LANES * kSpans) void k_gated_scan_chunks(ScanArgs a, int64_t chunk0) {
     chunk_effect<T, SIG, false, LANES>(a, static_cast<const elem<T>*>(a.gate), static_cast<const elem<T>*>(a.x),
-                                blockIdx.y);
+                                chunk0 + blockIdx.y);
 }
 
 template <typename T, bool SIG, int LANES>
-__global__ __launch_bounds__(LANES * kBackSpans) void k_gated_scan_chunks_back(ScanBackArgs a) {
+__global__ __launch_bounds__(LANES * kBackSpans) void k_gated_scan_chunks_back(ScanBackArgs a, int64_t chunk0) {
     chunk_effect<T, SIG, true, LANES>(a, static_cast<const elem<T>*>(a.gate), static_cast<const elem<T>*>(a.dh),
-                               blockIdx.y + 1);
+                               chunk0 + blockIdx.y);
 }
 
 // At most kSteps steps: no spans to compose, a lane takes a vector of channels.
@@ -714,19 +714,55 @@ ScanPlan scan_plan(int64_t batch, int64_t steps, int64_t d, det_dtype dtype, int
     return p;
 }
 
+// A grid holds fewer than 2^32 threads, and 65535 along y.
+constexpr int64_t kGridTiles = 4194303, kGridChunks = 65535;
+
+template <typename T>
+void from_sequence(ScanArgs& a, int64_t b) {
+    const int64_t n = b * a.steps * a.d * (int64_t)sizeof(T);
+    a.gate = static_cast<const char*>(a.gate) + n;
+    a.x = static_cast<const char*>(a.x) + n;
+    a.h = static_cast<char*>(a.h) + n;
+    if (a.state0) a.state0 += b * a.d;
+    if (a.state) a.state += b * a.d;
+    if (a.lengths) a.lengths += b;
+}
+
+template <typename T>
+void from_sequence(ScanBackArgs& a, int64_t b) {
+    const int64_t n = b * a.steps * a.d * (int64_t)sizeof(T);
+    a.dh = static_cast<const char*>(a.dh) + n;
+    a.gate = static_cast<const char*>(a.gate) + n;
+    a.x = static_cast<const char*>(a.x) + n;
+    a.h = static_cast<const char*>(a.h) + n;
+    a.dgate = static_cast<char*>(a.dgate) + n;
+    a.dx = static_cast<char*>(a.dx) + n;
+    if (a.state0) a.state0 += b * a.d;
+    if (a.dstate) a.dstate += b * a.d;
+    if (a.dstate0) a.dstate0 += b * a.d;
+    if (a.lengths) a.lengths += b;
+}
+
 template <typename T, bool SIG, int LANES>
-det_status scan_as(const ScanArgs& a, const ScanPlan& p, hipStream_t s) {
-    const unsigned wgs = (unsigned)(cdiv(p.tiles * a.batch, 8) * 8);
+det_status scan_as(const ScanArgs& all, const ScanPlan& p, hipStream_t s) {
     const dim3 block(LANES * kSpans);
-    if (p.parts > 1) {
-        KernelTimer kt("k_gated_scan_chunks", s);
-        k_gated_scan_chunks<T, SIG, LANES><<<dim3(wgs, (unsigned)(p.chunks - 1)), block, 0, s>>>(a);
+    const int64_t most = kGridTiles / p.tiles;      // sequences of a launch
+    for (int64_t b = 0; b < all.batch; b += most) {
+        ScanArgs a = all;
+        from_sequence<elem<T>>(a, b);
+        a.batch = all.batch - b < most ? all.batch - b : most;
+        const unsigned wgs = (unsigned)(cdiv(p.tiles * a.batch, 8) * 8);
+        for (int64_t k = 0; p.parts > 1 && k < p.chunks - 1; k += kGridChunks) {
+            const int64_t n = p.chunks - 1 - k < kGridChunks ? p.chunks - 1 - k : kGridChunks;
+            KernelTimer kt("k_gated_scan_chunks", s);
+            k_gated_scan_chunks<T, SIG, LANES><<<dim3(wgs, (unsigned)n), block, 0, s>>>(a, k);
+        }
+        KernelTimer kt("k_gated_scan", s);
+        k_gated_scan<T, SIG, LANES><<<dim3(wgs, (unsigned)p.parts), block, 0, s>>>(a);
         const det_status st = launch_status();
         if (st != DET_SUCCESS) return st;
     }
-    KernelTimer kt("k_gated_scan", s);
-    k_gated_scan<T, SIG, LANES><<<dim3(wgs, (unsigned)p.parts), block, 0, s>>>(a);
-    return launch_status();
+    return DET_SUCCESS;
 }
 
 template <typename T, bool SIG>
@@ -744,18 +780,25 @@ det_status scan_typed(const ScanArgs& a, const ScanPlan& p, hipStream_t s) {
 }
 
 template <typename T, bool SIG, int LANES>
-det_status scan_back_as(const ScanBackArgs& a, const ScanPlan& p, hipStream_t s) {
-    const unsigned wgs = (unsigned)(cdiv(p.tiles * a.batch, 8) * 8);
+det_status scan_back_as(const ScanBackArgs& all, const ScanPlan& p, hipStream_t s) {
     const dim3 block(LANES * kBackSpans);
-    if (p.parts > 1) {
-        KernelTimer kt("k_gated_scan_chunks_back", s);
-        k_gated_scan_chunks_back<T, SIG, LANES><<<dim3(wgs, (unsigned)(p.chunks - 1)), block, 0, s>>>(a);
+    const int64_t most = kGridTiles / p.tiles;
+    for (int64_t b = 0; b < all.batch; b += most) {
+        ScanBackArgs a = all;
+        from_sequence<elem<T>>(a, b);
+        a.batch = all.batch - b < most ? all.batch - b : most;
+        const unsigned wgs = (unsigned)(cdiv(p.tiles * a.batch, 8) * 8);
+        for (int64_t k = 1; p.parts > 1 && k < p.chunks; k += kGridChunks) {
+            const int64_t n = p.chunks - k < kGridChunks ? p.chunks - k : kGridChunks;
+            KernelTimer kt("k_gated_scan_chunks_back", s);
+            k_gated_scan_chunks_back<T, SIG, LANES><<<dim3(wgs, (unsigned)n), block, 0, s>>>(a, k);
+        }
+        KernelTimer kt("k_gated_scan_backward", s);
+        k_gated_scan_backward<T, SIG, LANES><<<dim3(wgs, (unsigned)p.parts), block, 0, s>>>(a);
         const det_status st = launch_status();
         if (st != DET_SUCCESS) return st;
     }
-    KernelTimer kt("k_gated_scan_backward", s);
-    k_gated_scan_backward<T, SIG, LANES><<<dim3(wgs, (unsigned)p.parts), block, 0, s>>>(a);
-    return launch_status();
+    return DET_SUCCESS;
 }
 
 template <typename T, bool SIG>

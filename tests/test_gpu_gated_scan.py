@@ -200,3 +200,54 @@ def test_autograd_paths(dev):
     r = det.det_gated_scan(gate, x, None, True)
     want = det.det_gated_scan_backward(torch.ones_like(x), gate, x, r.h, None, None, True)
     assert same_bits(a.grad, want[0]) and same_bits(b.grad, want[1])
+
+
+def since_reset(x, reset):
+    """Sums of x from the last reset on, whole numbers."""
+    total = x.cumsum(0)
+    at = torch.where(reset, torch.arange(len(x), device=x.device), torch.zeros_like(x)).cummax(0).values
+    return total - total[at] + x[at]
+
+
+def test_more_chunks_than_a_grid_holds(dev):
+    """Whole numbers and gates of 0 and 1, so that every sum is exact; more than 2 * 65535 chunks."""
+    n = 65536 * 128 + 77
+    gate = torch.ones(n, device=dev)
+    gate[torch.randint(0, n, (200,), generator=torch.Generator().manual_seed(1)).to(dev)] = 0
+    x = torch.randint(-1, 2, (n,), generator=torch.Generator().manual_seed(2)).to(dev)
+    dh = torch.zeros(n, dtype=torch.int64, device=dev)
+    dh[::1009] = 1 - x[::1009]
+    h = since_reset(x, gate == 0)
+    got = det.det_gated_scan(gate.view(1, n, 1), x.float().view(1, n, 1))
+    assert torch.equal(got.h.view(-1), h.float()) and got.state.item() == h[-1].item()
+    resets = torch.cat([torch.ones(1, device=dev), gate.flip(0)[:-1]]) == 0
+    g = since_reset(dh.flip(0), resets).flip(0)
+    before = torch.cat([h.new_zeros(1), h[:-1]])
+    assert (g * before).abs().max() < 2 ** 24
+    dgate, dx, first = det.det_gated_scan_backward(dh.float().view(1, n, 1), gate.view(1, n, 1),
+                                                   x.float().view(1, n, 1), got.h)
+    assert torch.equal(dx.view(-1), g.float()) and torch.equal(dgate.view(-1), (g * before).float())
+
+
+def test_more_sequences_than_a_grid_holds(dev):
+    batch, steps = (1 << 22) + 5, 9
+    gate = torch.randint(0, 2, (batch, steps, 1), generator=torch.Generator().manual_seed(3)).to(dev)
+    x = torch.randint(-3, 4, (batch, steps, 1), generator=torch.Generator().manual_seed(4)).to(dev)
+    lens = torch.arange(batch, dtype=torch.int32, device=dev) % 10
+    state = x[:, 0] * 2
+    h, now = torch.empty_like(x), state
+    for i in range(steps):
+        live = (i < lens)[:, None]
+        now = torch.where(live, gate[:, i] * now + x[:, i], now)
+        h[:, i] = torch.where(live, now, 0)
+    got = det.det_gated_scan(gate.half(), x.half(), state.float(), lengths=lens)
+    assert torch.equal(got.h, h.half()) and torch.equal(got.state, now.float())
+    dgate, dx, first = det.det_gated_scan_backward(x.half(), gate.half(), x.half(), got.h, state.float(),
+                                                   state.float(), lengths=lens)
+    e, before = state, torch.cat([state[:, None], h[:, :-1]], 1)
+    for i in reversed(range(steps)):
+        live = (i < lens)[:, None]
+        g = torch.where(live, x[:, i] + e, 0)
+        assert torch.equal(dx[:, i], g.half()) and torch.equal(dgate[:, i], (g * before[:, i]).half())
+        e = torch.where(live, gate[:, i] * g, e)
+    assert torch.equal(first, e.float())
