@@ -16,7 +16,7 @@ namespace {
 constexpr int64_t kBlockRows = 64;          // positions a block of the gradient's sums
 constexpr int64_t kChunk = 1024;            // tokens that a workgroup sorts
 constexpr int64_t kChunkSortMax = 65536;    // tokens sorted by chunks; more go through the radix sort
-constexpr int kSlabChunks = 8;              // chunks that a step of the ranking holds in LDS
+constexpr int kGroup = 4;                   // chunks that a wave of the ranking holds in LDS
 constexpr int64_t kSlab = 64;               // vectors of a row that a wave takes: one a lane
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -130,39 +130,54 @@ __global__ __launch_bounds__(1024) void k_sort_chunks(const void* tokens, bool w
 }
 
 // Place of every token among all: its place in its chunk, and the tokens before it in the others:
-// up to its own number in earlier chunks, below it in later ones.  A wave takes 64 tokens and searches
-// eight chunks at a time in LDS (32768 tokens: XX us, with 256 tokens a workgroup 17).
-__global__ __launch_bounds__(64) void k_rank_tokens(const uint32_t* tok, const uint32_t* pos,
-                                                    int64_t n, uint32_t* keys, uint32_t* src) {
-    __shared__ uint32_t s_tok[kSlabChunks * kChunk];
-    const int64_t e = (int64_t)blockIdx.x * 64 + threadIdx.x;      // of the padded length
-    const int chunks = (int)((n + kChunk - 1) / kChunk), own = (int)(e / kChunk);
+// up to its own number in earlier chunks, below it in later ones.  A workgroup takes 64 tokens; each of
+// its waves searches every fourth group of four chunks, in LDS of its own, whose loads are all in flight
+// at once (32768 tokens: RANK us; one wave, eight chunks at a time, 14).
+__global__ __launch_bounds__(256) void k_rank_tokens(const uint32_t* tok, const uint32_t* pos,
+                                                     int64_t n, uint32_t* keys, uint32_t* src) {
+    constexpr int kWaves = 4, kLoads = kGroup * (int)kChunk / 256;
+    __shared__ __attribute__((aligned(16))) uint32_t s_group[kWaves][kGroup * kChunk];
+    __shared__ uint32_t s_before[kWaves][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t e = (int64_t)blockIdx.x * 64 + lane;      // of the padded length
+    const int chunks = (int)((n + kChunk - 1) / kChunk), own = (int)((int64_t)blockIdx.x * 64 / kChunk);
     const uint32_t id = tok[e];
-    uint32_t place = (uint32_t)(e % kChunk);
-    for (int c0 = 0; c0 < chunks; c0 += kSlabChunks) {
-        const int here = chunks - c0 < kSlabChunks ? chunks - c0 : kSlabChunks;
-        __syncthreads();
-#pragma unroll 8
-        for (int k = threadIdx.x; k < here * (int)kChunk / 4; k += 64)
-            *reinterpret_cast<u32x4*>(s_tok + 4 * k) =
-                *reinterpret_cast<const u32x4*>(tok + (int64_t)c0 * kChunk + 4 * k);
-        __syncthreads();
-        uint32_t at[kSlabChunks] = {};
+    uint32_t* const s_tok = s_group[wave];
+    uint32_t before = 0;
+    for (int c0 = wave * kGroup; c0 < chunks; c0 += kWaves * kGroup) {
+        u32x4 raw[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {      // chunks past the last one as that
+            const int c = c0 + u * kGroup / kLoads < chunks ? c0 + u * kGroup / kLoads : chunks - 1;
+            raw[u] = *reinterpret_cast<const u32x4*>(tok + (int64_t)c * kChunk + u % (kLoads / kGroup) * 256 +
+                                                     lane * 4);
+        }
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) *reinterpret_cast<u32x4*>(s_tok + u * 256 + lane * 4) = raw[u];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        uint32_t at[kGroup] = {};
 #pragma unroll
         for (int step = kChunk / 2; step > 0; step /= 2)
 #pragma unroll
-            for (int c = 0; c < kSlabChunks; ++c) {
+            for (int c = 0; c < kGroup; ++c) {
                 const uint32_t bound = id + (c0 + c < own ? 1u : 0u);
                 if (s_tok[c * kChunk + at[c] + step - 1] < bound) at[c] += step;
             }
 #pragma unroll
-        for (int c = 0; c < kSlabChunks; ++c) {
+        for (int c = 0; c < kGroup; ++c) {
             const uint32_t bound = id + (c0 + c < own ? 1u : 0u);
             if (s_tok[c * kChunk + at[c]] < bound) at[c] += 1;
-            if (c < here && c0 + c != own) place += at[c];
+            if (c0 + c < chunks && c0 + c != own) before += at[c];
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
-    if (id != 0xFFFFFFFFu) {
+    s_before[wave][lane] = before;
+    __syncthreads();
+    if (wave == 0 && id != 0xFFFFFFFFu) {
+        const uint32_t place = (uint32_t)(e % kChunk) + s_before[0][lane] + s_before[1][lane] +
+                               s_before[2][lane] + s_before[3][lane];
         keys[place] = id;
         src[place] = pos[e];
     }
@@ -212,7 +227,7 @@ __device__ __forceinline__ int64_t block_slot(int64_t p, bool first) {
 template <typename T>
 __device__ __forceinline__ void add_rows(const EmbedBackArgs& a, int64_t begin, int64_t end,
                                          int64_t c, float (&acc)[kVec<T>]) {
-    constexpr int kAhead = 8;      // rows in flight
+    constexpr int kAhead = 16;      // rows in flight
     const int lane = threadIdx.x & 63, count = (int)(end - begin);
     const uint32_t mine = a.src[begin + (lane < count ? lane : count - 1)];
     const T* rows = static_cast<const T*>(a.dout);
@@ -276,7 +291,7 @@ constexpr int kVocabRows = 8;
 
 template <typename T>
 __device__ __forceinline__ void sum_rows(const EmbedBackArgs& a, int64_t item) {
-    constexpr int kAhead = 8;      // rows of dout in flight
+    constexpr int kAhead = 16;      // rows of dout in flight
     const int lane = threadIdx.x & 63;
     const int64_t v0 = item / a.slabs * kVocabRows, c = (item % a.slabs * kSlab + lane) * kVec<T>;
     const int64_t bound = v0 + lane < a.vocab ? v0 + lane : a.vocab;
@@ -483,9 +498,14 @@ det_status embedding_backward_launch(const EmbedBackCall& c, void* ws, hipStream
                 k_sort_chunks<<<dim3((unsigned)chunks), dim3(kChunk), 0, s>>>(c.tokens, c.wide, c.n,
                                                                              c.vocab, tok, pos);
             }
+        }
+        if (chunks > 1) {
             KernelTimer kt("k_rank_tokens", s);
-            k_rank_tokens<<<dim3((unsigned)(chunks * kChunk / 64)), dim3(64), 0, s>>>(
+            k_rank_tokens<<<dim3((unsigned)(chunks * kChunk / 64)), dim3(256), 0, s>>>(
                 tok, pos, c.n, keys, src);
+        } else {      // in order already
+            keys = tok;
+            src = pos;
         }
         int64_t g = cdiv(c.vocab + 1, 256);
         if (g > kGridMax) g = kGridMax;
