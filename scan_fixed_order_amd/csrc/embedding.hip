@@ -132,7 +132,7 @@ __global__ __launch_bounds__(1024) void k_sort_chunks(const void* tokens, bool w
 // Place of every token among all: its place in its chunk, and the tokens before it in the others:
 // up to its own number in earlier chunks, below it in later ones.  A workgroup takes 64 tokens; each of
 // its waves searches every fourth group of four chunks, in LDS of its own, whose loads are all in flight
-// at once (32768 tokens: RANK us; one wave, eight chunks at a time, 14).
+// at once (32768 tokens: 6.4 us; one wave, eight chunks at a time, 14).
 __global__ __launch_bounds__(256) void k_rank_tokens(const uint32_t* tok, const uint32_t* pos,
                                                      int64_t n, uint32_t* keys, uint32_t* src) {
     constexpr int kWaves = 4, kLoads = kGroup * (int)kChunk / 256;
@@ -227,7 +227,7 @@ __device__ __forceinline__ int64_t block_slot(int64_t p, bool first) {
 template <typename T>
 __device__ __forceinline__ void add_rows(const EmbedBackArgs& a, int64_t begin, int64_t end,
                                          int64_t c, float (&acc)[kVec<T>]) {
-    constexpr int kAhead = 16;      // rows in flight
+    constexpr int kAhead = 8;      // rows in flight
     const int lane = threadIdx.x & 63, count = (int)(end - begin);
     const uint32_t mine = a.src[begin + (lane < count ? lane : count - 1)];
     const T* rows = static_cast<const T*>(a.dout);
@@ -291,7 +291,7 @@ constexpr int kVocabRows = 8;
 
 template <typename T>
 __device__ __forceinline__ void sum_rows(const EmbedBackArgs& a, int64_t item) {
-    constexpr int kAhead = 16;      // rows of dout in flight
+    constexpr int kAhead = 8;      // rows of dout in flight
     const int lane = threadIdx.x & 63;
     const int64_t v0 = item / a.slabs * kVocabRows, c = (item % a.slabs * kSlab + lane) * kVec<T>;
     const int64_t bound = v0 + lane < a.vocab ? v0 + lane : a.vocab;
@@ -370,21 +370,30 @@ __global__ __launch_bounds__(256) void k_embedding_join(EmbedBackArgs a, int64_t
             if (begin != range * kBlockRows + at || c >= a.d) continue;
             const uint32_t v = a.keys[begin];
             double sum[kVec<T>] = {};
-#pragma unroll 8
-            for (int64_t p = begin; p < stop; p += kBlockRows) {
-                const float* part = a.part + block_slot(p, p == begin) * a.d + c;
-                if (c + kVec<T> <= a.d) {
+            if (c + kVec<T> <= a.d) {
+                constexpr int kAhead = 8;      // blocks in flight
+                for (int64_t p0 = begin; p0 < stop; p0 += kAhead * kBlockRows) {
+                    f32x4 q[kAhead][kVec<T> / 4];
 #pragma unroll
-                    for (int i = 0; i < kVec<T>; i += 4) {
-                        const f32x4 q = *reinterpret_cast<const f32x4_a4*>(part + i);
+                    for (int u = 0; u < kAhead; ++u) {      // past the last block the first again
+                        const int64_t p = p0 + u * kBlockRows < stop ? p0 + u * kBlockRows : begin;
+                        const float* part = a.part + block_slot(p, p == begin) * a.d + c;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sum[i + e] += (double)q[e];
+                        for (int i = 0; i < kVec<T> / 4; ++i)
+                            q[u][i] = *reinterpret_cast<const f32x4_a4*>(part + 4 * i);
                     }
-                } else {
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u)
+                        if (p0 + u * kBlockRows < stop) {
+#pragma unroll
+                            for (int i = 0; i < kVec<T>; ++i) sum[i] += (double)q[u][i / 4][i % 4];
+                        }
+                }
+            } else {
+                for (int64_t p = begin; p < stop; p += kBlockRows)
 #pragma unroll
                     for (int i = 0; i < kVec<T>; ++i)
-                        if (c + i < a.d) sum[i] += (double)part[i];
-                }
+                        if (c + i < a.d) sum[i] += (double)a.part[block_slot(p, p == begin) * a.d + c + i];
             }
             float acc[kVec<T>];
 #pragma unroll
