@@ -787,13 +787,13 @@ __global__ __launch_bounds__(256) void k_xent_zero(uint16_t* p, int64_t n) {
         p[i] = 0;
 }
 
-// the largest |dloss| of the rows that count (f16)
+// the largest |dloss| of the rows that count (f16); infinite where one is NaN, so that dweight is NaN
 __global__ __launch_bounds__(1024) void k_xent_unit(const float* dloss, const int64_t* targets,
                                                     int64_t rows, int64_t vocab, float* unit) {
     __shared__ float s[16];
     float m = 0.0f;
     for (int64_t r = threadIdx.x; r < rows; r += 1024)
-        if (targets[r] >= 0 && targets[r] < vocab) m = fmaxf(m, fabsf(dloss[r]));
+        if (targets[r] >= 0 && targets[r] < vocab) m = fmaxf(m, dloss[r] != dloss[r] ? INFINITY : fabsf(dloss[r]));
     m = wave_max(m);
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = m;
     __syncthreads();

@@ -201,3 +201,23 @@ def test_gradient_against_differences(dev):
         got = float((v.grad.double() * step).sum())
         size = float((v.grad.double() * step).abs().sum())
         assert abs(got - slope) <= 1e-5 * size + 1e-6, (n, got, slope)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("rows,vocab,d", [(3, 70001, 8), (40, 66000, 5), (150, 131100, 12), (1100, 61500, 8)])
+def test_vocabularies_of_several_pieces(dev, rows, vocab, d, t):
+    test_loss_and_gradients(dev, rows, vocab, d, t, 1.0)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_loss_gradient_that_is_not_finite_shows(dev, t, bad):
+    """In its own row of dx, and in all that it adds to."""
+    x, w, at = inputs(20, 300, 16, t, dev, 2)
+    at[3] = 5
+    f = det.det_linear_cross_entropy(x, w, at)
+    dl = torch.ones(20, device=dev)
+    dl[3] = bad
+    dx, dw = det.det_linear_cross_entropy_backward(x, w, at, f.lse, dl)
+    assert not torch.isfinite(dx[3]).any() and torch.isfinite(torch.cat([dx[:3], dx[4:]])).all()
+    assert not torch.isfinite(dw).any()

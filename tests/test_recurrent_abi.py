@@ -252,3 +252,11 @@ def test_workspaces_without_memory_of_their_own(call):
                torch.empty(1 << 21, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError, match="workspace must be contiguous"):
             call(ws)
+
+
+def test_gated_scan_takes_rows_up_to_a_width():
+    wide = 4194303      # DET_SCAN_MAX_CHANNELS
+    for call, size in ((scan, det.lib().det_gated_scan_workspace_size),
+                       (scan_back, det.lib().det_gated_scan_backward_workspace_size)):
+        refused(call, TOO_LARGE, [dict(batch=1, d=wide + 1)])
+        assert size(1, 8, wide, BF16) > 0 and size(1, 8, wide + 1, BF16) == 0
