@@ -92,6 +92,28 @@ __device__ __forceinline__ uint16_t half_bits(float v) {
     return __builtin_bit_cast(uint16_t, (H)v);
 }
 
+// A vector of a row, in `load_row`'s and `settle`'s two steps where it may reach past the row's end.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ u32x4 fetch_vec(const T* row, int64_t c, int64_t n) {
+    if constexpr (WHOLE)
+        return load_vec(row + c);
+    else
+        return load_row(row, c, n);
+}
+template <bool WHOLE, typename T>
+__device__ __forceinline__ u32x4 settle_vec(u32x4 raw, int64_t c, int64_t n) {
+    if constexpr (WHOLE)
+        return raw;
+    else
+        return settle<T>(raw, c, n);
+}
+struct Whole {
+    static constexpr bool value = true;
+};
+struct Partial {
+    static constexpr bool value = false;
+};
+
 enum Ending { kStats, kLogits, kDx, kDw };
 
 // Columns of a tile on their way to rows in memory: a lane holds four elements of a column, whose rows in
@@ -411,21 +433,35 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
         const auto column = [&](int step, int load) {      // past the last step: k
             return step < behind ? (int64_t)step * kDepth + chunk[load & 1] * 8 : a.k;
         };
-        const auto fetch = [&](int set, int step) {
+        // nearly every step is whole, and its vectors need no care (517 x 50021 x 1002 f16 107 -> 100 us; with k
+        // along the columns the second form of it costs more than it gives, 77 -> 80 for 8 x 30000 x 1000)
+        const auto whole = [&](int step) {
+            return !kAcross && step < behind && (int64_t)(step + 1) * kDepth <= a.k;
+        };
+        const auto fetch_as = [&](auto as, int set, int step) {
+            constexpr bool W = decltype(as)::value;
 #pragma unroll
             for (int u = 0; u < LA; ++u) {
                 if constexpr (kAcross) {
                     const int64_t k = (int64_t)step * kDepth + in_k + u, row = k < a.k ? k : a.k - 1;
                     ga[set][u] = load_row(reinterpret_cast<const T*>(a.A.p + row * a.A.ld), col, a.A.rows);
                 } else {
-                    ga[set][u] = load_row(reinterpret_cast<const T*>(at_a[u]), column(step, wave * LA + u), a.k);
+                    ga[set][u] =
+                        fetch_vec<W>(reinterpret_cast<const T*>(at_a[u]), column(step, wave * LA + u), a.k);
                 }
             }
 #pragma unroll
             for (int u = 0; u < LB; ++u)
-                gb[set][u] = load_row(reinterpret_cast<const T*>(at_b[u]), column(step, wave * LB + u), a.k);
+                gb[set][u] = fetch_vec<W>(reinterpret_cast<const T*>(at_b[u]), column(step, wave * LB + u), a.k);
         };
-        const auto put = [&](char* s, int set, int step) {
+        const auto fetch = [&](int set, int step) {
+            if (whole(step))
+                fetch_as(Whole{}, set, step);
+            else
+                fetch_as(Partial{}, set, step);
+        };
+        const auto put_as = [&](auto as, char* s, int set, int step) {
+            constexpr bool W = decltype(as)::value;
             if constexpr (kAcross) {
                 const int64_t k = step < behind ? (int64_t)step * kDepth + in_k : a.k;
                 u32x4 r[4];
@@ -446,12 +482,18 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
 #pragma unroll
                 for (int u = 0; u < LA; ++u)
                     *reinterpret_cast<u32x4*>(s + (wave * LA + u) * 1024 + lane * 16) =
-                        settle<T>(ga[set][u], column(step, wave * LA + u), a.k);
+                        settle_vec<W, T>(ga[set][u], column(step, wave * LA + u), a.k);
             }
 #pragma unroll
             for (int u = 0; u < LB; ++u)
                 *reinterpret_cast<u32x4*>(s + BI * kRow + (wave * LB + u) * 1024 + lane * 16) =
-                    settle<T>(gb[set][u], column(step, wave * LB + u), a.k);
+                    settle_vec<W, T>(gb[set][u], column(step, wave * LB + u), a.k);
+        };
+        const auto put = [&](char* s, int set, int step) {
+            if (whole(step))
+                put_as(Whole{}, s, set, step);
+            else
+                put_as(Partial{}, s, set, step);
         };
         const auto one = [&](const char* now, char* next, int set, int step) {
             products(now);
@@ -574,29 +616,41 @@ __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
     const int64_t col_a = i0 + wave * 32 + 4 * lo, col_b = j0 + wave / 2 * 32 + 4 * lo;
     const int in_a = 4 * hi, in_b = (wave & 1) * 16 + 2 * hi;
     u32x4 ga[kSets][LA], gb[kSets][LB];
+    // nearly every step is whole, and its vectors need no care (8 x 30000 x 1000 50 -> 42 us, 600 rows 265 ->
+    // 242; with k along the columns nothing gained)
+    const auto whole = [&](int step) {
+        return !AK && !BK && step < behind && (int64_t)(step + 1) * kDepthF32 <= a.k;
+    };
     const auto load_k = [&](const Operand& o, int64_t col, int64_t k) {
         const int64_t row = k < a.k ? k : a.k - 1;
         return load_row(reinterpret_cast<const float*>(o.p + row * o.ld), col < o.rows ? col : o.rows, o.rows);
     };
-    const auto fetch = [&](int set, int step) {
+    const auto fetch_as = [&](auto as, int set, int step) {
+        constexpr bool W = decltype(as)::value;
         const int64_t k = (int64_t)step * kDepthF32;
 #pragma unroll
         for (int u = 0; u < LA; ++u) {
             if constexpr (AK)
                 ga[set][u] = load_k(a.A, col_a, k + in_a + u);
             else
-                ga[set][u] = load_row(reinterpret_cast<const float*>(at_a[u]), k + 4 * lo, a.k);
+                ga[set][u] = fetch_vec<W>(reinterpret_cast<const float*>(at_a[u]), k + 4 * lo, a.k);
         }
 #pragma unroll
         for (int u = 0; u < LB; ++u) {
             if constexpr (BK)
                 gb[set][u] = load_k(a.B, col_b, k + in_b + u);
             else
-                gb[set][u] = load_row(reinterpret_cast<const float*>(at_b[u]), k + 4 * lo, a.k);
+                gb[set][u] = fetch_vec<W>(reinterpret_cast<const float*>(at_b[u]), k + 4 * lo, a.k);
         }
     };
-    const auto put_row = [&](char* s, int rows, int q, u32x4 raw, int64_t k) {
-        const u32x4 r = settle<float>(raw, k, a.k);
+    const auto fetch = [&](int set, int step) {
+        if (whole(step))
+            fetch_as(Whole{}, set, step);
+        else
+            fetch_as(Partial{}, set, step);
+    };
+    const auto put_row = [&](auto as, char* s, int rows, int q, u32x4 raw, int64_t k) {
+        const u32x4 r = settle_vec<decltype(as)::value, float>(raw, k, a.k);
         uint32_t p[3], h[3];
         parts_of(r[0], r[1], p);
         parts_of(r[2], r[3], h);
@@ -604,8 +658,9 @@ __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
 #pragma unroll
         for (int n = 0; n < 3; ++n) *reinterpret_cast<u32x2*>(at + n * kPart) = u32x2{p[n], h[n]};
     };
-    const auto put = [&](char* s, int set, int step) {      // past the last step: zeros
-        const int64_t k = step < behind ? (int64_t)step * kDepthF32 : a.k;
+    const auto put_as = [&](auto as, char* s, int set, int step) {      // past the last step: zeros
+        constexpr bool W = decltype(as)::value;
+        const int64_t k = W || step < behind ? (int64_t)step * kDepthF32 : a.k;
         if constexpr (AK) {
             u32x4 r[4];
 #pragma unroll
@@ -624,7 +679,7 @@ __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
             }
         } else {
 #pragma unroll
-            for (int u = 0; u < LA; ++u) put_row(s, BI, wave * LA + u, ga[set][u], k + 4 * lo);
+            for (int u = 0; u < LA; ++u) put_row(as, s, BI, wave * LA + u, ga[set][u], k + 4 * lo);
         }
         if constexpr (BK) {
             u32x4 r[2];
@@ -643,8 +698,14 @@ __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
             }
         } else {
 #pragma unroll
-            for (int u = 0; u < LB; ++u) put_row(s + BI * kRow, BJ, wave * LB + u, gb[set][u], k + 4 * lo);
+            for (int u = 0; u < LB; ++u) put_row(as, s + BI * kRow, BJ, wave * LB + u, gb[set][u], k + 4 * lo);
         }
+    };
+    const auto put = [&](char* s, int set, int step) {
+        if (whole(step))
+            put_as(Whole{}, s, set, step);
+        else
+            put_as(Partial{}, s, set, step);
     };
     f32x16 acc[MI][MJ] = {}, small[MI][MJ] = {};
     const auto products = [&](const char* s) {
