@@ -344,7 +344,8 @@ __device__ __forceinline__ float enter(const ARGS& a, const Place& p, const floa
 }
 
 // A workgroup walks chunks of 64 (or 32) words of channels, the next two chunks' words in flight while
-// this one's effects go round.  One pass over gate and x: bound by HBM.
+// this one's effects go round.  One pass over gate and x: bound by HBM.  8 x 2048 x 4096 bf16 88 us (403 MB,
+// 4.6 TB/s), 3 x 10007 x 2500 f32 183 (901 MB, 4.9; rows that are no whole number of lines).
 template <typename T, bool SIG, int LANES>
 __global__ __launch_bounds__(LANES * kSpans) void k_gated_scan(ScanArgs a) {
     constexpr int E = kCh<T>, CH = LANES * E, kChunkSteps = kSteps * kSpans, kMine = kSteps * 64 / LANES;
@@ -498,7 +499,8 @@ __global__ __launch_bounds__(LANES * kBackSpans) void k_gated_scan_chunks_back(S
                                chunk0 + blockIdx.y);
 }
 
-// At most kSteps steps: no spans to compose, a lane takes a vector of channels.
+// At most kSteps steps: no spans to compose, a lane takes a vector of channels.  One step of 64 x 4096 bf16
+// 3.5 us, a load's latency and a store's.
 template <typename T, bool SIG>
 __global__ __launch_bounds__(256) void k_gated_scan_steps(ScanArgs a) {
     constexpr int V = kVec<T>;
@@ -556,7 +558,8 @@ __device__ __forceinline__ void read_before(const ScanBackArgs& a, const Place& 
     }
 }
 
-// As k_gated_scan from the last step on.
+// As k_gated_scan from the last step on.  8 x 2048 x 4096 bf16 160 us: 821 MB at 5.1 TB/s, h read a step before
+// dh, gate and x.
 template <typename T, bool SIG, int LANES>
 __global__ __launch_bounds__(LANES * kBackSpans) void k_gated_scan_backward(ScanBackArgs a) {
     constexpr int E = kCh<T>, CH = LANES * E, kChunkSteps = kSteps * kBackSpans;

@@ -341,7 +341,14 @@ __device__ __forceinline__ bool tile_of(const GemmArgs& a, int64_t& i0, int64_t&
 // straight to LDS, two steps in turn: 8 rows of 128 bytes a load, whose 16-byte chunks lie in the order
 // chunk ^ (row / 2 % 8), so that the 16 rows that a read of the operands takes at a time lie in
 // different banks.  What lies past an operand's rows or k reads as zero (the buffer's bounds).
-// STAGED: rows that do not lie on 16 bytes go through registers instead.
+//
+// Bound by the matrix units and the clock that their power leaves: 4096 rows x 65536 entries x 4096 bf16
+// takes 1.71 ms (1.28 PFLOP/s) for the sums of the softmax, 445 to 465 us for a quarter of dx or of dweight (1.2)
+// and 505 for a quarter of D, which is stored twice; the matrix units work 62 % of the cycles at 1.87 GHz,
+// LDS has no bank conflicts.  A row takes 41 us (268 MB, 6.5 TB/s).  Slower by 3 and 10 %: steps of half the
+// depth, four in turn; four waves with tiles of 128 x 128.
+// STAGED: rows that do not lie on 16 bytes go through registers instead (517 x 50021 f16: 1003 elements a row 113
+// us, 1004 100, 1008 80; a vector off 16 bytes spans two lines).
 template <typename T, int WI, int WJ, int MI, int MJ, bool STAGED, int END>
 __device__ __forceinline__ void xent_product(const GemmArgs& a) {
     constexpr int BI = WI * MI * 32, BJ = WJ * MJ * 32, NW = WI * WJ;
@@ -580,7 +587,8 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
 //
 // Cutting a step into parts takes the vector units about as long as its products the matrix units: half
 // of the eight waves do the one while the others do the other.  A tile of few columns waits for
-// memory instead and has two steps on their way.
+// memory instead and has two steps on their way.  1024 rows x 20000 x 1024: 250 us (168 TFLOP/s, six times as
+// many in bfloat16; the library's f32 product reaches 152); 8 rows x 30000 x 1000 42 us, 2.9 TB/s.
 template <int WI, int WJ, int MI, int MJ, bool AK, bool BK, int END>
 __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
     constexpr int BI = WI * MI * 32, BJ = WJ * MJ * 32, NW = WI * WJ;
@@ -925,12 +933,27 @@ void product_as(GemmArgs a, int parts, hipStream_t s) {
         <<<dim3((unsigned)(cdiv(a.ni * a.nj * parts, 8) * 8)), dim3(WI * WJ * 64), 0, s>>>(a);
 }
 
-// Columns (rows of x) of a tile by their number: few need few, and many the width that leaves least of
-// the last tile unused, the widest of those (f32, whose parts take three times the room, 128).
-int tile_columns(int64_t rows, bool f32) {
-    if (rows <= 32) return 32;
-    if (rows <= 128 || f32) return 128;
-    return up(rows, 192) < up(rows, 256) ? 192 : 256;
+// Columns (rows of x) of a tile.  Up to 64 rows 32 (with 64 entries): such tiles are many and wait for memory
+// together, and dx takes weight as it lies.  bf16, 32768 entries x 4096: 1 row 45 us, in tiles of 256 x 128
+// 63; 64 rows 55 and 74; 96 rows 69 and 78, but 128 rows 92 and 83, and 96 rows of 100000 x 1000 70 and 51;
+// forward and backward of 64 rows x 32768 x 2048 140 and 241, f32 407 and 517.
+// More rows: the width whose rounds of workgroups (256 at a time, each 256 entries) cost least, a tile
+// about its width and 120 more.  bf16, 32768 entries x 4096, in tiles of 128, 192 and 256: 129 rows 74, 90, 96
+// us; 300 rows 130, 96, 102; 600 rows 191, 173, 190; 4096 rows x 65536 x 2048 both ways 5.05, 4.69, 4.05 ms.
+// f32, whose parts take three times the room, 128.
+int tile_columns(int64_t rows, int64_t vocab, bool f32) {
+    if (rows <= 64) return 32;
+    if (f32) return 128;
+    int best = 0;
+    int64_t least = 0;
+    for (const int w : {128, 192, 256}) {
+        const int64_t cost = cdiv(cdiv(vocab, 256) * cdiv(rows, w), 256) * (w + 120);
+        if (best == 0 || cost <= least) {
+            best = w;
+            least = cost;
+        }
+    }
+    return best;
 }
 
 // Rows (vocabulary entries) of such a tile.
@@ -949,7 +972,7 @@ void product_of(const GemmArgs& a, int columns, int parts, hipStream_t s) {
 }
 
 template <typename T, int END>
-void product(const GemmArgs& a, int parts, bool lies, hipStream_t s) {
+void product(const GemmArgs& a, int columns, int parts, bool lies, hipStream_t s) {
     static const char* const names[] = {"k_xent_stats", "k_xent_logits", "k_xent_dx", "k_xent_dweight"};
     KernelTimer kt(names[END], s);
     constexpr bool f32 = sizeof(T) == 4;
@@ -959,7 +982,6 @@ void product(const GemmArgs& a, int parts, bool lies, hipStream_t s) {
         else
             product_as<T, 2, 4, 4, 2, false, END>(a, parts, s);
     } else {
-        const int columns = tile_columns(a.B.rows, f32);
         if constexpr (!f32 && END == kDx) {
             if (columns == 32) return product_as<T, 2, 1, 1, 1, true, END>(a, parts, s);
         } else if constexpr (!f32) {
@@ -973,6 +995,7 @@ struct XentPlan {
     int64_t piece;
     int64_t wide_r;              // rows rounded up: zeros behind them
     int64_t ld_v, ld_r;          // rows of a piece and of the rows, in elements
+    int columns;                 // of a tile
     int64_t parts, dx_ld, tile_i, tiles;
     int64_t wt_rows;             // weight transposed for dx: its d rows, 0: read as it lies
 };
@@ -989,7 +1012,8 @@ XentPlan xent_plan(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype) {
     p.ld_v = apart(up(p.piece, kDepth));
     p.ld_r = apart(p.wide_r);
     p.dx_ld = up(d, 4);
-    const int columns = tile_columns(rows, dtype == DET_F32);
+    const int columns = tile_columns(rows, vocab, dtype == DET_F32);
+    p.columns = columns;
     p.tile_i = tile_rows(columns);
     p.wt_rows = dtype == DET_F32 || columns == 32 ? 0 : d;
     p.tiles = cdiv(vocab, p.tile_i);
@@ -1060,7 +1084,7 @@ det_status xent_typed(const XentCall& c, char* ws, hipStream_t s) {
         const int64_t n = c.vocab - v0 < piece ? c.vocab - v0 : piece;
         a.A = Operand{reinterpret_cast<const char*>(w + v0 * c.w_stride), n, c.w_stride * (int64_t)sizeof(T)};
         a.v0 = v0;
-        product<T, kStats>(a, 1, lies, s);
+        product<T, kStats>(a, p.columns, 1, lies, s);
         a.tile0 += cdiv(n, p.tile_i);
     }
     det_status st = launch_status();
@@ -1113,7 +1137,7 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
         a.dt_ld = p.ld_r * es;
         a.rows_up = p.wide_r;
         a.piece_up = wide;
-        product<T, kLogits>(a, 1, lies, s);
+        product<T, kLogits>(a, p.columns, 1, lies, s);
         // dx += D weight
         GemmArgs b = a;
         b.out = ws + L.sums;
@@ -1131,14 +1155,14 @@ det_status xent_back_typed(const XentBackCall& c, char* ws, hipStream_t s) {
             b.A = Operand{ws + L.wt, c.d, p.ld_v * es};
             b.k = wide;
         }
-        product<T, kDx>(b, (int)p.parts, true, s);
+        product<T, kDx>(b, p.columns, (int)p.parts, true, s);
         // dweight of the piece
         b.A = Operand{ws + L.xt, c.d, p.ld_r * es};
         b.B = es == 4 ? Operand{ws + L.d, n, a.d_ld} : Operand{ws + L.dt, n, a.dt_ld};
         b.k = es == 4 ? c.rows : p.wide_r;
         b.out = static_cast<T*>(c.dweight) + v0 * c.d;
         b.out_ld = c.d;
-        product<T, kDw>(b, 1, true, s);
+        product<T, kDw>(b, p.columns, 1, true, s);
         const det_status st = launch_status();
         if (st != DET_SUCCESS) return st;
     }
