@@ -490,7 +490,7 @@ size_t det_linear_cross_entropy_workspace_size(int64_t rows, int64_t vocab, int6
  * loss, lse: float [rows].
  * The products are of dtype's matrix instructions with f32 sums; f32 goes through them in three
  * parts of 8 bits each, with sums that are off by about 2^-23 relative to the sum of the
- * products' magnitudes.  rows <= 2^20, 1 <= d <= 2^20, vocab >= 1; scale > 0 and finite.
+ * products' magnitudes, and an infinite factor may give NaN there.  rows <= 2^20, 1 <= d <= 2^20, vocab >= 1; scale > 0 and finite.
  * Order: fixed by (rows, vocab, d, dtype). */
 det_status det_linear_cross_entropy(const void* x, int64_t x_stride, const void* weight,
                                     int64_t weight_stride, const int64_t* targets, int64_t rows,
@@ -504,7 +504,7 @@ size_t det_linear_cross_entropy_backward_workspace_size(int64_t rows, int64_t vo
 
 /* Gradients of det_linear_cross_entropy's loss, the logits made again piece by piece:
  *   D = exp(z - lse) - hit;  dx = scale * dloss * (D weight);  dweight = scale * (dloss D)^T x
- * D is rounded to dtype once.  A row that is not scored has dx 0 and adds nothing to dweight,
+ * D is rounded to dtype once (f32: and x times dloss once, for dweight).  A row that is not scored has dx 0 and adds nothing to dweight,
  * whatever it holds.  exp(z - lse) is off by about |lse| 2^-24 relative to it.
  * lse:      float [rows], as det_linear_cross_entropy wrote it for these x, weight and scale.
  * dloss:    float [rows].

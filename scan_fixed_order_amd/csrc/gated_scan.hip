@@ -345,7 +345,7 @@ __device__ __forceinline__ float enter(const ARGS& a, const Place& p, const floa
 
 // A workgroup walks chunks of 64 (or 32) words of channels, the next two chunks' words in flight while
 // this one's effects go round.  One pass over gate and x: bound by HBM.  8 x 2048 x 4096 bf16 88 us (403 MB,
-// 4.6 TB/s), 3 x 10007 x 2500 f32 183 (901 MB, 4.9; rows that are no whole number of lines).
+// 4.6 TB/s), 3 x 10007 x 2500 f32, ragged, 183 (847 MB, 4.6; rows are no whole number of lines).
 template <typename T, bool SIG, int LANES>
 __global__ __launch_bounds__(LANES * kSpans) void k_gated_scan(ScanArgs a) {
     constexpr int E = kCh<T>, CH = LANES * E, kChunkSteps = kSteps * kSpans, kMine = kSteps * 64 / LANES;
