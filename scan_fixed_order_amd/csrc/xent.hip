@@ -935,12 +935,12 @@ void product_as(GemmArgs a, int parts, hipStream_t s) {
 
 // Columns (rows of x) of a tile.  Up to 64 rows 32 (with 64 entries): such tiles are many and wait for memory
 // together, and dx takes weight as it lies.  bf16, 32768 entries x 4096: 1 row 45 us, in tiles of 256 x 128
-// 63; 64 rows 55 and 74; 96 rows 69 and 78, but 128 rows 92 and 83, and 96 rows of 100000 x 1000 70 and 51;
-// forward and backward of 64 rows x 32768 x 2048 140 and 241, f32 407 and 517.
-// More rows: the width whose rounds of workgroups (256 at a time, each 256 entries) cost least, a tile
-// about its width and 120 more.  bf16, 32768 entries x 4096, in tiles of 128, 192 and 256: 129 rows 74, 90, 96
-// us; 300 rows 130, 96, 102; 600 rows 191, 173, 190; 4096 rows x 65536 x 2048 both ways 5.05, 4.69, 4.05 ms.
-// f32, whose parts take three times the room, 128.
+// 63; 64 rows 55 and 74; 128 rows 92 and 83; 96 rows of 100000 x 1000 70 and 51; forward and backward of 64
+// rows x 32768 x 2048 140 and 241, f32 407 and 517.
+// More rows: the width whose rounds of workgroups (256 at a time with 256 entries, or 512 with 128) cost
+// least, a tile about its width and 120 more.  bf16, 32768 entries x 4096, in widths of 128, 192 and 256: 129
+// rows 70, 90, 96 us; 300 rows 130, 96, 102; 600 rows 191, 173, 190; 4096 rows x 65536 x 2048 both ways 5.05,
+// 4.69, 4.05 ms.  f32, whose parts take three times the room, 128 (with 256 entries).
 int tile_columns(int64_t rows, int64_t vocab, bool f32) {
     if (rows <= 64) return 32;
     if (f32) return 128;
@@ -956,8 +956,9 @@ int tile_columns(int64_t rows, int64_t vocab, bool f32) {
     return best;
 }
 
-// Rows (vocabulary entries) of such a tile.
-int64_t tile_rows(int columns) { return columns == 32 ? 64 : 256; }
+// Rows (vocabulary entries) of such a tile.  Width 128 with 128 of them, two workgroups a unit: 96 rows x 32768 x
+// 4096 bf16 68 us, with 256 81; 128 rows x 8000 47 and 57, but 128 rows x 100001 x 257 42 and 36.
+int64_t tile_rows(int columns, bool f32) { return columns == 32 ? 64 : columns == 128 && !f32 ? 128 : 256; }
 
 template <typename T, bool STAGED, int END>
 void product_of(const GemmArgs& a, int columns, int parts, hipStream_t s) {
@@ -968,7 +969,10 @@ void product_of(const GemmArgs& a, int columns, int parts, hipStream_t s) {
         if (columns == 256) return product_as<T, 2, 4, 4, 2, STAGED, END>(a, parts, s);
         if (columns == 192) return product_as<T, 4, 2, 2, 3, STAGED, END>(a, parts, s);
     }
-    product_as<T, 4, 2, 2, 2, STAGED, END>(a, parts, s);
+    if constexpr (sizeof(T) == 2)
+        product_as<T, 2, 2, 2, 2, STAGED, END>(a, parts, s);
+    else
+        product_as<T, 4, 2, 2, 2, STAGED, END>(a, parts, s);
 }
 
 template <typename T, int END>
@@ -1014,13 +1018,13 @@ XentPlan xent_plan(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype) {
     p.dx_ld = up(d, 4);
     const int columns = tile_columns(rows, vocab, dtype == DET_F32);
     p.columns = columns;
-    p.tile_i = tile_rows(columns);
+    p.tile_i = tile_rows(columns, dtype == DET_F32);
     p.wt_rows = dtype == DET_F32 || columns == 32 ? 0 : d;
     p.tiles = cdiv(vocab, p.tile_i);
     // workgroups that share dx's sum over a piece where its tiles are few
     const int64_t tiles = cdiv(d, p.tile_i) * cdiv(rows, columns);
     // (256 of them run at a time, of the narrow tiles 1024)
-    p.parts = (columns == 32 ? 1024 : 256) / tiles;
+    p.parts = (columns == 32 ? 1024 : p.tile_i == 128 ? 512 : 256) / tiles;
     const int64_t steps = cdiv(p.piece, dtype == DET_F32 ? kDepthF32 : kDepth);
     if (p.parts > cdiv(steps, 8)) p.parts = cdiv(steps, 8);
     if (p.parts < 1) p.parts = 1;
