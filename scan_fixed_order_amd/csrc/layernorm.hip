@@ -239,7 +239,7 @@ struct LayerRow {
 // 16 elements in LDS); the next row's loads are in flight while this one's sums go round the team.
 // The teams of a workgroup join their sums.  Bound by HBM: 16384 x 4096 bf16 with dh, dweight and dbias 88 us
 // (537 MB and 17 MB of strips, 6.2 TB/s); 1003 x 5001 f32 15 us, one round of rows a workgroup.  Rows of
-// 16384 keep one workgroup of 1024 lanes a unit, whose loads do not cover the sums (2048 rows 106 us, 3.8
+// 16384 keep one workgroup of 1024 lanes a unit, whose loads do not cover the sums (2048 rows 89 us, 4.5
 // TB/s).
 template <typename T, int TEAM, int NV, bool DH, bool BIAS, bool ONCE>
 __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_layer_norm_backward(LayerBackArgs a) {
@@ -328,6 +328,20 @@ __global__ __launch_bounds__(Team<TEAM>::kBlock) void k_layer_norm_backward(Laye
         for (int j = 0; j < NV; ++j) {
             const int64_t c = (int64_t)kVec<T> * (t + j * TEAM);
             float o[kVec<T>], e[kVec<T>];
+            if constexpr (kLdsSums) {
+                // from the words again, which take half of the registers across the sums (the empty asm keeps
+                // the compiler from holding the floats all the same, 24 registers of a lane in memory: 106 us)
+                asm("" : "+v"(cur.h[j]), "+v"(cur.dy[j]));
+                float g[kVec<T>];
+                unpack<T>(settle<T>(cur.h[j], c, a.d), h[j]);
+                unpack<T>(settle<T>(cur.dy[j], c, a.d), dy[j]);
+                unpack<T>(wraw[j], g);
+#pragma unroll
+                for (int i = 0; i < kVec<T>; ++i) {
+                    h[j][i] = (h[j][i] - mean) * rstd;
+                    dy[j][i] *= g[i];
+                }
+            }
             if constexpr (DH && kAhead) unpack<T>(settle<T>(cur.dh[j], c, a.d), e);
             if constexpr (DH && !kAhead)
                 read_vec<ONCE>(static_cast<const T*>(a.dh) +
