@@ -449,7 +449,8 @@ size_t det_gated_scan_workspace_size(int64_t batch, int64_t steps, int64_t d, de
  *             h is 0; gate and x there are not used, whatever they hold.  Values above steps mean
  *             steps, below 0 none.
  * Without DET_GATE_SIGMOID gates are taken to have |gate| <= 1: products of up to 128 neighbouring
- * gates are formed, and where one overflows h may be infinite or NaN.
+ * gates are formed, and where one overflows h may be infinite or NaN.  A gate that is NaN, or infinite
+ * beside a state of 0, makes h NaN from its step on, as the recurrence has it.
  * steps >= 1 when batch * d > 0; d <= DET_SCAN_MAX_CHANNELS, batch * d <= DET_MAX_N.
  * Order: fixed by the step's position alone (spans of 8 steps, chunks of 16 spans), so a sequence's
  * bits depend neither on the other channels nor on the steps that follow. */

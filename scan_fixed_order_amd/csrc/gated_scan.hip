@@ -140,10 +140,18 @@ __device__ __forceinline__ void sigmoids(float x, float& keep, float& take) {
     take = x >= 0.0f ? small : large;
 }
 
-// A state c after a span of effect (A, H).  Linear gates may make A infinite: a state of 0 leaves H.
+// A state c after a span of effect (A, H).  The product of a span's linear gates may overflow although
+// each is finite: a state of 0 leaves H.  (A gate that is not finite itself is in H: from_zero.)
 template <bool SIG>
 __device__ __forceinline__ float after_span(float A, float c, float H) {
     return !SIG && c == 0.0f ? H : fmaf(A, c, H);
+}
+
+// A span's chain begins at a state of 0, which a linear gate multiplies all the same: one of infinity or
+// NaN makes the chain NaN, as it makes every state behind it.
+template <bool SIG>
+__device__ __forceinline__ float from_zero(float a, float b) {
+    return SIG ? b : fmaf(a, 0.0f, b);
 }
 
 // what a span of steps does to a state: h -> A h + H
@@ -380,7 +388,7 @@ __global__ __launch_bounds__(LANES * kSpans) void k_gated_scan(ScanArgs a) {
         keep_past(begin + kMine <= len, len - t0, av, bv);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            Effect own{av[0][e], bv[0][e]};
+            Effect own{av[0][e], from_zero<SIG>(av[0][e], bv[0][e])};
 #pragma unroll
             for (int i = 1; i < kSteps; ++i) {
                 own.H = fmaf(av[i][e], own.H, bv[i][e]);
@@ -470,7 +478,7 @@ __device__ __forceinline__ void chunk_effect(const ARGS& a, const elem<T>* gate,
             if constexpr (BACK)      // E -> a (dh + E)
                 own.H = av[i][e] * (j ? bv[i][e] + own.H : bv[i][e]);
             else
-                own.H = j ? fmaf(av[i][e], own.H, bv[i][e]) : bv[i][e];
+                own.H = j ? fmaf(av[i][e], own.H, bv[i][e]) : from_zero<SIG>(av[i][e], bv[i][e]);
             own.A = j ? own.A * av[i][e] : av[i][e];
         }
         s_eff[p.span][p.at + e] = own;
