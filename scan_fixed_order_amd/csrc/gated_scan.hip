@@ -725,8 +725,10 @@ ScanPlan scan_plan(int64_t batch, int64_t steps, int64_t d, det_dtype dtype, int
     return p;
 }
 
-// A grid holds fewer than 2^32 threads, and 65535 along y.
-constexpr int64_t kGridTiles = 4194303, kGridChunks = 65535;
+// A grid holds fewer than 2^32 threads, and 65535 along y.  Workgroups have up to 1024 threads, and a
+// launch a multiple of 8 of them (item_of), so the most that fits is one too.
+constexpr int64_t kGridTiles = 4194296, kGridChunks = 65535;
+static_assert(kGridTiles % 8 == 0 && kGridTiles * 64 * kSpans < (int64_t)1 << 32, "threads of a grid");
 
 template <typename T>
 void from_sequence(ScanArgs& a, int64_t b) {

@@ -1,5 +1,5 @@
 """The recurrent model's operators where a shortcut, a grid's bound or a sum's order could show: gates
-that are not finite beside a state of zero."""
+that are not finite beside a state of zero, more tiles than a grid holds."""
 import pytest
 import torch
 
@@ -61,3 +61,29 @@ def test_negative_zeros_add_to_a_state_of_zero(dev, steps):
     x = torch.full((1, steps, 70), -0.0, device=dev)
     got = det.det_gated_scan(gate, x)
     assert not torch.signbit(got.h).any() and not torch.signbit(got.state).any()
+
+
+@pytest.mark.parametrize("batch", [4194297, (1 << 22) + 5])
+def test_more_tiles_than_a_grid_of_whole_workgroups_holds(dev, batch):
+    """Two channels a sequence take workgroups of 1024 threads, of which 4194303 fit into a grid and
+    4194304, the next multiple of 8, do not.  Whole numbers, so that every sum is exact."""
+    steps, d = 9, 2
+    g = torch.Generator(dev).manual_seed(3)
+    gate = torch.randint(0, 2, (batch, steps, d), generator=g, device=dev, dtype=torch.int8)
+    x = torch.randint(-3, 4, (batch, steps, d), generator=g, device=dev, dtype=torch.int8)
+    state = torch.randint(-6, 7, (batch, d), generator=g, device=dev, dtype=torch.int8)
+    h, now = torch.empty_like(x), state
+    for i in range(steps):
+        now = gate[:, i] * now + x[:, i]
+        h[:, i] = now
+    got = det.det_gated_scan(gate.half(), x.half(), state.float())
+    assert torch.equal(got.h, h.half()) and torch.equal(got.state, now.float())
+    dgate, dx, first = det.det_gated_scan_backward(x.half(), gate.half(), x.half(), got.h, state.float(),
+                                                   state.float())
+    e, before = state, torch.cat([state[:, None], h[:, :-1]], 1)
+    for i in reversed(range(steps)):
+        e = x[:, i] + e      # G of the step
+        assert torch.equal(dx[:, i], e.half())
+        assert torch.equal(dgate[:, i], (e.short() * before[:, i]).half())
+        e = gate[:, i] * e
+    assert torch.equal(first, e.float())
