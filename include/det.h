@@ -489,9 +489,10 @@ size_t det_linear_cross_entropy_workspace_size(int64_t rows, int64_t vocab, int6
  * targets:  int64 [rows]; one outside [0, vocab) is not scored: its loss is 0.  lse is written for
  *           every row.
  * loss, lse: float [rows].
- * The products are of dtype's matrix instructions with f32 sums; f32 goes through them in three
- * parts of 8 bits each, with sums that are off by about 2^-23 relative to the sum of the
- * products' magnitudes, and an infinite factor may give NaN there.  rows <= 2^20, 1 <= d <= 2^20, vocab >= 1; scale > 0 and finite.
+ * The products are of dtype's matrix instructions with f32 sums: a logit is off by at most (d + 8) 2^-23
+ * of the sum of its products' magnitudes, as each addition rounds.  f32 goes through them in three parts of 8
+ * bits each: each product is off by up to 2^-22 of itself besides, to either side, and an infinite factor
+ * may give NaN.  rows <= 2^20, 1 <= d <= 2^20, vocab >= 1; scale > 0 and finite.
  * Order: fixed by (rows, vocab, d, dtype). */
 det_status det_linear_cross_entropy(const void* x, int64_t x_stride, const void* weight,
                                     int64_t weight_stride, const int64_t* targets, int64_t rows,

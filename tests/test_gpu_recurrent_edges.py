@@ -1,9 +1,10 @@
 """The recurrent model's operators where a shortcut, a grid's bound or a sum's order could show: gates
-that are not finite beside a state of zero, more tiles than a grid holds."""
+that are not finite beside a state of zero, more tiles than a grid holds, factors whose parts err to
+one side."""
 import pytest
 import torch
 
-from lm_reference import IDS, TYPES
+from lm_reference import IDS, TYPES, randn
 from scan_fixed_order_amd import det
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +88,54 @@ def test_more_tiles_than_a_grid_of_whole_workgroups_holds(dev, batch):
         assert torch.equal(dgate[:, i], (e.short() * before[:, i]).half())
         e = gate[:, i] * e
     assert torch.equal(first, e.float())
+
+
+@pytest.mark.parametrize("rows", [64, 100])      # tiles of 32 columns, and of 128
+def test_f32_products_are_off_to_either_side(dev, rows):
+    """One entry and a width of one: lse is the product x w itself.  Of the parts of a factor the second is
+    at most 2^-7 of it and the third 2^-16, so the three products left out are at most (1 + 2^-9) 2^-22 of x
+    w; the five smaller sums are at most 2^-5 of it, each off by a step 2^-23 of that; the last addition
+    rounds by 2^-24.  In all below 2.7 * 2^-23.
+
+    The mean over many w: w's third part, either sign alike, times the mean of x's second, 2^-8, has a
+    standard deviation of 2^-24 / sqrt(3) a w; all else differs from row to row."""
+    at = torch.zeros(rows, dtype=torch.int64, device=dev)
+    special = torch.tensor([1 + 2.0 ** -7 - 2.0 ** -23, 2 - 2.0 ** -23, 1 + 2.0 ** -8, 1.0], device=dev)
+    errors, seeds = [], 256
+    for seed in range(seeds):
+        g = torch.Generator(dev).manual_seed(seed)
+        x, w = 1 + torch.rand(rows, 1, generator=g, device=dev), 1 + torch.rand(1, 1, generator=g, device=dev)
+        x[:4, 0] = special
+        for one in (w, special[seed % 4].view(1, 1)):
+            got = det.det_linear_cross_entropy(x, one, at)
+            want = (x.double() * one.double())[:, 0]
+            rel = (got.lse.double() - want) / want
+            assert rel.abs().max() <= 2.7 * 2.0 ** -23, float(rel.abs().max()) * 2 ** 23
+            assert (got.loss == 0).all()
+            if one is w:
+                errors.append(rel[4:])
+    errors = torch.cat(errors)
+    allowed = 2.0 ** -24 / (3 * seeds) ** 0.5 + 2.7 * 2.0 ** -23 / errors.numel() ** 0.5
+    assert errors.mean().abs() <= 4 * allowed
+
+
+@pytest.mark.parametrize("rows", [5, 100])
+def test_f32_entries_masked_by_the_lowest_float(dev, rows):
+    """Entries whose weight is the type's lowest value have a logit as low, or -infinity, and take no part;
+    a NaN still reaches its row alone."""
+    d = 40
+    x = 0.5 + randn((rows, d), torch.float32, dev, 1).abs()
+    w = randn((300, d), torch.float32, dev, 2, 0.1)
+    at = torch.arange(rows, device=dev) % 200
+    kept = det.det_linear_cross_entropy(x, w[:200].contiguous(), at)
+    w[200:] = torch.finfo(torch.float32).min
+    got = det.det_linear_cross_entropy(x, w, at)
+    # the same logits in other tiles: the sums' order, at most 300 terms
+    assert ((got.lse - kept.lse).abs() <= 300 * 2.0 ** -24 * (1 + kept.lse.abs())).all()
+    one = torch.zeros(300, d, device=dev)
+    one[200:, 3] = torch.finfo(torch.float32).min
+    got = det.det_linear_cross_entropy(x, one, at)      # finite, or -infinity where x is above 1
+    assert ((got.lse.double() - torch.log(torch.tensor(200.0).double())).abs() <= 1e-5).all()
+    x[2, 7] = float("nan")
+    got = det.det_linear_cross_entropy(x, w, at)
+    assert torch.equal(got.lse.isnan(), torch.arange(rows, device=dev) == 2)
