@@ -15,8 +15,8 @@
 // products of parts; the three left out are within 2^-22 of the whole one, to either side, and an infinite
 // factor may give NaN.
 //
-// Order: k ascending in steps of 16 inside the matrix instruction's own order, f32 accumulators; a
-// tile's logits, then the tiles of a row by lanes and the adjacent-lanes tree; dx adds pieces of the
+// Order: k ascending in steps of 16 inside the matrix instruction's own order, f32 accumulators (in tiles of
+// 32 columns several in turn, joined in pairs: chains_of); a tile's logits, then the tiles of a row by lanes and the adjacent-lanes tree; dx adds pieces of the
 // vocabulary in ascending order, then the parts that share a piece.  All of it fixed by (rows,
 // vocab, d, dtype).
 #include "det_internal.h"
@@ -127,6 +127,27 @@ struct Partial {
 };
 
 enum Ending { kStats, kLogits, kDx, kDw };
+
+// Accumulators of a wave's tile of 32 x 32, which take the steps of 16 in turn: a tile of 32 columns has one
+// such tile a wave and room for more, and its sums are four (f32: two) times as short.  Larger tiles have
+// none to spare.
+template <int MI, int MJ>
+constexpr int chains_of(int depth) {
+    return MI * MJ == 1 ? depth / 16 : 1;
+}
+
+// joined in pairs into the first
+template <int CHAINS, int MI, int MJ>
+__device__ __forceinline__ void join_chains(f32x16 (&acc)[CHAINS][MI][MJ]) {
+#pragma unroll
+    for (int step = 1; step < CHAINS; step *= 2)
+#pragma unroll
+        for (int c = 0; c < CHAINS; c += 2 * step)
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < MJ; ++j) acc[c][i][j] += acc[c + step][i][j];
+}
 
 // Columns of a tile on their way to rows in memory: a lane holds four elements of a column, whose rows in
 // memory it would write 8 or 16 bytes at a time; through LDS a row's elements leave side by side.
@@ -382,7 +403,8 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
     const int chunk[2] = {(lane & 7) ^ turn_of(in_load), (lane & 7) ^ turn_of(kRows + in_load)};
     const int first = (int)(part * a.per_part), steps = (int)((a.k + kDepth - 1) / kDepth);
     const int behind = first + a.per_part < steps ? (int)(first + a.per_part) : steps;
-    f32x16 acc[MI][MJ] = {};
+    constexpr int kChains = chains_of<MI, MJ>(kDepth);
+    f32x16 acc[kChains][MI][MJ] = {};
     const auto products = [&](const char* s) {
         const char* pa = s + (wi * MI * 32 + (lane & 31)) * kRow;
         const char* pb = s + (BI + wj * MJ * 32 + (lane & 31)) * kRow;
@@ -405,7 +427,8 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < MJ; ++j)
-                    acc[i][j] = mma(av[kk & 1][i], bv[kk & 1][j], acc[i][j], T{});
+                    acc[kk % kChains][i][j] =
+                        mma(av[kk & 1][i], bv[kk & 1][j], acc[kk % kChains][i][j], T{});
         }
         // In this order: the first operands, the next step's loads, and the operands behind them one by one
         // between matrix instructions.  (Left to the compiler each is waited for where it is read: forward of
@@ -583,7 +606,8 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
         }
         turn();
     }
-    xent_ending<T, WI, WJ, MI, MJ, END>(a, acc, i0, j0, part, wi, wj, s_0);
+    join_chains(acc);
+    xent_ending<T, WI, WJ, MI, MJ, END>(a, acc[0], i0, j0, part, wi, wj, s_0);
 }
 
 // f32.  A step's rows go through registers, are cut into their three parts and lie in LDS part by
@@ -727,7 +751,8 @@ __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
         else
             put_as(Partial{}, s, set, step);
     };
-    f32x16 acc[MI][MJ] = {}, small[MI][MJ] = {};
+    constexpr int kChains = chains_of<MI, MJ>(kDepthF32);
+    f32x16 acc[kChains][MI][MJ] = {}, small[MI][MJ] = {};
     const auto products = [&](const char* s) {
         const char* pa = s + ((lane & 3) * (BI / 4) + wi * MI * 8 + (lane & 31) / 4) * kRow;
         const char* pb = s + (BI + (lane & 3) * (BJ / 4) + wj * MJ * 8 + (lane & 31) / 4) * kRow;
@@ -748,7 +773,7 @@ __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < MJ; ++j) {
-                    acc[i][j] = mma(av[0][i], bv[0][j], acc[i][j], __bf16{});
+                    acc[kk % kChains][i][j] = mma(av[0][i], bv[0][j], acc[kk % kChains][i][j], __bf16{});
                     small[i][j] = mma(av[2][i], bv[0][j], small[i][j], __bf16{});
                     small[i][j] = mma(av[1][i], bv[1][j], small[i][j], __bf16{});
                     small[i][j] = mma(av[0][i], bv[2][j], small[i][j], __bf16{});
@@ -780,11 +805,12 @@ __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
         one(s_0, s_1, 1 % kSets, step);
         one(s_1, s_0, 0, step + 1);
     }
+    join_chains(acc);
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < MJ; ++j) acc[i][j] += small[i][j];
-    xent_ending<float, WI, WJ, MI, MJ, END>(a, acc, i0, j0, part, wi, wj, s_0);
+        for (int j = 0; j < MJ; ++j) acc[0][i][j] += small[i][j];
+    xent_ending<float, WI, WJ, MI, MJ, END>(a, acc[0], i0, j0, part, wi, wj, s_0);
 }
 
 // (The kernel's body is a device function: it uses types that the host's compiler pass lacks.)

@@ -1,6 +1,6 @@
 """The recurrent model's operators where a shortcut, a grid's bound or a sum's order could show: gates
 that are not finite beside a state of zero, more tiles than a grid holds, factors whose parts err to
-one side."""
+one side, long sums of a few rows' logits."""
 import pytest
 import torch
 
@@ -139,3 +139,17 @@ def test_f32_entries_masked_by_the_lowest_float(dev, rows):
     x[2, 7] = float("nan")
     got = det.det_linear_cross_entropy(x, w, at)
     assert torch.equal(got.lse.isnan(), torch.arange(rows, device=dev) == 2)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("rows,d", [(1, 4096), (64, 4096), (3, 1000), (5, 4095)])
+def test_long_sums_of_few_rows_go_through_several_accumulators(dev, rows, d, t):
+    """A logit of 1024 in its first product, behind it products that add half a step 2^-13 of it every 16: an
+    accumulator that holds the 1024 loses them.  Four take the steps in turn (f32: two), so that one loses a
+    quarter (half), each at most half a step, and the joins round three times.  One entry: lse is the logit."""
+    x, w = torch.ones(rows, d, device=dev), torch.full((1, d), 2.0 ** -18, device=dev)
+    w[0, 0] = 1024.0
+    got = det.det_linear_cross_entropy(x.to(t), w.to(t), torch.zeros(rows, dtype=torch.int64, device=dev))
+    want = 1024 + (d - 1) * 2.0 ** -18
+    steps = -(-d // 16) // (2 if t == torch.float32 else 4)
+    assert ((got.lse.double() - want).abs() <= (steps + 4) * 2.0 ** -14).all()
