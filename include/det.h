@@ -478,7 +478,8 @@ det_status det_gated_scan_backward(const void* dh, const void* gate, const void*
                                    void* dx, float* dstate0, void* ws, size_t ws_bytes,
                                    void* stream);
 
-/* Bytes of workspace det_linear_cross_entropy needs (0 when the arguments are invalid). */
+/* Bytes of workspace det_linear_cross_entropy needs (0 when the arguments are invalid): 8 for a row and
+ * tile of 64 to 256 entries, 4 for a row. */
 size_t det_linear_cross_entropy_workspace_size(int64_t rows, int64_t vocab, int64_t d,
                                                det_dtype dtype);
 
@@ -500,7 +501,13 @@ det_status det_linear_cross_entropy(const void* x, int64_t x_stride, const void*
                                     float* loss, float* lse, void* ws, size_t ws_bytes,
                                     void* stream);
 
-/* Bytes of workspace det_linear_cross_entropy_backward needs (0 when the arguments are invalid). */
+/* Bytes of workspace det_linear_cross_entropy_backward needs (0 when the arguments are invalid).  With
+ * P = min(vocab, max(4096, min(65536, 2^26 / rows))) entries a piece and s bytes an element:
+ *   D by rows, and in 16-bit types by columns:     rows P s each
+ *   x by columns:                                  rows d s
+ *   weight by columns, 16 bits above 64 rows:      P d s
+ *   dx's sums:                                     4 rows d, or up to 2^26 where workgroups share a sum
+ * and up to 64 more rows, entries or columns of each.  Above 16384 rows D grows with them. */
 size_t det_linear_cross_entropy_backward_workspace_size(int64_t rows, int64_t vocab, int64_t d,
                                                         det_dtype dtype);
 

@@ -27,8 +27,8 @@ namespace {
 
 constexpr int kDepth = 64, kDepthF32 = 32;    // elements of k a step: 128 bytes of a row
 constexpr int64_t kPieceUnit = 256;           // a piece's entries are a multiple of every tile's
-constexpr int64_t kPieceCells = 1 << 26;      // elements of D that a piece holds, about
-constexpr int64_t kPieceMin = 4096;
+constexpr int64_t kPieceCells = 1 << 26;      // elements of D that a piece holds, up to 16384 rows
+constexpr int64_t kPieceMin = 4096;           // above them a piece's entries: D has 4096 elements a row
 constexpr int64_t kPieceMax = 65536;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1042,7 +1042,8 @@ struct XentPlan {
     int64_t wt_rows;             // weight transposed for dx: its d rows, 0: read as it lies
 };
 
-// Vocabulary entries of a piece: D of a piece takes about kPieceCells elements, twice.
+// Vocabulary entries of a piece: D of a piece takes about kPieceCells elements (kPieceMin a row where that
+// is more), in 16-bit types twice.
 XentPlan xent_plan(int64_t rows, int64_t vocab, int64_t d, det_dtype dtype) {
     XentPlan p;
     int64_t piece = kPieceCells / (rows > 0 ? rows : 1) / kPieceUnit * kPieceUnit;
