@@ -21,9 +21,9 @@
 namespace det {
 namespace {
 
-// By measurement, 8 x 2048 x 4096 bf16 forward and backward, then 3 x 10007 x 2500 f32: 90 and 174, 228
-// and 432 us; 8 spans forward 90, 244; 16 backward 378 (spilled registers), 438; spans of 16 steps with
-// 8 of them 132, 208.
+// By measurement of calls, 8 x 2048 x 4096 bf16 forward and backward, then 3 x 10007 x 2500 f32, ragged: 93
+// and 148, 194 and 332 us; 8 spans forward 92, 206; 16 backward 348 (spilled registers), 308; spans of 16
+// steps with 8 of them 96 and 321, 196 and 316.
 constexpr int kSteps = 8;              // steps of a span: a lane's share of a chunk
 constexpr int kSpans = 16;             // spans of a chunk
 constexpr int kBackSpans = 8;          // the same backwards, where a step has twice the words
@@ -191,8 +191,8 @@ __device__ __forceinline__ int64_t length_of(const ARGS& a, int64_t b) {
 
 // The workgroup's tile; -1 past the last one.  Workgroup b runs on XCD b % 8: with `runs` each XCD takes
 // a run of neighbouring tiles, which share lines where a row is no whole number of 128-byte lines
-// (3 x 10007 x 2500 f32 179 us so, 228 tile by tile; where rows are whole lines tile by tile is
-// faster: 32 x 1024 x 2048 f16 88 us, 95 in runs).
+// (3 x 10007 x 2500 f32 194 us so, 247 tile by tile; where rows are whole lines tile by tile is
+// a little faster: 32 x 1024 x 2048 f16 92 us, 94 in runs).
 __device__ __forceinline__ int64_t item_of(int64_t items, bool runs) {
     if (!runs) return blockIdx.x < items ? (int64_t)blockIdx.x : -1;
     const int64_t per = (items + 7) / 8, at = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
@@ -702,15 +702,18 @@ struct ScanPlan {
     bool runs;
 };
 
-// One workgroup a tile of channels: of 64 words, or of 32 where that leaves compute units without one
-// (120 tiles of 64: 342 us for 3 x 10007 x 2500 f32, 240 of 32: 245; 256 tiles of 64: 100 us for 8 x 2048
-// x 4096 bf16, 512 of 32: 105).  Where those are still few, the chunks' effects are taken first (gate
-// and x read twice) and 512 workgroups share the sequences (1 x 32768 x 2048 bf16 131 us; a workgroup a
-// tile 1375; 240 tiles 245 us without it, 350 with it).
+// One workgroup a tile of channels: of 64 words, or of 32 where twice as many tiles still have a compute
+// unit each.  Forward and backward, us: 120 tiles of 64 (3 x 10007 x 2500 f32) 306 and 487, 240 of 32 194
+// and 332; 128 (16 x 1024 x 1024 bf16) 38 and 46, 256 of 32 23 and 38; but 144 (9 x 2048 x 2048 bf16) 52 and
+// 109, 288 of 32 53 and 124; 192 (6 x 2048 x 4096 bf16) 64 and 118, 384 of 32 74 and 144.  Where those are
+// still few, the chunks' effects are taken first (gate and x read twice) and 512 workgroups share the
+// sequences: 32 tiles of 32 (1 x 32768 x 2048 bf16) 133 and 211, a workgroup a tile 464 and 942; 128 (2 x
+// 4096 x 4096 bf16) 58 and 94, a workgroup a tile 60 and 129; but 240 (3 x 10007 x 2500 f32) 194 and 332
+// without it, 330 and 508 with it.
 ScanPlan scan_plan(int64_t batch, int64_t steps, int64_t d, det_dtype dtype, int spans) {
     ScanPlan p;
     const int64_t es = (int64_t)lm_size(dtype), ch = 4 / es;
-    p.lanes = d == 1 || cdiv(d, 64 * ch) * batch <= 160 ? 32 : 64;
+    p.lanes = d == 1 || cdiv(d, 64 * ch) * batch <= 128 ? 32 : 64;
     p.tiles = cdiv(d, p.lanes * (d == 1 ? 1 : ch));
     p.chunks = cdiv(steps, kSteps * spans);
     p.parts = 1;

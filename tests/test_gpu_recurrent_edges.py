@@ -153,3 +153,20 @@ def test_long_sums_of_few_rows_go_through_several_accumulators(dev, rows, d, t):
     want = 1024 + (d - 1) * 2.0 ** -18
     steps = -(-d // 16) // (2 if t == torch.float32 else 4)
     assert ((got.lse.double() - want).abs() <= (steps + 4) * 2.0 ** -14).all()
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+def test_sequences_keep_their_bits_across_the_widths_of_a_tile(dev, t):
+    """128 tiles of 64 words and one more: halved tiles, then whole ones, and a sequence alone."""
+    steps, d = 140, 128 if t != torch.float32 else 64      # a tile a sequence
+    gate, x = randn((129, steps, d), t, dev, 1), randn((129, steps, d), t, dev, 2)
+    dh = randn((129, steps, d), t, dev, 3)
+    outs = []
+    for n in (129, 128, 1):
+        r = det.det_gated_scan(gate[:n], x[:n], None, True)
+        outs.append([*r, *det.det_gated_scan_backward(dh[:n], gate[:n], x[:n], r.h, None, None, True)[:2]])
+    for more in outs[:2]:
+        for a, b in zip(more, outs[2]):
+            assert torch.equal(a[:1], b)
+    for a, b in zip(outs[0], outs[1]):
+        assert torch.equal(a[:128], b)
