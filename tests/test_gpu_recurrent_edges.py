@@ -1,6 +1,6 @@
 """The recurrent model's operators where a shortcut, a grid's bound or a sum's order could show: gates
 that are not finite beside a state of zero, more tiles than a grid holds, factors whose parts err to
-one side, long sums of a few rows' logits."""
+one side, long sums of a few rows' logits, tokens by the ten thousand of a small vocabulary."""
 import pytest
 import torch
 
@@ -170,3 +170,20 @@ def test_sequences_keep_their_bits_across_the_widths_of_a_tile(dev, t):
             assert torch.equal(a[:1], b)
     for a, b in zip(outs[0], outs[1]):
         assert torch.equal(a[:128], b)
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("n,vocab", [(65537, 1), (70000, 2), (65537, 256), (70001, 257), (66000, 100000)])
+def test_table_gradients_of_many_tokens_and_few_or_no_entries(dev, n, vocab, dtype):
+    """Through the radix sort: a vocabulary of one entry, around a digit's 256, and tokens of which none
+    counts.  Whole numbers below 2^24, so that every sum is exact."""
+    g = torch.Generator(dev).manual_seed(n)
+    ids = torch.randint(-1, vocab + 1, (n,), generator=g, device=dev).to(dtype)
+    dout = torch.randint(-3, 4, (n, 9), generator=g, device=dev).float()
+    got = det.det_embedding_backward(dout, ids, vocab)
+    on = (ids >= 0) & (ids < vocab)
+    want = torch.zeros(vocab + 1, 9, dtype=torch.float64, device=dev)
+    want.index_add_(0, torch.where(on, ids, vocab).long(), dout.double())
+    assert torch.equal(got.double(), want[:-1])
+    none = torch.where(on, torch.full_like(ids, vocab), ids)
+    assert (det.det_embedding_backward(torch.full_like(dout, float("nan")), none, vocab) == 0).all()
