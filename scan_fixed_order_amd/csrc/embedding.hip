@@ -40,8 +40,8 @@ struct EmbedArgs {
 };
 
 // A team of lanes takes R neighbouring rows, whose tokens and then whose vectors are in flight
-// together.  Bound by HBM, or for a few tokens by the latency of a token and of its row: 32768 tokens x 2048
-// bf16 36 us (89 MB fetched, since tokens repeat, and 134 written: 6.2 TB/s), one token 3.
+// together.  Bound by HBM, or for a few tokens by the latency of a token and of its row: 16384 tokens x 4096
+// bf16 36 us (89 MB fetched, since tokens repeat, and 134 written: 6.2 TB/s), 64 tokens 3.
 template <typename T, int R>
 __global__ __launch_bounds__(256) void k_embedding(EmbedArgs a) {
     const int lanes = 1 << a.lanes_log2;
@@ -344,7 +344,7 @@ __device__ __forceinline__ void sum_rows(const EmbedBackArgs& a, int64_t item) {
 }
 
 // Both in one launch, the blocks (the longer work) first.  Bound by HBM: dout is read once, the gradient
-// written once (32768 tokens x 2048 bf16 into 65536 rows 88 us, 402 MB, 4.6 TB/s; x 768 into 50257 rows 30,
+// written once (32768 tokens x 2048 bf16 into 65536 rows 84 us, 403 MB, 4.8 TB/s; x 768 into 50257 rows 30,
 // where frequent tokens' rows come one behind the other).
 template <typename T>
 __global__ __launch_bounds__(256) void k_embedding_sums(EmbedBackArgs a, int64_t blocks) {

@@ -6,6 +6,8 @@
 // h[t] from behind (the final state's, or 0, at the last step):
 //   G[t] = dh[t] + E[t+1];  E[t] = a[t] G[t];  the first state's gradient is E[0]
 //   dx = G, dgate = G h[t-1];  sigmoid gates: dx = (1 - a) G, dgate = a (1 - a) (h[t-1] - x) G
+// The backward pass takes h as it was stored, rounded to the storage type once: the unrounded one would be a
+// second recurrence, or 32 bits a step kept.  dgate is off by that half step of h times a (1 - a) G.
 // Steps at or past a sequence's length keep the state and have h, dx and dgate 0.
 //
 // Order, fixed by a step's own position: a span of 8 steps is a chain of fused multiply-adds from the
@@ -352,8 +354,8 @@ __device__ __forceinline__ float enter(const ARGS& a, const Place& p, const floa
 }
 
 // A workgroup walks chunks of 64 (or 32) words of channels, the next two chunks' words in flight while
-// this one's effects go round.  One pass over gate and x: bound by HBM.  8 x 2048 x 4096 bf16 88 us (403 MB,
-// 4.6 TB/s), 3 x 10007 x 2500 f32, ragged, 183 (847 MB, 4.6; rows are no whole number of lines).
+// this one's effects go round.  One pass over gate and x: bound by HBM.  8 x 2048 x 4096 bf16 89 us (403 MB,
+// 4.5 TB/s), 3 x 10007 x 2500 f32, ragged, 183 (847 MB, 4.6; rows are no whole number of lines).
 template <typename T, bool SIG, int LANES>
 __global__ __launch_bounds__(LANES * kSpans) void k_gated_scan(ScanArgs a) {
     constexpr int E = kCh<T>, CH = LANES * E, kChunkSteps = kSteps * kSpans, kMine = kSteps * 64 / LANES;
@@ -566,7 +568,7 @@ __device__ __forceinline__ void read_before(const ScanBackArgs& a, const Place& 
     }
 }
 
-// As k_gated_scan from the last step on.  8 x 2048 x 4096 bf16 160 us: 821 MB at 5.1 TB/s, h read a step before
+// As k_gated_scan from the last step on.  8 x 2048 x 4096 bf16 159 us: 821 MB at 5.2 TB/s, h read a step before
 // dh, gate and x.
 template <typename T, bool SIG, int LANES>
 __global__ __launch_bounds__(LANES * kBackSpans) void k_gated_scan_backward(ScanBackArgs a) {

@@ -8,7 +8,8 @@
 // Every product is C[i][j] = sum over k of A[i][k] B[j][k], one kernel with four endings:
 //   stats    i vocabulary, j rows of x, k width:  largest logit and sum of a tile's logits per row
 //   dlogits  the same product again: D by rows (for dx) and by columns (for dweight), rounded to the
-//            storage type once
+//            storage type once, as the matrix instructions take both their factors in it: the gradients of
+//            4096 x 65536 x 4096 bf16 are off by 1.45 times what a D of 32 bits gives
 //   dx       i width, j rows, k a piece of the vocabulary: weight transposed, D
 //   dweight  i width, j vocabulary, k rows: x transposed, D's columns times dloss (f32: x times dloss)
 // f32 goes through the matrix units in three bfloat16 parts of 8 bits each (exact together) and six
@@ -376,10 +377,11 @@ __device__ __forceinline__ bool tile_of(const GemmArgs& a, int64_t& i0, int64_t&
 // different banks.  What lies past an operand's rows or k reads as zero (the buffer's bounds).
 //
 // Bound by the matrix units and the clock that their power leaves: 4096 rows x 65536 entries x 4096 bf16
-// takes 1.71 ms (1.28 PFLOP/s) for the sums of the softmax, 445 to 465 us for a quarter of dx or of dweight (1.2)
-// and 505 for a quarter of D, which is stored twice; the matrix units work 62 % of the cycles at 1.87 GHz,
-// LDS has no bank conflicts.  A row takes 41 us (268 MB, 6.5 TB/s).  Slower by 3 and 10 %: steps of half the
-// depth, four in turn; four waves with tiles of 128 x 128.
+// takes 1.79 ms (1.23 PFLOP/s) for the sums of the softmax, 460 us for a quarter of dx or of dweight (1.2) and
+// 518 for a quarter of D, which is stored twice; of the cycles (1.7 GHz over the sums) the matrix units work
+// 70, 63 and 56 %, LDS has no bank conflicts in the products.  (Another card: 1.71 ms, 445 and 502 us.)  A row
+// takes 42 us (268 MB, 6.4 TB/s).  Slower by 3 and 10 %: steps of half the depth, four in turn; four waves
+// with tiles of 128 x 128.
 // STAGED: rows that do not lie on 16 bytes go through registers instead (517 x 50021 f16: 1003 elements a row 113
 // us, 1004 100, 1008 80; a vector off 16 bytes spans two lines).
 template <typename T, int WI, int WJ, int MI, int MJ, bool STAGED, int END>
@@ -624,7 +626,7 @@ __device__ __forceinline__ void xent_product(const GemmArgs& a) {
 // Cutting a step into parts takes the vector units about as long as its products the matrix units: half
 // of the eight waves do the one while the others do the other.  A tile of few columns waits for
 // memory instead and has two steps on their way.  1024 rows x 20000 x 1024: 250 us (168 TFLOP/s, six times as
-// many in bfloat16; the library's f32 product reaches 152); 8 rows x 30000 x 1000 42 us, 2.9 TB/s.
+// many in bfloat16; the library's f32 product reaches 152); 8 rows x 30000 x 1000 42 to 45 us, 2.8 TB/s.
 template <int WI, int WJ, int MI, int MJ, bool AK, bool BK, int END>
 __device__ __forceinline__ void xent_product_f32(const GemmArgs& a) {
     constexpr int BI = WI * MI * 32, BJ = WJ * MJ * 32, NW = WI * WJ;
@@ -995,7 +997,8 @@ int tile_columns(int64_t rows, int64_t vocab, bool f32) {
 }
 
 // Rows (vocabulary entries) of such a tile.  Width 128 with 128 of them, two workgroups a unit: 96 rows x 32768 x
-// 4096 bf16 68 us, with 256 81; 128 rows x 8000 47 and 57, but 128 rows x 100001 x 257 42 and 36.
+// 4096 bf16 68 us, with 256 81; 128 rows x 8000 47 and 57.  The rule does not look at d: with five steps of k
+// the larger tile would be the better one (128 rows x 100001 x 257 42 us, with 256 36).
 int64_t tile_rows(int columns, bool f32) { return columns == 32 ? 64 : columns == 128 && !f32 ? 128 : 256; }
 
 template <typename T, bool STAGED, int END>
