@@ -7,7 +7,7 @@
 //   G[t] = dh[t] + E[t+1];  E[t] = a[t] G[t];  the first state's gradient is E[0]
 //   dx = G, dgate = G h[t-1];  sigmoid gates: dx = (1 - a) G, dgate = a (1 - a) (h[t-1] - x) G
 // The backward pass takes h as it was stored, rounded to the storage type once: the unrounded one would be a
-// second recurrence, or 32 bits a step kept.  dgate is off by that half step of h times a (1 - a) G.
+// second recurrence, or 32 bits a step kept.  dgate is off by that half step of h times G (or a (1 - a) G).
 // Steps at or past a sequence's length keep the state and have h, dx and dgate 0.
 //
 // Order, fixed by a step's own position: a span of 8 steps is a chain of fused multiply-adds from the

@@ -16,10 +16,10 @@
 // products of parts; the three left out are within 2^-22 of the whole one, to either side, and an infinite
 // factor may give NaN.
 //
-// Order: k ascending in steps of 16 inside the matrix instruction's own order, f32 accumulators (in tiles of
-// 32 columns several in turn, joined in pairs: chains_of); a tile's logits, then the tiles of a row by lanes and the adjacent-lanes tree; dx adds pieces of the
-// vocabulary in ascending order, then the parts that share a piece.  All of it fixed by (rows,
-// vocab, d, dtype).
+// Order: k ascending in steps of 16 inside the matrix instruction's own order, f32 accumulators (in tiles
+// of 32 columns several in turn, joined in pairs: chains_of); a tile's logits, then the tiles of a row by
+// lanes and the adjacent-lanes tree; dx adds pieces of the vocabulary in ascending order, then the parts
+// that share a piece.  All of it fixed by (rows, vocab, d, dtype).
 #include "det_internal.h"
 #include "lm_device.h"
 
